@@ -91,7 +91,10 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_INT8 = 1, PA_KV_NVFP4 = 2, PA_KV_FP8 = 3 } 
 #define PA_ERRF_LEN_LT_QLEN       0x8u  /* verify: 0 < seq_len < q_len: rows with no key get 0 */
 #define PA_ERRF_WAIT_TIMEOUT      0x10u /* an in-kernel wait hit its iteration cap: outputs invalid */
 #define PA_ERRF_PLAN_OVERFLOW     0x20u /* the split plan did not fit the workspace: nothing computed */
-#define PA_ERRF_BAD_SLOT          0x40u /* pa_append_kv: slot outside [-1, 16 * num_blocks): row skipped */
+#define PA_ERRF_BAD_SLOT          0x40u /* pa_append_kv, pa_rope_append: slot outside
+                                           [-1, 16 * num_blocks): row skipped */
+#define PA_ERRF_BAD_Q_START       0x80u /* pa_prefill: q_starts descending or outside
+                                           [0, num_tokens]: clamped */
 
 /* The paged KV pool.  block_size must be 16; head_dim 128 or 256. */
 typedef struct pa_kv_cache {
@@ -327,6 +330,121 @@ int pa_decode_wo(const pa_kv_cache *kv, const pa_problem *prob, const pa_wo *wo,
  * PA_ERR_UNSUPPORTED (head_dim, block_size) or PA_ERR_CUDA. */
 int pa_append_kv(const pa_kv_cache *kv, const void *k_new, const void *v_new, int32_t num_tokens,
                  const int64_t *slot_mapping, void *ws, pa_stream_t stream);
+
+/* Norm, position rotation and cache write of new tokens in one pass: the
+ * step between the QKV projection and the attention.  For every (token,
+ * head) row x of the queries and keys, in fp32:
+ *   norm (optional)  x_d <- x_d * w_d / sqrt(mean_d(x_d^2) + eps)
+ *   rotation         pair i < rot_dim / 2 turns by a = position * inv_freq[i]:
+ *                    (x, y) <- attn_factor * (x cos a - y sin a,
+ *                                             x sin a + y cos a)
+ *                    with (x, y) = (x_i, x_{i + rot_dim / 2}), or, if
+ *                    interleaved, (x_{2 i}, x_{2 i + 1}); the dims from
+ *                    rot_dim on pass through.  The angle is exact: no
+ *                    rounding of position * inv_freq, at any int32 position.
+ * Queries are rounded to bf16 into q_out; keys and values (values are
+ * neither normalised nor rotated) are encoded from fp32 into the pool as
+ * pa_append_kv encodes them, at slot_mapping[t] (-1: a padded row, whose
+ * queries are still written and whose keys and values are dropped).
+ * q, k, v and q_out rows are [heads, head_dim] contiguous with any distance
+ * between tokens, so they can be slices of one fused projection; q_out may
+ * be q itself (same pointer and stride), else it must not overlap the inputs. */
+typedef struct pa_rope {
+  int32_t num_tokens;           /* T >= 0 */
+  int32_t num_q_heads;          /* Hq >= 0 (0: keys and values only) */
+  const void *q;                /* bf16 [T, Hq, D] */
+  const void *k;                /* bf16 [T, Hkv, D] */
+  const void *v;                /* bf16 [T, Hkv, D] */
+  void *q_out;                  /* bf16 [T, Hq, D] */
+  int64_t q_stride;             /* elements between tokens, multiples of 8 */
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t q_out_stride;
+  const int32_t *positions;     /* int32 [T] */
+  const int64_t *slot_mapping;  /* int64 [T], distinct, as in pa_append_kv */
+  int32_t rot_dim;              /* a multiple of 32, 0..D (0: no rotation) */
+  int32_t interleaved;          /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+  const float *inv_freq;        /* fp32 [rot_dim / 2] radians per position, finite */
+  float attn_factor;            /* scales the rotated pairs; 1 normally */
+  const void *q_norm;           /* bf16 [D] norm weights, or NULL: no norm */
+  const void *k_norm;
+  float eps;                    /* >= 0 */
+} pa_rope;
+
+/* kv: the pool, its code and scale arrays are written.  ws: NULL, or >= 256
+ * bytes whose header receives the flags (PA_ERRF_BAD_SLOT). */
+int pa_rope_append(const pa_kv_cache *kv, const pa_rope *rope, void *ws, pa_stream_t stream);
+
+/* (host) The inverse frequencies base^(-2 i / rot_dim) of rot_dim / 2 pairs,
+ * scaled for contexts `factor` times the original one:
+ *   PA_ROPE_PLAIN   not scaled (factor ignored)
+ *   PA_ROPE_LINEAR  divided by factor (positions interpolated)
+ *   PA_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)): the fastest pair
+ *                   is kept, the slowest divided by factor
+ *   PA_ROPE_YARN    by wavelength: pairs that turn more than `beta_fast` times
+ *                   over original_len positions are kept, those that turn less
+ *                   than `beta_slow` times are divided by factor, and a linear
+ *                   ramp over the pair index joins the two; *attn_factor =
+ *                   0.1 ln(factor) + 1 (1 for the other kinds)
+ * inv_freq: (host) float [rot_dim / 2]; attn_factor: (host) float or NULL. */
+enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_NTK = 2, PA_ROPE_YARN = 3 };
+int pa_rope_frequencies(int32_t rot_dim, double base, int32_t kind, double factor,
+                        int32_t original_len, double beta_fast, double beta_slow,
+                        float *inv_freq, float *attn_factor);
+
+/* Score options of pa_prefill and pa_decode_scored (NULL or all zero: plain
+ * softmax).  For the query at position p and the key at position t:
+ *   s = softmax_scale * <q, k>
+ *   softcap c > 0:   s <- c * tanh(s / c)
+ *   alibi_slopes:    s <- s - alibi_slopes[head] * |p - t|
+ *   visible iff      0 <= t < seq_len, t <= p or t < prefix_lens[b],
+ *                    t >= first_key[query], and (window > 0) t > p - window
+ * first_key separates documents packed into one sequence; a query that sees
+ * no key has output 0 and lse -inf.  Keys hidden from every query of a
+ * sequence's chunk are never read. */
+typedef struct pa_score {
+  float softcap;               /* 0: none; else > 0 and finite */
+  int32_t window;              /* 0: none; else the last `window` keys up to the query's own */
+  const float *alibi_slopes;   /* fp32 [num_q_heads], or NULL */
+  const int32_t *first_key;    /* int32, one per query token: [num_tokens] (pa_prefill) or
+                                  [batch] (pa_decode_scored), or NULL */
+  const int32_t *prefix_lens;  /* int32 [batch], or NULL (pa_prefill; no effect on decode) */
+} pa_score;
+
+/* Decode (q_len 1) with score options: arguments, split plan, outputs and
+ * flags as pa_decode; a window (or first_key) also shortens what is read.
+ * opt->kernel: 0, 2 or 5 (else PA_ERR_UNSUPPORTED). */
+int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_score *score,
+                     const pa_options *opt, void *ws, size_t ws_bytes, pa_stream_t stream);
+
+/* Prompts: a ragged batch of chunks of new tokens attends over the paged
+ * cache, which already holds them (pa_rope_append / pa_append_kv).  Sequence
+ * b owns the query rows q_starts[b] .. q_starts[b + 1] - 1, its last tokens:
+ * the row i of q_len is at position p = seq_lens[b] - q_len + i and sees the
+ * keys t <= p, subject to `score`.  Rows of q before q_starts[0] or from
+ * q_starts[batch] on are neither read nor written.  Any Hq / Hkv up to 8,
+ * any chunk length from one token. */
+typedef struct pa_prefill_problem {
+  int32_t batch;               /* B >= 0 */
+  int32_t num_q_heads;         /* Hq, a multiple of num_kv_heads; Hq / Hkv <= 8 */
+  int32_t num_tokens;          /* rows of q, >= 0 */
+  const void *q;               /* bf16 [num_tokens, Hq, D] */
+  const int32_t *q_starts;     /* int32 [B + 1], ascending, within [0, num_tokens] */
+  const int32_t *block_tables; /* int32 [B, block_table_stride] physical block ids */
+  int32_t block_table_stride;
+  const int32_t *seq_lens;     /* int32 [B] keys in the cache per sequence, new ones included */
+  int32_t max_seq_len;         /* (host) upper bound of seq_lens: sizes the key splits */
+  float softmax_scale;
+  void *out;                   /* bf16 (or fp32 if out_fp32) [num_tokens, Hq, D] */
+  int32_t out_fp32;
+  float *lse_out;              /* optional fp32 [num_tokens, Hq] natural-log LSE, or NULL */
+} pa_prefill_problem;
+
+/* Workspace of pa_prefill (0 on invalid arguments): 256 bytes, more where the
+ * chunks are too few to fill the GPU and the key axis is split. */
+size_t pa_prefill_workspace_bytes(const pa_kv_cache *kv, const pa_prefill_problem *prob);
+int pa_prefill(const pa_kv_cache *kv, const pa_prefill_problem *prob, const pa_score *score,
+               void *ws, size_t ws_bytes, pa_stream_t stream);
 
 /* Copies the device error flags (PA_ERRF_*) of the last call that used ws
  * to *host_flags (host).  Synchronises `stream`. */

@@ -12,7 +12,8 @@ import importlib
 
 _SUBMODULES = ("pa", "workloads", "build")
 _API = ("decode", "verify", "merge", "dequant_gather", "workspace_bytes", "read_error",
-        "status_string", "KvCache", "PaError", "library_path")
+        "status_string", "KvCache", "PaError", "library_path", "Score", "rope_append",
+        "rope_frequencies", "prefill", "decode_scored")
 
 
 def __getattr__(name):

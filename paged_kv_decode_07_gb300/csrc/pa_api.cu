@@ -40,26 +40,59 @@ int decode_tc_occupancy_int8(int D, int R);
 int decode_tc_occupancy_nvfp4(int D, int R);
 int decode_tc_occupancy_fp8(int D, int R);
 
+// the scored variants (pa_score)
+cudaError_t launch_scored_tc_bf16(const AttnParams &p, int grid, cudaStream_t s);
+cudaError_t launch_scored_tc_int8(const AttnParams &p, int grid, cudaStream_t s);
+cudaError_t launch_scored_tc_nvfp4(const AttnParams &p, int grid, cudaStream_t s);
+cudaError_t launch_scored_tc_fp8(const AttnParams &p, int grid, cudaStream_t s);
+cudaError_t launch_scored_tc_cluster_bf16(const AttnParams &p, int P, cudaStream_t s);
+cudaError_t launch_scored_tc_cluster_int8(const AttnParams &p, int P, cudaStream_t s);
+cudaError_t launch_scored_tc_cluster_nvfp4(const AttnParams &p, int P, cudaStream_t s);
+cudaError_t launch_scored_tc_cluster_fp8(const AttnParams &p, int P, cudaStream_t s);
+int scored_tc_occupancy_bf16(int D, int R);
+int scored_tc_occupancy_int8(int D, int R);
+int scored_tc_occupancy_nvfp4(int D, int R);
+int scored_tc_occupancy_fp8(int D, int R);
+
+cudaError_t launch_scored_tc(const AttnParams &p, int grid, cudaStream_t s) {
+  switch (p.kv.dtype) {
+    case PA_KV_BF16: return launch_scored_tc_bf16(p, grid, s);
+    case PA_KV_INT8: return launch_scored_tc_int8(p, grid, s);
+    case PA_KV_NVFP4: return launch_scored_tc_nvfp4(p, grid, s);
+    case PA_KV_FP8: return launch_scored_tc_fp8(p, grid, s);
+  }
+  return cudaErrorInvalidValue;
+}
+cudaError_t launch_scored_tc_cluster(const AttnParams &p, int P, cudaStream_t s) {
+  switch (p.kv.dtype) {
+    case PA_KV_BF16: return launch_scored_tc_cluster_bf16(p, P, s);
+    case PA_KV_INT8: return launch_scored_tc_cluster_int8(p, P, s);
+    case PA_KV_NVFP4: return launch_scored_tc_cluster_nvfp4(p, P, s);
+    case PA_KV_FP8: return launch_scored_tc_cluster_fp8(p, P, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
 // CTAs of the tensor-core decode kernel one SM holds at once, 0 if unknown;
 // queried once per (device, format, head dim, rows) and kept
-int decode_tc_occupancy(int dtype, int D, int R) {
+int decode_tc_occupancy(int dtype, int D, int R, bool scored = false) {
   constexpr int kDevs = 16;
-  static std::atomic<int> known[kDevs][4][2][kMaxG + 1];   // occupancy + 1, 0 = not yet asked
+  static std::atomic<int> known[kDevs][2][4][2][kMaxG + 1];   // occupancy + 1, 0 = not yet asked
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dtype < PA_KV_BF16 || dtype > PA_KV_FP8 || R < 1 || R > kMaxG || (D != 128 && D != 256))
     return 0;
-  std::atomic<int> *slot = dev >= 0 && dev < kDevs ? &known[dev][dtype][D == 256][R] : nullptr;
+  std::atomic<int> *slot = dev >= 0 && dev < kDevs ? &known[dev][scored][dtype][D == 256][R] : nullptr;
   if (slot) {
     const int v = slot->load(std::memory_order_relaxed);
     if (v > 0) return v - 1;
   }
   int n = 0;
   switch (dtype) {
-    case PA_KV_BF16: n = decode_tc_occupancy_bf16(D, R); break;
-    case PA_KV_INT8: n = decode_tc_occupancy_int8(D, R); break;
-    case PA_KV_NVFP4: n = decode_tc_occupancy_nvfp4(D, R); break;
-    case PA_KV_FP8: n = decode_tc_occupancy_fp8(D, R); break;
+    case PA_KV_BF16: n = scored ? scored_tc_occupancy_bf16(D, R) : decode_tc_occupancy_bf16(D, R); break;
+    case PA_KV_INT8: n = scored ? scored_tc_occupancy_int8(D, R) : decode_tc_occupancy_int8(D, R); break;
+    case PA_KV_NVFP4: n = scored ? scored_tc_occupancy_nvfp4(D, R) : decode_tc_occupancy_nvfp4(D, R); break;
+    case PA_KV_FP8: n = scored ? scored_tc_occupancy_fp8(D, R) : decode_tc_occupancy_fp8(D, R); break;
   }
   if (slot && n > 0) slot->store(n + 1, std::memory_order_relaxed);
   return n;
@@ -265,9 +298,33 @@ KvView view_of(const pa_kv_cache *kv) {
   return v;
 }
 
+int check_score(const pa_score *sc) {
+  if (!sc) return PA_OK;
+  if (!std::isfinite(sc->softcap) || sc->softcap < 0.f || sc->window < 0) return PA_ERR_INVALID_ARG;
+  if (!aligned4(sc->alibi_slopes) || !aligned4(sc->first_key) || !aligned4(sc->prefix_lens))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+ScoreView score_view(const pa_score *sc, float softmax_scale) {
+  ScoreView v;
+  std::memset(&v, 0, sizeof v);
+  if (!sc) return v;
+  if (sc->softcap > 0.f) {
+    v.cap_in = 2.0f * 1.4426950408889634f * softmax_scale / sc->softcap;
+    v.cap_log2 = sc->softcap * 1.4426950408889634f;
+  }
+  v.slopes = sc->alibi_slopes;
+  v.window = sc->window;
+  v.first_key = sc->first_key;
+  v.prefix = sc->prefix_lens;
+  return v;
+}
+
+// sc: scored decode (pa_decode_scored), else null
 int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *o, void *ws,
                   size_t ws_bytes, cudaStream_t stream, bool verify,
-                  const uint32_t *extra_err = nullptr) {
+                  const uint32_t *extra_err = nullptr, const pa_score *sc = nullptr) {
   int st = check_kv(kv);
   if (st) return st;
   st = check_problem(kv, p, verify ? kMaxQLen : 1);
@@ -277,6 +334,10 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   if (o && (o->split_blocks < 0 || o->target_items < 0)) return PA_ERR_INVALID_ARG;
   const int test_flags = o ? o->test_flags : 0;
   if (test_flags & ~PA_TEST_EXPIRE_WAIT) return PA_ERR_INVALID_ARG;
+  // scored decode is built into the tensor-core decode kernel
+  if (sc && (kernel == 1 || kernel == 3 || kernel == 4 || test_flags ||
+             !tc_supported(kv->dtype, kv->head_dim, p->num_q_heads / kv->num_kv_heads)))
+    return PA_ERR_UNSUPPORTED;
   if (p->batch == 0) return PA_OK;
   const int G = p->num_q_heads / kv->num_kv_heads;
   // Kernel choice.  auto: tensor cores (the CUDA cores cannot issue the
@@ -313,7 +374,10 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   // blocks fit 8 per CTA of a cluster of at most 8, and all clusters run at
   // once; the planner and the merge kernel (two launches) are then pure
   // latency
-  const int maxblk_all = ceil_div(std::max(p->max_seq_len, 1), kBlock);
+  // (a window bounds what any sequence reads: its keys and one partial block)
+  int span = std::max(p->max_seq_len, 1);
+  if (sc && sc->window > 0) span = (int)std::min<long long>(span, (long long)sc->window + kBlock);
+  const int maxblk_all = ceil_div(span, kBlock);
   int cluster = std::min(kClusterMax, std::max(1, ceil_div(maxblk_all, kClusterBlocksPerCta)));
   if (kernel == 0 && use_tc && !dense && !verify && Q == 1 && !extra_err &&
       !(o && (o->split_blocks > 0 || o->target_items > 0)) &&
@@ -351,7 +415,10 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
     if (o && o->event_begin &&
         cudaEventRecord(static_cast<cudaEvent_t>(o->event_begin), stream) != cudaSuccess)
       return PA_ERR_CUDA;
-    if (launch_decode_tc_cluster(ap, cluster, stream) != cudaSuccess) return PA_ERR_CUDA;
+    if (sc) ap.sc = score_view(sc, p->softmax_scale);
+    if ((sc ? launch_scored_tc_cluster(ap, cluster, stream)
+            : launch_decode_tc_cluster(ap, cluster, stream)) != cudaSuccess)
+      return PA_ERR_CUDA;
     if (o && o->event_end &&
         cudaEventRecord(static_cast<cudaEvent_t>(o->event_end), stream) != cudaSuccess)
       return PA_ERR_CUDA;
@@ -396,7 +463,7 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
     pp.resident = sms;
     pp.item_cost = kItemCostVerify;
   } else if (sms > 0 && use_tc && !dense) {
-    pp.resident = sms * decode_tc_occupancy(kv->dtype, kv->head_dim, L.R);
+    pp.resident = sms * decode_tc_occupancy(kv->dtype, kv->head_dim, L.R, sc != nullptr);
     pp.item_cost = kItemCostDecode;
   }
   pp.split_blocks = o ? o->split_blocks : 0;
@@ -409,6 +476,10 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   pp.prefix_a = reinterpret_cast<int *>(w + L.prefix_a);
   pp.prefix_b = reinterpret_cast<int *>(w + L.prefix_b);
   pp.extra_err = extra_err;
+  if (sc) {
+    pp.window = sc->window;
+    pp.first_key = sc->first_key;
+  }
 
   AttnParams ap;
   std::memset(&ap, 0, sizeof ap);
@@ -437,12 +508,15 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   ap.R = L.R;
   ap.test_expire = (test_flags & PA_TEST_EXPIRE_WAIT) ? 1 : 0;
 
+  if (sc) ap.sc = score_view(sc, p->softmax_scale);
+
   if (launch_plan(pp, stream) != cudaSuccess) return PA_ERR_CUDA;
   if (o && o->event_begin &&
       cudaEventRecord(static_cast<cudaEvent_t>(o->event_begin), stream) != cudaSuccess)
     return PA_ERR_CUDA;
   if ((umma    ? launch_verify_umma(ap, L.max_items, stream)
        : dense ? launch_verify_dense(ap, L.max_items, stream)
+       : sc    ? launch_scored_tc(ap, L.max_items, stream)
              : use_tc ? launch_decode_tc(ap, L.max_items, stream)
                       : launch_decode_simt(ap, L.max_items, stream)) != cudaSuccess)
     return PA_ERR_CUDA;
@@ -539,6 +613,39 @@ WoLayout wo_layout(const pa_kv_cache *kv, const pa_problem *p, const pa_wo *wo,
   W.part = W.o + up((size_t)W.M * W.K * 4);
   W.total = W.part + up(W.splits > 1 ? (size_t)W.splits * W.M * wo->hidden * 4 : 0);
   return W;
+}
+
+// ---- ragged prefill
+struct PrefillLayout {
+  int splits;
+  size_t part_lse, part_o, total;
+};
+
+int check_prefill_sizes(const pa_kv_cache *kv, const pa_prefill_problem *p) {
+  if (!p || p->batch < 0 || p->num_tokens < 0 || p->max_seq_len < 0) return PA_ERR_INVALID_ARG;
+  if (p->num_q_heads < 1 || p->num_q_heads % kv->num_kv_heads) return PA_ERR_INVALID_ARG;
+  if (p->num_q_heads / kv->num_kv_heads > kMaxG) return PA_ERR_UNSUPPORTED;
+  if (!std::isfinite(p->softmax_scale)) return PA_ERR_INVALID_ARG;
+  if (p->batch > 0 && (p->block_table_stride < 1 || p->block_table_stride > (1 << 26)))
+    return PA_ERR_INVALID_ARG;
+  // rows (token, head) and tiles stay within 32-bit indices
+  if ((long long)p->num_tokens * p->num_q_heads > (1LL << 30) || p->batch > (1 << 24) ||
+      ((long long)p->num_tokens + p->batch) * p->num_q_heads > (1LL << 30))
+    return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+PrefillLayout prefill_layout(const pa_kv_cache *kv, const pa_prefill_problem *p) {
+  PrefillLayout L;
+  L.splits = p->batch > 0 && p->num_tokens > 0
+                 ? prefill_splits(p->num_tokens, p->batch, kv->num_kv_heads,
+                                  p->num_q_heads / kv->num_kv_heads, kv->head_dim, p->max_seq_len)
+                 : 1;
+  const size_t rows = L.splits > 1 ? (size_t)L.splits * p->num_tokens * p->num_q_heads : 0;
+  L.part_lse = kHdrWords * 4;
+  L.part_o = L.part_lse + up(rows * 4);
+  L.total = L.part_o + up(rows * kv->head_dim * 4);
+  return L;
 }
 
 }  // namespace
@@ -716,6 +823,154 @@ int pa_append_kv(const pa_kv_cache *kv, const void *k_new, const void *v_new, in
   if (num_tokens == 0) return PA_OK;
   if (launch_append(view_of(kv), k_new, v_new, num_tokens, slot_mapping, hdr, s) != cudaSuccess)
     return PA_ERR_CUDA;
+  return PA_OK;
+}
+
+int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_score *score,
+                     const pa_options *opt, void *ws, size_t ws_bytes, pa_stream_t stream) {
+  const pa_score none = {0.f, 0, nullptr, nullptr, nullptr};
+  if (!score) score = &none;
+  const int st = check_score(score);
+  if (st) return st;
+  return run_attention(kv, prob, opt, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream), false,
+                       nullptr, score);
+}
+
+size_t pa_prefill_workspace_bytes(const pa_kv_cache *kv, const pa_prefill_problem *prob) {
+  if (check_kv(kv) != PA_OK || check_prefill_sizes(kv, prob) != PA_OK) return 0;
+  return prefill_layout(kv, prob).total;
+}
+
+int pa_prefill(const pa_kv_cache *kv, const pa_prefill_problem *p, const pa_score *score, void *ws,
+               size_t ws_bytes, pa_stream_t stream) {
+  int st = check_kv(kv);
+  if (st) return st;
+  st = check_prefill_sizes(kv, p);
+  if (st) return st;
+  st = check_score(score);
+  if (st) return st;
+  if (p->batch == 0 || p->num_tokens == 0) return PA_OK;
+  if (!p->q || !p->q_starts || !p->block_tables || !p->seq_lens || !p->out) return PA_ERR_INVALID_ARG;
+  if (!aligned16(p->q) || !aligned16(p->out) || !aligned4(p->q_starts) ||
+      !aligned4(p->block_tables) || !aligned4(p->seq_lens) || !aligned4(p->lse_out))
+    return PA_ERR_INVALID_ARG;
+  if (!ws || !aligned16(ws)) return PA_ERR_INVALID_ARG;
+  const PrefillLayout L = prefill_layout(kv, p);
+  if (ws_bytes < L.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  PrefillParams a;
+  std::memset(&a, 0, sizeof a);
+  a.kv = view_of(kv);
+  a.q = static_cast<const __nv_bfloat16 *>(p->q);
+  a.T = p->num_tokens;
+  a.B = p->batch;
+  a.Hq = p->num_q_heads;
+  a.G = p->num_q_heads / kv->num_kv_heads;
+  a.q_starts = p->q_starts;
+  a.tables = p->block_tables;
+  a.stride = p->block_table_stride;
+  a.seq_lens = p->seq_lens;
+  a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  a.sc = score_view(score, p->softmax_scale);
+  a.out = p->out;
+  a.out_fp32 = p->out_fp32 ? 1 : 0;
+  a.lse_out = p->lse_out;
+  a.hdr = static_cast<uint32_t *>(ws);
+  a.splits = L.splits;
+  a.part_lse = reinterpret_cast<float *>(w + L.part_lse);
+  a.part_o = reinterpret_cast<float *>(w + L.part_o);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(ws, 0, 16, s) != cudaSuccess) return PA_ERR_CUDA;
+  return launch_prefill(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_rope_append(const pa_kv_cache *kv, const pa_rope *r, void *ws, pa_stream_t stream) {
+  int st = check_kv(kv);
+  if (st) return st;
+  if (!r || r->num_tokens < 0 || r->num_q_heads < 0) return PA_ERR_INVALID_ARG;
+  if (ws && !aligned16(ws)) return PA_ERR_INVALID_ARG;
+  if (r->rot_dim < 0 || r->rot_dim > kv->head_dim) return PA_ERR_INVALID_ARG;
+  if (r->rot_dim % 32) return PA_ERR_UNSUPPORTED;
+  if (!std::isfinite(r->attn_factor) || !std::isfinite(r->eps) || r->eps < 0.f) return PA_ERR_INVALID_ARG;
+  if ((long long)r->num_tokens * ((long long)r->num_q_heads + 2LL * kv->num_kv_heads) > (1LL << 30))
+    return PA_ERR_UNSUPPORTED;
+  if (r->num_tokens > 0) {
+    const long long q_row = (long long)r->num_q_heads * kv->head_dim;
+    if (!r->k || !r->v || !r->positions || !r->slot_mapping) return PA_ERR_INVALID_ARG;
+    if (r->num_q_heads > 0 && (!r->q || !r->q_out)) return PA_ERR_INVALID_ARG;
+    if (r->rot_dim > 0 && !r->inv_freq) return PA_ERR_INVALID_ARG;
+    if (!aligned16(r->q) || !aligned16(r->k) || !aligned16(r->v) || !aligned16(r->q_out) ||
+        !aligned16(r->q_norm) || !aligned16(r->k_norm) || !aligned4(r->positions) ||
+        !aligned4(r->inv_freq) || reinterpret_cast<uintptr_t>(r->slot_mapping) % 8 != 0)
+      return PA_ERR_INVALID_ARG;
+    if (r->q_stride % 8 || r->k_stride % 8 || r->v_stride % 8 || r->q_out_stride % 8)
+      return PA_ERR_INVALID_ARG;
+    if (r->num_tokens > 1 && (r->q_out_stride < q_row || r->q_stride < 0 || r->k_stride < 0 ||
+                              r->v_stride < 0))
+      return PA_ERR_INVALID_ARG;
+  }
+  uint32_t *hdr = static_cast<uint32_t *>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (hdr && cudaMemsetAsync(hdr, 0, 4, s) != cudaSuccess) return PA_ERR_CUDA;
+  if (r->num_tokens == 0) return PA_OK;
+  RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.kv = view_of(kv);
+  p.q = static_cast<const __nv_bfloat16 *>(r->q);
+  p.k = static_cast<const __nv_bfloat16 *>(r->k);
+  p.v = static_cast<const __nv_bfloat16 *>(r->v);
+  p.q_out = static_cast<__nv_bfloat16 *>(r->q_out);
+  p.q_stride = r->q_stride;
+  p.k_stride = r->k_stride;
+  p.v_stride = r->v_stride;
+  p.q_out_stride = r->q_out_stride;
+  p.positions = r->positions;
+  p.slots = r->slot_mapping;
+  p.T = r->num_tokens;
+  p.Hq = r->num_q_heads;
+  p.rot = r->rot_dim;
+  p.interleaved = r->interleaved ? 1 : 0;
+  p.inv_freq = r->inv_freq;
+  p.factor = r->attn_factor;
+  p.eps = r->eps;
+  p.q_norm = static_cast<const __nv_bfloat16 *>(r->q_norm);
+  p.k_norm = static_cast<const __nv_bfloat16 *>(r->k_norm);
+  p.hdr = hdr;
+  return launch_rope(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_rope_frequencies(int32_t rot_dim, double base, int32_t kind, double factor,
+                        int32_t original_len, double beta_fast, double beta_slow, float *inv_freq,
+                        float *attn_factor) {
+  if (rot_dim < 2 || rot_dim % 2 || !inv_freq) return PA_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !std::isfinite(base)) return PA_ERR_INVALID_ARG;
+  if (kind < PA_ROPE_PLAIN || kind > PA_ROPE_YARN) return PA_ERR_INVALID_ARG;
+  if (kind != PA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return PA_ERR_INVALID_ARG;
+  if (kind == PA_ROPE_NTK && rot_dim == 2) return PA_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  double lo = 0.0, hi = 0.0;
+  if (kind == PA_ROPE_YARN) {
+    if (original_len < 1 || !(beta_fast > beta_slow) || !(beta_slow > 0.0) || !std::isfinite(beta_fast))
+      return PA_ERR_INVALID_ARG;
+    // the pair index that turns `beta` times over original_len positions
+    auto pair_of = [&](double beta) {
+      return rot_dim * std::log(original_len / (beta * two_pi)) / (2.0 * std::log(base));
+    };
+    lo = std::max(0.0, std::floor(pair_of(beta_fast)));
+    hi = std::min(rot_dim - 1.0, std::ceil(pair_of(beta_slow)));
+    if (hi <= lo) hi = lo + 0.001;
+  }
+  if (kind == PA_ROPE_NTK) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (kind == PA_ROPE_LINEAR) f /= factor;
+    if (kind == PA_ROPE_YARN) {
+      const double slow = std::min(1.0, std::max(0.0, (i - lo) / (hi - lo)));
+      f = f * (1.0 - slow) + f / factor * slow;
+    }
+    inv_freq[i] = (float)f;
+  }
+  if (attn_factor) *attn_factor = kind == PA_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
   return PA_OK;
 }
 

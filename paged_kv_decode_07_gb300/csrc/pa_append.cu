@@ -11,7 +11,7 @@
 // NVFP4 gives each lane one 16-element scale block instead (two or four
 // rows per warp step).  Every rounding decision is
 // that of the IEEE fp32 quotient (formed without a division per element,
-// see the bracket below), so the codes are the format definitions' own:
+// see the bracket in pa_codec.cuh), so the codes are the format definitions' own:
 //   int8  : s = fp16_RN(amax / 127), code = clamp(RN_even(x / s), +-127)
 //   FP8   : code = E4M3_RN_satfinite(|x / g|) with the sign of x / g unless
 //           the magnitude code is 0
@@ -22,10 +22,12 @@
 // The conversions to fp16 / E4M3 / E2M1 are the hardware's round-to-nearest
 // (satfinite) cvt instructions on signed values; the FP8 rule for zero is
 // applied to the packed codes afterwards.
-#include "pa_internal.cuh"
+#include "pa_codec.cuh"
 
 namespace pa {
 namespace {
+
+using namespace codec;
 
 constexpr int kAppendWarps = 8;
 
@@ -36,32 +38,6 @@ struct AppendParams {
   int T;
   uint32_t *hdr;                        // may be null
 };
-
-// (lo, hi) -> two E4M3 codes, lo in the low byte; round to nearest even,
-// saturating at 448
-__device__ __forceinline__ uint32_t e4m3x2_rn_sat(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// eight magnitudes -> eight E2M1 codes, element 2i in the low nibble of byte i
-__device__ __forceinline__ uint32_t e2m1x8_rn_sat(const float (&a)[8]) {
-  uint32_t r;
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
-      " mov.b32 %0, {b0, b1, b2, b3};\n}\n"
-      : "=r"(r)
-      : "f"(a[0]), "f"(a[1]), "f"(a[2]), "f"(a[3]), "f"(a[4]), "f"(a[5]), "f"(a[6]), "f"(a[7]));
-  return r;
-}
-
-__device__ __forceinline__ float e4m3_to_float(uint32_t code) {
-  return __half2float(__ushort_as_half((uint16_t)(e4m3x2_u16_to_h2(code) & 0xFFFFu)));
-}
 
 template <int EPL>
 struct Chunk {   // EPL bf16 of one lane
@@ -89,74 +65,6 @@ __device__ __forceinline__ void to_float(const Chunk<EPL> &c, float (&x)[EPL]) {
     x[2 * i] = f.x;
     x[2 * i + 1] = f.y;
   }
-}
-
-// ---- quotients without a division per element.  With r an approximate
-// reciprocal of the divisor d (rcp.approx, at most 1 ulp off, i.e. a
-// relative error below 2^-23), RN(x * r) lies within 2^-22 of the IEEE
-// quotient RN(x / d), relatively.  Rounding onto a grid (integers, fp16,
-// E4M3, E2M1) is monotone, so the decision is taken at both ends of a
-// bracket that must hold the exact quotient -- x * RN(r * (1 -+ 2^-20)) --
-// and when the two ends agree that is the decision of RN(x / d) itself.
-// Otherwise (a few in 10^5 elements) the quotient is formed exactly.  For
-// int8 the bracket is the distance to the nearest half integer instead:
-// |x / d| < 2^8 there, so RN(x * r) is within 2^-14 of RN(x / d) and a
-// margin of 2^-13 decides.
-constexpr float kBracketLo = 1.0f - 0x1p-20f;
-constexpr float kBracketHi = 1.0f + 0x1p-20f;
-constexpr float kInf = __builtin_huge_valf();
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(*reinterpret_cast<unsigned long long *>(&d))
-      : "l"(*reinterpret_cast<unsigned long long *>(&a)),
-        "l"(*reinterpret_cast<unsigned long long *>(&b)));
-  return d;
-}
-
-__device__ __forceinline__ float2 fsub2(float2 a, float2 b) {
-  float2 d;
-  asm("sub.rn.f32x2 %0, %1, %2;"
-      : "=l"(*reinterpret_cast<unsigned long long *>(&d))
-      : "l"(*reinterpret_cast<unsigned long long *>(&a)),
-        "l"(*reinterpret_cast<unsigned long long *>(&b)));
-  return d;
-}
-
-// low bytes of four words -> one word
-__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040u), __byte_perm(c, d, 0x0040u), 0x5410u);
-}
-
-// E4M3 codes of RN(x / d) for EPL values, 4 per word; `ok` = false when the
-// bracket could not decide (the caller then forms exact quotients)
-template <int EPL>
-__device__ __forceinline__ void e4m3_codes(const float (&x)[EPL], float rlo, float rhi,
-                                           uint32_t (&w)[EPL / 4], bool &ok) {
-#pragma unroll
-  for (int k = 0; k < EPL / 4; ++k) {
-    const float2 a = fmul2(make_float2(x[4 * k], x[4 * k + 1]), make_float2(rlo, rlo));
-    const float2 b = fmul2(make_float2(x[4 * k + 2], x[4 * k + 3]), make_float2(rlo, rlo));
-    const float2 c = fmul2(make_float2(x[4 * k], x[4 * k + 1]), make_float2(rhi, rhi));
-    const float2 e = fmul2(make_float2(x[4 * k + 2], x[4 * k + 3]), make_float2(rhi, rhi));
-    const uint32_t lo = __byte_perm(e4m3x2_rn_sat(a.x, a.y), e4m3x2_rn_sat(b.x, b.y), 0x5410u);
-    const uint32_t hi = __byte_perm(e4m3x2_rn_sat(c.x, c.y), e4m3x2_rn_sat(e.x, e.y), 0x5410u);
-    ok = ok && lo == hi;
-    w[k] = lo;
-  }
-}
-
-// a byte whose magnitude bits are 0 is written +0
-__device__ __forceinline__ uint32_t plus_zero(uint32_t w) {
-  const uint32_t nz = (w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu;   // bit 7 set iff magnitude != 0
-  return w & (nz | 0x7F7F7F7Fu);
 }
 
 template <int DT, int D>

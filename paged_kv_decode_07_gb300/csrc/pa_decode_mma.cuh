@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "pa_internal.cuh"
+#include "pa_score.cuh"
 
 namespace pa {
 namespace tc {
@@ -287,7 +288,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // i % Hkv), its CTAs split the sequence's blocks evenly, and after the
 // in-CTA merge each CTA merges one slice of the head dim over the cluster's
 // partials, read from the other CTAs' shared memory.
-template <int DT, int D, int R, bool CL = false>
+// SC = true: scored decode (pa_score.cuh): the score is capped and biased
+// before the softmax, and the keys start at the sequence's first visible one
+// (whole blocks before it are never planned; the rest of its block is masked
+// and its V rows are zeroed, since pages behind a window may hold anything).
+template <int DT, int D, int R, bool CL = false, bool SC = false>
 __global__ void __launch_bounds__(kThreads, 3)
     decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV) {
@@ -304,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   WorkItem it;
   int len;
+  [[maybe_unused]] int key_lo = 0;   // first visible key (SC)
   if constexpr (CL) {
     // the cluster's (sequence, kv head) and this CTA's share of its blocks
     const int cid = (int)cluster_index(), rank = (int)cluster_rank(), nr = (int)cluster_size();
@@ -320,10 +326,18 @@ __global__ void __launch_bounds__(kThreads, 3)
       L = (int)cap;
     }
     if (e && rank == 0 && threadIdx.x == 0) set_err(p.hdr, e);
-    const int nblk = (L + kBlock - 1) / kBlock, chunk = (nblk + nr - 1) / nr;
+    int first = 0;
+    if constexpr (SC) {
+      const KeyRange kr =
+          key_range(p.sc, L - 1, L, p.sc.first_key ? __ldg(p.sc.first_key + unit) : 0, 0);
+      key_lo = kr.lo;
+      L = kr.hi;
+      first = key_lo / kBlock;
+    }
+    const int nblk = (L + kBlock - 1) / kBlock, chunk = (nblk - first + nr - 1) / nr;
     it.unit = unit;
     it.kvh = cid % p.kv.hkv;
-    it.blk_begin = min(nblk, rank * chunk);
+    it.blk_begin = min(nblk, first + rank * chunk);
     it.blk_end = min(nblk, it.blk_begin + chunk);
     it.part = rank;
     it.parts = nr;
@@ -337,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (blockIdx.x >= num_items) return;
     it = p.items[blockIdx.x];
     len = p.units[it.unit].len;
+    if constexpr (SC)
+      key_lo = key_range(p.sc, len - 1, len, p.sc.first_key ? __ldg(p.sc.first_key + it.unit) : 0, 0).lo;
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -378,7 +394,16 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
     }
   }
-  const float qscale = p.scale_log2 * (has_global_scale(DT) ? p.kv.kg : 1.0f);
+  const bool cap = SC && p.sc.cap_log2 != 0.f;
+  const float qscale = (cap ? p.sc.cap_in : p.scale_log2) * (has_global_scale(DT) ? p.kv.kg : 1.0f);
+  [[maybe_unused]] float slope[2] = {0.f, 0.f};   // distance bias of this lane's two heads
+  if constexpr (SC) {
+    if (p.sc.slopes) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (2 * c + h < R) slope[h] = __ldg(p.sc.slopes + kvh * p.G + 2 * c + h) * 1.4426950408889634f;
+    }
+  }
 
   // ---- this warp's blocks
   const int t_begin = it.blk_begin * kBlock;
@@ -477,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       const uint8_t *sKs = st + 2 * Gm::CODE, *sVs = sKs + Gm::SC;
       const int tok0 = t_begin + (warp + j * kWarps) * kBlock;
       const int nvalid = min(kBlock, t_end - tok0);
+      const int nskip = SC ? key_lo - tok0 : 0;   // leading tokens of the block that are hidden
 
       // ---- S^T = K . Q^T; int8 alternates k-steps over two accumulators and
       // NVFP4 over four, so that the MMAs form independent dependency chains
@@ -552,12 +578,28 @@ __global__ void __launch_bounds__(kThreads, 3)
         f0 *= fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sKs)[r]);
         f1 *= fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sKs)[r + 8]);
       }
-      const bool v0 = r < nvalid, v1 = r + 8 < nvalid;
+      const bool v0 = r < nvalid && (!SC || r >= nskip), v1 = r + 8 < nvalid && (!SC || r + 8 >= nskip);
       float sc[4];
-      sc[0] = v0 ? sacc[0] * f0 : kNegInf;
-      sc[1] = v0 ? sacc[1] * f0 : kNegInf;
-      sc[2] = v1 ? sacc[2] * f1 : kNegInf;
-      sc[3] = v1 ? sacc[3] * f1 : kNegInf;
+      if constexpr (SC) {
+        sc[0] = sacc[0] * f0;
+        sc[1] = sacc[1] * f0;
+        sc[2] = sacc[2] * f1;
+        sc[3] = sacc[3] * f1;
+        if (cap) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[k] = capped(sc[k], p.sc.cap_log2);
+        }
+        const float d0 = (float)(len - 1 - tok0 - r), d1 = d0 - 8.f;   // distance to the query
+        sc[0] = v0 ? fmaf(-slope[0], d0, sc[0]) : kNegInf;
+        sc[1] = v0 ? fmaf(-slope[1], d0, sc[1]) : kNegInf;
+        sc[2] = v1 ? fmaf(-slope[0], d1, sc[2]) : kNegInf;
+        sc[3] = v1 ? fmaf(-slope[1], d1, sc[3]) : kNegInf;
+      } else {
+        sc[0] = v0 ? sacc[0] * f0 : kNegInf;
+        sc[1] = v0 ? sacc[1] * f0 : kNegInf;
+        sc[2] = v1 ? sacc[2] * f1 : kNegInf;
+        sc[3] = v1 ? sacc[3] * f1 : kNegInf;
+      }
 
       // ---- online softmax over the block's tokens, per column.  The lane's
       // own scores decide whether the running max must move (some score above
@@ -629,6 +671,19 @@ __global__ void __launch_bounds__(kThreads, 3)
           fence_async_smem_cta();   // ordered before the next copy into this stage
           __syncwarp();
         }
+        if constexpr (SC) {
+          if (nskip > 0) {   // and the rows before the first visible key
+            uint8_t *vz = const_cast<uint8_t *>(sV);
+            constexpr int RC = ROW / 16;
+            for (int i = lane; i < min(nskip, kBlock) * RC; i += 32) {
+              const int t = i / RC, j = i % RC;
+              *reinterpret_cast<uint4 *>(vz + (j >> 3) * (kBlock * 128) + t * 128 + (j & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem_cta();
+            __syncwarp();
+          }
+        }
         // m-tile m: matrices (tokens 0-7 | 8-15) x (d 16m .. +7 | 16m+8 .. +15),
         // transposed: lane l addresses token row (l & 7) + 8 ((l >> 4) & 1),
         // chunk (l >> 3) & 1
@@ -654,7 +709,8 @@ __global__ void __launch_bounds__(kThreads, 3)
         uint32_t vsb[4][2];   // NVFP4: raw E4M3 scale bytes of the lane's 1-2 blocks
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const bool ok = tk[t] < nvalid;   // poisoned tail slots must not reach the MMA
+          // poisoned tail slots (and hidden leading ones) must not reach the MMA
+          const bool ok = tk[t] < nvalid && (!SC || tk[t] >= nskip);
           const uint8_t *src = sV + (Gm::SW ? sw_off(tk[t], boff) : tk[t] * ROW + boff);
           if constexpr (VB == 16) {
             uint4 u = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
@@ -869,10 +925,10 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
 }
 
-template <int DT, int D, int R>
+template <int DT, int D, int R, bool SC = false>
 cudaError_t launch_one(const AttnParams &p, int grid, cudaStream_t s) {
   using Gm = Geo<DT, D>;
-  auto kern = decode_kernel<DT, D, R>;
+  auto kern = decode_kernel<DT, D, R, false, SC>;
   CUtensorMap tk, tv;
   std::memset(&tk, 0, sizeof tk);
   std::memset(&tv, 0, sizeof tv);
@@ -887,10 +943,10 @@ cudaError_t launch_one(const AttnParams &p, int grid, cudaStream_t s) {
 }
 
 // single-launch variant: B * Hkv clusters of P <= kMaxCluster CTAs
-template <int DT, int D, int R>
+template <int DT, int D, int R, bool SC = false>
 cudaError_t launch_cluster_one(const AttnParams &p, int P, cudaStream_t s) {
   using Gm = Geo<DT, D, true>;
-  auto kern = decode_kernel<DT, D, R, true>;
+  auto kern = decode_kernel<DT, D, R, true, SC>;
   CUtensorMap tk, tv;
   std::memset(&tk, 0, sizeof tk);
   std::memset(&tv, 0, sizeof tv);
@@ -918,11 +974,11 @@ cudaError_t launch_cluster_one(const AttnParams &p, int P, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, p, tk, tv);
 }
 
-template <int DT>
+template <int DT, bool SC = false>
 cudaError_t launch_cluster_dtype(const AttnParams &p, int P, cudaStream_t s) {
   const int D = p.kv.D, R = p.R;
 #define PA_TC_CASE(DD, RR) \
-  if (D == DD && R == RR) return launch_cluster_one<DT, DD, RR>(p, P, s);
+  if (D == DD && R == RR) return launch_cluster_one<DT, DD, RR, SC>(p, P, s);
   PA_TC_CASE(128, 1) PA_TC_CASE(128, 2) PA_TC_CASE(128, 4) PA_TC_CASE(128, 6)
   PA_TC_CASE(128, 8) PA_TC_CASE(256, 1) PA_TC_CASE(256, 2) PA_TC_CASE(256, 4)
   PA_TC_CASE(256, 6) PA_TC_CASE(256, 8)
@@ -931,10 +987,10 @@ cudaError_t launch_cluster_dtype(const AttnParams &p, int P, cudaStream_t s) {
 }
 
 // CTAs of decode_kernel<DT, D, R> one SM holds at once (0 if unknown)
-template <int DT, int D, int R>
+template <int DT, int D, int R, bool SC = false>
 int occupancy_one() {
   using Gm = Geo<DT, D>;
-  auto kern = decode_kernel<DT, D, R>;
+  auto kern = decode_kernel<DT, D, R, false, SC>;
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, Gm::SMEM) != cudaSuccess)
@@ -942,10 +998,10 @@ int occupancy_one() {
   return n;
 }
 
-template <int DT>
+template <int DT, bool SC = false>
 int occupancy_dtype(int D, int R) {
 #define PA_TC_CASE(DD, RR) \
-  if (D == DD && R == RR) return occupancy_one<DT, DD, RR>();
+  if (D == DD && R == RR) return occupancy_one<DT, DD, RR, SC>();
   PA_TC_CASE(128, 1) PA_TC_CASE(128, 2) PA_TC_CASE(128, 4) PA_TC_CASE(128, 6)
   PA_TC_CASE(128, 8) PA_TC_CASE(256, 1) PA_TC_CASE(256, 2) PA_TC_CASE(256, 4)
   PA_TC_CASE(256, 6) PA_TC_CASE(256, 8)
@@ -953,11 +1009,11 @@ int occupancy_dtype(int D, int R) {
   return 0;
 }
 
-template <int DT>
+template <int DT, bool SC = false>
 cudaError_t launch_dtype(const AttnParams &p, int grid, cudaStream_t s) {
   const int D = p.kv.D, R = p.R;
 #define PA_TC_CASE(DD, RR) \
-  if (D == DD && R == RR) return launch_one<DT, DD, RR>(p, grid, s);
+  if (D == DD && R == RR) return launch_one<DT, DD, RR, SC>(p, grid, s);
   PA_TC_CASE(128, 1) PA_TC_CASE(128, 2) PA_TC_CASE(128, 4) PA_TC_CASE(128, 6)
   PA_TC_CASE(128, 8) PA_TC_CASE(256, 1) PA_TC_CASE(256, 2) PA_TC_CASE(256, 4)
   PA_TC_CASE(256, 6) PA_TC_CASE(256, 8)

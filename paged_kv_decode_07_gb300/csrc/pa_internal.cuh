@@ -59,6 +59,16 @@ struct WorkItem {      // two int4 in the workspace
   int part, parts, slot, pad;
 };
 
+// Score options as the kernels see them (pa_score; all zero: plain softmax).
+struct ScoreView {
+  float cap_in;             // 2 log2(e) softmax_scale / softcap, or 0
+  float cap_log2;           // softcap * log2(e), or 0: no cap
+  const float *slopes;      // [Hq] distance bias, or null
+  int window;               // 0: none
+  const int *first_key;     // per query token, or null
+  const int *prefix;        // [B], or null
+};
+
 // Everything an attention kernel needs; passed by value.
 struct AttnParams {
   KvView kv;
@@ -83,6 +93,7 @@ struct AttnParams {
   int R;                    // rows per item: G (virtual), Q*G (dense), rows per group (mode 2)
   int RG;                   // row groups per sequence (mode 2), else 1
   int test_expire;          // PA_TEST_EXPIRE_WAIT: first copies withheld, short wait cap
+  ScoreView sc;             // scored decode only
 };
 
 struct PlanParams {
@@ -102,6 +113,46 @@ struct PlanParams {
   UnitInfo *units;
   int *prefix_a, *prefix_b; // [units] scratch
   const uint32_t *extra_err; // flags of an earlier kernel of the same call, or null
+  // scored decode (Q = 1): only the keys from the first visible one on are
+  // planned (window, first_key); 0 / null otherwise
+  int window;
+  const int *first_key;
+};
+
+// A ragged batch of prompt chunks over the paged cache (pa_prefill).
+struct PrefillParams {
+  KvView kv;
+  const __nv_bfloat16 *q;   // [T, Hq, D]
+  int T, B, Hq, G;
+  const int *q_starts;      // [B + 1]
+  const int *tables;
+  int stride;
+  const int *seq_lens;
+  float scale_log2;         // softmax_scale * log2(e)
+  ScoreView sc;
+  void *out;
+  int out_fp32;
+  float *lse_out;
+  uint32_t *hdr;
+  int splits;               // key splits per row tile (1: outputs are written directly)
+  float *part_o;            // [splits][T][Hq][D], normalised partial outputs
+  float *part_lse;          // [splits][T][Hq]
+};
+
+// Norm, rotation and cache write of new tokens (pa_rope_append).
+struct RopeParams {
+  KvView kv;
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_stride, k_stride, v_stride, q_out_stride;   // elements between tokens
+  const int *positions;
+  const int64_t *slots;
+  int T, Hq, rot, interleaved;
+  const float *inv_freq;
+  float factor, eps;
+  const __nv_bfloat16 *q_norm, *k_norm;   // [D] or null
+  __nv_bfloat16 *q_out;
+  uint32_t *hdr;
+  int parts, rows_per_part;               // warps per token, rows each takes
 };
 
 // ------------------------------------------------------------- PTX helpers

@@ -27,6 +27,9 @@ cudaError_t launch_wo(const float *o, int M, int K, const void *w, int N, int sp
                       void *y, int y_fp32, uint32_t *hdr, cudaStream_t s);
 cudaError_t launch_append(const KvView &kv, const void *k_new, const void *v_new, int T,
                           const int64_t *slots, uint32_t *hdr, cudaStream_t s);
+cudaError_t launch_rope(RopeParams p, cudaStream_t s);
+cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s);
+int prefill_splits(int T, int B, int Hkv, int G, int D, int max_seq_len);
 cudaError_t launch_gather(const KvView &kv, const int *tables, int stride, const int *seq_lens,
                           int B, int max_len, float *k_out, float *v_out, uint32_t *hdr,
                           cudaStream_t s);

@@ -59,6 +59,17 @@ __device__ __forceinline__ int unit_len(const PlanParams &p, int u, uint32_t &er
   return n > 0 ? n : 0;
 }
 
+// first block that holds a visible key of the unit (0 unless scored); the
+// unit's length `n` becomes 0 when nothing is visible
+template <bool SC>
+__device__ __forceinline__ int unit_first(const PlanParams &p, int u, int &n) {
+  if constexpr (!SC) return 0;
+  int lo = p.first_key ? max(0, __ldg(p.first_key + u)) : 0;
+  if (p.window > 0) lo = max(lo, n - p.window);
+  if (lo >= n) n = lo = 0;
+  return lo / kBlock;
+}
+
 // exclusive block-wide scan of a pair of ints; returns totals in tot
 __device__ __forceinline__ int2 block_scan2(int2 v, int2 &tot) {
   __shared__ int2 warp_sums[kThreads / 32];
@@ -110,6 +121,8 @@ __device__ __forceinline__ int upper_bound_minus1(const P *pre, int n, int j) {
   return lo - 1;
 }
 
+// SC: scored decode (the first visible key bounds what is planned)
+template <bool SC>
 __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
   __shared__ unsigned long long s_total;
   __shared__ uint32_t s_err;
@@ -140,7 +153,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
   unsigned long long tot = 0;
   for (int u = tid; u < U; u += kThreads) {
     int n = unit_len(p, u, err);
-    tot += (unsigned long long)((n + kBlock - 1) / kBlock);
+    const int first = unit_first<SC>(p, u, n);
+    tot += (unsigned long long)((n + kBlock - 1) / kBlock - first);
   }
   // the blocks every group partitions (those of its longest unit): the same
   // in every group when the sequences have equal lengths
@@ -150,7 +164,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
     for (int g = tid; g < NG; g += kThreads) {
       int nmax = 0;
       for (int i = 0; i < GS; ++i) nmax = max(nmax, unit_len(p, g * GS + i, e1));
-      const int nb = (nmax + kBlock - 1) / kBlock;
+      const int first = unit_first<SC>(p, g, nmax);
+      const int nb = (nmax + kBlock - 1) / kBlock - first;
       gmin = min(gmin, nb);
       gmax = max(gmax, nb);
     }
@@ -221,7 +236,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
     int nmax = 0;
     if (g < NG)
       for (int i = 0; i < GS; ++i) nmax = max(nmax, unit_len(p, g * GS + i, e2));
-    const int nblk = (nmax + kBlock - 1) / kBlock;
+    const int first = g < NG ? unit_first<SC>(p, g, nmax) : 0;
+    const int nblk = (nmax + kBlock - 1) / kBlock - first;
     const int parts = nblk ? (nblk + W - 1) / W : 0;
     const int multi = parts > 1;
     int2 v = make_int2(multi ? parts * GS * p.hkv : 0, multi ? parts * GS : 0);
@@ -239,6 +255,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
         ui.slot_base = multi ? carry.y + ex.y + i * parts : -1;
         ui.nblk = nblk;
         ui.len = unit_len(p, g * GS + i, e2);
+        (void)unit_first<SC>(p, g * GS + i, ui.len);
         p.units[g * GS + i] = ui;
       }
     }
@@ -295,11 +312,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
       slot_base = ui.slot_base;
     }
     const int chunk = (nblk + parts - 1) / parts;
+    uint32_t e3 = 0;
+    int n = SC ? unit_len(p, u, e3) : 0;
+    const int first = unit_first<SC>(p, u, n);
     WorkItem it;
     it.unit = u;
     it.kvh = kvh;
-    it.blk_begin = part * chunk;
-    it.blk_end = min(nblk, it.blk_begin + chunk);
+    it.blk_begin = first + part * chunk;
+    it.blk_end = min(first + nblk, it.blk_begin + chunk);
     it.part = part;
     it.parts = parts;
     it.slot = parts > 1 ? slot_base + part : -1;
@@ -318,7 +338,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
 }  // namespace
 
 cudaError_t launch_plan(const PlanParams &pp, cudaStream_t s) {
-  plan_kernel<<<1, kThreads, 0, s>>>(pp);
+  if (pp.window > 0 || pp.first_key)
+    plan_kernel<true><<<1, kThreads, 0, s>>>(pp);
+  else
+    plan_kernel<false><<<1, kThreads, 0, s>>>(pp);
   return cudaGetLastError();
 }
 

@@ -34,12 +34,17 @@ PA_ERRF_LEN_LT_QLEN = 0x8
 PA_ERRF_WAIT_TIMEOUT = 0x10
 PA_ERRF_PLAN_OVERFLOW = 0x20
 PA_ERRF_BAD_SLOT = 0x40
+PA_ERRF_BAD_Q_START = 0x80
+
+ROPE_KINDS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 PA_TEST_EXPIRE_WAIT = 0x1
 
 EXPORTED = ("pa_workspace_bytes", "pa_decode", "pa_verify", "pa_merge", "pa_dequant_gather",
             "pa_append_kv", "pa_block_means", "pa_sparse_workspace_bytes", "pa_decode_sparse",
             "pa_decode_wo_workspace_bytes", "pa_decode_wo",
+            "pa_rope_append", "pa_rope_frequencies", "pa_decode_scored",
+            "pa_prefill_workspace_bytes", "pa_prefill",
             "pa_read_error", "pa_status_string", "pa_version")
 
 
@@ -76,6 +81,34 @@ class _Sparse(ctypes.Structure):
 class _Wo(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("hidden", ctypes.c_int32), ("y", ctypes.c_void_p),
                 ("y_fp32", ctypes.c_int32), ("k_split", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("slot_mapping", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("attn_factor", ctypes.c_float), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class _Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+
+class _Prefill(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_tokens", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("q_starts", ctypes.c_void_p), ("block_tables", ctypes.c_void_p),
+                ("block_table_stride", ctypes.c_int32), ("seq_lens", ctypes.c_void_p),
+                ("max_seq_len", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("out", ctypes.c_void_p), ("out_fp32", ctypes.c_int32),
+                ("lse_out", ctypes.c_void_p)]
 
 
 class _Options(ctypes.Structure):
@@ -120,6 +153,17 @@ def lib():
         L.pa_decode_wo_workspace_bytes.argtypes = [P, P, P, P]
         L.pa_decode_wo.restype = ctypes.c_int
         L.pa_decode_wo.argtypes = [P, P, P, P, P, ctypes.c_size_t, P]
+        L.pa_rope_append.restype = ctypes.c_int
+        L.pa_rope_append.argtypes = [P, P, P, P]
+        L.pa_rope_frequencies.restype = ctypes.c_int
+        L.pa_rope_frequencies.argtypes = [i32, ctypes.c_double, i32, ctypes.c_double, i32,
+                                          ctypes.c_double, ctypes.c_double, P, P]
+        L.pa_decode_scored.restype = ctypes.c_int
+        L.pa_decode_scored.argtypes = [P, P, P, P, P, ctypes.c_size_t, P]
+        L.pa_prefill_workspace_bytes.restype = ctypes.c_size_t
+        L.pa_prefill_workspace_bytes.argtypes = [P, P]
+        L.pa_prefill.restype = ctypes.c_int
+        L.pa_prefill.argtypes = [P, P, P, P, ctypes.c_size_t, P]
         L.pa_append_kv.restype = ctypes.c_int
         L.pa_append_kv.argtypes = [P, P, P, i32, P, P, P]
         L.pa_read_error.restype = ctypes.c_int
@@ -381,6 +425,209 @@ def append_kv(kv: KvCache, k_new, v_new, slot_mapping, workspace=None, stream=No
                             _ptr(slot_mapping), _ptr(workspace), _stream(stream))
     if st != PA_OK:
         raise PaError("pa_append_kv", st)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: Optional[str] = None,
+                     factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device="cpu"):
+    """Inverse frequencies fp32 [rot_dim / 2] for rope_append and the factor
+    its rotated pairs are scaled by.  scaling: None, "linear", "ntk" or
+    "yarn" (needs original_len, the length the model was trained on)."""
+    if scaling not in ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {list(ROPE_KINDS)}: got {scaling!r}")
+    inv = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float32)
+    att = ctypes.c_float(1.0)
+    st = lib().pa_rope_frequencies(int(rot_dim), float(base), ROPE_KINDS[scaling], float(factor),
+                                   int(original_len), float(beta_fast), float(beta_slow),
+                                   _ptr(inv), ctypes.byref(att))
+    if st != PA_OK:
+        raise PaError("pa_rope_frequencies", st)
+    return inv.to(device), float(att.value)
+
+
+def _check(t, name, dtype, shape, device, strided=False):
+    """A tensor argument's type, shape and place.  `strided`: [tokens, heads,
+    head_dim] whose tokens may lie any distance apart."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}: got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    if strided:
+        ok = (t.stride(2) == 1 and (t.shape[1] < 2 or t.stride(1) == shape[2])) or t.numel() == 0
+    else:
+        ok = t.is_contiguous()
+    if not ok:
+        raise ValueError(f"{name} must be contiguous{' within a token' if strided else ''}: "
+                         f"got strides {t.stride()}")
+
+
+class _on:
+    """Makes a tensor's device current for a call (its kernels are launched
+    on that device's current stream)."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def rope_append(kv: KvCache, q, k, v, positions, slot_mapping, inv_freq, *, interleaved=False,
+                attn_factor=1.0, q_norm=None, k_norm=None, eps=1e-6, q_out=None, workspace=None,
+                stream=None):
+    """Per-head RMS norm (q_norm / k_norm bf16 [D], optional) and position
+    rotation of the new tokens' queries and keys, and the quantised write of
+    their keys and values into the pool (in place), in one pass.
+
+    q bf16 [T, Hq, D], k / v bf16 [T, Hkv, D]: contiguous within a token, any
+    distance between tokens (slices of one fused projection).  positions
+    int32 [T]; slot_mapping int64 [T] (-1 = padded row); inv_freq fp32
+    [rot_dim / 2] (rope_frequencies).  Returns the rotated queries bf16
+    [T, Hq, D]; q_out=q rotates them in place."""
+    T, Hq, D = q.shape
+    dev = kv.k_cache.device
+    Hkv = kv.num_kv_heads
+    _check(q, "q", torch.bfloat16, (T, Hq, kv.head_dim), dev, True)
+    _check(k, "k", torch.bfloat16, (T, Hkv, D), dev, True)
+    _check(v, "v", torch.bfloat16, (T, Hkv, D), dev, True)
+    _check(positions, "positions", torch.int32, (T,), dev)
+    _check(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
+    _check(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev)
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _check(w, name, torch.bfloat16, (D,), dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check(q_out, "q_out", torch.bfloat16, (T, Hq, D), dev, True)
+    a = _Rope(T, Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), q.stride(0),
+              k.stride(0), v.stride(0), q_out.stride(0), positions.data_ptr(),
+              slot_mapping.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0,
+              inv_freq.data_ptr(), attn_factor, None if q_norm is None else q_norm.data_ptr(),
+              None if k_norm is None else k_norm.data_ptr(), eps)
+    with _on(dev):
+        st = lib().pa_rope_append(ctypes.byref(kv.struct()), ctypes.byref(a), _ptr(workspace),
+                                  _stream(stream))
+    if st != PA_OK:
+        raise PaError("pa_rope_append", st)
+    return q_out
+
+
+@dataclass
+class Score:
+    """Score options of prefill and decode_scored (defaults: plain softmax).
+
+    softcap c: s <- c tanh(s / c); slopes fp32 [Hq]: s <- s - slope |p - t|;
+    window: the last `window` keys up to the query's own; first_key int32
+    (per query token: [T] for prefill, [B] for decode): earlier keys are
+    hidden; prefix_lens int32 [B] (prefill): the first prefix_lens[b] keys
+    are visible to every query of the sequence."""
+    softcap: float = 0.0
+    slopes: Optional[torch.Tensor] = None
+    window: int = 0
+    first_key: Optional[torch.Tensor] = None
+    prefix_lens: Optional[torch.Tensor] = None
+
+    def struct(self, num_q_heads: int, tokens: int, batch: int, device) -> _Score:
+        for t, name, dt, n in ((self.slopes, "slopes", torch.float32, num_q_heads),
+                               (self.first_key, "first_key", torch.int32, tokens),
+                               (self.prefix_lens, "prefix_lens", torch.int32, batch)):
+            if t is not None:
+                _check(t, name, dt, (n,), device)
+        return _Score(float(self.softcap), int(self.window),
+                      None if self.slopes is None else self.slopes.data_ptr(),
+                      None if self.first_key is None else self.first_key.data_ptr(),
+                      None if self.prefix_lens is None else self.prefix_lens.data_ptr())
+
+
+def decode_scored(kv: KvCache, q, block_tables, seq_lens, softmax_scale, *, score=None, out=None,
+                  out_fp32=False, return_lse=False, max_seq_len=None, workspace=None, kernel=0,
+                  split_blocks=0, target_items=0, events=None, stream=None):
+    """decode with score options: q bf16 [B, 1, Hq, D] -> (out, [lse,]
+    workspace).  A workspace that is too small is replaced."""
+    B, Q, Hq, D = q.shape
+    dev = kv.k_cache.device
+    _check(q, "q", torch.bfloat16, (B, 1, Hq, kv.head_dim), dev)
+    _check(block_tables, "block_tables", torch.int32, (B, int(block_tables.shape[1])), dev)
+    _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((B, Q, Hq, D), dtype=torch.float32 if out_fp32 else torch.bfloat16,
+                          device=dev)
+    elif out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out must be bf16 or fp32: got {out.dtype}")
+    else:
+        _check(out, "out", out.dtype, (B, Q, Hq, D), dev)
+    lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    if max_seq_len is None:
+        max_seq_len = int(block_tables.shape[1]) * kv.block_size
+    sc = (score if score is not None else Score()).struct(Hq, B, B, dev)
+    opts = _options(kernel, split_blocks, target_items, events)
+    kvs = kv.struct()
+    prob = _problem(kv, q, block_tables, seq_lens, softmax_scale, out, lse, max_seq_len)
+    need = int(lib().pa_workspace_bytes(ctypes.byref(kvs), ctypes.byref(prob), ctypes.byref(opts)))
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = lib().pa_decode_scored(ctypes.byref(kvs), ctypes.byref(prob), ctypes.byref(sc),
+                                    ctypes.byref(opts), _ptr(workspace), workspace.numel(),
+                                    _stream(stream))
+    if st != PA_OK:
+        raise PaError("pa_decode_scored", st)
+    return (out, lse, workspace) if return_lse else (out, workspace)
+
+
+def _prefill_struct(q, q_starts, block_tables, seq_lens, max_seq_len, softmax_scale, out, lse):
+    return _Prefill(int(seq_lens.shape[0]), int(q.shape[1]), int(q.shape[0]), q.data_ptr(),
+                    q_starts.data_ptr(), block_tables.data_ptr(), int(block_tables.shape[1]),
+                    seq_lens.data_ptr(), int(max_seq_len), float(softmax_scale), out.data_ptr(),
+                    1 if out.dtype == torch.float32 else 0,
+                    None if lse is None else lse.data_ptr())
+
+
+def prefill(kv: KvCache, q, q_starts, block_tables, seq_lens, softmax_scale, *, score=None,
+            out=None, out_fp32=False, return_lse=False, max_seq_len=None, workspace=None,
+            stream=None):
+    """Attention of a ragged batch of prompt chunks over the paged cache.
+
+    q bf16 [T, Hq, D]; sequence b owns the rows q_starts[b] .. q_starts[b + 1]
+    - 1 (q_starts int32 [B + 1]), the last of its seq_lens[b] keys; rows
+    outside are left as they are.  Returns (out [T, Hq, D], [lse [T, Hq],]
+    workspace).  A workspace that is too small is replaced."""
+    T, Hq, D = q.shape
+    B = int(seq_lens.shape[0])
+    dev = kv.k_cache.device
+    _check(q, "q", torch.bfloat16, (T, Hq, kv.head_dim), dev)
+    _check(q_starts, "q_starts", torch.int32, (B + 1,), dev)
+    _check(block_tables, "block_tables", torch.int32, (B, int(block_tables.shape[1])), dev)
+    _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.float32 if out_fp32 else torch.bfloat16,
+                          device=dev)
+    elif out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out must be bf16 or fp32: got {out.dtype}")
+    else:
+        _check(out, "out", out.dtype, (T, Hq, D), dev)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    if max_seq_len is None:
+        max_seq_len = int(block_tables.shape[1]) * kv.block_size
+    sc = (score if score is not None else Score()).struct(Hq, T, B, dev)
+    kvs = kv.struct()
+    prob = _prefill_struct(q, q_starts, block_tables, seq_lens, max_seq_len, softmax_scale, out, lse)
+    need = int(lib().pa_prefill_workspace_bytes(ctypes.byref(kvs), ctypes.byref(prob)))
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = lib().pa_prefill(ctypes.byref(kvs), ctypes.byref(prob), ctypes.byref(sc),
+                              _ptr(workspace), workspace.numel(), _stream(stream))
+    if st != PA_OK:
+        raise PaError("pa_prefill", st)
+    return (out, lse, workspace) if return_lse else (out, workspace)
 
 
 def read_error(workspace: torch.Tensor, stream=None) -> int:
