@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 FMTS = ["bf16", "int8", "fp8", "nvfp4"]
 # how the weights are rounded before the product with V
-EPS_P = {"bf16": S.EPS_BF16, "int8": S.EPS_BF16, "fp8": S.EPS_BF16, "nvfp4": S.EPS_BF16}
+EPS_P = {"bf16": S.EPS_BF16, "int8": S.EPS_FP16, "fp8": S.EPS_FP16, "nvfp4": S.EPS_FP16}
 
 
 def build(fmt, new, lens, hkv, G, D, seed=0):
@@ -36,7 +36,8 @@ def check(fmt, new, lens, hkv, G, D, seed=0, flags=0, **opt):
     out, lse, ws = pa.prefill(kv, q, starts, tables, sl, scale, score=sc, out_fp32=True, return_lse=True,
                               max_seq_len=max(max(lens), 1))
     assert pa.read_error(ws) == flags
-    ref, rl, bound = S.reference(vals(kv), q, new, lens, tables, scale, eps_p=EPS_P[fmt], **opt)
+    ref, rl, bound = S.reference(vals(kv), q, new, lens, tables, scale, eps_p=EPS_P[fmt],
+                                 v_unit=kv.v_scale if fmt == "int8" else None, **opt)
     what = f"{fmt} new {new} lens {lens} hkv {hkv} G {G} D {D}"
     S.within(out, ref, bound, what)
     S.lse_within(lse, rl, what)
@@ -135,7 +136,8 @@ def test_values_no_query_sees_may_be_anything(fmt):
     new, lens, hkv, G, D = [20, 33], [301, 44], 2, 2, 128
     kv, q, starts, tables, sl = build(fmt, new, lens, hkv, G, D)
     clean = vals(kv)
-    ref, rl, bound = S.reference(clean, q, new, lens, tables, 0.1, window=30, eps_p=EPS_P[fmt])
+    ref, rl, bound = S.reference(clean, q, new, lens, tables, 0.1, window=30, eps_p=EPS_P[fmt],
+                                 v_unit=kv.v_scale.clone() if fmt == "int8" else None)
     for b, (m, n) in enumerate(zip(new, lens)):
         hidden = list(range(0, max(0, n - m - 29))) + list(range(n, -(-n // 16) * 16))
         for t in hidden:
