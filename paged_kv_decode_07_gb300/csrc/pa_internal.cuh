@@ -152,7 +152,7 @@ struct RopeParams {
   const __nv_bfloat16 *q_norm, *k_norm;   // [D] or null
   __nv_bfloat16 *q_out;
   uint32_t *hdr;
-  int parts, rows_per_part;               // warps per token, rows each takes
+  int parts, steps_per_part;              // warps per token, steps each takes
 };
 
 // ------------------------------------------------------------- PTX helpers

@@ -22,18 +22,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // the sequence and row tile of tile index `tile` (tiles of all sequences in
 // order, `per` tokens each): every thread of a warp gets the answer
 struct TileOf {
-  int b, first, start, len;   // sequence (-1: none), first token in it, its tokens' start, count
+  // sequence (-1: none), tile in it, its query rows' start and count, its keys
+  int b, first, start, len, n;
 };
 __device__ __forceinline__ TileOf find_tile(const PrefillParams &p, int tile, int rows_per_tile) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   uint32_t err = 0;
-  TileOf r = {-1, 0, 0, 0};
+  TileOf r = {-1, 0, 0, 0, 0};
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int start = 0, len = 0;
+    int start = 0, len = 0, keys = 0;
     if (b < p.B) {
       const int s0 = __ldg(p.q_starts + b), s1 = __ldg(p.q_starts + b + 1);
+      keys = __ldg(p.seq_lens + b);
       start = min(max(s0, 0), p.T);
       const int end = min(max(s1, start), p.T);
       if (start != s0 || end != s1) err = 1;
@@ -53,6 +55,7 @@ __device__ __forceinline__ TileOf find_tile(const PrefillParams &p, int tile, in
       r.first = tile - (before + __shfl_sync(0xffffffffu, inc - n, l));
       r.start = __shfl_sync(0xffffffffu, start, l);
       r.len = __shfl_sync(0xffffffffu, len, l);
+      r.n = __shfl_sync(0xffffffffu, keys, l);
       break;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);

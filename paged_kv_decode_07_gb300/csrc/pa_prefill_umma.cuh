@@ -10,10 +10,12 @@
 // rescale of O is then rare), and one division by the sum at the end.
 //
 // K and V tiles arrive in a ring of 32 KB units [128 keys x 128 dims], used
-// as they lie: K is K-major, V MN-major.  bf16 pages come by 2-D TMA (16 rows
-// x 128 bytes a box, 128-byte swizzle); the quantised formats are read as
-// codes and turned into f16 (exact for all of them) by a warpgroup of their
-// own, so the MMAs see one layout whatever the cache holds.
+// as they lie: K is K-major, V MN-major.  A warpgroup of its own fills them:
+// bf16 rows by 16-byte asynchronous copies, the quantised formats as codes
+// that it turns into f16 (exact for all of them), so the MMAs see one layout
+// whatever the cache holds.  (One TMA box per page and 128 bytes of row, the
+// largest the swizzled layout allows over scattered 16-token pages, moves 24
+// bytes per cycle and SM; D = 256 needs twice that.)
 //
 // D = 128: a CTA takes two row tiles (256 rows), one per softmax group, that
 // share every K and V unit; while one group is at its softmax the MMAs of the
@@ -21,8 +23,8 @@
 // takes one row tile with two S buffers, and the two softmax groups share the
 // tile, each 64 of its 128 keys.
 //
-// Roles: warps 0-7 softmax (two groups), warp 8 MMA issue (one thread), warp 9
-// TMA (bf16), warps 12-15 dequantisation (other formats).  Hand-offs are
+// Roles: warps 0-7 softmax (two groups), warp 8 MMA issue (one thread), warps
+// 12-15 copies or dequantisation.  Hand-offs are
 // mbarriers; every wait is capped, and a timeout sets PA_ERRF_WAIT_TIMEOUT,
 // raises the CTA's abort flag and lets copies and MMAs in flight finish.
 #pragma once
@@ -39,6 +41,19 @@ constexpr int kKeys = 128;           // keys per tile
 constexpr int kUnitBytes = 32768;    // [128 keys][128 dims] of 16-bit values
 constexpr int kChunkBytes = 16384;   // 64 dims of it
 constexpr float kLazy = 8.0f;        // log2 of how far a score may pass the running maximum
+// Registers per thread at launch and after the split (D = 128, whose softmax
+// threads hold a row of 128 scores): MMA group, copies or dequantisation, and
+// the two softmax groups the rest.
+constexpr int kLaunchRegsPf = 128, kRegMma = 48;
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+      : "l"(*reinterpret_cast<unsigned long long *>(&a)),
+        "l"(*reinterpret_cast<unsigned long long *>(&b)));
+  return d;
+}
 
 template <int DT, int D_>
 struct PGeo {
@@ -49,7 +64,10 @@ struct PGeo {
   static constexpr int H = D / 128;                // units per K or V tile
   static constexpr int NU = QUANT ? 4 : 5;         // ring
   static constexpr int NC = D == 128 ? 128 : 64;   // S columns per softmax thread
-  static constexpr int THREADS = QUANT ? 512 : 384;
+  static constexpr int THREADS = 512;
+  static constexpr int REG_COPY = QUANT ? 112 : 64;
+  static constexpr int REG_SM = (4 * kLaunchRegsPf - kRegMma - REG_COPY) / 16 * 8;
+  static_assert(2 * REG_SM + kRegMma + REG_COPY <= 4 * kLaunchRegsPf, "register split");
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int OFF_U = QBYTES;
   static constexpr int OFF_SC = OFF_U + NU * kUnitBytes;   // int8: K and V row scales, per warp
@@ -67,11 +85,10 @@ struct PCtl {
   // odd tiles; S of tile j complete means PV of j - 2 complete, so a wait for
   // tile j - 1 or j is never two phases ahead of its barrier.
   uint64_t odone[2];
-  uint64_t fix;                 // copies of a V unit whose rows are partly zeroed
   uint64_t done;                // every MMA complete
   uint32_t tmem;
   int abort;
-  int lo, hi;
+  int lo[8], hi[8];             // keys that some row of each softmax warp sees
   float red[2][128];            // D = 256: the halves' maxima, at the end their sums
 };
 
@@ -87,15 +104,6 @@ __device__ __forceinline__ bool wait_p(uint64_t *bar, uint32_t parity, PCtl &c, 
   *ab = 1;
   set_err(hdr, PA_ERRF_WAIT_TIMEOUT);
   return false;
-}
-
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                        uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
 }
 
 // what every role knows of the CTA's work
@@ -115,16 +123,56 @@ __host__ __device__ constexpr uint32_t idesc_pf(bool bf16, int N, bool b_mn) {
 
 // ------------------------------------------------------------------ MMA issue
 
+// The whole warp runs the issue loop on warp-uniform values and one elected
+// lane issues, by predicate: the operands of tcgen05.mma are uniform
+// registers, and a loop run by a single lane would move every descriptor into
+// them by hand (75 to 105 cycles per MMA instead of its own 64).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
 template <int DT, int D>
-__device__ void role_mma(const Work &w, uint8_t *smem, PCtl &c, uint32_t *hdr, uint32_t tmem) {
+__device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, uint32_t tmem) {
   using Gm = PGeo<DT, D>;
   constexpr uint32_t IQK = idesc_pf(!Gm::QUANT, 128, false);
   constexpr uint32_t IPV = idesc_pf(!Gm::QUANT, 128, true);
+  const uint32_t lead = elect_one();
   const uint64_t dQ = sdesc(smem_u32(smem), 16, 1024);
   const uint64_t dK = sdesc(smem_u32(smem + Gm::OFF_U), 16, 1024);
   const uint64_t dV = sdesc(smem_u32(smem + Gm::OFF_U), kChunkBytes, 1024);
   uint32_t u = 0;
-  auto wait_full = [&](uint32_t i) { return wait_p(&c.full[i % Gm::NU], (i / Gm::NU) & 1, c, hdr); };
+  auto wait = [&](uint64_t *bar, uint32_t par) {
+    const bool ok = __all_sync(0xffffffffu, wait_p(bar, par, c, hdr));
+    tc_fence_after();
+    return ok;
+  };
+  auto wait_full = [&](uint32_t i) { return wait(&c.full[i % Gm::NU], (i / Gm::NU) & 1); };
   // S(buffer) (+)= Q tile t, dims 128 h .. + 127, times K unit i
   auto qk = [&](uint32_t i, int t, int h, uint32_t buf) {
     const uint64_t kb = dK + (uint64_t)((i % Gm::NU) * (kUnitBytes >> 4));
@@ -132,7 +180,7 @@ __device__ void role_mma(const Work &w, uint8_t *smem, PCtl &c, uint32_t *hdr, u
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       const uint64_t off = (uint64_t)(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
-      mma_ss(tmem + buf * 128, qb + off, kb + off, IQK, (h > 0 || ks > 0) ? 1u : 0u);
+      mma_ss_if(lead, tmem + buf * 128, qb + off, kb + off, IQK, (h > 0 || ks > 0) ? 1u : 0u);
     }
   };
   // O (+)= P(buffer) times V unit i; P sits in two runs of 32 columns, `half` columns apart
@@ -140,47 +188,40 @@ __device__ void role_mma(const Work &w, uint8_t *smem, PCtl &c, uint32_t *hdr, u
     const uint64_t vb = dV + (uint64_t)((i % Gm::NU) * (kUnitBytes >> 4));
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
-      mma_ts(o, tmem + buf * 128 + (ks >> 2) * half + (ks & 3) * 8,
-             vb + (uint64_t)((ks * 2048) >> 4), IPV, (!first || ks > 0) ? 1u : 0u);
+      mma_ts_if(lead, o, tmem + buf * 128 + (ks >> 2) * half + (ks & 3) * 8,
+                vb + (uint64_t)((ks * 2048) >> 4), IPV, (!first || ks > 0) ? 1u : 0u);
   };
-  const int n = w.ntiles;
   if constexpr (D == 128) {
-    const int nm = w.nrows > 128 ? 2 : 1;
     bool ok = n > 0 && wait_full(u);
     if (ok) {
-      tc_fence_after();
       for (int t = 0; t < nm; ++t) {
         qk(u, t, 0, t);
-        tc_commit(&c.sfull[t]);
+        commit_if(lead, &c.sfull[t]);
       }
-      tc_commit(&c.empty[u % Gm::NU]);
+      commit_if(lead, &c.empty[u % Gm::NU]);
       ++u;
     }
     for (int j = 0; j < n && ok; ++j) {
       const uint32_t uv = u++;
       const uint32_t uk = j + 1 < n ? u++ : 0;
       for (int t = 0; t < nm && ok; ++t) {
-        if ((t == 0 && !wait_full(uv)) || !wait_p(&c.pready[t], j & 1, c, hdr)) {
+        if ((t == 0 && !wait_full(uv)) || !wait(&c.pready[t], j & 1)) {
           ok = false;
           break;
         }
-        tc_fence_after();
         pv(uv, tmem + Gm::COL_O + t * 128, t, 32, j == 0);
-        if (t == nm - 1) tc_commit(&c.empty[uv % Gm::NU]);
+        if (t == nm - 1) commit_if(lead, &c.empty[uv % Gm::NU]);
         if (j + 1 == n) {
-          tc_commit(&c.odone[t]);
+          commit_if(lead, &c.odone[t]);
           continue;
         }
-        if (t == 0) {
-          if (!wait_full(uk)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (t == 0 && !wait_full(uk)) {
+          ok = false;
+          break;
         }
         qk(uk, t, 0, t);
-        tc_commit(&c.sfull[t]);
-        if (t == nm - 1) tc_commit(&c.empty[uk % Gm::NU]);
+        commit_if(lead, &c.sfull[t]);
+        if (t == nm - 1) commit_if(lead, &c.empty[uk % Gm::NU]);
       }
     }
   } else {
@@ -188,111 +229,148 @@ __device__ void role_mma(const Work &w, uint8_t *smem, PCtl &c, uint32_t *hdr, u
     auto tile_qk = [&](int j) {
       for (int h = 0; h < Gm::H; ++h, ++u) {
         if (!wait_full(u)) return false;
-        tc_fence_after();
         qk(u, 0, h, j & 1);
-        tc_commit(&c.empty[u % Gm::NU]);
+        commit_if(lead, &c.empty[u % Gm::NU]);
       }
-      tc_commit(&c.sfull[j & 1]);
+      commit_if(lead, &c.sfull[j & 1]);
       return true;
     };
     if (n > 0) ok = tile_qk(0);
     if (n > 1 && ok) ok = tile_qk(1);
     for (int j = 0; j < n && ok; ++j) {
-      if (!wait_p(&c.pready[j & 1], (j >> 1) & 1, c, hdr)) break;
+      if (!wait(&c.pready[j & 1], (j >> 1) & 1)) break;
       for (int h = 0; h < Gm::H; ++h, ++u) {
         if (!wait_full(u)) {
           ok = false;
           break;
         }
-        tc_fence_after();
         pv(u, tmem + Gm::COL_O + h * 128, j & 1, 64, j == 0);
-        tc_commit(&c.empty[u % Gm::NU]);
+        commit_if(lead, &c.empty[u % Gm::NU]);
       }
       if (!ok) break;
-      tc_commit(&c.odone[j & 1]);
+      commit_if(lead, &c.odone[j & 1]);
       if (j + 2 < n) ok = tile_qk(j + 2);
     }
   }
-  tc_commit(&c.done);   // tensor memory is released only after every MMA completes
+  commit_if(lead, &c.done);   // tensor memory is released only after every MMA completes
   drain_wait(&c.done, 0);
+  __syncwarp();
 }
 
-// the order in which units are consumed: f(is_v, tile, h) until it returns false
-template <int D, typename F>
-__device__ __forceinline__ void each_unit(int n, F &&f) {
-  constexpr int H = D / 128, AHEAD = D == 128 ? 1 : 2;
-  for (int j = 0; j < AHEAD && j < n; ++j)
-    for (int h = 0; h < H; ++h)
-      if (!f(false, j, h)) return;
-  for (int j = 0; j < n; ++j) {
-    for (int h = 0; h < H; ++h)
-      if (!f(true, j, h)) return;
-    if (j + AHEAD < n)
-      for (int h = 0; h < H; ++h)
-        if (!f(false, j + AHEAD, h)) return;
-  }
-}
-
-// ------------------------------------------------------------- bf16: TMA copies
-
-// Lane l < 16 copies page l / 2, dims chunk l % 2 of a unit.  Pages that no
-// row sees, or whose id is out of range, read past the tensor: zeros.  Rows of
-// a V unit that no row sees but that share a page with one that is seen are
-// zeroed here before the unit is handed over (a zero weight times whatever the
-// slot holds must be zero).
+// The order in which the MMA thread uses K and V tiles: K runs one tile (D =
+// 128) or two (D = 256, two S buffers) ahead of V.  Tile q of that order; the
+// places past the last K tile are skipped (j >= n).
 template <int D>
-__device__ void role_tma(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c,
-                         const CUtensorMap *tmK, const CUtensorMap *tmV, int lane) {
+struct Order {
+  int q, n, j;
+  bool is_v;
+  __device__ __forceinline__ Order(int tiles) : q(0), n(tiles), j(0), is_v(false) {}
+  __device__ __forceinline__ bool done() const { return q > 2 * n || n == 0; }
+  __device__ __forceinline__ void next() {
+    do {
+      ++q;
+      is_v = D == 128 ? (q & 1) : !(q & 1);
+      j = D == 128 ? q >> 1 : is_v ? (q >> 1) - 1 : (q + 1) >> 1;
+    } while (j >= n && !done());
+  }
+};
+
+// ---------------------------------------------------- bf16: asynchronous copies
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// zeros instead of the source unless `valid` (the address is not read then)
+__device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // all but the last N committed groups complete
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 128 threads, 16 lanes per key row; rows that no query sees, or whose page id
+// is out of range, are filled with zeros (a zero weight times whatever a slot
+// holds must be zero).  Three units are in flight; a unit is handed over once
+// this thread's copies of it have landed.
+template <int D>
+__device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t) {
   using Gm = PGeo<PA_KV_BF16, D>;
-  const uint32_t ubase = smem_u32(smem + Gm::OFF_U);
-  const int oob = p.kv.num_blocks * p.kv.hkv * kBlock;
-  uint32_t u = 0, fixes = 0;
-  each_unit<D>(w.ntiles, [&](bool is_v, int j, int h) {
-    const int st = u % Gm::NU;
-    const int k0 = (w.kt0 + j) * kKeys, pg = lane >> 1, key = k0 + pg * kBlock;
-    int y = oob;
-    if (lane < 16 && key < w.see_hi && key + kBlock > w.see_lo) {
-      const int id = __ldg(w.trow + key / kBlock);
-      if (id >= 0 && id < p.kv.num_blocks) y = (id * p.kv.hkv + w.kvh) * kBlock;
-    }
-    if (u >= Gm::NU) {
-      const bool ok = wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-    }
-    const int z_lo = w.see_lo - k0, z_hi = w.see_hi - k0;   // seen rows of this tile
-    const bool fix = is_v && ((z_lo > 0 && z_lo < kKeys && (z_lo & 15)) ||
-                              (z_hi > 0 && z_hi < kKeys && (z_hi & 15)));
-    uint64_t *bar = fix ? &c.fix : &c.full[st];
-    if (lane == 0) mbar_arrive_expect_tx(bar, kUnitBytes);
+  constexpr int FLY = 3;
+  // piece `piece` of rows r0, r0 + 8, ..: two rows of every page, 1 KB apart
+  // in a chunk (r0 is the row modulo 8 that the swizzle wants)
+  const int r0 = t >> 4, piece = t & 15;
+  const uint32_t dst0 = smem_u32(smem + Gm::OFF_U) + (piece >> 3) * kChunkBytes + r0 * 128 +
+                        (((piece & 7) ^ r0) << 4);
+  const size_t page = (size_t)p.kv.hkv * kBlock * D * 2;   // bytes between pages
+  const size_t off0 = ((size_t)w.kvh * kBlock + r0) * D * 2 + piece * 16;
+  const uint8_t *const kbase = static_cast<const uint8_t *>(p.kv.k) + off0;
+  const uint8_t *const vbase = static_cast<const uint8_t *>(p.kv.v) + off0;
+  uint32_t u = 0;
+  auto hand_over = [&](uint32_t i) {   // one arrival a warp: 128 on one barrier would queue up
+    fence_async_smem();
     __syncwarp();
-    if (lane < 16)
-      tma_box(ubase + st * kUnitBytes + (lane & 1) * kChunkBytes + pg * 2048, is_v ? tmV : tmK,
-              h * 256 + (lane & 1) * 128, y, bar);
-    if (fix) {
-      if (!__all_sync(0xffffffffu, wait_p(&c.fix, fixes & 1, c, p.hdr))) {
-        drain_wait(&c.fix, fixes & 1);
-        return false;
-      }
-      ++fixes;
-      uint8_t *base = smem + Gm::OFF_U + st * kUnitBytes;
-      auto zero = [&](int r0, int r1) {
-        for (int i = lane; i < (r1 - r0) * 16; i += 32)
-          *reinterpret_cast<uint4 *>(base + (i & 8 ? kChunkBytes : 0) + (r0 + (i >> 4)) * 128 +
-                                     (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-      };
-      if (z_lo > 0 && z_lo < kKeys) zero(z_lo & ~15, z_lo);
-      if (z_hi > 0 && z_hi < kKeys) zero(z_hi, (z_hi + 15) & ~15);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.full[st]);
+    if ((t & 31) == 0) mbar_arrive(&c.full[i % Gm::NU]);
+  };
+  // the page ids of the next tile are requested a tile ahead
+  auto ids = [&](const Order<D> &o, int (&id)[8]) {
+    const int k0 = (w.kt0 + o.j) * kKeys;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const int key = k0 + g * kBlock;
+      id[g] = !o.done() && key < w.see_hi && key + kBlock > w.see_lo ? __ldg(w.trow + key / kBlock) : -1;
     }
-    ++u;
-    return true;
-  });
-  // after a failure the last copies of each stage may still be in flight
-  if (*(volatile int *)&c.abort)
-    for (uint32_t i = u > Gm::NU ? u - Gm::NU : 0; i < u; ++i)
-      drain_wait(&c.full[i % Gm::NU], (i / Gm::NU) & 1);
+  };
+  Order<D> o(w.ntiles);
+  int id[8], id_next[8];
+  ids(o, id);
+  bool ok = true;
+  while (!o.done() && ok) {
+    Order<D> on = o;
+    on.next();
+    ids(on, id_next);
+    const int k0 = (w.kt0 + o.j) * kKeys;
+    const uint8_t *const base = o.is_v ? vbase : kbase;
+    bool dense = k0 >= w.see_lo && k0 + kKeys <= w.see_hi;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) dense = dense && (uint32_t)id[g] < (uint32_t)p.kv.num_blocks;
+#pragma unroll
+    for (int h = 0; h < Gm::H; ++h) {
+      const int st = u % Gm::NU;
+      if (u >= FLY) {   // before the wait for a stage, so that no landed unit waits with it
+        copy_wait<FLY - 1>();
+        hand_over(u - FLY);
+      }
+      if (u >= Gm::NU)
+        ok = __all_sync(0xffffffffu, wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr));
+      if (!ok) break;
+      const uint32_t dst = dst0 + st * kUnitBytes;
+      if (dense) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const uint8_t *src = base + h * 256 + (size_t)(uint32_t)id[g] * page;
+          copy16(dst + g * 2048, src);
+          copy16(dst + g * 2048 + 1024, src + 8 * D * 2);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {   // rows 8 i + r0: page i / 2
+          const int g = id[i >> 1], key = k0 + i * 8 + r0;
+          const bool valid = (uint32_t)g < (uint32_t)p.kv.num_blocks && key >= w.see_lo && key < w.see_hi;
+          copy16z(dst + i * 1024, base + h * 256 + (valid ? (size_t)g * page + (i & 1) * (8 * D * 2) : 0), valid);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++u;
+    }
+#pragma unroll
+    for (int g = 0; g < 8; ++g) id[g] = id_next[g];
+    o = on;
+  }
+  copy_wait<0>();
+  for (uint32_t i = u > FLY ? u - FLY : 0; i < u; ++i) hand_over(i);
 }
 
 // ------------------------------------------- other formats: codes to f16 units
@@ -310,23 +388,27 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
   const uint32_t ubase = smem_u32(smem + Gm::OFF_U);
   uint4 code[IT], next[IT];
   uint32_t sc[FP4 ? IT : 1], next_sc[FP4 ? IT : 1];
-  auto load = [&](bool is_v, int j, int h) {
-    const int k0 = (w.kt0 + j) * kKeys;
+  int id[IT], id_next[IT];
+  auto ids = [&](const Order<D> &o, int (&d)[IT]) {   // -1: nothing of this thread's row is read
+    const int k0 = (w.kt0 + o.j) * kKeys;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int key = k0 + i * RPI + r0;
+      d[i] = !o.done() && key >= w.see_lo && key < w.see_hi ? __ldg(w.trow + key / kBlock) : -1;
+    }
+  };
+  auto load = [&](bool is_v, int h) {
     const uint8_t *base = static_cast<const uint8_t *>(is_v ? p.kv.v : p.kv.k);
     const uint8_t *sbase = static_cast<const uint8_t *>(is_v ? p.kv.vs : p.kv.ks);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int key = k0 + i * RPI + r0;
       next[i] = make_uint4(0, 0, 0, 0);
       if constexpr (FP4) next_sc[i] = 0;
-      if (key >= w.see_lo && key < w.see_hi) {
-        const int id = __ldg(w.trow + key / kBlock);
-        if (id >= 0 && id < p.kv.num_blocks) {
-          const size_t row = ((size_t)id * p.kv.hkv + w.kvh) * kBlock + (key & (kBlock - 1));
-          next[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ROW + h * (ROW * 128 / D)) + sub);
-          if constexpr (FP4)
-            next_sc[i] = __ldg(reinterpret_cast<const uint16_t *>(sbase + row * (D / 16) + h * 8) + sub);
-        }
+      if ((uint32_t)id[i] < (uint32_t)p.kv.num_blocks) {
+        const size_t row = ((size_t)id[i] * p.kv.hkv + w.kvh) * kBlock + ((i * RPI + r0) & (kBlock - 1));
+        next[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ROW + h * (ROW * 128 / D)) + sub);
+        if constexpr (FP4)
+          next_sc[i] = __ldg(reinterpret_cast<const uint16_t *>(sbase + row * (D / 16) + h * 8) + sub);
       }
     }
   };
@@ -334,7 +416,9 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
   // converts the loaded unit into its stage
   auto store = [&]() {
     const int st = u % Gm::NU;
-    if (u >= Gm::NU && !wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr)) return false;
+    if (u >= Gm::NU &&
+        !__all_sync(0xffffffffu, wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr)))
+      return false;
     const uint32_t dst = ubase + st * kUnitBytes;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -372,23 +456,34 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
       }
     }
     fence_async_smem();
-    mbar_arrive(&c.full[st]);
+    __syncwarp();
+    if ((t & 31) == 0) mbar_arrive(&c.full[st]);   // one arrival a warp
     ++u;
     return true;
   };
   bool have = false, ok = true;
-  each_unit<D>(w.ntiles, [&](bool is_v, int j, int h) {
-    load(is_v, j, h);
-    if (have) ok = store();
-    if (!ok) return false;
+  Order<D> o(w.ntiles);
+  ids(o, id);
+  while (!o.done() && ok) {
+    Order<D> on = o;
+    on.next();
+    ids(on, id_next);
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      code[i] = next[i];
-      if constexpr (FP4) sc[i] = next_sc[i];
+    for (int h = 0; h < Gm::H; ++h) {
+      load(o.is_v, h);
+      if (have) ok = store();
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        code[i] = next[i];
+        if constexpr (FP4) sc[i] = next_sc[i];
+      }
+      have = true;
     }
-    have = true;
-    return true;
-  });
+#pragma unroll
+    for (int i = 0; i < IT; ++i) id[i] = id_next[i];
+    o = on;
+  }
   if (ok && have) (void)store();
 }
 
@@ -415,6 +510,39 @@ __device__ __forceinline__ void st32f(uint32_t taddr, const float (&v)[32]) {
       : "memory");
 }
 
+// 32 consecutive columns of this thread's lane, without a wait
+__device__ __forceinline__ void ld32_issue(uint32_t taddr, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// waits for this thread's loads; ties the registers to the wait so that none
+// is used before it
+__device__ __forceinline__ void ld_wait(float *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
+
+// u * H(u^2) = tanh(u) for |u| <= 1: the Chebyshev interpolant of
+// tanh(sqrt v) / sqrt v on [0, 1], degree 6; relative error 6e-8 (the
+// singularity nearest to the interval, v = -pi^2 / 4, makes the terms fall by
+// 11.8 each).  Nine fp32 operations, two elements at a time, against two
+// special-function operations that the exponentials need as well.
+__device__ __forceinline__ float2 tanh_small(float2 u) {
+  const float2 v = fmul2(u, u);
+  auto k = [](float x) { return make_float2(x, x); };
+  float2 h = ffma2(v, k(0.00103802513f), k(-0.0061943247f));
+  h = ffma2(v, h, k(0.0202797074f));
+  h = ffma2(v, h, k(-0.0534516461f));
+  h = ffma2(v, h, k(0.133250758f));
+  h = ffma2(v, h, k(-0.333328277f));
+  h = ffma2(v, h, k(0.99999994f));
+  return fmul2(u, h);
+}
+
 template <int DT, int D>
 __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c,
                              uint32_t tmem, int split, int r_lo, int r_hi, int r_pos, bool live,
@@ -433,27 +561,31 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   const float kg = has_global_scale(DT) ? p.kv.kg : 1.f;
   const bool cap = p.sc.cap_log2 != 0.f;
   const float f = (cap ? p.sc.cap_in : p.scale_log2) * kg;
-  // plain scores: the maximum of the raw products is that of the scores
-  const bool plain = DT != PA_KV_INT8 && !cap && p.sc.slopes == nullptr && f > 0.f;
+  // direct: the largest product has the largest score, which is a factor or
+  // a cap away from it
+  const bool direct = DT != PA_KV_INT8 && p.sc.slopes == nullptr && f > 0.f;
+  const float fu = f * 0.34657359027997264f;   // cap: u = score / cap (f is 2 log2 e / cap times the scale)
   float *const wsc = reinterpret_cast<float *>(smem + Gm::OFF_SC) + (tid >> 5) * 2 * kKeys;
 
+  // the tile's page ids, one page in each of lanes 0-7 (again in 8-15, ..)
+  auto page_id = [&](int j) {
+    const int key = (w.kt0 + j) * kKeys + (lane & 7) * kBlock;
+    return j < n && key < w.see_hi && key + kBlock > w.see_lo ? __ldg(w.trow + key / kBlock) : 0;
+  };
+  int id_next = page_id(0);
   float m = kNegInf, l = 0.f;
   bool ok = true;
+#pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int buf = D == 128 ? wg : (j & 1);
     const uint32_t par = D == 128 ? (j & 1) : ((j >> 1) & 1);
     const int k0t = (w.kt0 + j) * kKeys;              // the tile's first key
     const int k0 = k0t + (D == 256 ? wg * 64 : 0);    // this thread's
-    // ids of the tile's pages: keys of a page out of range are hidden
-    int id = 0;
-    uint32_t bad = 0;
-    {
-      const int key = k0t + (lane & 7) * kBlock;
-      const bool in = key < w.see_hi && key + kBlock > w.see_lo;
-      if (in) id = __ldg(w.trow + key / kBlock);
-      bad = __ballot_sync(0xffffffffu, in && (id < 0 || id >= p.kv.num_blocks)) & 0xffu;
-      if (bad && lane == 0) set_err(p.hdr, PA_ERRF_BAD_BLOCK_ID);
-    }
+    // keys of a page whose id is out of range are hidden
+    const int id = id_next;
+    id_next = page_id(j + 1);
+    const uint32_t bad = __ballot_sync(0xffffffffu, id < 0 || id >= p.kv.num_blocks) & 0xffu;
+    if (bad && lane == 0) set_err(p.hdr, PA_ERRF_BAD_BLOCK_ID);
     if constexpr (DT == PA_KV_INT8) {
       // row scales of the tile: lanes 0-15 K, 16-31 V, eight keys each
       const int pg = (lane & 15) >> 1, key = k0t + (lane & 15) * 8;
@@ -483,61 +615,83 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     tc_fence_after();
     const uint32_t S = tmem + lane_off + buf * 128 + (D == 256 ? wg * 64 : 0);
     const float *ksc = wsc + (k0 - k0t), *vsc = ksc + kKeys;
-
-    // ---- scores and their maximum.  Where they are not just the products
-    // times a factor, they are written back over S.
     const bool none = k0 >= a_hi || k0 + NC <= a_lo;
     const bool dense = k0 >= f_lo && k0 + NC <= f_hi && !bad;
-    float mx = kNegInf;
-    float fs = f;
-    if (ok && !none) {
-      if (plain && dense) {
+
+    // Scores that are not one operation away from the products are formed in
+    // place, 32 columns at a time (the ends of the visible range, biased or
+    // int8 scores, and capped ones past the polynomial's interval).
+    auto form = [&]() {
 #pragma unroll 1
-        for (int ch = 0; ch < NC; ch += 32) {
-          float s[32];
-          tmem_ld32(S + ch, s);
-          float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+      for (int ch = 0; ch < NC; ch += 32) {
+        float x[32];
+        tmem_ld32(S + ch, x);
 #pragma unroll
-          for (int i = 4; i < 32; i += 4) {
-            x0 = fmaxf(x0, s[i]);
-            x1 = fmaxf(x1, s[i + 1]);
-            x2 = fmaxf(x2, s[i + 2]);
-            x3 = fmaxf(x3, s[i + 3]);
-          }
-          mx = fmaxf(mx, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
+        for (int i = 0; i < 32; ++i) {
+          x[i] *= f;
+          if constexpr (DT == PA_KV_INT8) x[i] *= ksc[ch + i];
         }
-        mx *= f;
-      } else {
-        fs = 1.f;
-#pragma unroll 1
-        for (int ch = 0; ch < NC; ch += 32) {
-          float s[32];
-          tmem_ld32(S + ch, s);
+        if (cap) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = capped(x[i], p.sc.cap_log2);
+        }
+        if (p.sc.slopes) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            x[i] = fmaf(-slope, fabsf((float)(r_pos - k0 - ch - i)), x[i]);
+        }
+        if (!dense) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            float x = s[i] * f;
-            if constexpr (DT == PA_KV_INT8) x *= ksc[ch + i];
-            if (cap) x = capped(x, p.sc.cap_log2);
-            s[i] = x;
+            const int key = k0 + ch + i;
+            const bool see = key >= r_lo && key < r_hi && !((bad >> ((key - k0t) >> 4)) & 1);
+            x[i] = see ? x[i] : kNegInf;
           }
-          if (p.sc.slopes) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              s[i] = fmaf(-slope, fabsf((float)(r_pos - k0 - ch - i)), s[i]);
-          }
-          if (!dense) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int key = k0 + ch + i;
-              const bool see = key >= r_lo && key < r_hi && !((bad >> ((key - k0t) >> 4)) & 1);
-              s[i] = see ? s[i] : kNegInf;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, s[i]);
-          st32f(S + ch, s);
         }
-        tmem_st_wait();
+        st32f(S + ch, x);
+      }
+      tmem_st_wait();
+    };
+    float s[NC];
+    auto load = [&]() {
+#pragma unroll
+      for (int ch = 0; ch < NC; ch += 32) ld32_issue(S + ch, s + ch);
+#pragma unroll
+      for (int ch = 0; ch < NC; ch += 32) ld_wait(s + ch);
+    };
+    float mx = kNegInf;      // this thread's largest score of the tile (log2 units)
+    float fs = 1.f;          // score = fs * s
+    bool poly = false;       // score = cap_log2 * tanh(fu * s)
+    if (ok && !none) {
+      const bool formed = !(direct && dense);
+      if (formed) form();
+      load();
+      float x0 = s[0], x1 = s[1], y0 = s[0], y1 = s[1];
+#pragma unroll
+      for (int i = 2; i < NC; i += 2) {
+        x0 = fmaxf(x0, s[i]);
+        x1 = fmaxf(x1, s[i + 1]);
+      }
+      mx = fmaxf(x0, x1);
+      if (!formed) {
+        if (cap) {
+#pragma unroll
+          for (int i = 2; i < NC; i += 2) {
+            y0 = fminf(y0, s[i]);
+            y1 = fminf(y1, s[i + 1]);
+          }
+          poly = __all_sync(0xffffffffu, fmaxf(mx, -fminf(y0, y1)) * fu <= 1.f);
+          if (poly) {
+            mx = tanh_small(make_float2(mx * fu, 0.f)).x * p.sc.cap_log2;
+          } else {
+            mx = capped(mx * f, p.sc.cap_log2);
+            form();
+            load();
+          }
+        } else {
+          fs = f;
+          mx *= f;
+        }
       }
     }
     // ---- the running maximum moves when some score passes it by 2^kLazy
@@ -565,49 +719,63 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
           tc_fence_after();
           const uint32_t O = tmem + lane_off + Gm::COL_O + wg * 128;
 #pragma unroll 1
-          for (int ch = 0; ch < 128; ch += 32) {
-            float o[32];
-            tmem_ld32(O + ch, o);
+          for (int ch = 0; ch < 128; ch += 16) {
+            float o[16];
+            tmem_ld16(O + ch, o);
+            uint32_t v[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= al;
-            st32f(O + ch, o);
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(o[i] * al);
+            tmem_st16(O + ch, v);
           }
           tmem_st_wait();
         }
       }
     }
     // ---- weights
-    const float mu = m == kNegInf ? 0.f : m;
     if (ok) {
-      float l0 = 0.f, l1 = 0.f;
-#pragma unroll 1
-      for (int ch = 0; ch < NC; ch += 32) {
-        uint32_t pk[16];
-        if (none) {
+      const float mu = m == kNegInf ? 0.f : m;
+      const float2 nm = make_float2(-mu, -mu), ff = make_float2(fs, fs);
+      const float2 uu = make_float2(fu, fu), cc = make_float2(p.sc.cap_log2, p.sc.cap_log2);
+      float2 l2 = make_float2(0.f, 0.f);
+      if (none) {
+        const uint32_t z[16] = {};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = 0;
+        for (int ch = 0; ch < NC / 2; ch += 16) tmem_st16(S + ch, z);
+      } else {
+        if (poly) {
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) {
+            const float2 x = tanh_small(fmul2(make_float2(s[i], s[i + 1]), uu));
+            const float2 y = ffma2(x, cc, nm);
+            s[i] = y.x;
+            s[i + 1] = y.y;
+          }
         } else {
-          float s[32];
-          tmem_ld32(S + ch, s);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 x = ffma2(make_float2(s[i], s[i + 1]), make_float2(fs, fs), make_float2(-mu, -mu));
-            float a = ex2_approx(x.x), b = ex2_approx(x.y);
-            l0 += a;
-            l1 += b;
-            if constexpr (DT == PA_KV_INT8) {
-              a *= vsc[ch + i];
-              b *= vsc[ch + i + 1];
-            }
-            pk[i / 2] = Gm::QUANT ? tc::f2_to_h2(a, b) : tc::f2_to_bf2(a, b);
+          for (int i = 0; i < NC; i += 2) {
+            const float2 y = ffma2(make_float2(s[i], s[i + 1]), ff, nm);
+            s[i] = y.x;
+            s[i + 1] = y.y;
           }
         }
-        tmem_st16(S + ch / 2, pk);
+#pragma unroll
+        for (int ch = 0; ch < NC; ch += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float2 a = make_float2(ex2_approx(s[ch + i]), ex2_approx(s[ch + i + 1]));
+            l2 = fadd2(l2, a);
+            if constexpr (DT == PA_KV_INT8) a = fmul2(a, make_float2(vsc[ch + i], vsc[ch + i + 1]));
+            pk[i / 2] = Gm::QUANT ? tc::f2_to_h2(a.x, a.y) : tc::f2_to_bf2(a.x, a.y);
+          }
+          tmem_st16(S + ch / 2, pk);
+        }
       }
-      l += l0 + l1;
+      l += l2.x + l2.y;
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&c.pready[buf]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.pready[buf]);
     }
   }
   // ---- the sum, the last PV, the output
@@ -667,26 +835,42 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 
 template <int DT, int D>
 __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
-    prefill_umma_kernel(const PrefillParams p, int max_tiles, const __grid_constant__ CUtensorMap tmK,
-                        const __grid_constant__ CUtensorMap tmV) {
+    prefill_umma_kernel(const PrefillParams p, int max_tiles) {
   using Gm = PGeo<DT, D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ PCtl c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int Hkv = p.kv.hkv, G = p.G;
   Work w;
   w.kvh = blockIdx.x % Hkv;
   const int rest = blockIdx.x / Hkv, split = rest % p.splits;
   const TileOf to = find_tile(p, max_tiles - 1 - rest / p.splits, Gm::ROWS);   // the last tokens see most: first
   if (to.b < 0) return;
+  if (warp == 8) {
+    tmem_alloc(&c.tmem, 512);
+    tmem_relinquish();
+  } else if (tid == 9 * 32) {
+    for (int i = 0; i < Gm::NU; ++i) {
+      mbar_init(&c.full[i], 4);        // the copy group's warps
+      mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.sfull[i], 1);
+      mbar_init(&c.pready[i], D == 128 ? 4 : 8);   // softmax warps
+      mbar_init(&c.odone[i], 1);
+    }
+    mbar_init(&c.done, 1);
+    c.abort = 0;
+    fence_mbar_init();
+  }
   w.b = to.b;
   w.start = to.start;
   w.len = to.len;
   w.row0 = to.first * Gm::ROWS;
   w.nrows = min(Gm::ROWS, to.len * G - w.row0);
   w.trow = p.tables + (size_t)to.b * p.stride;
-  int n = __ldg(p.seq_lens + to.b);
+  int n = to.n;
   const int capacity = (int)min((long long)p.stride * kBlock, 0x7fffffffLL);
   if (n < to.len || n > capacity) {
     if (tid == 0 && n != 0)
@@ -694,38 +878,36 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     n = min(max(n, 0), capacity);
   }
   w.n = n;
-
-  if (tid == 0) {
-    for (int i = 0; i < Gm::NU; ++i) {
-      mbar_init(&c.full[i], Gm::QUANT ? 128 : 1);
-      mbar_init(&c.empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.sfull[i], 1);
-      mbar_init(&c.pready[i], D == 128 ? 128 : 256);
-      mbar_init(&c.odone[i], 1);
-    }
-    mbar_init(&c.fix, 1);
-    mbar_init(&c.done, 1);
-    c.abort = 0;
-    c.lo = 0x7fffffff;
-    c.hi = 0;
-    fence_mbar_init();
-  }
-  if (warp == 8) {
-    tmem_alloc(&c.tmem, 512);
-    tmem_relinquish();
-  }
-  __syncthreads();
+  // row r of the tile: token tok0 + (rem0 + r) / G, head (rem0 + r) % G; the
+  // quotient by a 16-bit reciprocal (exact: rem0 + r < 264, G <= 8)
+  const int tok0 = w.row0 / G, rem0 = w.row0 - tok0 * G, inv_g = 65536 / G + 1;
+  auto split_row = [&](int r, int &tok, int &head) {
+    const int x = rem0 + r, q = (x * inv_g) >> 16;
+    tok = tok0 + q;
+    head = w.kvh * G + x - q * G;
+  };
   // ---- rows of the softmax threads, and the queries
   int r_lo = 0, r_hi = 0, r_pos = 0;
   bool live = false;
   size_t r_out = 0;
   float slope = 0.f;
   if (warp < 8) {
+    // queries: 16 pieces of 16 bytes per thread, all requested before any is used
+    constexpr int CH = D / 8, NQ = Gm::ROWS * CH / 256;
+    uint4 qv[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = (i * 256 + tid) / CH, k = (i * 256 + tid) % CH;
+      int tok, head;
+      split_row(q, tok, head);
+      qv[i] = make_uint4(0, 0, 0, 0);
+      if (q < w.nrows)
+        qv[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.start + tok) * p.Hq + head) * D) + k);
+    }
     const int r = (D == 128 ? tid & ~127 : 0) + (tid & 127);
     live = r < w.nrows;
-    const int rr = w.row0 + (live ? r : 0), tok = rr / G, head = w.kvh * G + rr % G;
+    int tok, head;
+    split_row(live ? r : 0, tok, head);
     r_pos = n - w.len + tok;
     if (live) {
       const KeyRange kr = key_range(p.sc, r_pos, n, p.sc.first_key ? __ldg(p.sc.first_key + w.start + tok) : 0,
@@ -738,24 +920,18 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     const bool sees = r_hi > r_lo;
     const int lo = __reduce_min_sync(0xffffffffu, sees ? r_lo : 0x7fffffff);
     const int hi = __reduce_max_sync(0xffffffffu, sees ? r_hi : 0);
-    if (lane == 0 && hi > 0) {
-      atomicMin(&c.lo, lo);
-      atomicMax(&c.hi, hi);
+    if (lane == 0) {
+      c.lo[warp] = lo;
+      c.hi[warp] = hi;
     }
-    constexpr int CH = D / 8;
-    for (int i = tid; i < Gm::ROWS * CH; i += 256) {
-      const int q = i / CH, k = i % CH;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (q < w.nrows) {
-        const int qr = w.row0 + q;
-        u = __ldg(reinterpret_cast<const uint4 *>(
-                      p.q + ((size_t)(w.start + qr / G) * p.Hq + w.kvh * G + qr % G) * D) + k);
-        if constexpr (Gm::QUANT) {   // f16 operands (exact in f16's normal range)
-          const float2 a = bf16x2_to_f2(u.x), b = bf16x2_to_f2(u.y), d = bf16x2_to_f2(u.z), e = bf16x2_to_f2(u.w);
-          u = make_uint4(tc::f2_to_h2(a.x, a.y), tc::f2_to_h2(b.x, b.y), tc::f2_to_h2(d.x, d.y), tc::f2_to_h2(e.x, e.y));
-        }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = (i * 256 + tid) / CH, k = (i * 256 + tid) % CH, r2 = q & 127;
+      uint4 u = qv[i];
+      if constexpr (Gm::QUANT) {   // f16 operands (exact in f16's normal range)
+        const float2 a = bf16x2_to_f2(u.x), b = bf16x2_to_f2(u.y), d = bf16x2_to_f2(u.z), e = bf16x2_to_f2(u.w);
+        u = make_uint4(tc::f2_to_h2(a.x, a.y), tc::f2_to_h2(b.x, b.y), tc::f2_to_h2(d.x, d.y), tc::f2_to_h2(e.x, e.y));
       }
-      const int r2 = q & 127;
       *reinterpret_cast<uint4 *>(smem + (q >> 7) * (128 * D * 2) + (k >> 3) * kChunkBytes + r2 * 128 +
                                  (((k & 7) ^ (r2 & 7)) << 4)) = u;
     }
@@ -765,8 +941,13 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-  w.see_lo = c.lo;
-  w.see_hi = c.hi;
+  w.see_lo = 0x7fffffff;
+  w.see_hi = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w.see_lo = min(w.see_lo, c.lo[i]);
+    w.see_hi = max(w.see_hi, c.hi[i]);
+  }
   {
     const int t0 = w.see_lo < w.see_hi ? w.see_lo / kKeys : 0;
     const int t1 = w.see_lo < w.see_hi ? (w.see_hi + kKeys - 1) / kKeys : 0;
@@ -774,17 +955,23 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     w.kt0 = t0 + min(t1 - t0, split * per);
     w.ntiles = t0 + min(t1 - t0, (split + 1) * per) - w.kt0;
   }
+  constexpr bool REGS = D == 128;   // registers move to the threads that hold whole rows
   if (warp < 8) {
+    if constexpr (REGS) setmaxnreg_to<kLaunchRegsPf, Gm::REG_SM>();
     // D = 128: the second row tile's group has nothing to do when it is empty
     if (D == 256 || warp < 4 || w.nrows > 128)
       role_softmax<DT, D>(p, w, smem, c, tmem, split, r_lo, r_hi, r_pos, live, r_out, slope);
-  } else if (warp == 8) {
-    if (lane == 0) role_mma<DT, D>(w, smem, c, p.hdr, tmem);
-    __syncwarp();
-  } else if (!Gm::QUANT && warp == 9) {
-    if constexpr (!Gm::QUANT) role_tma<D>(p, w, smem, c, &tmK, &tmV, lane);
-  } else if (Gm::QUANT && warp >= 12) {
-    if constexpr (Gm::QUANT) role_dequant<DT, D>(p, w, smem, c, tid - 384);
+  } else if (warp < 12) {
+    if constexpr (REGS) setmaxnreg_to<kLaunchRegsPf, kRegMma>();
+    if (warp == 8)
+      role_mma<DT, D>(__shfl_sync(0xffffffffu, w.ntiles, 0), __shfl_sync(0xffffffffu, w.nrows > 128 ? 2 : 1, 0),
+                      smem, c, p.hdr, __shfl_sync(0xffffffffu, tmem, 0));
+  } else {
+    if constexpr (REGS) setmaxnreg_to<kLaunchRegsPf, Gm::REG_COPY>();
+    if constexpr (Gm::QUANT)
+      role_dequant<DT, D>(p, w, smem, c, tid - 384);
+    else
+      role_copy<D>(p, w, smem, c, tid - 384);
   }
   tc_fence_before();
   __syncthreads();
@@ -798,22 +985,21 @@ template <int DT, int D>
 cudaError_t launch_umma(const PrefillParams &p, cudaStream_t s) {
   using Gm = PGeo<DT, D>;
   auto kern = prefill_umma_kernel<DT, D>;
-  CUtensorMap tk, tv;
-  std::memset(&tk, 0, sizeof tk);
-  std::memset(&tv, 0, sizeof tv);
-  if constexpr (!Gm::QUANT) {
-    const uint64_t rows = (uint64_t)p.kv.num_blocks * p.kv.hkv * kBlock;
-    if (rows > 0x7fffffffull || !tc::make_row_map(&tk, p.kv.k, D * 2, rows) ||
-        !tc::make_row_map(&tv, p.kv.v, D * 2, rows))
-      return cudaErrorInvalidValue;
-  }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
   if (e != cudaSuccess) return e;
+  if constexpr (D == 128) {
+    // the register split starts from kLaunchRegsPf (allocated in eights): a
+    // build that gave the kernel another count is refused, never launched
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if ((fa.numRegs + 7) / 8 * 8 != kLaunchRegsPf) return cudaErrorInvalidDeviceFunction;
+  }
   // every sequence has at most one tile that is not full
   const long long tiles = (long long)p.T * p.G / Gm::ROWS + p.B;
   const long long grid = tiles * p.kv.hkv * p.splits;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kern<<<(unsigned)grid, Gm::THREADS, Gm::SMEM, s>>>(p, (int)tiles, tk, tv);
+  kern<<<(unsigned)grid, Gm::THREADS, Gm::SMEM, s>>>(p, (int)tiles);
   return cudaGetLastError();
 }
 

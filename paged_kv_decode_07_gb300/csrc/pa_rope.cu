@@ -48,7 +48,7 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
   return f < 0.f ? 0 - t : t;
 }
 
-// norm, rotate and round 16 values of a row held by a lane (two chunks)
+// the 16 values of a row that a lane holds (two chunks of 8)
 struct Pair16 {
   float a[8], b[8];
 };
@@ -78,51 +78,58 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 template <int D>
 __device__ __forceinline__ void rms_norm(Pair16 &x, const uint4 &wa, const uint4 &wb, float eps) {
   constexpr int L = D / 16;
-  float s0 = 0.f, s1 = 0.f;
+  float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    s0 = fmaf(x.a[i], x.a[i], s0);
-    s1 = fmaf(x.b[i], x.b[i], s1);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 a = make_float2(x.a[i], x.a[i + 1]), b = make_float2(x.b[i], x.b[i + 1]);
+    s0 = ffma2(a, a, s0);
+    s1 = ffma2(b, b, s1);
   }
-  float s = s0 + s1;
+  float s = (s0.x + s0.y) + (s1.x + s1.y);
 #pragma unroll
   for (int o = L / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   const float r = rsqrtf(s * (1.0f / D) + eps);
-  float w[8];
-  unpack8(wa, w);
+  const float2 rr = make_float2(r, r);
+  const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x.a[i] = x.a[i] * r * w[i];
-  unpack8(wb, w);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x.b[i] = x.b[i] * r * w[i];
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = fmul2(fmul2(make_float2(x.a[2 * i], x.a[2 * i + 1]), rr), bf16x2_to_f2(ua[i]));
+    const float2 z = fmul2(fmul2(make_float2(x.b[2 * i], x.b[2 * i + 1]), rr), bf16x2_to_f2(ub[i]));
+    x.a[2 * i] = y.x;
+    x.a[2 * i + 1] = y.y;
+    x.b[2 * i] = z.x;
+    x.b[2 * i + 1] = z.y;
+  }
 }
 
+// (x, y) <- (x c - y s, x s + y c) for every pair of the lane; cs, sn hold the
+// pairs' cosines and sines (times the factor)
 template <bool IL>
 __device__ __forceinline__ void rotate(Pair16 &x, const float (&cs)[8], const float (&sn)[8],
                                        bool ra, bool rb) {
-  if constexpr (IL) {   // pairs inside each chunk
-    if (ra) {
+  auto inside = [&](float (&v)[8], int k) {   // pairs (2 i, 2 i + 1) of one chunk
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = x.a[2 * i], v = x.a[2 * i + 1];
-        x.a[2 * i] = u * cs[i] - v * sn[i];
-        x.a[2 * i + 1] = u * sn[i] + v * cs[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = ffma2(make_float2(v[2 * i + 1], v[2 * i + 1]), make_float2(-sn[k + i], cs[k + i]),
+                             fmul2(make_float2(v[2 * i], v[2 * i]), make_float2(cs[k + i], sn[k + i])));
+      v[2 * i] = y.x;
+      v[2 * i + 1] = y.y;
     }
-    if (rb) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = x.b[2 * i], v = x.b[2 * i + 1];
-        x.b[2 * i] = u * cs[4 + i] - v * sn[4 + i];
-        x.b[2 * i + 1] = u * sn[4 + i] + v * cs[4 + i];
-      }
-    }
+  };
+  if constexpr (IL) {
+    if (ra) inside(x.a, 0);
+    if (rb) inside(x.b, 4);
   } else if (ra) {      // element i of the first chunk with element i of the second
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = x.a[i], v = x.b[i];
-      x.a[i] = u * cs[i] - v * sn[i];
-      x.b[i] = u * sn[i] + v * cs[i];
+    for (int i = 0; i < 8; i += 2) {
+      const float2 u = make_float2(x.a[i], x.a[i + 1]), v = make_float2(x.b[i], x.b[i + 1]);
+      const float2 c = make_float2(cs[i], cs[i + 1]), t = make_float2(sn[i], sn[i + 1]);
+      const float2 y = ffma2(make_float2(-v.x, -v.y), t, fmul2(u, c));
+      const float2 z = ffma2(v, c, fmul2(u, t));
+      x.a[i] = y.x;
+      x.a[i + 1] = y.y;
+      x.b[i] = z.x;
+      x.b[i + 1] = z.y;
     }
   }
 }
@@ -182,18 +189,19 @@ __device__ __forceinline__ void encode_row(const KvView &kv, int which, size_t r
   }
 }
 
-// One warp takes rows [part * per, ...) of a token's Hq + 2 Hkv rows (q
-// heads, then k, then v); 32 / L rows at a time.
+// A token's rows are taken in steps of 32 / L heads of one kind: first the
+// queries, then the keys, then the values.  One warp takes a run of a token's
+// steps, two at a time so that both are in flight before either is used.
 template <int DT, int D, bool IL>
 __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams p) {
   constexpr int L = D / 16, RPW = 32 / L;
   const int lane = threadIdx.x & 31, sub = lane / L, j = lane % L;
-  const long long w = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int t = (int)(w / p.parts), part = (int)(w % p.parts);
+  const int w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int t = w / p.parts, part = w % p.parts;
   if (t >= p.T) return;
   const int Hq = p.Hq, Hkv = p.kv.hkv;
-  const int rows = Hq + 2 * Hkv;
-  const int r_end = min(rows, (part + 1) * p.rows_per_part);
+  const int sq = (Hq + RPW - 1) / RPW, skv = (Hkv + RPW - 1) / RPW;
+  const int s0 = part * p.steps_per_part, s1 = min(sq + 2 * skv, s0 + p.steps_per_part);
 
   // this lane's two chunks
   const int nr = p.rot / 16;   // chunks per half of the rotated part
@@ -209,67 +217,92 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
     ca = ra ? j : nr + j;        // past the rotated part: 2 nr + (j - nr)
     cb = ra ? j + nr : ca + (L - nr);
   }
+  // one step: its kind (uniform in the warp), this lane's head and chunks
+  struct Step {
+    int kind, h;
+    bool live;
+    uint4 a, b;
+  };
+  auto load = [&](int s) {
+    Step x;
+    x.kind = s < sq ? 0 : s < sq + skv ? 1 : 2;
+    x.h = (x.kind == 0 ? s : x.kind == 1 ? s - sq : s - sq - skv) * RPW + sub;
+    x.live = s < s1 && x.h < (x.kind == 0 ? Hq : Hkv);
+    x.a = x.b = make_uint4(0, 0, 0, 0);
+    if (x.live) {
+      const __nv_bfloat16 *src = x.kind == 0   ? p.q + (size_t)t * p.q_stride
+                                 : x.kind == 1 ? p.k + (size_t)t * p.k_stride
+                                               : p.v + (size_t)t * p.v_stride;
+      const uint4 *s4 = reinterpret_cast<const uint4 *>(src + (size_t)x.h * D);
+      x.a = __ldcs(s4 + ca);
+      x.b = __ldcs(s4 + cb);
+    }
+    return x;
+  };
+  Step x0 = load(s0), x1 = load(s0 + 1);
+  uint4 wq[2] = {}, wk[2] = {};
+  if (p.q_norm) {
+    wq[0] = __ldg(reinterpret_cast<const uint4 *>(p.q_norm) + ca);
+    wq[1] = __ldg(reinterpret_cast<const uint4 *>(p.q_norm) + cb);
+  }
+  if (p.k_norm) {
+    wk[0] = __ldg(reinterpret_cast<const uint4 *>(p.k_norm) + ca);
+    wk[1] = __ldg(reinterpret_cast<const uint4 *>(p.k_norm) + cb);
+  }
   // the angles of this lane's pairs, once for every head of the token
   float cs[8], sn[8];
   const int pos = __ldg(p.positions + t);
-  if (ra || rb) {
+  const int64_t slot = __ldg(p.slots + t);
+  if ((ra || rb) && s0 < sq + skv) {
+    float fr[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int pair = IL ? (i < 4 ? 4 * ca + i : 4 * cb + i - 4) : 8 * j + i;
-      float c = 1.f, s = 0.f;
-      if (pair < p.rot / 2) {
-        const uint64_t ph = turns_per_position(__ldg(p.inv_freq + pair)) * (uint64_t)(int64_t)pos;
-        // half turns in [-1, 1): the top 32 bits of the phase, as a signed number
-        sincospif((float)(int32_t)(uint32_t)(ph >> 32) * 0x1p-31f, &s, &c);
-      }
-      cs[i] = c * p.factor;
-      sn[i] = s * p.factor;
+      fr[i] = pair < p.rot / 2 ? __ldg(p.inv_freq + pair) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t ph = turns_per_position(fr[i]) * (uint64_t)(int64_t)pos;
+      // half turns in [-1, 1): the top 32 bits of the phase, as a signed number
+      sincospif((float)(int32_t)(uint32_t)(ph >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+      cs[i] *= p.factor;
+      sn[i] *= p.factor;
     }
   }
-  const int64_t slot = __ldg(p.slots + t);
   const int64_t nslots = (int64_t)p.kv.num_blocks * kBlock;
   const bool bad = slot < -1 || slot >= nslots;
   if (bad && part == 0 && lane == 0) set_err(p.hdr, PA_ERRF_BAD_SLOT);
   const bool keep = slot >= 0 && !bad;
+  const size_t row0 = keep ? (size_t)(slot >> 4) * Hkv * kBlock + (size_t)(slot & 15) : 0;
 
-  for (int r0 = part * p.rows_per_part; r0 < r_end; r0 += RPW) {
-    const int r = r0 + sub;
-    const bool live = r < r_end;
-    const int kind = r < Hq ? 0 : r < Hq + Hkv ? 1 : 2;
-    const int h = kind == 0 ? r : kind == 1 ? r - Hq : r - Hq - Hkv;
-    const __nv_bfloat16 *src = kind == 0   ? p.q + (size_t)t * p.q_stride
-                               : kind == 1 ? p.k + (size_t)t * p.k_stride
-                                           : p.v + (size_t)t * p.v_stride;
+  auto finish = [&](const Step &st) {
     Pair16 x;
-    if (live) {
-      const uint4 *s4 = reinterpret_cast<const uint4 *>(src + (size_t)h * D);
-      unpack8(__ldcs(s4 + ca), x.a);
-      unpack8(__ldcs(s4 + cb), x.b);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x.a[i] = x.b[i] = 0.f;
-    }
-    if (p.q_norm || p.k_norm) {
-      Pair16 y = x;
-      const __nv_bfloat16 *w = kind == 0 ? p.q_norm : p.k_norm;
-      uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-      if (w) {
-        wa = __ldg(reinterpret_cast<const uint4 *>(w) + ca);
-        wb = __ldg(reinterpret_cast<const uint4 *>(w) + cb);
+    unpack8(st.a, x.a);
+    unpack8(st.b, x.b);
+    if (st.kind == 0) {
+      if (p.q_norm) rms_norm<D>(x, wq[0], wq[1], p.eps);
+      rotate<IL>(x, cs, sn, ra, rb);
+      if (st.live) {
+        uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + (size_t)t * p.q_out_stride + (size_t)st.h * D);
+        dst[ca] = pack8(x.a);
+        dst[cb] = pack8(x.b);
       }
-      rms_norm<D>(y, wa, wb, p.eps);
-      if (kind < 2 && w) x = y;
+      return;
     }
-    if (kind < 2) rotate<IL>(x, cs, sn, ra, rb);
-    if (kind == 0 && live) {
-      uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + (size_t)t * p.q_out_stride + (size_t)h * D);
-      dst[ca] = pack8(x.a);
-      dst[cb] = pack8(x.b);
+    if (st.kind == 1) {
+      if (p.k_norm) rms_norm<D>(x, wk[0], wk[1], p.eps);
+      rotate<IL>(x, cs, sn, ra, rb);
     }
-    if (__any_sync(0xffffffffu, kind > 0)) {
-      const size_t row = keep ? ((size_t)(slot >> 4) * Hkv + h) * kBlock + (size_t)(slot & 15) : 0;
-      encode_row<DT, D>(p.kv, kind == 2, row, ca, cb, x, live && kind > 0 && keep);
+    encode_row<DT, D>(p.kv, st.kind == 2, row0 + (size_t)st.h * kBlock, ca, cb, x, st.live && keep);
+  };
+  for (int s = s0; s < s1; s += 2) {
+    const Step y0 = x0, y1 = x1;
+    if (s + 2 < s1) {
+      x0 = load(s + 2);
+      x1 = load(s + 3);
     }
+    finish(y0);
+    if (s + 1 < s1) finish(y1);
   }
 }
 
@@ -285,10 +318,14 @@ cudaError_t launch_dt(const RopeParams &p, unsigned grid, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rope(RopeParams p, cudaStream_t s) {
-  const int rpw = 512 / p.kv.D;   // rows a warp takes at a time
-  const int rows = p.Hq + 2 * p.kv.hkv;
-  p.parts = 1;
-  p.rows_per_part = (rows + rpw - 1) / rpw * rpw;
+  const int rpw = 512 / p.kv.D;   // heads a step takes
+  const int steps = (p.Hq + rpw - 1) / rpw + 2 * ((p.kv.hkv + rpw - 1) / rpw);
+  // few tokens: a token's steps are spread over several warps, about eight
+  // warps per SM in all
+  const int want = (1216 + p.T - 1) / p.T;
+  const int parts = want < 1 ? 1 : want > steps ? steps : want;
+  p.steps_per_part = (steps + parts - 1) / parts;
+  p.parts = (steps + p.steps_per_part - 1) / p.steps_per_part;
   const long long warps = (long long)p.T * p.parts;
   const unsigned grid = (unsigned)((warps + kRopeWarps - 1) / kRopeWarps);
   switch (p.kv.dtype * 2 + (p.kv.D == 256)) {

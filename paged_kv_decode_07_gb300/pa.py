@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -116,6 +117,18 @@ class _Options(ctypes.Structure):
                 ("target_items", ctypes.c_int32), ("event_begin", ctypes.c_void_p),
                 ("event_end", ctypes.c_void_p), ("test_flags", ctypes.c_int32)]
 
+
+def _packer(cls):
+    """Fields of a ctypes structure -> its bytes, in one call (a structure
+    object's construction takes several times as long)."""
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f"}
+    fmt = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0P")
+    assert fmt.size == ctypes.sizeof(cls)
+    return fmt.pack
+
+
+_pack_kv, _pack_problem, _pack_rope = _packer(_KvCache), _packer(_Problem), _packer(_Rope)
+_pack_score, _pack_prefill, _pack_options = _packer(_Score), _packer(_Prefill), _packer(_Options)
 
 _lib = None
 
@@ -445,37 +458,44 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: Optional[s
     return inv.to(device), float(att.value)
 
 
-def _check(t, name, dtype, shape, device, strided=False):
-    """A tensor argument's type, shape and place.  `strided`: [tokens, heads,
-    head_dim] whose tokens may lie any distance apart."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}: got {t.dtype} "
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _need(t, name, dtype, shape, idx, strided=False):
+    """Raises ValueError unless the tensor has this type, shape, device index
+    (-1: the CPU) and layout.  strided: [tokens, heads, head_dim], the tokens
+    any distance apart."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx:
+        where = "cpu" if idx < 0 else f"cuda:{idx}"
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {where}: got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
-    if strided:
-        ok = (t.stride(2) == 1 and (t.shape[1] < 2 or t.stride(1) == shape[2])) or t.numel() == 0
-    else:
-        ok = t.is_contiguous()
-    if not ok:
-        raise ValueError(f"{name} must be contiguous{' within a token' if strided else ''}: "
-                         f"got strides {t.stride()}")
+    if not t.is_contiguous():
+        st = t.stride()
+        if not strided or st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
+            raise ValueError(f"{name} must be contiguous{' within a token' if strided else ''}: "
+                             f"got strides {st}")
 
 
-class _on:
-    """Makes a tensor's device current for a call (its kernels are launched
-    on that device's current stream)."""
+def _elsewhere(idx, stream):
+    """A context for a call whose stream or device is not the current one
+    (its outputs are then allocated there too), or None."""
+    if idx < 0:
+        raise ValueError("the KV cache must be on a CUDA device")
+    if stream is not None:
+        if stream.device.index != idx:
+            raise ValueError(f"stream is on {stream.device}, the KV cache on cuda:{idx}")
+        return torch.cuda.stream(stream)
+    if torch._C._cuda_getDevice() != idx:
+        return torch.cuda.device(idx)
+    return None
 
-    __slots__ = ("guard",)
 
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _kv_bytes(kv: "KvCache", hkv: int, D: int):
+    ks, vs = kv.k_scale, kv.v_scale
+    return _pack_kv(DTYPE_CODES[kv.dtype], kv.k_cache.shape[0], kv.block_size, hkv, D,
+                    kv.k_cache.data_ptr(), kv.v_cache.data_ptr(),
+                    0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
+                    kv.k_global, kv.v_global)
 
 
 def rope_append(kv: KvCache, q, k, v, positions, slot_mapping, inv_freq, *, interleaved=False,
@@ -491,29 +511,37 @@ def rope_append(kv: KvCache, q, k, v, positions, slot_mapping, inv_freq, *, inte
     [rot_dim / 2] (rope_frequencies).  Returns the rotated queries bf16
     [T, Hq, D]; q_out=q rotates them in place."""
     T, Hq, D = q.shape
-    dev = kv.k_cache.device
-    Hkv = kv.num_kv_heads
-    _check(q, "q", torch.bfloat16, (T, Hq, kv.head_dim), dev, True)
-    _check(k, "k", torch.bfloat16, (T, Hkv, D), dev, True)
-    _check(v, "v", torch.bfloat16, (T, Hkv, D), dev, True)
-    _check(positions, "positions", torch.int32, (T,), dev)
-    _check(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
-    _check(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev)
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _check(w, name, torch.bfloat16, (D,), dev)
+    kc = kv.k_cache
+    idx, hkv = kc.get_device(), kc.shape[1]
+    half = inv_freq.numel()
+    _need(q, "q", _BF16, (T, Hq, kv.head_dim), idx, True)
+    _need(k, "k", _BF16, (T, hkv, D), idx, True)
+    _need(v, "v", _BF16, (T, hkv, D), idx, True)
+    _need(positions, "positions", _I32, (T,), idx)
+    _need(slot_mapping, "slot_mapping", _I64, (T,), idx)
+    _need(inv_freq, "inv_freq", _F32, (half,), idx)
+    if q_norm is not None:
+        _need(q_norm, "q_norm", _BF16, (D,), idx)
+    if k_norm is not None:
+        _need(k_norm, "k_norm", _BF16, (D,), idx)
+    if q_out is not None:
+        _need(q_out, "q_out", _BF16, (T, Hq, D), idx, True)
+    there = _elsewhere(idx, stream)
+    if there is not None:
+        with there:
+            return rope_append(kv, q, k, v, positions, slot_mapping, inv_freq,
+                               interleaved=interleaved, attn_factor=attn_factor, q_norm=q_norm,
+                               k_norm=k_norm, eps=eps, q_out=q_out, workspace=workspace)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    else:
-        _check(q_out, "q_out", torch.bfloat16, (T, Hq, D), dev, True)
-    a = _Rope(T, Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), q.stride(0),
-              k.stride(0), v.stride(0), q_out.stride(0), positions.data_ptr(),
-              slot_mapping.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0,
-              inv_freq.data_ptr(), attn_factor, None if q_norm is None else q_norm.data_ptr(),
-              None if k_norm is None else k_norm.data_ptr(), eps)
-    with _on(dev):
-        st = lib().pa_rope_append(ctypes.byref(kv.struct()), ctypes.byref(a), _ptr(workspace),
-                                  _stream(stream))
+        q_out = torch.empty((T, Hq, D), dtype=_BF16, device=kc.device)
+    a = _pack_rope(T, Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), q.stride(0),
+                   k.stride(0), v.stride(0), q_out.stride(0), positions.data_ptr(),
+                   slot_mapping.data_ptr(), 2 * half, 1 if interleaved else 0, inv_freq.data_ptr(),
+                   attn_factor, 0 if q_norm is None else q_norm.data_ptr(),
+                   0 if k_norm is None else k_norm.data_ptr(), eps)
+    st = lib().pa_rope_append(_kv_bytes(kv, hkv, D), a,
+                              None if workspace is None else workspace.data_ptr(),
+                              torch._C._cuda_getCurrentRawStream(idx))
     if st != PA_OK:
         raise PaError("pa_rope_append", st)
     return q_out
@@ -534,16 +562,47 @@ class Score:
     first_key: Optional[torch.Tensor] = None
     prefix_lens: Optional[torch.Tensor] = None
 
-    def struct(self, num_q_heads: int, tokens: int, batch: int, device) -> _Score:
-        for t, name, dt, n in ((self.slopes, "slopes", torch.float32, num_q_heads),
-                               (self.first_key, "first_key", torch.int32, tokens),
-                               (self.prefix_lens, "prefix_lens", torch.int32, batch)):
-            if t is not None:
-                _check(t, name, dt, (n,), device)
-        return _Score(float(self.softcap), int(self.window),
-                      None if self.slopes is None else self.slopes.data_ptr(),
-                      None if self.first_key is None else self.first_key.data_ptr(),
-                      None if self.prefix_lens is None else self.prefix_lens.data_ptr())
+    def pack(self, num_q_heads: int, tokens: int, batch: int, idx: int) -> bytes:
+        sl, fk, pl = self.slopes, self.first_key, self.prefix_lens
+        if sl is not None:
+            _need(sl, "slopes", _F32, (num_q_heads,), idx)
+        if fk is not None:
+            _need(fk, "first_key", _I32, (tokens,), idx)
+        if pl is not None:
+            _need(pl, "prefix_lens", _I32, (batch,), idx)
+        if not -2 ** 31 <= self.window < 2 ** 31:
+            raise ValueError(f"window must fit 32 bits: got {self.window}")
+        return _pack_score(self.softcap, self.window, 0 if sl is None else sl.data_ptr(),
+                           0 if fk is None else fk.data_ptr(), 0 if pl is None else pl.data_ptr())
+
+
+_PLAIN = _pack_score(0.0, 0, 0, 0, 0)
+
+
+def _check_out(out, shape, idx):
+    if out.dtype is not _F32 and out.dtype is not _BF16:
+        raise ValueError(f"out must be bf16 or fp32: got {out.dtype}")
+    _need(out, "out", out.dtype, shape, idx)
+
+
+def _call(fn, kvb, prob, score, opts, workspace, device, idx):
+    """A call that needs a workspace: the caller's, or a new one where that is
+    missing or too small.  Returns the workspace used."""
+    L = lib()
+    tail = (prob, score) if opts is None else (prob, score, opts)
+    raw = torch._C._cuda_getCurrentRawStream(idx)
+    f = getattr(L, fn)
+    st = PA_ERR_WORKSPACE_TOO_SMALL
+    if workspace is not None:
+        st = f(kvb, *tail, workspace.data_ptr(), workspace.nbytes, raw)
+    if st == PA_ERR_WORKSPACE_TOO_SMALL:
+        need = (L.pa_prefill_workspace_bytes(kvb, prob) if opts is None
+                else L.pa_workspace_bytes(kvb, prob, opts))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        st = f(kvb, *tail, workspace.data_ptr(), workspace.nbytes, raw)
+    if st != PA_OK:
+        raise PaError(fn, st)
+    return workspace
 
 
 def decode_scored(kv: KvCache, q, block_tables, seq_lens, softmax_scale, *, score=None, out=None,
@@ -552,42 +611,35 @@ def decode_scored(kv: KvCache, q, block_tables, seq_lens, softmax_scale, *, scor
     """decode with score options: q bf16 [B, 1, Hq, D] -> (out, [lse,]
     workspace).  A workspace that is too small is replaced."""
     B, Q, Hq, D = q.shape
-    dev = kv.k_cache.device
-    _check(q, "q", torch.bfloat16, (B, 1, Hq, kv.head_dim), dev)
-    _check(block_tables, "block_tables", torch.int32, (B, int(block_tables.shape[1])), dev)
-    _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    kc = kv.k_cache
+    idx, hkv = kc.get_device(), kc.shape[1]
+    _need(q, "q", _BF16, (B, 1, Hq, kv.head_dim), idx)
+    _need(block_tables, "block_tables", _I32, (B, block_tables.shape[1]), idx)
+    _need(seq_lens, "seq_lens", _I32, (B,), idx)
+    if out is not None:
+        _check_out(out, (B, 1, Hq, D), idx)
+    sc = _PLAIN if score is None else score.pack(Hq, B, B, idx)
+    there = _elsewhere(idx, stream)
+    if there is not None:
+        with there:
+            return decode_scored(kv, q, block_tables, seq_lens, softmax_scale, score=score, out=out,
+                                 out_fp32=out_fp32, return_lse=return_lse, max_seq_len=max_seq_len,
+                                 workspace=workspace, kernel=kernel, split_blocks=split_blocks,
+                                 target_items=target_items, events=events)
     if out is None:
-        out = torch.empty((B, Q, Hq, D), dtype=torch.float32 if out_fp32 else torch.bfloat16,
-                          device=dev)
-    elif out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"out must be bf16 or fp32: got {out.dtype}")
-    else:
-        _check(out, "out", out.dtype, (B, Q, Hq, D), dev)
-    lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=dev) if return_lse else None
+        out = torch.empty((B, 1, Hq, D), dtype=_F32 if out_fp32 else _BF16, device=kc.device)
+    lse = torch.empty((B, 1, Hq), dtype=_F32, device=kc.device) if return_lse else None
     if max_seq_len is None:
-        max_seq_len = int(block_tables.shape[1]) * kv.block_size
-    sc = (score if score is not None else Score()).struct(Hq, B, B, dev)
-    opts = _options(kernel, split_blocks, target_items, events)
-    kvs = kv.struct()
-    prob = _problem(kv, q, block_tables, seq_lens, softmax_scale, out, lse, max_seq_len)
-    need = int(lib().pa_workspace_bytes(ctypes.byref(kvs), ctypes.byref(prob), ctypes.byref(opts)))
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        st = lib().pa_decode_scored(ctypes.byref(kvs), ctypes.byref(prob), ctypes.byref(sc),
-                                    ctypes.byref(opts), _ptr(workspace), workspace.numel(),
-                                    _stream(stream))
-    if st != PA_OK:
-        raise PaError("pa_decode_scored", st)
+        max_seq_len = block_tables.shape[1] * kv.block_size
+    opts = _pack_options(kernel, split_blocks, target_items,
+                         0 if events is None else events[0].cuda_event,
+                         0 if events is None else events[1].cuda_event, 0)
+    prob = _pack_problem(B, Hq, 1, q.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+                         seq_lens.data_ptr(), max_seq_len, softmax_scale, out.data_ptr(),
+                         1 if out.dtype is _F32 else 0, 0 if lse is None else lse.data_ptr())
+    workspace = _call("pa_decode_scored", _kv_bytes(kv, hkv, D), prob, sc, opts, workspace,
+                      kc.device, idx)
     return (out, lse, workspace) if return_lse else (out, workspace)
-
-
-def _prefill_struct(q, q_starts, block_tables, seq_lens, max_seq_len, softmax_scale, out, lse):
-    return _Prefill(int(seq_lens.shape[0]), int(q.shape[1]), int(q.shape[0]), q.data_ptr(),
-                    q_starts.data_ptr(), block_tables.data_ptr(), int(block_tables.shape[1]),
-                    seq_lens.data_ptr(), int(max_seq_len), float(softmax_scale), out.data_ptr(),
-                    1 if out.dtype == torch.float32 else 0,
-                    None if lse is None else lse.data_ptr())
 
 
 def prefill(kv: KvCache, q, q_starts, block_tables, seq_lens, softmax_scale, *, score=None,
@@ -600,33 +652,32 @@ def prefill(kv: KvCache, q, q_starts, block_tables, seq_lens, softmax_scale, *, 
     outside are left as they are.  Returns (out [T, Hq, D], [lse [T, Hq],]
     workspace).  A workspace that is too small is replaced."""
     T, Hq, D = q.shape
-    B = int(seq_lens.shape[0])
-    dev = kv.k_cache.device
-    _check(q, "q", torch.bfloat16, (T, Hq, kv.head_dim), dev)
-    _check(q_starts, "q_starts", torch.int32, (B + 1,), dev)
-    _check(block_tables, "block_tables", torch.int32, (B, int(block_tables.shape[1])), dev)
-    _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    B = seq_lens.shape[0]
+    kc = kv.k_cache
+    idx, hkv = kc.get_device(), kc.shape[1]
+    _need(q, "q", _BF16, (T, Hq, kv.head_dim), idx)
+    _need(q_starts, "q_starts", _I32, (B + 1,), idx)
+    _need(block_tables, "block_tables", _I32, (B, block_tables.shape[1]), idx)
+    _need(seq_lens, "seq_lens", _I32, (B,), idx)
+    if out is not None:
+        _check_out(out, (T, Hq, D), idx)
+    sc = _PLAIN if score is None else score.pack(Hq, T, B, idx)
+    there = _elsewhere(idx, stream)
+    if there is not None:
+        with there:
+            return prefill(kv, q, q_starts, block_tables, seq_lens, softmax_scale, score=score,
+                           out=out, out_fp32=out_fp32, return_lse=return_lse,
+                           max_seq_len=max_seq_len, workspace=workspace)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float32 if out_fp32 else torch.bfloat16,
-                          device=dev)
-    elif out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"out must be bf16 or fp32: got {out.dtype}")
-    else:
-        _check(out, "out", out.dtype, (T, Hq, D), dev)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+        out = torch.empty((T, Hq, D), dtype=_F32 if out_fp32 else _BF16, device=kc.device)
+    lse = torch.empty((T, Hq), dtype=_F32, device=kc.device) if return_lse else None
     if max_seq_len is None:
-        max_seq_len = int(block_tables.shape[1]) * kv.block_size
-    sc = (score if score is not None else Score()).struct(Hq, T, B, dev)
-    kvs = kv.struct()
-    prob = _prefill_struct(q, q_starts, block_tables, seq_lens, max_seq_len, softmax_scale, out, lse)
-    need = int(lib().pa_prefill_workspace_bytes(ctypes.byref(kvs), ctypes.byref(prob)))
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        st = lib().pa_prefill(ctypes.byref(kvs), ctypes.byref(prob), ctypes.byref(sc),
-                              _ptr(workspace), workspace.numel(), _stream(stream))
-    if st != PA_OK:
-        raise PaError("pa_prefill", st)
+        max_seq_len = block_tables.shape[1] * kv.block_size
+    prob = _pack_prefill(B, Hq, T, q.data_ptr(), q_starts.data_ptr(), block_tables.data_ptr(),
+                         block_tables.shape[1], seq_lens.data_ptr(), max_seq_len, softmax_scale,
+                         out.data_ptr(), 1 if out.dtype is _F32 else 0,
+                         0 if lse is None else lse.data_ptr())
+    workspace = _call("pa_prefill", _kv_bytes(kv, hkv, D), prob, sc, None, workspace, kc.device, idx)
     return (out, lse, workspace) if return_lse else (out, workspace)
 
 
