@@ -17,14 +17,17 @@
 // largest the swizzled layout allows over scattered 16-token pages, moves 24
 // bytes per cycle and SM; D = 256 needs twice that.)
 //
-// D = 128: a CTA takes two row tiles (256 rows), one per softmax group, that
-// share every K and V unit; while one group is at its softmax the MMAs of the
-// other run.  D = 256: O alone takes 256 columns of tensor memory, so a CTA
-// takes one row tile with two S buffers, and the two softmax groups share the
-// tile, each 64 of its 128 keys.
+// Two softmax groups share a row tile, each 64 of a key tile's 128 keys, so
+// that two warps of every SM sub-partition are at the same tile: one alone
+// takes twice as long over it (its instructions wait for each other), and the
+// tile's next products wait for its weights.
+// D = 128: a CTA takes two row tiles (256 rows) that share every K and V unit;
+// while one is at its softmax the MMAs of the other run.  D = 256: O alone
+// takes 256 columns of tensor memory, so a CTA takes one row tile, with two S
+// buffers.
 //
-// Roles: warps 0-7 softmax (two groups), warp 8 MMA issue (one thread), warps
-// 12-15 copies or dequantisation.  Hand-offs are
+// Roles: softmax groups (D = 128: four, D = 256: two), a group whose first
+// warp issues the MMAs, a group for copies or dequantisation.  Hand-offs are
 // mbarriers; every wait is capped, and a timeout sets PA_ERRF_WAIT_TIMEOUT,
 // raises the CTA's abort flag and lets copies and MMAs in flight finish.
 #pragma once
@@ -41,10 +44,6 @@ constexpr int kKeys = 128;           // keys per tile
 constexpr int kUnitBytes = 32768;    // [128 keys][128 dims] of 16-bit values
 constexpr int kChunkBytes = 16384;   // 64 dims of it
 constexpr float kLazy = 8.0f;        // log2 of how far a score may pass the running maximum
-// Registers per thread at launch and after the split (D = 128, whose softmax
-// threads hold a row of 128 scores): MMA group, copies or dequantisation, and
-// the two softmax groups the rest.
-constexpr int kLaunchRegsPf = 128, kRegMma = 48;
 
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   float2 d;
@@ -63,15 +62,19 @@ struct PGeo {
   static constexpr int ROWS = 128 * MT;
   static constexpr int H = D / 128;                // units per K or V tile
   static constexpr int NU = QUANT ? 4 : 5;         // ring
-  static constexpr int NC = D == 128 ? 128 : 64;   // S columns per softmax thread
-  static constexpr int THREADS = 512;
-  static constexpr int REG_COPY = QUANT ? 112 : 64;
-  static constexpr int REG_SM = (4 * kLaunchRegsPf - kRegMma - REG_COPY) / 16 * 8;
-  static_assert(2 * REG_SM + kRegMma + REG_COPY <= 4 * kLaunchRegsPf, "register split");
+  static constexpr int NC = 64;                    // S columns per softmax thread
+  static constexpr int NO = D / 2;                 // O columns per softmax thread
+  static constexpr int SMW = 8 * MT;               // softmax warps
+  static constexpr int THREADS = (SMW + 8) * 32;
+  // Registers per thread at launch, and after the split (D = 128): MMA group,
+  // copies or dequantisation, softmax groups
+  static constexpr int LAUNCH_REGS = D == 128 ? 80 : 128;
+  static constexpr int REG_MMA = 40, REG_COPY = QUANT ? 88 : 56, REG_SM = QUANT ? 88 : 96;
+  static_assert(4 * REG_SM + REG_MMA + REG_COPY <= 6 * 80, "register split");
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int OFF_U = QBYTES;
   static constexpr int OFF_SC = OFF_U + NU * kUnitBytes;   // int8: K and V row scales, per warp
-  static constexpr int SC_BYTES = DT == PA_KV_INT8 ? 8 * 2 * kKeys * 4 : 0;
+  static constexpr int SC_BYTES = DT == PA_KV_INT8 ? SMW * 2 * kKeys * 4 : 0;
   static constexpr int SMEM = OFF_SC + SC_BYTES + 1024;    // + alignment slack
   static constexpr uint32_t COL_O = 256;
   static_assert(SMEM + 2048 <= 227 * 1024, "shared memory (with the static control block)");
@@ -88,8 +91,8 @@ struct PCtl {
   uint64_t done;                // every MMA complete
   uint32_t tmem;
   int abort;
-  int lo[8], hi[8];             // keys that some row of each softmax warp sees
-  float red[2][128];            // D = 256: the halves' maxima, at the end their sums
+  int lo[16], hi[16];           // keys that some row of each softmax warp sees
+  float red[256];               // a row's maximum (at the end its sum), from one half to the other
 };
 
 // capped wait that also gives up once another role has given up
@@ -183,12 +186,13 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
       mma_ss_if(lead, tmem + buf * 128, qb + off, kb + off, IQK, (h > 0 || ks > 0) ? 1u : 0u);
     }
   };
-  // O (+)= P(buffer) times V unit i; P sits in two runs of 32 columns, `half` columns apart
-  auto pv = [&](uint32_t i, uint32_t o, uint32_t buf, uint32_t half, bool first) {
+  // O (+)= P(buffer) times V unit i; P sits in two runs of 32 columns, one in
+  // each softmax group's half of S
+  auto pv = [&](uint32_t i, uint32_t o, uint32_t buf, bool first) {
     const uint64_t vb = dV + (uint64_t)((i % Gm::NU) * (kUnitBytes >> 4));
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
-      mma_ts_if(lead, o, tmem + buf * 128 + (ks >> 2) * half + (ks & 3) * 8,
+      mma_ts_if(lead, o, tmem + buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
                 vb + (uint64_t)((ks * 2048) >> 4), IPV, (!first || ks > 0) ? 1u : 0u);
   };
   if constexpr (D == 128) {
@@ -209,7 +213,7 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
           ok = false;
           break;
         }
-        pv(uv, tmem + Gm::COL_O + t * 128, t, 32, j == 0);
+        pv(uv, tmem + Gm::COL_O + t * 128, t, j == 0);
         if (t == nm - 1) commit_if(lead, &c.empty[uv % Gm::NU]);
         if (j + 1 == n) {
           commit_if(lead, &c.odone[t]);
@@ -244,7 +248,7 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
           ok = false;
           break;
         }
-        pv(u, tmem + Gm::COL_O + h * 128, j & 1, 64, j == 0);
+        pv(u, tmem + Gm::COL_O + h * 128, j & 1, j == 0);
         commit_if(lead, &c.empty[u % Gm::NU]);
       }
       if (!ok) break;
@@ -375,37 +379,38 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
 
 // ------------------------------------------- other formats: codes to f16 units
 
-// 128 threads; the codes of the next unit are requested before the present
+// 128 threads, half a unit (64 keys) at a time; the codes of the next half are requested before the present
 // one is converted, so that their latency passes meanwhile.  int8 and FP8: 8 lanes per key row, 16 codes a lane; NVFP4: 4
 // lanes per row, 32 codes (two scale blocks) a lane.
 template <int DT, int D>
 __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t) {
   using Gm = PGeo<DT, D>;
   constexpr bool FP4 = DT == PA_KV_NVFP4;
-  constexpr int IT = FP4 ? 4 : 8, LPR = FP4 ? 4 : 8, RPI = 128 / LPR;
+  constexpr int IT = FP4 ? 2 : 4, LPR = FP4 ? 4 : 8, RPI = 128 / LPR;   // loads per half unit
   constexpr int ROW = FP4 ? D / 2 : D;
   const int sub = t % LPR, r0 = t / LPR;
   const uint32_t ubase = smem_u32(smem + Gm::OFF_U);
   uint4 code[IT], next[IT];
   uint32_t sc[FP4 ? IT : 1], next_sc[FP4 ? IT : 1];
-  int id[IT], id_next[IT];
-  auto ids = [&](const Order<D> &o, int (&d)[IT]) {   // -1: nothing of this thread's row is read
+  int id[2 * IT], id_next[2 * IT];
+  auto ids = [&](const Order<D> &o, int (&d)[2 * IT]) {   // -1: nothing of this thread's row is read
     const int k0 = (w.kt0 + o.j) * kKeys;
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
+    for (int i = 0; i < 2 * IT; ++i) {
       const int key = k0 + i * RPI + r0;
       d[i] = !o.done() && key >= w.see_lo && key < w.see_hi ? __ldg(w.trow + key / kBlock) : -1;
     }
   };
-  auto load = [&](bool is_v, int h) {
+  auto load = [&](bool is_v, int h, int half) {
     const uint8_t *base = static_cast<const uint8_t *>(is_v ? p.kv.v : p.kv.k);
     const uint8_t *sbase = static_cast<const uint8_t *>(is_v ? p.kv.vs : p.kv.ks);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       next[i] = make_uint4(0, 0, 0, 0);
       if constexpr (FP4) next_sc[i] = 0;
-      if ((uint32_t)id[i] < (uint32_t)p.kv.num_blocks) {
-        const size_t row = ((size_t)id[i] * p.kv.hkv + w.kvh) * kBlock + ((i * RPI + r0) & (kBlock - 1));
+      const int pg = id[half * IT + i];
+      if ((uint32_t)pg < (uint32_t)p.kv.num_blocks) {
+        const size_t row = ((size_t)pg * p.kv.hkv + w.kvh) * kBlock + ((i * RPI + r0) & (kBlock - 1));
         next[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ROW + h * (ROW * 128 / D)) + sub);
         if constexpr (FP4)
           next_sc[i] = __ldg(reinterpret_cast<const uint16_t *>(sbase + row * (D / 16) + h * 8) + sub);
@@ -413,16 +418,16 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
     }
   };
   uint32_t u = 0;
-  // converts the loaded unit into its stage
-  auto store = [&]() {
+  // converts the loaded half unit into its stage
+  auto store = [&](int half) {
     const int st = u % Gm::NU;
-    if (u >= Gm::NU &&
+    if (half == 0 && u >= Gm::NU &&
         !__all_sync(0xffffffffu, wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr)))
       return false;
     const uint32_t dst = ubase + st * kUnitBytes;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int r = i * RPI + r0;
+      const int r = half * 64 + i * RPI + r0;
       const uint32_t word[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
       if constexpr (FP4) {
         uint32_t s0, s1;
@@ -455,10 +460,12 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
         sts_u4(at + (((p0 + 1) ^ (r & 7)) << 4), x[4], x[5], x[6], x[7]);
       }
     }
-    fence_async_smem();
-    __syncwarp();
-    if ((t & 31) == 0) mbar_arrive(&c.full[st]);   // one arrival a warp
-    ++u;
+    if (half == 1) {
+      fence_async_smem();
+      __syncwarp();
+      if ((t & 31) == 0) mbar_arrive(&c.full[st]);   // one arrival a warp
+      ++u;
+    }
     return true;
   };
   bool have = false, ok = true;
@@ -470,21 +477,23 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
     ids(on, id_next);
 #pragma unroll
     for (int h = 0; h < Gm::H; ++h) {
-      load(o.is_v, h);
-      if (have) ok = store();
-      if (!ok) break;
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        code[i] = next[i];
-        if constexpr (FP4) sc[i] = next_sc[i];
+      for (int half = 0; half < 2; ++half) {
+        load(o.is_v, h, half);
+        if (have && ok) ok = store(half ^ 1);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          code[i] = next[i];
+          if constexpr (FP4) sc[i] = next_sc[i];
+        }
+        have = true;
       }
-      have = true;
     }
 #pragma unroll
-    for (int i = 0; i < IT; ++i) id[i] = id_next[i];
+    for (int i = 0; i < 2 * IT; ++i) id[i] = id_next[i];
     o = on;
   }
-  if (ok && have) (void)store();
+  if (ok && have) (void)store(1);
 }
 
 // -------------------------------------------------------------------- softmax
@@ -526,20 +535,37 @@ __device__ __forceinline__ void ld_wait(float *v) {
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
 }
 
-// u * H(u^2) = tanh(u) for |u| <= 1: the Chebyshev interpolant of
-// tanh(sqrt v) / sqrt v on [0, 1], degree 6; relative error 6e-8 (the
-// singularity nearest to the interval, v = -pi^2 / 4, makes the terms fall by
-// 11.8 each).  Nine fp32 operations, two elements at a time, against two
-// special-function operations that the exponentials need as well.
-__device__ __forceinline__ float2 tanh_small(float2 u) {
+// cap * tanh(u) from the score's own u = s / cap by a polynomial in u^2 (the
+// Chebyshev interpolant of tanh(sqrt v) / sqrt v on the interval; the terms
+// fall fast since the nearest singularity is at v = -pi^2 / 4): relative error
+// 1.2e-7 for |u| <= 0.4 with four coefficients and 6e-8 for |u| <= 1 with
+// seven.  ex2 and rcp would take the special-function unit, which the
+// softmax's own exponentials keep busy.
+constexpr float kSmallU = 0.4f;
+struct TanhSmall {   // scaled: x -> scale * tanh(fu * x) = x * H(x^2)
+  float c0, c1, c2, c3;
+};
+__device__ __forceinline__ TanhSmall tanh_small_coefs(float fu, float scale) {
+  const float f2 = fu * fu, a = scale * fu;
+  return {a * 0.999999881f, a * f2 * -0.333313555f, a * f2 * f2 * 0.132708743f, a * f2 * f2 * f2 * -0.0475493483f};
+}
+__device__ __forceinline__ float2 f2_of(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 tanh_small(float2 x, const TanhSmall &t, float2 add) {
+  const float2 v = fmul2(x, x);
+  float2 h = ffma2(v, f2_of(t.c3), f2_of(t.c2));
+  h = ffma2(v, h, f2_of(t.c1));
+  h = ffma2(v, h, f2_of(t.c0));
+  return ffma2(x, h, add);
+}
+// tanh(u), |u| <= 1
+__device__ __forceinline__ float2 tanh_unit(float2 u) {
   const float2 v = fmul2(u, u);
-  auto k = [](float x) { return make_float2(x, x); };
-  float2 h = ffma2(v, k(0.00103802513f), k(-0.0061943247f));
-  h = ffma2(v, h, k(0.0202797074f));
-  h = ffma2(v, h, k(-0.0534516461f));
-  h = ffma2(v, h, k(0.133250758f));
-  h = ffma2(v, h, k(-0.333328277f));
-  h = ffma2(v, h, k(0.99999994f));
+  float2 h = ffma2(v, f2_of(0.00103802513f), f2_of(-0.0061943247f));
+  h = ffma2(v, h, f2_of(0.0202797074f));
+  h = ffma2(v, h, f2_of(-0.0534516461f));
+  h = ffma2(v, h, f2_of(0.133250758f));
+  h = ffma2(v, h, f2_of(-0.333328277f));
+  h = ffma2(v, h, f2_of(0.99999994f));
   return fmul2(u, h);
 }
 
@@ -549,8 +575,11 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
                              size_t r_out, float slope) {
   using Gm = PGeo<DT, D>;
   constexpr int NC = Gm::NC;
-  const int tid = threadIdx.x, wg = tid >> 7, row = tid & 127, wq = (tid >> 5) & 3, lane = tid & 31;
+  // row tile `rt`, half `hf` of its columns; a pair of warps shares 32 rows
+  const int tid = threadIdx.x, hf = (tid >> 7) & 1, rt = tid >> 8, wq = (tid >> 5) & 3, lane = tid & 31;
+  const int row = rt * 128 + (tid & 127), pair = 1 + rt * 4 + wq;
   const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+  const uint32_t O = tmem + lane_off + Gm::COL_O + rt * 128 + hf * Gm::NO;
   const int n = w.ntiles;
   // this warp's key ranges: where no row, and where every row, sees a key
   const bool sees = r_hi > r_lo;
@@ -565,6 +594,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   // a cap away from it
   const bool direct = DT != PA_KV_INT8 && p.sc.slopes == nullptr && f > 0.f;
   const float fu = f * 0.34657359027997264f;   // cap: u = score / cap (f is 2 log2 e / cap times the scale)
+  // (a factor so small that the scaled coefficients would leave fp32's range
+  // takes the other polynomial)
+  const TanhSmall small = tanh_small_coefs(fu, p.sc.cap_log2);
+  const float small_max = fu >= 0x1p-16f ? kSmallU : 0.f;
   float *const wsc = reinterpret_cast<float *>(smem + Gm::OFF_SC) + (tid >> 5) * 2 * kKeys;
 
   // the tile's page ids, one page in each of lanes 0-7 (again in 8-15, ..)
@@ -577,10 +610,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   bool ok = true;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
-    const int buf = D == 128 ? wg : (j & 1);
+    const int buf = D == 128 ? rt : (j & 1);
     const uint32_t par = D == 128 ? (j & 1) : ((j >> 1) & 1);
     const int k0t = (w.kt0 + j) * kKeys;              // the tile's first key
-    const int k0 = k0t + (D == 256 ? wg * 64 : 0);    // this thread's
+    const int k0 = k0t + hf * NC;                     // this thread's
     // keys of a page whose id is out of range are hidden
     const int id = id_next;
     id_next = page_id(j + 1);
@@ -611,9 +644,8 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     }
     const bool got = wait_p(&c.sfull[buf], par, c, p.hdr);
     ok = __all_sync(0xffffffffu, got) && ok;
-    if (D == 128 && !ok) break;
     tc_fence_after();
-    const uint32_t S = tmem + lane_off + buf * 128 + (D == 256 ? wg * 64 : 0);
+    const uint32_t S = tmem + lane_off + buf * 128 + hf * NC;
     const float *ksc = wsc + (k0 - k0t), *vsc = ksc + kKeys;
     const bool none = k0 >= a_hi || k0 + NC <= a_lo;
     const bool dense = k0 >= f_lo && k0 + NC <= f_hi && !bad;
@@ -661,7 +693,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     };
     float mx = kNegInf;      // this thread's largest score of the tile (log2 units)
     float fs = 1.f;          // score = fs * s
-    bool poly = false;       // score = cap_log2 * tanh(fu * s)
+    int poly = 0;            // score = cap_log2 * tanh(fu * s), by either polynomial
     if (ok && !none) {
       const bool formed = !(direct && dense);
       if (formed) form();
@@ -680,9 +712,13 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
             y0 = fminf(y0, s[i]);
             y1 = fminf(y1, s[i + 1]);
           }
-          poly = __all_sync(0xffffffffu, fmaxf(mx, -fminf(y0, y1)) * fu <= 1.f);
-          if (poly) {
-            mx = tanh_small(make_float2(mx * fu, 0.f)).x * p.sc.cap_log2;
+          const float top = fmaxf(mx, -fminf(y0, y1)) * fu;
+          if (__all_sync(0xffffffffu, top <= small_max)) {
+            poly = 1;
+            mx = tanh_small(f2_of(mx), small, f2_of(0.f)).x;
+          } else if (__all_sync(0xffffffffu, top <= 1.f)) {
+            poly = 2;
+            mx = tanh_unit(f2_of(mx * fu)).x * p.sc.cap_log2;
           } else {
             mx = capped(mx * f, p.sc.cap_log2);
             form();
@@ -696,30 +732,32 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     }
     // ---- the running maximum moves when some score passes it by 2^kLazy
     const bool need = ok && mx > m + kLazy;
-    const bool any = D == 128 ? __any_sync(0xffffffffu, need)
-                              : named_sync_or(1 + wq, 64, need || !ok);
-    if (any) {
-      if constexpr (D == 256) {   // the other half of the row's keys
-        if (named_sync_or(1 + wq, 64, !ok)) {
-          ok = false;
-          break;   // both warps of the pair
-        }
-        c.red[wg][row] = mx;
-        named_sync(1 + wq, 64);
-        mx = fmaxf(mx, c.red[wg ^ 1][row]);
+    if (named_sync_or(pair, 64, need || !ok)) {
+      if (named_sync_or(pair, 64, !ok)) {
+        ok = false;
+        break;   // both warps of the pair
       }
+      // the row's other keys
+      if (hf == 0) c.red[row] = mx;
+      named_sync(pair, 64);
+      if (hf == 1) {
+        mx = fmaxf(mx, c.red[row]);
+        c.red[row] = mx;
+      }
+      named_sync(pair, 64);
+      if (hf == 0) mx = c.red[row];
       const float mn = fmaxf(m, mx);
       const float al = mn == kNegInf ? 1.f : ex2_approx(m - mn);
       m = mn;
       l *= al;
       if (j > 0) {
+        // D = 128: S of this tile complete means the PV before it complete
         if constexpr (D == 256)
           ok = __all_sync(0xffffffffu, wait_p(&c.odone[(j - 1) & 1], ((j - 1) >> 1) & 1, c, p.hdr));
         if (ok) {
           tc_fence_after();
-          const uint32_t O = tmem + lane_off + Gm::COL_O + wg * 128;
 #pragma unroll 1
-          for (int ch = 0; ch < 128; ch += 16) {
+          for (int ch = 0; ch < Gm::NO; ch += 16) {
             float o[16];
             tmem_ld16(O + ch, o);
             uint32_t v[16];
@@ -742,11 +780,17 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 #pragma unroll
         for (int ch = 0; ch < NC / 2; ch += 16) tmem_st16(S + ch, z);
       } else {
-        if (poly) {
+        if (poly == 1) {
 #pragma unroll
           for (int i = 0; i < NC; i += 2) {
-            const float2 x = tanh_small(fmul2(make_float2(s[i], s[i + 1]), uu));
-            const float2 y = ffma2(x, cc, nm);
+            const float2 y = tanh_small(make_float2(s[i], s[i + 1]), small, nm);
+            s[i] = y.x;
+            s[i + 1] = y.y;
+          }
+        } else if (poly == 2) {
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) {
+            const float2 y = ffma2(tanh_unit(fmul2(make_float2(s[i], s[i + 1]), uu)), cc, nm);
             s[i] = y.x;
             s[i + 1] = y.y;
           }
@@ -779,14 +823,17 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     }
   }
   // ---- the sum, the last PV, the output
-  if constexpr (D == 256) {
-    named_sync(1 + wq, 64);   // the other warp has read the last maxima
-    c.red[wg][row] = l;
-    named_sync(1 + wq, 64);
-    l += c.red[wg ^ 1][row];
+  named_sync(pair, 64);   // the other warp has read the last maximum
+  if (hf == 0) c.red[row] = l;
+  named_sync(pair, 64);
+  if (hf == 1) {
+    l += c.red[row];
+    c.red[row] = l;
   }
+  named_sync(pair, 64);
+  if (hf == 0) l = c.red[row];
   if (n > 0 && ok) {
-    const bool got = D == 128 ? wait_p(&c.odone[wg], 0, c, p.hdr)
+    const bool got = D == 128 ? wait_p(&c.odone[rt], 0, c, p.hdr)
                               : wait_p(&c.odone[(n - 1) & 1], ((n - 1) >> 1) & 1, c, p.hdr);
     ok = __all_sync(0xffffffffu, got);
     tc_fence_after();
@@ -795,11 +842,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
   const float inv = l > 0.f ? vg / l : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
-  const uint32_t O = tmem + lane_off + Gm::COL_O + wg * 128;
-  const int d0 = D == 256 ? wg * 128 : 0;
+  const int d0 = hf * Gm::NO;
   const size_t orow = p.splits > 1 ? (size_t)split * p.T * p.Hq + r_out : r_out;
 #pragma unroll 1
-  for (int ch = 0; ch < 128; ch += 32) {
+  for (int ch = 0; ch < Gm::NO; ch += 32) {
     float o[32];
     if (n > 0) {
       tmem_ld32(O + ch, o);
@@ -847,17 +893,17 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   const int rest = blockIdx.x / Hkv, split = rest % p.splits;
   const TileOf to = find_tile(p, max_tiles - 1 - rest / p.splits, Gm::ROWS);   // the last tokens see most: first
   if (to.b < 0) return;
-  if (warp == 8) {
+  if (warp == Gm::SMW) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
-  } else if (tid == 9 * 32) {
+  } else if (tid == (Gm::SMW + 1) * 32) {
     for (int i = 0; i < Gm::NU; ++i) {
       mbar_init(&c.full[i], 4);        // the copy group's warps
       mbar_init(&c.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.sfull[i], 1);
-      mbar_init(&c.pready[i], D == 128 ? 4 : 8);   // softmax warps
+      mbar_init(&c.pready[i], 8);   // softmax warps of a row tile
       mbar_init(&c.odone[i], 1);
     }
     mbar_init(&c.done, 1);
@@ -891,20 +937,20 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   bool live = false;
   size_t r_out = 0;
   float slope = 0.f;
-  if (warp < 8) {
-    // queries: 16 pieces of 16 bytes per thread, all requested before any is used
-    constexpr int CH = D / 8, NQ = Gm::ROWS * CH / 256;
+  if (warp < Gm::SMW) {
+    // queries: 8 or 16 pieces of 16 bytes per thread, all requested before any is used
+    constexpr int CH = D / 8, NT = Gm::SMW * 32, NQ = Gm::ROWS * CH / NT;
     uint4 qv[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int q = (i * 256 + tid) / CH, k = (i * 256 + tid) % CH;
+      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH;
       int tok, head;
       split_row(q, tok, head);
       qv[i] = make_uint4(0, 0, 0, 0);
       if (q < w.nrows)
         qv[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.start + tok) * p.Hq + head) * D) + k);
     }
-    const int r = (D == 128 ? tid & ~127 : 0) + (tid & 127);
+    const int r = (tid >> 8) * 128 + (tid & 127);
     live = r < w.nrows;
     int tok, head;
     split_row(live ? r : 0, tok, head);
@@ -926,7 +972,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int q = (i * 256 + tid) / CH, k = (i * 256 + tid) % CH, r2 = q & 127;
+      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH, r2 = q & 127;
       uint4 u = qv[i];
       if constexpr (Gm::QUANT) {   // f16 operands (exact in f16's normal range)
         const float2 a = bf16x2_to_f2(u.x), b = bf16x2_to_f2(u.y), d = bf16x2_to_f2(u.z), e = bf16x2_to_f2(u.w);
@@ -944,7 +990,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   w.see_lo = 0x7fffffff;
   w.see_hi = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < Gm::SMW; ++i) {
     w.see_lo = min(w.see_lo, c.lo[i]);
     w.see_hi = max(w.see_hi, c.hi[i]);
   }
@@ -955,27 +1001,27 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     w.kt0 = t0 + min(t1 - t0, split * per);
     w.ntiles = t0 + min(t1 - t0, (split + 1) * per) - w.kt0;
   }
-  constexpr bool REGS = D == 128;   // registers move to the threads that hold whole rows
-  if (warp < 8) {
-    if constexpr (REGS) setmaxnreg_to<kLaunchRegsPf, Gm::REG_SM>();
-    // D = 128: the second row tile's group has nothing to do when it is empty
-    if (D == 256 || warp < 4 || w.nrows > 128)
+  constexpr bool REGS = D == 128;   // 768 threads: registers move to the softmax groups
+  if (warp < Gm::SMW) {
+    if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_SM>();
+    // the second row tile's groups have nothing to do when it is empty
+    if (warp < 8 || w.nrows > 128)
       role_softmax<DT, D>(p, w, smem, c, tmem, split, r_lo, r_hi, r_pos, live, r_out, slope);
-  } else if (warp < 12) {
-    if constexpr (REGS) setmaxnreg_to<kLaunchRegsPf, kRegMma>();
-    if (warp == 8)
+  } else if (warp < Gm::SMW + 4) {
+    if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_MMA>();
+    if (warp == Gm::SMW)
       role_mma<DT, D>(__shfl_sync(0xffffffffu, w.ntiles, 0), __shfl_sync(0xffffffffu, w.nrows > 128 ? 2 : 1, 0),
                       smem, c, p.hdr, __shfl_sync(0xffffffffu, tmem, 0));
   } else {
-    if constexpr (REGS) setmaxnreg_to<kLaunchRegsPf, Gm::REG_COPY>();
+    if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_COPY>();
     if constexpr (Gm::QUANT)
-      role_dequant<DT, D>(p, w, smem, c, tid - 384);
+      role_dequant<DT, D>(p, w, smem, c, tid - (Gm::SMW + 4) * 32);
     else
-      role_copy<D>(p, w, smem, c, tid - 384);
+      role_copy<D>(p, w, smem, c, tid - (Gm::SMW + 4) * 32);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == Gm::SMW) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -988,12 +1034,12 @@ cudaError_t launch_umma(const PrefillParams &p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
   if (e != cudaSuccess) return e;
   if constexpr (D == 128) {
-    // the register split starts from kLaunchRegsPf (allocated in eights): a
+    // the register split starts from LAUNCH_REGS (allocated in eights): a
     // build that gave the kernel another count is refused, never launched
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
-    if ((fa.numRegs + 7) / 8 * 8 != kLaunchRegsPf) return cudaErrorInvalidDeviceFunction;
+    if ((fa.numRegs + 7) / 8 * 8 != Gm::LAUNCH_REGS) return cudaErrorInvalidDeviceFunction;
   }
   // every sequence has at most one tile that is not full
   const long long tiles = (long long)p.T * p.G / Gm::ROWS + p.B;
