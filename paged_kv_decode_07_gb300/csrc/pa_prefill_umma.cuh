@@ -28,8 +28,7 @@
 //
 // Roles: softmax groups (D = 128: four, D = 256: two), a group whose first
 // warp issues the MMAs, a group for copies or dequantisation.  Hand-offs are
-// mbarriers; every wait is capped, and a timeout sets PA_ERRF_WAIT_TIMEOUT,
-// raises the CTA's abort flag and lets copies and MMAs in flight finish.
+// mbarriers; every wait is capped (see wait_slow).
 #pragma once
 
 #include "pa_prefill.cuh"
@@ -95,18 +94,22 @@ struct PCtl {
   float red[256];               // a row's maximum (at the end its sum), from one half to the other
 };
 
-// capped wait that also gives up once another role has given up
-__device__ __forceinline__ bool wait_p(uint64_t *bar, uint32_t parity, PCtl &c, uint32_t *hdr) {
-  if (mbar_test(bar, parity)) return true;
+// Capped wait.  When one runs out (PA_ERRF_WAIT_TIMEOUT) the CTA's abort flag
+// is raised and every later wait returns at once: the roles run to their ends
+// on whatever their buffers hold, so that each barrier between warps meets its
+// arrivals and copies and MMAs in flight end before the CTA does; the outputs
+// of such a call are invalid.
+__device__ __forceinline__ void wait_slow(uint64_t *bar, uint32_t parity, PCtl &c, uint32_t *hdr) {
   volatile int *ab = &c.abort;
 #pragma unroll 1
   for (uint32_t i = 0; i < kSleepCap; ++i) {
-    if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
-    if (*ab) return false;
+    if (mbar_try_wait_sleep(bar, parity, kSleepNs) || *ab) return;
   }
   *ab = 1;
   set_err(hdr, PA_ERRF_WAIT_TIMEOUT);
-  return false;
+}
+__device__ __forceinline__ void wait_p(uint64_t *bar, uint32_t parity, PCtl &c, uint32_t *hdr) {
+  if (!mbar_test(bar, parity)) wait_slow(bar, parity, c, hdr);
 }
 
 // what every role knows of the CTA's work
@@ -170,12 +173,12 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
   const uint64_t dK = sdesc(smem_u32(smem + Gm::OFF_U), 16, 1024);
   const uint64_t dV = sdesc(smem_u32(smem + Gm::OFF_U), kChunkBytes, 1024);
   uint32_t u = 0;
-  auto wait = [&](uint64_t *bar, uint32_t par) {
-    const bool ok = __all_sync(0xffffffffu, wait_p(bar, par, c, hdr));
+  auto full = [&](uint32_t i) { return &c.full[i % Gm::NU]; };
+  auto fpar = [&](uint32_t i) { return (i / Gm::NU) & 1; };
+  auto wait_full = [&](uint32_t i) {
+    wait_p(full(i), fpar(i), c, hdr);
     tc_fence_after();
-    return ok;
   };
-  auto wait_full = [&](uint32_t i) { return wait(&c.full[i % Gm::NU], (i / Gm::NU) & 1); };
   // S(buffer) (+)= Q tile t, dims 128 h .. + 127, times K unit i
   auto qk = [&](uint32_t i, int t, int h, uint32_t buf) {
     const uint64_t kb = dK + (uint64_t)((i % Gm::NU) * (kUnitBytes >> 4));
@@ -196,8 +199,8 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
                 vb + (uint64_t)((ks * 2048) >> 4), IPV, (!first || ks > 0) ? 1u : 0u);
   };
   if constexpr (D == 128) {
-    bool ok = n > 0 && wait_full(u);
-    if (ok) {
+    if (n > 0) {
+      wait_full(u);
       for (int t = 0; t < nm; ++t) {
         qk(u, t, 0, t);
         commit_if(lead, &c.sfull[t]);
@@ -205,23 +208,28 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
       commit_if(lead, &c.empty[u % Gm::NU]);
       ++u;
     }
-    for (int j = 0; j < n && ok; ++j) {
-      const uint32_t uv = u++;
-      const uint32_t uk = j + 1 < n ? u++ : 0;
-      for (int t = 0; t < nm && ok; ++t) {
-        if ((t == 0 && !wait_full(uv)) || !wait(&c.pready[t], j & 1)) {
-          ok = false;
-          break;
-        }
+    for (int j = 0; j < n; ++j) {
+      // the checks of a tile's V, next K and first weights are issued together
+      const uint32_t uv = u, uk = u + 1;
+      const bool more = j + 1 < n;
+      u += more ? 2 : 1;
+      const bool r0 = mbar_test(&c.pready[0], j & 1);
+      const bool rv = mbar_test(full(uv), fpar(uv));
+      const bool rk = !more || mbar_test(full(uk), fpar(uk));
+      if (!rv) wait_slow(full(uv), fpar(uv), c, hdr);
+      if (!r0) wait_slow(&c.pready[0], j & 1, c, hdr);
+      for (int t = 0; t < nm; ++t) {
+        if (t == 1) wait_p(&c.pready[1], j & 1, c, hdr);
+        tc_fence_after();
         pv(uv, tmem + Gm::COL_O + t * 128, t, j == 0);
         if (t == nm - 1) commit_if(lead, &c.empty[uv % Gm::NU]);
-        if (j + 1 == n) {
+        if (!more) {
           commit_if(lead, &c.odone[t]);
           continue;
         }
-        if (t == 0 && !wait_full(uk)) {
-          ok = false;
-          break;
+        if (t == 0 && !rk) {
+          wait_slow(full(uk), fpar(uk), c, hdr);
+          tc_fence_after();
         }
         qk(uk, t, 0, t);
         commit_if(lead, &c.sfull[t]);
@@ -229,31 +237,29 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
       }
     }
   } else {
-    bool ok = true;
     auto tile_qk = [&](int j) {
       for (int h = 0; h < Gm::H; ++h, ++u) {
-        if (!wait_full(u)) return false;
+        wait_full(u);
         qk(u, 0, h, j & 1);
         commit_if(lead, &c.empty[u % Gm::NU]);
       }
       commit_if(lead, &c.sfull[j & 1]);
-      return true;
     };
-    if (n > 0) ok = tile_qk(0);
-    if (n > 1 && ok) ok = tile_qk(1);
-    for (int j = 0; j < n && ok; ++j) {
-      if (!wait(&c.pready[j & 1], (j >> 1) & 1)) break;
+    if (n > 0) tile_qk(0);
+    if (n > 1) tile_qk(1);
+    for (int j = 0; j < n; ++j) {
+      const bool rp = mbar_test(&c.pready[j & 1], (j >> 1) & 1);
+      const bool rv = mbar_test(full(u), fpar(u));
+      if (!rv) wait_slow(full(u), fpar(u), c, hdr);
+      if (!rp) wait_slow(&c.pready[j & 1], (j >> 1) & 1, c, hdr);
+      tc_fence_after();
       for (int h = 0; h < Gm::H; ++h, ++u) {
-        if (!wait_full(u)) {
-          ok = false;
-          break;
-        }
+        if (h > 0) wait_full(u);
         pv(u, tmem + Gm::COL_O + h * 128, j & 1, j == 0);
         commit_if(lead, &c.empty[u % Gm::NU]);
       }
-      if (!ok) break;
       commit_if(lead, &c.odone[j & 1]);
-      if (j + 2 < n) ok = tile_qk(j + 2);
+      if (j + 2 < n) tile_qk(j + 2);
     }
   }
   commit_if(lead, &c.done);   // tensor memory is released only after every MMA completes
@@ -330,8 +336,7 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
   Order<D> o(w.ntiles);
   int id[8], id_next[8];
   ids(o, id);
-  bool ok = true;
-  while (!o.done() && ok) {
+  while (!o.done()) {
     Order<D> on = o;
     on.next();
     ids(on, id_next);
@@ -347,9 +352,7 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
         copy_wait<FLY - 1>();
         hand_over(u - FLY);
       }
-      if (u >= Gm::NU)
-        ok = __all_sync(0xffffffffu, wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr));
-      if (!ok) break;
+      if (u >= Gm::NU) wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr);
       const uint32_t dst = dst0 + st * kUnitBytes;
       if (dense) {
 #pragma unroll
@@ -421,9 +424,7 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
   // converts the loaded half unit into its stage
   auto store = [&](int half) {
     const int st = u % Gm::NU;
-    if (half == 0 && u >= Gm::NU &&
-        !__all_sync(0xffffffffu, wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr)))
-      return false;
+    if (half == 0 && u >= Gm::NU) wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr);
     const uint32_t dst = ubase + st * kUnitBytes;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -466,12 +467,11 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
       if ((t & 31) == 0) mbar_arrive(&c.full[st]);   // one arrival a warp
       ++u;
     }
-    return true;
   };
-  bool have = false, ok = true;
+  bool have = false;
   Order<D> o(w.ntiles);
   ids(o, id);
-  while (!o.done() && ok) {
+  while (!o.done()) {
     Order<D> on = o;
     on.next();
     ids(on, id_next);
@@ -480,7 +480,7 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         load(o.is_v, h, half);
-        if (have && ok) ok = store(half ^ 1);
+        if (have) store(half ^ 1);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           code[i] = next[i];
@@ -493,7 +493,7 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
     for (int i = 0; i < 2 * IT; ++i) id[i] = id_next[i];
     o = on;
   }
-  if (ok && have) (void)store(1);
+  if (have) store(1);
 }
 
 // -------------------------------------------------------------------- softmax
@@ -607,7 +607,6 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   };
   int id_next = page_id(0);
   float m = kNegInf, l = 0.f;
-  bool ok = true;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int buf = D == 128 ? rt : (j & 1);
@@ -642,8 +641,8 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       d[1] = make_float4(x[4], x[5], x[6], x[7]);
       __syncwarp();
     }
-    const bool got = wait_p(&c.sfull[buf], par, c, p.hdr);
-    ok = __all_sync(0xffffffffu, got) && ok;
+    wait_p(&c.sfull[buf], par, c, p.hdr);
+    __syncwarp();
     tc_fence_after();
     const uint32_t S = tmem + lane_off + buf * 128 + hf * NC;
     const float *ksc = wsc + (k0 - k0t), *vsc = ksc + kKeys;
@@ -694,7 +693,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     float mx = kNegInf;      // this thread's largest score of the tile (log2 units)
     float fs = 1.f;          // score = fs * s
     int poly = 0;            // score = cap_log2 * tanh(fu * s), by either polynomial
-    if (ok && !none) {
+    if (!none) {
       const bool formed = !(direct && dense);
       if (formed) form();
       load();
@@ -731,13 +730,8 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       }
     }
     // ---- the running maximum moves when some score passes it by 2^kLazy
-    const bool need = ok && mx > m + kLazy;
-    if (named_sync_or(pair, 64, need || !ok)) {
-      if (named_sync_or(pair, 64, !ok)) {
-        ok = false;
-        break;   // both warps of the pair
-      }
-      // the row's other keys
+    if (named_sync_or(pair, 64, mx > m + kLazy)) {
+      // with the row's other keys
       if (hf == 0) c.red[row] = mx;
       named_sync(pair, 64);
       if (hf == 1) {
@@ -752,25 +746,25 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       l *= al;
       if (j > 0) {
         // D = 128: S of this tile complete means the PV before it complete
-        if constexpr (D == 256)
-          ok = __all_sync(0xffffffffu, wait_p(&c.odone[(j - 1) & 1], ((j - 1) >> 1) & 1, c, p.hdr));
-        if (ok) {
-          tc_fence_after();
-#pragma unroll 1
-          for (int ch = 0; ch < Gm::NO; ch += 16) {
-            float o[16];
-            tmem_ld16(O + ch, o);
-            uint32_t v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(o[i] * al);
-            tmem_st16(O + ch, v);
-          }
-          tmem_st_wait();
+        if constexpr (D == 256) {
+          wait_p(&c.odone[(j - 1) & 1], ((j - 1) >> 1) & 1, c, p.hdr);
+          __syncwarp();
         }
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < Gm::NO; ch += 16) {
+          float o[16];
+          tmem_ld16(O + ch, o);
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(o[i] * al);
+          tmem_st16(O + ch, v);
+        }
+        tmem_st_wait();
       }
     }
     // ---- weights
-    if (ok) {
+    {
       const float mu = m == kNegInf ? 0.f : m;
       const float2 nm = make_float2(-mu, -mu), ff = make_float2(fs, fs);
       const float2 uu = make_float2(fu, fu), cc = make_float2(p.sc.cap_log2, p.sc.cap_log2);
@@ -832,13 +826,11 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   }
   named_sync(pair, 64);
   if (hf == 0) l = c.red[row];
-  if (n > 0 && ok) {
-    const bool got = D == 128 ? wait_p(&c.odone[rt], 0, c, p.hdr)
-                              : wait_p(&c.odone[(n - 1) & 1], ((n - 1) >> 1) & 1, c, p.hdr);
-    ok = __all_sync(0xffffffffu, got);
+  if (n > 0) {
+    wait_p(&c.odone[D == 128 ? rt : (n - 1) & 1], D == 128 ? 0 : ((n - 1) >> 1) & 1, c, p.hdr);
+    __syncwarp();
     tc_fence_after();
   }
-  if (!ok) return;
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
   const float inv = l > 0.f ? vg / l : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
