@@ -27,7 +27,7 @@
 // buffers.
 //
 // Roles: softmax groups (D = 128: four, D = 256: two), a group whose first
-// warp issues the MMAs, a group for copies or dequantisation.  Hand-offs are
+// one or two warps issue the MMAs, a group for copies or dequantisation.  Hand-offs are
 // mbarriers; every wait is capped (see wait_slow).
 #pragma once
 
@@ -127,6 +127,24 @@ __host__ __device__ constexpr uint32_t idesc_pf(bool bf16, int N, bool b_mn) {
          ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// The order in which K and V tiles are copied and used: K runs one tile (D =
+// 128) or two (D = 256, two S buffers) ahead of V.  Tile q of that order; the
+// places past the last K tile are skipped (j >= n).
+template <int D>
+struct Order {
+  int q, n, j;
+  bool is_v;
+  __device__ __forceinline__ Order(int tiles) : q(0), n(tiles), j(0), is_v(false) {}
+  __device__ __forceinline__ bool done() const { return q > 2 * n || n == 0; }
+  __device__ __forceinline__ void next() {
+    do {
+      ++q;
+      is_v = D == 128 ? (q & 1) : !(q & 1);
+      j = D == 128 ? q >> 1 : is_v ? (q >> 1) - 1 : (q + 1) >> 1;
+    } while (j >= n && !done());
+  }
+};
+
 // ------------------------------------------------------------------ MMA issue
 
 // The whole warp runs the issue loop on warp-uniform values and one elected
@@ -163,8 +181,14 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
       : "memory");
 }
 
+// D = 128: a warp per row tile issues, so that one's waits and commits (some
+// 200 cycles each, as long as three MMAs) pass under the other's MMAs.  D =
+// 256: one warp, in the order that lets the products of tile j + 2 follow the
+// weights of tile j in their columns without a wait (a second warp for P V
+// would have to wait for each tile's completion: 390 against 358 us where the
+// tensor pipe is all that runs).
 template <int DT, int D>
-__device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, uint32_t tmem) {
+__device__ void role_mma(int t, int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, uint32_t tmem) {
   using Gm = PGeo<DT, D>;
   constexpr uint32_t IQK = idesc_pf(!Gm::QUANT, 128, false);
   constexpr uint32_t IPV = idesc_pf(!Gm::QUANT, 128, true);
@@ -172,12 +196,15 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
   const uint64_t dQ = sdesc(smem_u32(smem), 16, 1024);
   const uint64_t dK = sdesc(smem_u32(smem + Gm::OFF_U), 16, 1024);
   const uint64_t dV = sdesc(smem_u32(smem + Gm::OFF_U), kChunkBytes, 1024);
-  uint32_t u = 0;
   auto full = [&](uint32_t i) { return &c.full[i % Gm::NU]; };
   auto fpar = [&](uint32_t i) { return (i / Gm::NU) & 1; };
+  auto landed = [&]() {   // bf16: asynchronous copies are generic-proxy writes
+    if constexpr (!Gm::QUANT) fence_async_smem();
+    tc_fence_after();
+  };
   auto wait_full = [&](uint32_t i) {
     wait_p(full(i), fpar(i), c, hdr);
-    tc_fence_after();
+    landed();
   };
   // S(buffer) (+)= Q tile t, dims 128 h .. + 127, times K unit i
   auto qk = [&](uint32_t i, int t, int h, uint32_t buf) {
@@ -199,44 +226,37 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
                 vb + (uint64_t)((ks * 2048) >> 4), IPV, (!first || ks > 0) ? 1u : 0u);
   };
   if constexpr (D == 128) {
+    if (t >= nm) n = 0;
     if (n > 0) {
-      wait_full(u);
-      for (int t = 0; t < nm; ++t) {
-        qk(u, t, 0, t);
-        commit_if(lead, &c.sfull[t]);
-      }
-      commit_if(lead, &c.empty[u % Gm::NU]);
-      ++u;
+      wait_full(0);
+      qk(0, t, 0, t);
+      commit_if(lead, &c.sfull[t]);
+      commit_if(lead, &c.empty[0]);
     }
     for (int j = 0; j < n; ++j) {
-      // the checks of a tile's V, next K and first weights are issued together
-      const uint32_t uv = u, uk = u + 1;
+      // the checks of a tile's V, next K and weights are issued together
+      const uint32_t uv = 2 * j + 1, uk = 2 * j + 2;
       const bool more = j + 1 < n;
-      u += more ? 2 : 1;
-      const bool r0 = mbar_test(&c.pready[0], j & 1);
+      const bool rp = mbar_test(&c.pready[t], j & 1);
       const bool rv = mbar_test(full(uv), fpar(uv));
       const bool rk = !more || mbar_test(full(uk), fpar(uk));
       if (!rv) wait_slow(full(uv), fpar(uv), c, hdr);
-      if (!r0) wait_slow(&c.pready[0], j & 1, c, hdr);
-      for (int t = 0; t < nm; ++t) {
-        if (t == 1) wait_p(&c.pready[1], j & 1, c, hdr);
-        tc_fence_after();
-        pv(uv, tmem + Gm::COL_O + t * 128, t, j == 0);
-        if (t == nm - 1) commit_if(lead, &c.empty[uv % Gm::NU]);
-        if (!more) {
-          commit_if(lead, &c.odone[t]);
-          continue;
-        }
-        if (t == 0 && !rk) {
-          wait_slow(full(uk), fpar(uk), c, hdr);
-          tc_fence_after();
-        }
-        qk(uk, t, 0, t);
-        commit_if(lead, &c.sfull[t]);
-        if (t == nm - 1) commit_if(lead, &c.empty[uk % Gm::NU]);
+      if (!rp) wait_slow(&c.pready[t], j & 1, c, hdr);
+      landed();
+      pv(uv, tmem + Gm::COL_O + t * 128, t, j == 0);
+      commit_if(lead, &c.empty[uv % Gm::NU]);
+      if (!more) break;
+      if (!rk) {
+        wait_slow(full(uk), fpar(uk), c, hdr);
+        landed();
       }
+      qk(uk, t, 0, t);
+      commit_if(lead, &c.sfull[t]);
+      commit_if(lead, &c.empty[uk % Gm::NU]);
     }
+    if (n > 0) commit_if(lead, &c.odone[t]);
   } else {
+    uint32_t u = 0;
     auto tile_qk = [&](int j) {
       for (int h = 0; h < Gm::H; ++h, ++u) {
         wait_full(u);
@@ -252,7 +272,7 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
       const bool rv = mbar_test(full(u), fpar(u));
       if (!rv) wait_slow(full(u), fpar(u), c, hdr);
       if (!rp) wait_slow(&c.pready[j & 1], (j >> 1) & 1, c, hdr);
-      tc_fence_after();
+      landed();
       for (int h = 0; h < Gm::H; ++h, ++u) {
         if (h > 0) wait_full(u);
         pv(u, tmem + Gm::COL_O + h * 128, j & 1, j == 0);
@@ -267,24 +287,6 @@ __device__ void role_mma(int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, u
   __syncwarp();
 }
 
-// The order in which the MMA thread uses K and V tiles: K runs one tile (D =
-// 128) or two (D = 256, two S buffers) ahead of V.  Tile q of that order; the
-// places past the last K tile are skipped (j >= n).
-template <int D>
-struct Order {
-  int q, n, j;
-  bool is_v;
-  __device__ __forceinline__ Order(int tiles) : q(0), n(tiles), j(0), is_v(false) {}
-  __device__ __forceinline__ bool done() const { return q > 2 * n || n == 0; }
-  __device__ __forceinline__ void next() {
-    do {
-      ++q;
-      is_v = D == 128 ? (q & 1) : !(q & 1);
-      j = D == 128 ? q >> 1 : is_v ? (q >> 1) - 1 : (q + 1) >> 1;
-    } while (j >= n && !done());
-  }
-};
-
 // ---------------------------------------------------- bf16: asynchronous copies
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
@@ -296,19 +298,20 @@ __device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool vali
                "r"(valid ? 16 : 0)
                : "memory");
 }
-template <int N>
-__device__ __forceinline__ void copy_wait() {   // all but the last N committed groups complete
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// arrives on `bar` (one of its expected arrivals) once this thread's copies so
+// far have landed
+__device__ __forceinline__ void copy_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // 128 threads, 16 lanes per key row; rows that no query sees, or whose page id
 // is out of range, are filled with zeros (a zero weight times whatever a slot
-// holds must be zero).  Three units are in flight; a unit is handed over once
-// this thread's copies of it have landed.
+// holds must be zero).  A unit's barrier counts the threads' copies as they
+// land, so the whole ring is in flight; the MMA warps order their reads after
+// these generic-proxy writes by a proxy fence behind the wait.
 template <int D>
 __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t) {
   using Gm = PGeo<PA_KV_BF16, D>;
-  constexpr int FLY = 3;
   // piece `piece` of rows r0, r0 + 8, ..: two rows of every page, 1 KB apart
   // in a chunk (r0 is the row modulo 8 that the swizzle wants)
   const int r0 = t >> 4, piece = t & 15;
@@ -319,11 +322,6 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
   const uint8_t *const kbase = static_cast<const uint8_t *>(p.kv.k) + off0;
   const uint8_t *const vbase = static_cast<const uint8_t *>(p.kv.v) + off0;
   uint32_t u = 0;
-  auto hand_over = [&](uint32_t i) {   // one arrival a warp: 128 on one barrier would queue up
-    fence_async_smem();
-    __syncwarp();
-    if ((t & 31) == 0) mbar_arrive(&c.full[i % Gm::NU]);
-  };
   // the page ids of the next tile are requested a tile ahead
   auto ids = [&](const Order<D> &o, int (&id)[8]) {
     const int k0 = (w.kt0 + o.j) * kKeys;
@@ -348,10 +346,6 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
 #pragma unroll
     for (int h = 0; h < Gm::H; ++h) {
       const int st = u % Gm::NU;
-      if (u >= FLY) {   // before the wait for a stage, so that no landed unit waits with it
-        copy_wait<FLY - 1>();
-        hand_over(u - FLY);
-      }
       if (u >= Gm::NU) wait_p(&c.empty[st], ((u / Gm::NU) - 1) & 1, c, p.hdr);
       const uint32_t dst = dst0 + st * kUnitBytes;
       if (dense) {
@@ -369,15 +363,14 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
           copy16z(dst + i * 1024, base + h * 256 + (valid ? (size_t)g * page + (i & 1) * (8 * D * 2) : 0), valid);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      copy_arrive(&c.full[st]);
       ++u;
     }
 #pragma unroll
     for (int g = 0; g < 8; ++g) id[g] = id_next[g];
     o = on;
   }
-  copy_wait<0>();
-  for (uint32_t i = u > FLY ? u - FLY : 0; i < u; ++i) hand_over(i);
+  asm volatile("cp.async.wait_all;" ::: "memory");   // nothing lands after the CTA's end
 }
 
 // ------------------------------------------- other formats: codes to f16 units
@@ -890,15 +883,16 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     tmem_relinquish();
   } else if (tid == (Gm::SMW + 1) * 32) {
     for (int i = 0; i < Gm::NU; ++i) {
-      mbar_init(&c.full[i], 4);        // the copy group's warps
-      mbar_init(&c.empty[i], 1);
+      mbar_init(&c.full[i], Gm::QUANT ? 4 : 128);   // the copy group's warps, or threads
+      // D = 128: both row tiles use a unit; D = 256: one MMA warp does
+      mbar_init(&c.empty[i], D == 128 && to.len * G - to.first * Gm::ROWS > 128 ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.sfull[i], 1);
       mbar_init(&c.pready[i], 8);   // softmax warps of a row tile
       mbar_init(&c.odone[i], 1);
     }
-    mbar_init(&c.done, 1);
+    mbar_init(&c.done, Gm::MT);
     c.abort = 0;
     fence_mbar_init();
   }
@@ -1001,8 +995,8 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       role_softmax<DT, D>(p, w, smem, c, tmem, split, r_lo, r_hi, r_pos, live, r_out, slope);
   } else if (warp < Gm::SMW + 4) {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_MMA>();
-    if (warp == Gm::SMW)
-      role_mma<DT, D>(__shfl_sync(0xffffffffu, w.ntiles, 0), __shfl_sync(0xffffffffu, w.nrows > 128 ? 2 : 1, 0),
+    if (warp < Gm::SMW + Gm::MT)
+      role_mma<DT, D>(warp - Gm::SMW, __shfl_sync(0xffffffffu, w.ntiles, 0), __shfl_sync(0xffffffffu, w.nrows > 128 ? 2 : 1, 0),
                       smem, c, p.hdr, __shfl_sync(0xffffffffu, tmem, 0));
   } else {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_COPY>();
