@@ -87,6 +87,7 @@ struct PCtl {
   // odd tiles; S of tile j complete means PV of j - 2 complete, so a wait for
   // tile j - 1 or j is never two phases ahead of its barrier.
   uint64_t odone[2];
+  uint64_t qfull;               // queries in shared memory
   uint64_t done;                // every MMA complete
   uint32_t tmem;
   int abort;
@@ -193,6 +194,7 @@ __device__ void role_mma(int t, int n, int nm, uint8_t *smem, PCtl &c, uint32_t 
   constexpr uint32_t IQK = idesc_pf(!Gm::QUANT, 128, false);
   constexpr uint32_t IPV = idesc_pf(!Gm::QUANT, 128, true);
   const uint32_t lead = elect_one();
+  wait_p(&c.qfull, 0, c, hdr);
   const uint64_t dQ = sdesc(smem_u32(smem), 16, 1024);
   const uint64_t dK = sdesc(smem_u32(smem + Gm::OFF_U), 16, 1024);
   const uint64_t dV = sdesc(smem_u32(smem + Gm::OFF_U), kChunkBytes, 1024);
@@ -491,27 +493,6 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
 
 // -------------------------------------------------------------------- softmax
 
-__device__ __forceinline__ void st32f(uint32_t taddr, const float (&v)[32]) {
-  uint32_t a[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    a[i] = __float_as_uint(v[i]);
-    b[i] = __float_as_uint(v[16 + i]);
-  }
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
-      "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7]),
-      "r"(a[8]), "r"(a[9]), "r"(a[10]), "r"(a[11]), "r"(a[12]), "r"(a[13]), "r"(a[14]), "r"(a[15])
-      : "memory");
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr + 16),
-      "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(b[5]), "r"(b[6]), "r"(b[7]),
-      "r"(b[8]), "r"(b[9]), "r"(b[10]), "r"(b[11]), "r"(b[12]), "r"(b[13]), "r"(b[14]), "r"(b[15])
-      : "memory");
-}
-
 // 32 consecutive columns of this thread's lane, without a wait
 __device__ __forceinline__ void ld32_issue(uint32_t taddr, float *v) {
   asm volatile(
@@ -643,36 +624,39 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     const bool dense = k0 >= f_lo && k0 + NC <= f_hi && !bad;
 
     // Scores that are not one operation away from the products are formed in
-    // place, 32 columns at a time (the ends of the visible range, biased or
-    // int8 scores, and capped ones past the polynomial's interval).
+    // place, 16 columns at a time (the ends of the visible range, biased or int8
+    // scores).  The loop stays rolled: a short prompt runs it once, and then
+    // takes as long as its instructions take to arrive.
     auto form = [&]() {
 #pragma unroll 1
-      for (int ch = 0; ch < NC; ch += 32) {
-        float x[32];
-        tmem_ld32(S + ch, x);
+      for (int ch = 0; ch < NC; ch += 16) {
+        float x[16];
+        tmem_ld16(S + ch, x);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           x[i] *= f;
           if constexpr (DT == PA_KV_INT8) x[i] *= ksc[ch + i];
         }
         if (cap) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = capped(x[i], p.sc.cap_log2);
+          for (int i = 0; i < 16; ++i) x[i] = capped(x[i], p.sc.cap_log2);
         }
         if (p.sc.slopes) {
+          const float far = (float)(r_pos - k0 - ch);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            x[i] = fmaf(-slope, fabsf((float)(r_pos - k0 - ch - i)), x[i]);
+          for (int i = 0; i < 16; ++i) x[i] = fmaf(-slope, fabsf(far - (float)i), x[i]);
         }
         if (!dense) {
+          // 16 columns are one page's: hidden as a whole if its id is out of range
+          const bool hide = (bad >> ((k0 + ch - k0t) >> 4)) & 1;
+          const int lo = hide ? 16 : r_lo - k0 - ch, hi = r_hi - k0 - ch;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int key = k0 + ch + i;
-            const bool see = key >= r_lo && key < r_hi && !((bad >> ((key - k0t) >> 4)) & 1);
-            x[i] = see ? x[i] : kNegInf;
-          }
+          for (int i = 0; i < 16; ++i) x[i] = i >= lo && i < hi ? x[i] : kNegInf;
         }
-        st32f(S + ch, x);
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(x[i]);
+        tmem_st16(S + ch, v);
       }
       tmem_st_wait();
     };
@@ -830,26 +814,26 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   const int d0 = hf * Gm::NO;
   const size_t orow = p.splits > 1 ? (size_t)split * p.T * p.Hq + r_out : r_out;
 #pragma unroll 1
-  for (int ch = 0; ch < Gm::NO; ch += 32) {
-    float o[32];
+  for (int ch = 0; ch < Gm::NO; ch += 16) {
+    float o[16];
     if (n > 0) {
-      tmem_ld32(O + ch, o);
+      tmem_ld16(O + ch, o);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = 0.f;
+      for (int i = 0; i < 16; ++i) o[i] = 0.f;
     }
     if (!live) continue;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
+    for (int i = 0; i < 16; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
     if (p.splits > 1 || p.out_fp32) {
       float4 *dst = reinterpret_cast<float4 *>((p.splits > 1 ? p.part_o : static_cast<float *>(p.out)) +
                                                orow * D + d0 + ch);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     } else {
       uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + orow * D + d0 + ch);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
         dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
                             pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
     }
@@ -892,6 +876,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       mbar_init(&c.pready[i], 8);   // softmax warps of a row tile
       mbar_init(&c.odone[i], 1);
     }
+    mbar_init(&c.qfull, Gm::SMW);
     mbar_init(&c.done, Gm::MT);
     c.abort = 0;
     fence_mbar_init();
@@ -918,15 +903,15 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     tok = tok0 + q;
     head = w.kvh * G + x - q * G;
   };
-  // ---- rows of the softmax threads, and the queries
+  // ---- the queries are requested, the rows' key ranges found, and the copies
+  // may begin while the queries are on their way
+  constexpr int CH = D / 8, NT = Gm::SMW * 32, NQ = Gm::ROWS * CH / NT;
+  uint4 qv[NQ];
   int r_lo = 0, r_hi = 0, r_pos = 0;
   bool live = false;
   size_t r_out = 0;
   float slope = 0.f;
   if (warp < Gm::SMW) {
-    // queries: 8 or 16 pieces of 16 bytes per thread, all requested before any is used
-    constexpr int CH = D / 8, NT = Gm::SMW * 32, NQ = Gm::ROWS * CH / NT;
-    uint4 qv[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH;
@@ -948,7 +933,6 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       r_hi = kr.hi;
     }
     r_out = (size_t)(w.start + tok) * p.Hq + head;
-    if (p.sc.slopes) slope = __ldg(p.sc.slopes + head) * 1.4426950408889634f;
     const bool sees = r_hi > r_lo;
     const int lo = __reduce_min_sync(0xffffffffu, sees ? r_lo : 0x7fffffff);
     const int hi = __reduce_max_sync(0xffffffffu, sees ? r_hi : 0);
@@ -956,18 +940,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       c.lo[warp] = lo;
       c.hi[warp] = hi;
     }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH, r2 = q & 127;
-      uint4 u = qv[i];
-      if constexpr (Gm::QUANT) {   // f16 operands (exact in f16's normal range)
-        const float2 a = bf16x2_to_f2(u.x), b = bf16x2_to_f2(u.y), d = bf16x2_to_f2(u.z), e = bf16x2_to_f2(u.w);
-        u = make_uint4(tc::f2_to_h2(a.x, a.y), tc::f2_to_h2(b.x, b.y), tc::f2_to_h2(d.x, d.y), tc::f2_to_h2(e.x, e.y));
-      }
-      *reinterpret_cast<uint4 *>(smem + (q >> 7) * (128 * D * 2) + (k >> 3) * kChunkBytes + r2 * 128 +
-                                 (((k & 7) ^ (r2 & 7)) << 4)) = u;
-    }
-    fence_async_smem();
+    if (p.sc.slopes) slope = __ldg(p.sc.slopes + head) * 1.4426950408889634f;
   }
   tc_fence_before();
   __syncthreads();
@@ -986,6 +959,22 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     const int per = (t1 - t0 + p.splits - 1) / p.splits;
     w.kt0 = t0 + min(t1 - t0, split * per);
     w.ntiles = t0 + min(t1 - t0, (split + 1) * per) - w.kt0;
+  }
+  if (warp < Gm::SMW) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH, r2 = q & 127;
+      uint4 u = qv[i];
+      if constexpr (Gm::QUANT) {   // f16 operands (exact in f16's normal range)
+        const float2 a = bf16x2_to_f2(u.x), b = bf16x2_to_f2(u.y), d = bf16x2_to_f2(u.z), e = bf16x2_to_f2(u.w);
+        u = make_uint4(tc::f2_to_h2(a.x, a.y), tc::f2_to_h2(b.x, b.y), tc::f2_to_h2(d.x, d.y), tc::f2_to_h2(e.x, e.y));
+      }
+      *reinterpret_cast<uint4 *>(smem + (q >> 7) * (128 * D * 2) + (k >> 3) * kChunkBytes + r2 * 128 +
+                                 (((k & 7) ^ (r2 & 7)) << 4)) = u;
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.qfull);
   }
   constexpr bool REGS = D == 128;   // 768 threads: registers move to the softmax groups
   if (warp < Gm::SMW) {
