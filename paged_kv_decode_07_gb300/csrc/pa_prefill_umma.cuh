@@ -64,12 +64,17 @@ struct PGeo {
   static constexpr int NC = 64;                    // S columns per softmax thread
   static constexpr int NO = D / 2;                 // O columns per softmax thread
   static constexpr int SMW = 8 * MT;               // softmax warps
-  static constexpr int THREADS = (SMW + 8) * 32;
-  // Registers per thread at launch, and after the split (D = 128): MMA group,
+  // copy warps: one group; for the quantised formats one per unit of a tile (a
+  // group takes about 1400 cycles to convert a unit, its MMAs take 550)
+  static constexpr int GROUPS = QUANT ? H : 1, CPW = 4 * GROUPS;
+  static constexpr int THREADS = (SMW + 4 + CPW) * 32;
+  // Registers per thread at launch, and after the split (not where 512 threads
+  // have 128 each): MMA group,
   // copies or dequantisation, softmax groups
-  static constexpr int LAUNCH_REGS = D == 128 ? 80 : 128;
-  static constexpr int REG_MMA = 40, REG_COPY = QUANT ? 88 : 56, REG_SM = QUANT ? 88 : 96;
-  static_assert(4 * REG_SM + REG_MMA + REG_COPY <= 6 * 80, "register split");
+  static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
+  static constexpr int REG_MMA = 40, REG_COPY = QUANT ? 88 : 56;
+  static constexpr int REG_SM =
+      (LAUNCH_REGS * (THREADS / 128) - REG_MMA - GROUPS * REG_COPY) / (SMW / 4) / 8 * 8;
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int OFF_U = QBYTES;
   static constexpr int OFF_SC = OFF_U + NU * kUnitBytes;   // int8: K and V row scales, per warp
@@ -377,11 +382,11 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
 
 // ------------------------------------------- other formats: codes to f16 units
 
-// 128 threads, half a unit (64 keys) at a time; the codes of the next half are requested before the present
+// 128 threads convert unit h of every tile, half a unit (64 keys) at a time; the codes of the next half are requested before the present
 // one is converted, so that their latency passes meanwhile.  int8 and FP8: 8 lanes per key row, 16 codes a lane; NVFP4: 4
 // lanes per row, 32 codes (two scale blocks) a lane.
 template <int DT, int D>
-__device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t) {
+__device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t, int h) {
   using Gm = PGeo<DT, D>;
   constexpr bool FP4 = DT == PA_KV_NVFP4;
   constexpr int IT = FP4 ? 2 : 4, LPR = FP4 ? 4 : 8, RPI = 128 / LPR;   // loads per half unit
@@ -399,7 +404,7 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
       d[i] = !o.done() && key >= w.see_lo && key < w.see_hi ? __ldg(w.trow + key / kBlock) : -1;
     }
   };
-  auto load = [&](bool is_v, int h, int half) {
+  auto load = [&](bool is_v, int half) {
     const uint8_t *base = static_cast<const uint8_t *>(is_v ? p.kv.v : p.kv.k);
     const uint8_t *sbase = static_cast<const uint8_t *>(is_v ? p.kv.vs : p.kv.ks);
 #pragma unroll
@@ -415,7 +420,7 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
       }
     }
   };
-  uint32_t u = 0;
+  uint32_t u = h;
   // converts the loaded half unit into its stage
   auto store = [&](int half) {
     const int st = u % Gm::NU;
@@ -460,7 +465,7 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
       fence_async_smem();
       __syncwarp();
       if ((t & 31) == 0) mbar_arrive(&c.full[st]);   // one arrival a warp
-      ++u;
+      u += Gm::H;
     }
   };
   bool have = false;
@@ -471,18 +476,15 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
     on.next();
     ids(on, id_next);
 #pragma unroll
-    for (int h = 0; h < Gm::H; ++h) {
+    for (int half = 0; half < 2; ++half) {
+      load(o.is_v, half);
+      if (have) store(half ^ 1);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        load(o.is_v, h, half);
-        if (have) store(half ^ 1);
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          code[i] = next[i];
-          if constexpr (FP4) sc[i] = next_sc[i];
-        }
-        have = true;
+      for (int i = 0; i < IT; ++i) {
+        code[i] = next[i];
+        if constexpr (FP4) sc[i] = next_sc[i];
       }
+      have = true;
     }
 #pragma unroll
     for (int i = 0; i < 2 * IT; ++i) id[i] = id_next[i];
@@ -976,7 +978,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.qfull);
   }
-  constexpr bool REGS = D == 128;   // 768 threads: registers move to the softmax groups
+  constexpr bool REGS = Gm::THREADS > 512;   // registers move to the softmax groups
   if (warp < Gm::SMW) {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_SM>();
     // the second row tile's groups have nothing to do when it is empty
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   } else {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_COPY>();
     if constexpr (Gm::QUANT)
-      role_dequant<DT, D>(p, w, smem, c, tid - (Gm::SMW + 4) * 32);
+      role_dequant<DT, D>(p, w, smem, c, (tid - (Gm::SMW + 4) * 32) & 127, (warp - Gm::SMW - 4) >> 2);
     else
       role_copy<D>(p, w, smem, c, tid - (Gm::SMW + 4) * 32);
   }
@@ -1008,7 +1010,7 @@ cudaError_t launch_umma(const PrefillParams &p, cudaStream_t s) {
   auto kern = prefill_umma_kernel<DT, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
   if (e != cudaSuccess) return e;
-  if constexpr (D == 128) {
+  if constexpr (Gm::THREADS > 512) {
     // the register split starts from LAUNCH_REGS (allocated in eights): a
     // build that gave the kernel another count is refused, never launched
     cudaFuncAttributes fa;
