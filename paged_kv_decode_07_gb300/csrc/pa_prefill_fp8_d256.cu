@@ -1,0 +1,9 @@
+// pa_prefill_fp8_d256.cu -- instantiations of the tcgen05 prefill kernel for the
+// FP8 KV format, head dim 256.
+#include "pa_prefill_umma.cuh"
+
+namespace pa {
+cudaError_t launch_prefill_fp8_d256(const PrefillParams &p, cudaStream_t s) {
+  return pf::launch_umma<PA_KV_FP8, 256>(p, s);
+}
+}  // namespace pa

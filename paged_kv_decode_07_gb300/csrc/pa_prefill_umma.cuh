@@ -545,7 +545,9 @@ __device__ __forceinline__ float2 tanh_unit(float2 u) {
   return fmul2(u, h);
 }
 
-template <int DT, int D>
+// CAP, BIAS: whether scores are capped and biased (kernels of their own: either
+// costs the others registers)
+template <int DT, int D, bool CAP, bool BIAS>
 __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c,
                              uint32_t tmem, int split, int r_lo, int r_hi, int r_pos, bool live,
                              size_t r_out, float slope) {
@@ -562,13 +564,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   const int a_lo = __reduce_min_sync(0xffffffffu, sees ? r_lo : 0x7fffffff);
   const int a_hi = __reduce_max_sync(0xffffffffu, sees ? r_hi : 0);
   const int f_lo = __reduce_max_sync(0xffffffffu, live ? r_lo : 0);
+  const int a_pos = __reduce_min_sync(0xffffffffu, live ? r_pos : 0x7fffffff);
   const int f_hi = __reduce_min_sync(0xffffffffu, live ? r_hi : 0x7fffffff);
   const float kg = has_global_scale(DT) ? p.kv.kg : 1.f;
-  const bool cap = p.sc.cap_log2 != 0.f;
-  const float f = (cap ? p.sc.cap_in : p.scale_log2) * kg;
-  // direct: the largest product has the largest score, which is a factor or
-  // a cap away from it
-  const bool direct = DT != PA_KV_INT8 && p.sc.slopes == nullptr && f > 0.f;
+  const float f = (CAP ? p.sc.cap_in : p.scale_log2) * kg;
   const float fu = f * 0.34657359027997264f;   // cap: u = score / cap (f is 2 log2 e / cap times the scale)
   // (a factor so small that the scaled coefficients would leave fp32's range
   // takes the other polynomial)
@@ -625,10 +624,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     const bool none = k0 >= a_hi || k0 + NC <= a_lo;
     const bool dense = k0 >= f_lo && k0 + NC <= f_hi && !bad;
 
-    // Scores that are not one operation away from the products are formed in
-    // place, 16 columns at a time (the ends of the visible range, biased or int8
-    // scores).  The loop stays rolled: a short prompt runs it once, and then
-    // takes as long as its instructions take to arrive.
+    // Scores of tiles at the ends of the visible range (and capped ones past the
+    // polynomials' interval) are formed in place, 16 columns at a time.  The loop
+    // stays rolled: a short prompt runs it once, and then takes as long as its
+    // instructions take to arrive.
     auto form = [&]() {
 #pragma unroll 1
       for (int ch = 0; ch < NC; ch += 16) {
@@ -639,11 +638,11 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
           x[i] *= f;
           if constexpr (DT == PA_KV_INT8) x[i] *= ksc[ch + i];
         }
-        if (cap) {
+        if constexpr (CAP) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[i] = capped(x[i], p.sc.cap_log2);
         }
-        if (p.sc.slopes) {
+        if constexpr (BIAS) {
           const float far = (float)(r_pos - k0 - ch);
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[i] = fmaf(-slope, fabsf(far - (float)i), x[i]);
@@ -673,39 +672,78 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     float fs = 1.f;          // score = fs * s
     int poly = 0;            // score = cap_log2 * tanh(fu * s), by either polynomial
     if (!none) {
-      const bool formed = !(direct && dense);
+      auto largest = [&]() {
+        float x0 = s[0], x1 = s[1];
+#pragma unroll
+        for (int i = 2; i < NC; i += 2) {
+          x0 = fmaxf(x0, s[i]);
+          x1 = fmaxf(x1, s[i + 1]);
+        }
+        return fmaxf(x0, x1);
+      };
+      // (a negative factor would turn the products' order around; the distance
+      // to keys past a query, of a prefix, has the other sign)
+      bool formed = !dense || !(f > 0.f) || (BIAS && k0 + NC - 1 > a_pos);
       if (formed) form();
       load();
-      float x0 = s[0], x1 = s[1], y0 = s[0], y1 = s[1];
-#pragma unroll
-      for (int i = 2; i < NC; i += 2) {
-        x0 = fmaxf(x0, s[i]);
-        x1 = fmaxf(x1, s[i + 1]);
-      }
-      mx = fmaxf(x0, x1);
       if (!formed) {
-        if (cap) {
+        if constexpr (DT == PA_KV_INT8) {
 #pragma unroll
-          for (int i = 2; i < NC; i += 2) {
-            y0 = fminf(y0, s[i]);
-            y1 = fminf(y1, s[i + 1]);
+          for (int i = 0; i < NC; i += 4) {
+            const float4 k = *reinterpret_cast<const float4 *>(ksc + i);
+            s[i] *= k.x;
+            s[i + 1] *= k.y;
+            s[i + 2] *= k.z;
+            s[i + 3] *= k.w;
           }
-          const float top = fmaxf(mx, -fminf(y0, y1)) * fu;
-          if (__all_sync(0xffffffffu, top <= small_max)) {
-            poly = 1;
-            mx = tanh_small(f2_of(mx), small, f2_of(0.f)).x;
-          } else if (__all_sync(0xffffffffu, top <= 1.f)) {
-            poly = 2;
-            mx = tanh_unit(f2_of(mx * fu)).x * p.sc.cap_log2;
-          } else {
-            mx = capped(mx * f, p.sc.cap_log2);
-            form();
-            load();
-          }
-        } else {
-          fs = f;
-          mx *= f;
         }
+      }
+      mx = largest();
+      if (CAP && !formed) {
+        float y0 = s[0], y1 = s[1];
+#pragma unroll
+        for (int i = 2; i < NC; i += 2) {
+          y0 = fminf(y0, s[i]);
+          y1 = fminf(y1, s[i + 1]);
+        }
+        const float top = fmaxf(mx, -fminf(y0, y1)) * fu;
+        if (__all_sync(0xffffffffu, top <= small_max)) {
+          poly = 1;
+          mx = tanh_small(f2_of(mx), small, f2_of(0.f)).x;
+        } else if (__all_sync(0xffffffffu, top <= 1.f)) {
+          poly = 2;
+          mx = tanh_unit(f2_of(mx * fu)).x * p.sc.cap_log2;
+        } else {
+          formed = true;
+          form();
+          load();
+          mx = largest();
+        }
+      } else if (!formed) {
+        fs = f;
+        mx *= f;
+      }
+      if (BIAS && !formed) {   // the bias moves the maximum: scores here, factor 1 below
+        const float b0 = slope * (float)(k0 - r_pos);
+        auto bias = [&](int i) { return make_float2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0)); };
+        auto put = [&](int i, float2 y) {
+          s[i] = y.x;
+          s[i + 1] = y.y;
+        };
+        if (!CAP || poly == 0) {
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) put(i, ffma2(make_float2(s[i], s[i + 1]), f2_of(fs), bias(i)));
+        } else if (poly == 1) {
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) put(i, tanh_small(make_float2(s[i], s[i + 1]), small, bias(i)));
+        } else {
+#pragma unroll
+          for (int i = 0; i < NC; i += 2)
+            put(i, ffma2(tanh_unit(fmul2(make_float2(s[i], s[i + 1]), f2_of(fu))), f2_of(p.sc.cap_log2), bias(i)));
+        }
+        poly = 0;
+        fs = 1.f;
+        mx = largest();
       }
     }
     // ---- the running maximum moves when some score passes it by 2^kLazy
@@ -753,14 +791,14 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 #pragma unroll
         for (int ch = 0; ch < NC / 2; ch += 16) tmem_st16(S + ch, z);
       } else {
-        if (poly == 1) {
+        if (CAP && poly == 1) {
 #pragma unroll
           for (int i = 0; i < NC; i += 2) {
             const float2 y = tanh_small(make_float2(s[i], s[i + 1]), small, nm);
             s[i] = y.x;
             s[i + 1] = y.y;
           }
-        } else if (poly == 2) {
+        } else if (CAP && poly == 2) {
 #pragma unroll
           for (int i = 0; i < NC; i += 2) {
             const float2 y = ffma2(tanh_unit(fmul2(make_float2(s[i], s[i + 1]), uu)), cc, nm);
@@ -850,7 +888,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 
 // --------------------------------------------------------------------- kernel
 
-template <int DT, int D>
+template <int DT, int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     prefill_umma_kernel(const PrefillParams p, int max_tiles) {
   using Gm = PGeo<DT, D>;
@@ -983,7 +1021,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_SM>();
     // the second row tile's groups have nothing to do when it is empty
     if (warp < 8 || w.nrows > 128)
-      role_softmax<DT, D>(p, w, smem, c, tmem, split, r_lo, r_hi, r_pos, live, r_out, slope);
+      role_softmax<DT, D, CAP, BIAS>(p, w, smem, c, tmem, split, r_lo, r_hi, r_pos, live, r_out, slope);
   } else if (warp < Gm::SMW + 4) {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_MMA>();
     if (warp < Gm::SMW + Gm::MT)
@@ -1004,10 +1042,10 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   }
 }
 
-template <int DT, int D>
-cudaError_t launch_umma(const PrefillParams &p, cudaStream_t s) {
+template <int DT, int D, bool CAP, bool BIAS>
+cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
   using Gm = PGeo<DT, D>;
-  auto kern = prefill_umma_kernel<DT, D>;
+  auto kern = prefill_umma_kernel<DT, D, CAP, BIAS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
   if (e != cudaSuccess) return e;
   if constexpr (Gm::THREADS > 512) {
@@ -1024,6 +1062,13 @@ cudaError_t launch_umma(const PrefillParams &p, cudaStream_t s) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   kern<<<(unsigned)grid, Gm::THREADS, Gm::SMEM, s>>>(p, (int)tiles);
   return cudaGetLastError();
+}
+
+template <int DT, int D>
+cudaError_t launch_umma(const PrefillParams &p, cudaStream_t s) {
+  if (p.sc.cap_log2 != 0.f)
+    return p.sc.slopes ? launch_one<DT, D, true, true>(p, s) : launch_one<DT, D, true, false>(p, s);
+  return p.sc.slopes ? launch_one<DT, D, false, true>(p, s) : launch_one<DT, D, false, false>(p, s);
 }
 
 }  // namespace pf
