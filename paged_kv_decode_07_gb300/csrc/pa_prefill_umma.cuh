@@ -581,6 +581,21 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     return j < n && key < w.see_hi && key + kBlock > w.see_lo ? __ldg(w.trow + key / kBlock) : 0;
   };
   int id_next = page_id(0);
+  // int8: the row scales of a tile, lanes 0-15 K, 16-31 V, eight keys each,
+  // requested a tile ahead (and the ids they need two)
+  [[maybe_unused]] int id_after = DT == PA_KV_INT8 ? page_id(1) : 0;
+  auto row_scales = [&](int j, int ids) {
+    const int key = (w.kt0 + j) * kKeys + (lane & 15) * 8;
+    const int pid = __shfl_sync(0xffffffffu, ids, (lane & 15) >> 1);
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (j < n && key < w.see_hi && key + 8 > w.see_lo && (uint32_t)pid < (uint32_t)p.kv.num_blocks)
+      u = __ldg(reinterpret_cast<const uint4 *>(
+                    static_cast<const uint16_t *>(lane < 16 ? p.kv.ks : p.kv.vs) +
+                    ((size_t)pid * p.kv.hkv + w.kvh) * kBlock) + (lane & 1));
+    return u;
+  };
+  [[maybe_unused]] uint4 sc_next = make_uint4(0, 0, 0, 0);
+  if constexpr (DT == PA_KV_INT8) sc_next = row_scales(0, id_next);
   float m = kNegInf, l = 0.f;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
@@ -590,18 +605,14 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     const int k0 = k0t + hf * NC;                     // this thread's
     // keys of a page whose id is out of range are hidden
     const int id = id_next;
-    id_next = page_id(j + 1);
+    id_next = DT == PA_KV_INT8 ? id_after : page_id(j + 1);
+    if constexpr (DT == PA_KV_INT8) id_after = page_id(j + 2);
     const uint32_t bad = __ballot_sync(0xffffffffu, id < 0 || id >= p.kv.num_blocks) & 0xffu;
     if (bad && lane == 0) set_err(p.hdr, PA_ERRF_BAD_BLOCK_ID);
     if constexpr (DT == PA_KV_INT8) {
-      // row scales of the tile: lanes 0-15 K, 16-31 V, eight keys each
-      const int pg = (lane & 15) >> 1, key = k0t + (lane & 15) * 8;
-      const int pid = __shfl_sync(0xffffffffu, id, pg);
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (key < w.see_hi && key + 8 > w.see_lo && !((bad >> pg) & 1))
-        u = __ldg(reinterpret_cast<const uint4 *>(
-                      static_cast<const uint16_t *>(lane < 16 ? p.kv.ks : p.kv.vs) +
-                      ((size_t)pid * p.kv.hkv + w.kvh) * kBlock) + (lane & 1));
+      const int key = k0t + (lane & 15) * 8;
+      const uint4 u = sc_next;
+      sc_next = row_scales(j + 1, id_next);
       const uint32_t h2[4] = {u.x, u.y, u.z, u.w};
       float x[8];
 #pragma unroll
