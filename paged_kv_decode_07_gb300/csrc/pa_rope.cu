@@ -31,7 +31,7 @@ namespace {
 
 using namespace codec;
 
-constexpr int kRopeWarps = 4;
+constexpr int kRopeWarps = 4, kRopeCtas = 7;
 
 // inv_freq (radians per position) -> turns per position in units of 2^-64.
 // f = m * 2^(e - 126) with m in [1/2, 1) held as 64 fraction bits; 1 / 2 pi as
@@ -191,9 +191,9 @@ __device__ __forceinline__ void encode_row(const KvView &kv, int which, size_t r
 
 // A token's rows are taken in steps of 32 / L heads of one kind: first the
 // queries, then the keys, then the values.  One warp takes a run of a token's
-// steps, two at a time so that both are in flight before either is used.
+// steps, the next one's rows on their way while it is at one.
 template <int DT, int D, bool IL>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) rope_kernel(const RopeParams p) {
   constexpr int L = D / 16, RPW = 32 / L;
   const int lane = threadIdx.x & 31, sub = lane / L, j = lane % L;
   const int w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
@@ -239,30 +239,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
     }
     return x;
   };
-  Step x0 = load(s0), x1 = load(s0 + 1);
-  uint4 wq[2] = {}, wk[2] = {};
-  if (p.q_norm) {
-    wq[0] = __ldg(reinterpret_cast<const uint4 *>(p.q_norm) + ca);
-    wq[1] = __ldg(reinterpret_cast<const uint4 *>(p.q_norm) + cb);
-  }
-  if (p.k_norm) {
-    wk[0] = __ldg(reinterpret_cast<const uint4 *>(p.k_norm) + ca);
-    wk[1] = __ldg(reinterpret_cast<const uint4 *>(p.k_norm) + cb);
-  }
+  Step x0 = load(s0);
   // the angles of this lane's pairs, once for every head of the token
   float cs[8], sn[8];
   const int pos = __ldg(p.positions + t);
   const int64_t slot = __ldg(p.slots + t);
   if ((ra || rb) && s0 < sq + skv) {
-    float fr[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int pair = IL ? (i < 4 ? 4 * ca + i : 4 * cb + i - 4) : 8 * j + i;
-      fr[i] = pair < p.rot / 2 ? __ldg(p.inv_freq + pair) : 0.f;
+      cs[i] = pair < p.rot / 2 ? __ldg(p.inv_freq + pair) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint64_t ph = turns_per_position(fr[i]) * (uint64_t)(int64_t)pos;
+      const uint64_t ph = turns_per_position(cs[i]) * (uint64_t)(int64_t)pos;
       // half turns in [-1, 1): the top 32 bits of the phase, as a signed number
       sincospif((float)(int32_t)(uint32_t)(ph >> 32) * 0x1p-31f, &sn[i], &cs[i]);
       cs[i] *= p.factor;
@@ -279,9 +269,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
     Pair16 x;
     unpack8(st.a, x.a);
     unpack8(st.b, x.b);
+    const __nv_bfloat16 *const w = st.kind == 0 ? p.q_norm : st.kind == 1 ? p.k_norm : nullptr;
+    if (w) {
+      const uint4 *w4 = reinterpret_cast<const uint4 *>(w);
+      rms_norm<D>(x, __ldg(w4 + ca), __ldg(w4 + cb), p.eps);
+    }
+    if (st.kind < 2) rotate<IL>(x, cs, sn, ra, rb);
     if (st.kind == 0) {
-      if (p.q_norm) rms_norm<D>(x, wq[0], wq[1], p.eps);
-      rotate<IL>(x, cs, sn, ra, rb);
       if (st.live) {
         uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + (size_t)t * p.q_out_stride + (size_t)st.h * D);
         dst[ca] = pack8(x.a);
@@ -289,20 +283,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
       }
       return;
     }
-    if (st.kind == 1) {
-      if (p.k_norm) rms_norm<D>(x, wk[0], wk[1], p.eps);
-      rotate<IL>(x, cs, sn, ra, rb);
-    }
     encode_row<DT, D>(p.kv, st.kind == 2, row0 + (size_t)st.h * kBlock, ca, cb, x, st.live && keep);
   };
-  for (int s = s0; s < s1; s += 2) {
-    const Step y0 = x0, y1 = x1;
-    if (s + 2 < s1) {
-      x0 = load(s + 2);
-      x1 = load(s + 3);
-    }
-    finish(y0);
-    if (s + 1 < s1) finish(y1);
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
+    const Step y = x0;
+    if (s + 1 < s1) x0 = load(s + 1);
+    finish(y);
   }
 }
 
