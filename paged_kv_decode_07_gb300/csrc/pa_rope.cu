@@ -31,7 +31,9 @@ namespace {
 
 using namespace codec;
 
-constexpr int kRopeWarps = 4, kRopeCtas = 7;
+// one warp per CTA: a warp's slot is refilled as soon as it ends (28 per SM; with
+// four warps a CTA 8191 tokens took 53 us instead of 48)
+constexpr int kRopeCtas = 28;
 
 // inv_freq (radians per position) -> turns per position in units of 2^-64.
 // f = m * 2^(e - 126) with m in [1/2, 1) held as 64 fraction bits; 1 / 2 pi as
@@ -193,12 +195,10 @@ __device__ __forceinline__ void encode_row(const KvView &kv, int which, size_t r
 // queries, then the keys, then the values.  One warp takes a run of a token's
 // steps, the next one's rows on their way while it is at one.
 template <int DT, int D, bool IL>
-__global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32, kRopeCtas) rope_kernel(const RopeParams p) {
   constexpr int L = D / 16, RPW = 32 / L;
-  const int lane = threadIdx.x & 31, sub = lane / L, j = lane % L;
-  const int w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int t = w / p.parts, part = w % p.parts;
-  if (t >= p.T) return;
+  const int lane = threadIdx.x, sub = lane / L, j = lane % L;
+  const int t = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const int Hq = p.Hq, Hkv = p.kv.hkv;
   const int sq = (Hq + RPW - 1) / RPW, skv = (Hkv + RPW - 1) / RPW;
   const int s0 = part * p.steps_per_part, s1 = min(sq + 2 * skv, s0 + p.steps_per_part);
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) rope_kernel(const 
                                  : x.kind == 1 ? p.k + (size_t)t * p.k_stride
                                                : p.v + (size_t)t * p.v_stride;
       const uint4 *s4 = reinterpret_cast<const uint4 *>(src + (size_t)x.h * D);
-      x.a = __ldcs(s4 + ca);
-      x.b = __ldcs(s4 + cb);
+      x.a = __ldg(s4 + ca);
+      x.b = __ldg(s4 + cb);
     }
     return x;
   };
@@ -296,9 +296,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) rope_kernel(const 
 template <int DT, int D>
 cudaError_t launch_dt(const RopeParams &p, unsigned grid, cudaStream_t s) {
   if (p.interleaved)
-    rope_kernel<DT, D, true><<<grid, kRopeWarps * 32, 0, s>>>(p);
+    rope_kernel<DT, D, true><<<grid, 32, 0, s>>>(p);
   else
-    rope_kernel<DT, D, false><<<grid, kRopeWarps * 32, 0, s>>>(p);
+    rope_kernel<DT, D, false><<<grid, 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -307,14 +307,13 @@ cudaError_t launch_dt(const RopeParams &p, unsigned grid, cudaStream_t s) {
 cudaError_t launch_rope(RopeParams p, cudaStream_t s) {
   const int rpw = 512 / p.kv.D;   // heads a step takes
   const int steps = (p.Hq + rpw - 1) / rpw + 2 * ((p.kv.hkv + rpw - 1) / rpw);
-  // few tokens: a token's steps are spread over several warps, about eight
-  // warps per SM in all
-  const int want = (1216 + p.T - 1) / p.T;
+  // few tokens: a token's steps are spread over several warps, about
+  // sixteen warps per SM in all (255 tokens: 6.0 us, with eight 7.0, with 56 6.5)
+  const int want = (2432 + p.T - 1) / p.T;
   const int parts = want < 1 ? 1 : want > steps ? steps : want;
   p.steps_per_part = (steps + parts - 1) / parts;
   p.parts = (steps + p.steps_per_part - 1) / p.steps_per_part;
-  const long long warps = (long long)p.T * p.parts;
-  const unsigned grid = (unsigned)((warps + kRopeWarps - 1) / kRopeWarps);
+  const unsigned grid = (unsigned)p.T * (unsigned)p.parts;   // below 2^30 (rows are)
   switch (p.kv.dtype * 2 + (p.kv.D == 256)) {
     case PA_KV_BF16 * 2: return launch_dt<PA_KV_BF16, 128>(p, grid, s);
     case PA_KV_BF16 * 2 + 1: return launch_dt<PA_KV_BF16, 256>(p, grid, s);
