@@ -4,13 +4,16 @@ Every step of the attention runs in libpa.so's CUDA kernels; this module
 only turns torch tensors into pointers and sizes, picks the current CUDA
 stream, and allocates outputs / workspace with torch when the caller does
 not pass them.  There is no fallback: if libpa.so is missing or a call
-fails, it raises.
+fails, it raises.  rope_append, prefill and decode_scored do the same in the
+extension _pa_py (csrc/pa_py.cpp); here only what it declines is looked at:
+arguments to refuse by name, another stream, another device.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -18,6 +21,7 @@ import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpa.so")
+EXT_PATH = os.path.join(HERE, "_pa_py.so")
 
 PA_OK = 0
 PA_ERR_INVALID_ARG = -1
@@ -118,19 +122,8 @@ class _Options(ctypes.Structure):
                 ("event_end", ctypes.c_void_p), ("test_flags", ctypes.c_int32)]
 
 
-def _packer(cls):
-    """Fields of a ctypes structure -> its bytes, in one call (a structure
-    object's construction takes several times as long)."""
-    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f"}
-    fmt = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0P")
-    assert fmt.size == ctypes.sizeof(cls)
-    return fmt.pack
-
-
-_pack_kv, _pack_problem, _pack_rope = _packer(_KvCache), _packer(_Problem), _packer(_Rope)
-_pack_score, _pack_prefill, _pack_options = _packer(_Score), _packer(_Prefill), _packer(_Options)
-
 _lib = None
+_ext = None
 
 
 def library_path() -> str:
@@ -187,6 +180,25 @@ def lib():
         L.pa_version.argtypes = []
         _lib = L
     return _lib
+
+
+def _fast():
+    """The extension, with the entry points of the loaded library."""
+    global _ext
+    if _ext is None:
+        L = lib()
+        if not os.path.exists(EXT_PATH):
+            raise RuntimeError(
+                f"{EXT_PATH} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("_pa_py", EXT_PATH)
+        ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_py", loader))
+        loader.exec_module(ext)
+        ext.entry_points(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "pa_rope_append", "pa_prefill", "pa_prefill_workspace_bytes", "pa_decode_scored",
+            "pa_workspace_bytes")))
+        _ext = ext
+    return _ext
 
 
 def status_string(status: int) -> str:
@@ -465,6 +477,8 @@ def _need(t, name, dtype, shape, idx, strided=False):
     """Raises ValueError unless the tensor has this type, shape, device index
     (-1: the CPU) and layout.  strided: [tokens, heads, head_dim], the tokens
     any distance apart."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor: got {type(t).__name__}")
     if t.dtype is not dtype or t.shape != shape or t.get_device() != idx:
         where = "cpu" if idx < 0 else f"cuda:{idx}"
         raise ValueError(f"{name} must be {dtype} {list(shape)} on {where}: got {t.dtype} "
@@ -476,26 +490,31 @@ def _need(t, name, dtype, shape, idx, strided=False):
                              f"got strides {st}")
 
 
+def _need_out(out, shape, idx):
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dtype not in (_F32, _BF16):
+            raise ValueError("out must be a bf16 or fp32 tensor")
+        _need(out, "out", out.dtype, shape, idx)
+
+
+def _need_workspace(ws, idx):
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != idx or ws.nbytes < 256):
+        raise ValueError(f"workspace must be a tensor of at least 256 bytes on cuda:{idx}")
+
+
 def _elsewhere(idx, stream):
-    """A context for a call whose stream or device is not the current one
-    (its outputs are then allocated there too), or None."""
+    """A context for a call that the extension declined although its tensors
+    are as they should be: its stream or its device is not the current one
+    (outputs are then allocated there too)."""
     if idx < 0:
         raise ValueError("the KV cache must be on a CUDA device")
     if stream is not None:
         if stream.device.index != idx:
             raise ValueError(f"stream is on {stream.device}, the KV cache on cuda:{idx}")
         return torch.cuda.stream(stream)
-    if torch._C._cuda_getDevice() != idx:
+    if torch.cuda.current_device() != idx:
         return torch.cuda.device(idx)
-    return None
-
-
-def _kv_bytes(kv: "KvCache", hkv: int, D: int):
-    ks, vs = kv.k_scale, kv.v_scale
-    return _pack_kv(DTYPE_CODES[kv.dtype], kv.k_cache.shape[0], kv.block_size, hkv, D,
-                    kv.k_cache.data_ptr(), kv.v_cache.data_ptr(),
-                    0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
-                    kv.k_global, kv.v_global)
+    raise ValueError("a number among the arguments is none, or out of range")
 
 
 def rope_append(kv: KvCache, q, k, v, positions, slot_mapping, inv_freq, *, interleaved=False,
@@ -510,41 +529,33 @@ def rope_append(kv: KvCache, q, k, v, positions, slot_mapping, inv_freq, *, inte
     int32 [T]; slot_mapping int64 [T] (-1 = padded row); inv_freq fp32
     [rot_dim / 2] (rope_frequencies).  Returns the rotated queries bf16
     [T, Hq, D]; q_out=q rotates them in place."""
+    if stream is None:
+        r = (_ext or _fast()).rope_append(
+            DTYPE_CODES[kv.dtype], kv.block_size, kv.k_cache, kv.v_cache, kv.k_scale, kv.v_scale,
+            kv.k_global, kv.v_global, q, k, v, positions, slot_mapping, inv_freq, interleaved,
+            attn_factor, q_norm, k_norm, eps, q_out, workspace)
+        if type(r) is int:
+            raise PaError("pa_rope_append", r)
+        if r is not None:
+            return r
     T, Hq, D = q.shape
-    kc = kv.k_cache
-    idx, hkv = kc.get_device(), kc.shape[1]
-    half = inv_freq.numel()
+    idx, hkv = kv.k_cache.get_device(), kv.num_kv_heads
     _need(q, "q", _BF16, (T, Hq, kv.head_dim), idx, True)
     _need(k, "k", _BF16, (T, hkv, D), idx, True)
     _need(v, "v", _BF16, (T, hkv, D), idx, True)
     _need(positions, "positions", _I32, (T,), idx)
     _need(slot_mapping, "slot_mapping", _I64, (T,), idx)
-    _need(inv_freq, "inv_freq", _F32, (half,), idx)
-    if q_norm is not None:
-        _need(q_norm, "q_norm", _BF16, (D,), idx)
-    if k_norm is not None:
-        _need(k_norm, "k_norm", _BF16, (D,), idx)
+    _need(inv_freq, "inv_freq", _F32, (inv_freq.numel(),), idx)
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _need(t, name, _BF16, (D,), idx)
     if q_out is not None:
         _need(q_out, "q_out", _BF16, (T, Hq, D), idx, True)
-    there = _elsewhere(idx, stream)
-    if there is not None:
-        with there:
-            return rope_append(kv, q, k, v, positions, slot_mapping, inv_freq,
-                               interleaved=interleaved, attn_factor=attn_factor, q_norm=q_norm,
-                               k_norm=k_norm, eps=eps, q_out=q_out, workspace=workspace)
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=_BF16, device=kc.device)
-    a = _pack_rope(T, Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), q.stride(0),
-                   k.stride(0), v.stride(0), q_out.stride(0), positions.data_ptr(),
-                   slot_mapping.data_ptr(), 2 * half, 1 if interleaved else 0, inv_freq.data_ptr(),
-                   attn_factor, 0 if q_norm is None else q_norm.data_ptr(),
-                   0 if k_norm is None else k_norm.data_ptr(), eps)
-    st = lib().pa_rope_append(_kv_bytes(kv, hkv, D), a,
-                              None if workspace is None else workspace.data_ptr(),
-                              torch._C._cuda_getCurrentRawStream(idx))
-    if st != PA_OK:
-        raise PaError("pa_rope_append", st)
-    return q_out
+    _need_workspace(workspace, idx)
+    with _elsewhere(idx, stream):
+        return rope_append(kv, q, k, v, positions, slot_mapping, inv_freq, interleaved=interleaved,
+                           attn_factor=attn_factor, q_norm=q_norm, k_norm=k_norm, eps=eps,
+                           q_out=q_out, workspace=workspace)
 
 
 @dataclass
@@ -562,47 +573,15 @@ class Score:
     first_key: Optional[torch.Tensor] = None
     prefix_lens: Optional[torch.Tensor] = None
 
-    def pack(self, num_q_heads: int, tokens: int, batch: int, idx: int) -> bytes:
-        sl, fk, pl = self.slopes, self.first_key, self.prefix_lens
-        if sl is not None:
-            _need(sl, "slopes", _F32, (num_q_heads,), idx)
-        if fk is not None:
-            _need(fk, "first_key", _I32, (tokens,), idx)
-        if pl is not None:
-            _need(pl, "prefix_lens", _I32, (batch,), idx)
-        if not -2 ** 31 <= self.window < 2 ** 31:
-            raise ValueError(f"window must fit 32 bits: got {self.window}")
-        return _pack_score(self.softcap, self.window, 0 if sl is None else sl.data_ptr(),
-                           0 if fk is None else fk.data_ptr(), 0 if pl is None else pl.data_ptr())
+    def _need(self, num_q_heads: int, tokens: int, batch: int, idx: int):
+        for t, name, dt, n in ((self.slopes, "slopes", _F32, num_q_heads),
+                               (self.first_key, "first_key", _I32, tokens),
+                               (self.prefix_lens, "prefix_lens", _I32, batch)):
+            if t is not None:
+                _need(t, name, dt, (n,), idx)
 
 
-_PLAIN = _pack_score(0.0, 0, 0, 0, 0)
-
-
-def _check_out(out, shape, idx):
-    if out.dtype is not _F32 and out.dtype is not _BF16:
-        raise ValueError(f"out must be bf16 or fp32: got {out.dtype}")
-    _need(out, "out", out.dtype, shape, idx)
-
-
-def _call(fn, kvb, prob, score, opts, workspace, device, idx):
-    """A call that needs a workspace: the caller's, or a new one where that is
-    missing or too small.  Returns the workspace used."""
-    L = lib()
-    tail = (prob, score) if opts is None else (prob, score, opts)
-    raw = torch._C._cuda_getCurrentRawStream(idx)
-    f = getattr(L, fn)
-    st = PA_ERR_WORKSPACE_TOO_SMALL
-    if workspace is not None:
-        st = f(kvb, *tail, workspace.data_ptr(), workspace.nbytes, raw)
-    if st == PA_ERR_WORKSPACE_TOO_SMALL:
-        need = (L.pa_prefill_workspace_bytes(kvb, prob) if opts is None
-                else L.pa_workspace_bytes(kvb, prob, opts))
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-        st = f(kvb, *tail, workspace.data_ptr(), workspace.nbytes, raw)
-    if st != PA_OK:
-        raise PaError(fn, st)
-    return workspace
+_PLAIN = Score()
 
 
 def decode_scored(kv: KvCache, q, block_tables, seq_lens, softmax_scale, *, score=None, out=None,
@@ -610,36 +589,32 @@ def decode_scored(kv: KvCache, q, block_tables, seq_lens, softmax_scale, *, scor
                   split_blocks=0, target_items=0, events=None, stream=None):
     """decode with score options: q bf16 [B, 1, Hq, D] -> (out, [lse,]
     workspace).  A workspace that is too small is replaced."""
+    sc = _PLAIN if score is None else score
+    if stream is None:
+        r = (_ext or _fast()).decode_scored(
+            DTYPE_CODES[kv.dtype], kv.block_size, kv.k_cache, kv.v_cache, kv.k_scale, kv.v_scale,
+            kv.k_global, kv.v_global, q, block_tables, seq_lens, softmax_scale, sc.softcap,
+            sc.slopes, sc.window, sc.first_key, sc.prefix_lens, out, out_fp32, return_lse,
+            max_seq_len, workspace, kernel, split_blocks, target_items,
+            0 if events is None else events[0].cuda_event,
+            0 if events is None else events[1].cuda_event)
+        if type(r) is int:
+            raise PaError("pa_decode_scored", r)
+        if r is not None:
+            return r
     B, Q, Hq, D = q.shape
-    kc = kv.k_cache
-    idx, hkv = kc.get_device(), kc.shape[1]
+    idx = kv.k_cache.get_device()
     _need(q, "q", _BF16, (B, 1, Hq, kv.head_dim), idx)
     _need(block_tables, "block_tables", _I32, (B, block_tables.shape[1]), idx)
     _need(seq_lens, "seq_lens", _I32, (B,), idx)
-    if out is not None:
-        _check_out(out, (B, 1, Hq, D), idx)
-    sc = _PLAIN if score is None else score.pack(Hq, B, B, idx)
-    there = _elsewhere(idx, stream)
-    if there is not None:
-        with there:
-            return decode_scored(kv, q, block_tables, seq_lens, softmax_scale, score=score, out=out,
-                                 out_fp32=out_fp32, return_lse=return_lse, max_seq_len=max_seq_len,
-                                 workspace=workspace, kernel=kernel, split_blocks=split_blocks,
-                                 target_items=target_items, events=events)
-    if out is None:
-        out = torch.empty((B, 1, Hq, D), dtype=_F32 if out_fp32 else _BF16, device=kc.device)
-    lse = torch.empty((B, 1, Hq), dtype=_F32, device=kc.device) if return_lse else None
-    if max_seq_len is None:
-        max_seq_len = block_tables.shape[1] * kv.block_size
-    opts = _pack_options(kernel, split_blocks, target_items,
-                         0 if events is None else events[0].cuda_event,
-                         0 if events is None else events[1].cuda_event, 0)
-    prob = _pack_problem(B, Hq, 1, q.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-                         seq_lens.data_ptr(), max_seq_len, softmax_scale, out.data_ptr(),
-                         1 if out.dtype is _F32 else 0, 0 if lse is None else lse.data_ptr())
-    workspace = _call("pa_decode_scored", _kv_bytes(kv, hkv, D), prob, sc, opts, workspace,
-                      kc.device, idx)
-    return (out, lse, workspace) if return_lse else (out, workspace)
+    _need_out(out, (B, 1, Hq, D), idx)
+    sc._need(Hq, B, B, idx)
+    _need_workspace(workspace, idx)
+    with _elsewhere(idx, stream):
+        return decode_scored(kv, q, block_tables, seq_lens, softmax_scale, score=score, out=out,
+                             out_fp32=out_fp32, return_lse=return_lse, max_seq_len=max_seq_len,
+                             workspace=workspace, kernel=kernel, split_blocks=split_blocks,
+                             target_items=target_items, events=events)
 
 
 def prefill(kv: KvCache, q, q_starts, block_tables, seq_lens, softmax_scale, *, score=None,
@@ -651,34 +626,31 @@ def prefill(kv: KvCache, q, q_starts, block_tables, seq_lens, softmax_scale, *, 
     - 1 (q_starts int32 [B + 1]), the last of its seq_lens[b] keys; rows
     outside are left as they are.  Returns (out [T, Hq, D], [lse [T, Hq],]
     workspace).  A workspace that is too small is replaced."""
+    sc = _PLAIN if score is None else score
+    if stream is None:
+        r = (_ext or _fast()).prefill(
+            DTYPE_CODES[kv.dtype], kv.block_size, kv.k_cache, kv.v_cache, kv.k_scale, kv.v_scale,
+            kv.k_global, kv.v_global, q, q_starts, block_tables, seq_lens, softmax_scale,
+            sc.softcap, sc.slopes, sc.window, sc.first_key, sc.prefix_lens, out, out_fp32,
+            return_lse, max_seq_len, workspace)
+        if type(r) is int:
+            raise PaError("pa_prefill", r)
+        if r is not None:
+            return r
     T, Hq, D = q.shape
     B = seq_lens.shape[0]
-    kc = kv.k_cache
-    idx, hkv = kc.get_device(), kc.shape[1]
+    idx = kv.k_cache.get_device()
     _need(q, "q", _BF16, (T, Hq, kv.head_dim), idx)
     _need(q_starts, "q_starts", _I32, (B + 1,), idx)
     _need(block_tables, "block_tables", _I32, (B, block_tables.shape[1]), idx)
     _need(seq_lens, "seq_lens", _I32, (B,), idx)
-    if out is not None:
-        _check_out(out, (T, Hq, D), idx)
-    sc = _PLAIN if score is None else score.pack(Hq, T, B, idx)
-    there = _elsewhere(idx, stream)
-    if there is not None:
-        with there:
-            return prefill(kv, q, q_starts, block_tables, seq_lens, softmax_scale, score=score,
-                           out=out, out_fp32=out_fp32, return_lse=return_lse,
-                           max_seq_len=max_seq_len, workspace=workspace)
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=_F32 if out_fp32 else _BF16, device=kc.device)
-    lse = torch.empty((T, Hq), dtype=_F32, device=kc.device) if return_lse else None
-    if max_seq_len is None:
-        max_seq_len = block_tables.shape[1] * kv.block_size
-    prob = _pack_prefill(B, Hq, T, q.data_ptr(), q_starts.data_ptr(), block_tables.data_ptr(),
-                         block_tables.shape[1], seq_lens.data_ptr(), max_seq_len, softmax_scale,
-                         out.data_ptr(), 1 if out.dtype is _F32 else 0,
-                         0 if lse is None else lse.data_ptr())
-    workspace = _call("pa_prefill", _kv_bytes(kv, hkv, D), prob, sc, None, workspace, kc.device, idx)
-    return (out, lse, workspace) if return_lse else (out, workspace)
+    _need_out(out, (T, Hq, D), idx)
+    sc._need(Hq, T, B, idx)
+    _need_workspace(workspace, idx)
+    with _elsewhere(idx, stream):
+        return prefill(kv, q, q_starts, block_tables, seq_lens, softmax_scale, score=score, out=out,
+                       out_fp32=out_fp32, return_lse=return_lse, max_seq_len=max_seq_len,
+                       workspace=workspace)
 
 
 def read_error(workspace: torch.Tensor, stream=None) -> int:
