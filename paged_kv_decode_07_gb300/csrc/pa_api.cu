@@ -411,7 +411,8 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
     ap.RG = 1;
     ap.R = G;
     ap.test_expire = (test_flags & PA_TEST_EXPIRE_WAIT) ? 1 : 0;
-    if (cudaMemsetAsync(ws, 0, 16, stream) != cudaSuccess) return PA_ERR_CUDA;
+    if ((sc ? launch_clear(ap.hdr, stream) : cudaMemsetAsync(ws, 0, 16, stream)) != cudaSuccess)
+      return PA_ERR_CUDA;
     if (o && o->event_begin &&
         cudaEventRecord(static_cast<cudaEvent_t>(o->event_begin), stream) != cudaSuccess)
       return PA_ERR_CUDA;
@@ -880,7 +881,7 @@ int pa_prefill(const pa_kv_cache *kv, const pa_prefill_problem *p, const pa_scor
   a.part_lse = reinterpret_cast<float *>(w + L.part_lse);
   a.part_o = reinterpret_cast<float *>(w + L.part_o);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, 16, s) != cudaSuccess) return PA_ERR_CUDA;
+  if (launch_clear(a.hdr, s) != cudaSuccess) return PA_ERR_CUDA;
   return launch_prefill(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

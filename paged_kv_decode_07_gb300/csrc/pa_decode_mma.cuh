@@ -307,6 +307,11 @@ __global__ void __launch_bounds__(kThreads, 3)
   __shared__ __align__(8) uint64_t bars[kWarps][NSTAGE];
   __shared__ float s_m[kWarps][8], s_l[kWarps][8];
 
+  // (the single-launch scored kernel may start before its header is cleared)
+  auto flag = [&](uint32_t bits) {
+    if constexpr (CL && SC) griddep_wait();
+    set_err(p.hdr, bits);
+  };
   WorkItem it;
   int len;
   [[maybe_unused]] int key_lo = 0;   // first visible key (SC)
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       e |= PA_ERRF_LEN_OVER_CAPACITY;
       L = (int)cap;
     }
-    if (e && rank == 0 && threadIdx.x == 0) set_err(p.hdr, e);
+    if (e && rank == 0 && threadIdx.x == 0) flag(e);
     int first = 0;
     if constexpr (SC) {
       const KeyRange kr =
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (lane == 0) {
       uint64_t *bar = &bars[warp][s];
       if (!ok) {
-        set_err(p.hdr, PA_ERRF_BAD_BLOCK_ID);
+        flag(PA_ERRF_BAD_BLOCK_ID);
         mbar_arrive(bar);
       } else {
         uint8_t *st = wsm + s * Gm::STAGE;
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     const bool arrived = mbar_wait(&bars[warp][s], (j / NSTAGE) & 1, wait_cap);
     if (!__all_sync(0xffffffffu, arrived)) {
       failed = true;
-      if (lane == 0) set_err(p.hdr, PA_ERRF_WAIT_TIMEOUT);
+      if (lane == 0) flag(PA_ERRF_WAIT_TIMEOUT);
       break;
     }
     if (valid_bits & (1u << s)) {
@@ -964,13 +969,15 @@ cudaError_t launch_cluster_one(const AttnParams &p, int P, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Gm::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)P;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // scored: after launch_clear
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = SC ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p, tk, tv);
 }
 

@@ -9,6 +9,7 @@
 namespace pa {
 
 cudaError_t launch_plan(const PlanParams &pp, cudaStream_t s);
+cudaError_t launch_clear(uint32_t *hdr, cudaStream_t s);
 cudaError_t launch_decode_simt(const AttnParams &p, int grid, cudaStream_t s);
 int simt_supported(int dtype, int D, int R);
 cudaError_t launch_merge_plan(const AttnParams &p, cudaStream_t s);

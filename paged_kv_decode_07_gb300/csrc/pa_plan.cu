@@ -123,7 +123,7 @@ __device__ __forceinline__ int upper_bound_minus1(const P *pre, int n, int j) {
 
 // SC: scored decode (the first visible key bounds what is planned)
 template <bool SC>
-__global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
+__global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
   __shared__ unsigned long long s_total;
   __shared__ uint32_t s_err;
   __shared__ int2 s_tot;
@@ -336,6 +336,18 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
 }
 
 }  // namespace
+
+// clears the header of a call that has no plan; its attention kernel is
+// launched by launch_pdl and waits for this one only before it sets a flag
+__global__ void clear_kernel(uint32_t *hdr) {
+  griddep_launch();
+  if (threadIdx.x < 4) hdr[threadIdx.x] = 0;
+}
+
+cudaError_t launch_clear(uint32_t *hdr, cudaStream_t s) {
+  clear_kernel<<<1, 32, 0, s>>>(hdr);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_plan(const PlanParams &pp, cudaStream_t s) {
   if (pp.window > 0 || pp.first_key)

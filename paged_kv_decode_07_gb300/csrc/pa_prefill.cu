@@ -36,11 +36,8 @@ cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s) {
   if (e != cudaSuccess || p.splits == 1) return e;
   const long long rows = (long long)p.T * p.Hq;
   const unsigned grid = (unsigned)((rows + 7) / 8);
-  if (d128)
-    pf::prefill_join_kernel<128><<<grid, 256, 0, s>>>(p);
-  else
-    pf::prefill_join_kernel<256><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return d128 ? launch_pdl(pf::prefill_join_kernel<128>, grid, 256, 0, s, p)
+              : launch_pdl(pf::prefill_join_kernel<256>, grid, 256, 0, s, p);
 }
 
 }  // namespace pa

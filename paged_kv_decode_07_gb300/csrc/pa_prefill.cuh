@@ -19,6 +19,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// sets a flag once the header has been cleared (the kernel before this one)
+__device__ __forceinline__ void flag(uint32_t *hdr, uint32_t bits) {
+  griddep_wait();
+  set_err(hdr, bits);
+}
+
 // the sequence and row tile of tile index `tile` (tiles of all sequences in
 // order, `per` tokens each): every thread of a warp gets the answer
 struct TileOf {
@@ -60,13 +66,14 @@ __device__ __forceinline__ TileOf find_tile(const PrefillParams &p, int tile, in
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (err) set_err(p.hdr, PA_ERRF_BAD_Q_START);
+  if (err) flag(p.hdr, PA_ERRF_BAD_Q_START);
   return r;
 }
 
 // joins the key splits of every row of the batch's sequences: one warp a row
 template <int D>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p) {
+  griddep_wait();   // the splits are complete
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const long long rows = (long long)p.T * p.Hq;

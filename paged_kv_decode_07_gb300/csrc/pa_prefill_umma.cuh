@@ -112,7 +112,7 @@ __device__ __forceinline__ void wait_slow(uint64_t *bar, uint32_t parity, PCtl &
     if (mbar_try_wait_sleep(bar, parity, kSleepNs) || *ab) return;
   }
   *ab = 1;
-  set_err(hdr, PA_ERRF_WAIT_TIMEOUT);
+  flag(hdr, PA_ERRF_WAIT_TIMEOUT);
 }
 __device__ __forceinline__ void wait_p(uint64_t *bar, uint32_t parity, PCtl &c, uint32_t *hdr) {
   if (!mbar_test(bar, parity)) wait_slow(bar, parity, c, hdr);
@@ -608,7 +608,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     id_next = DT == PA_KV_INT8 ? id_after : page_id(j + 1);
     if constexpr (DT == PA_KV_INT8) id_after = page_id(j + 2);
     const uint32_t bad = __ballot_sync(0xffffffffu, id < 0 || id >= p.kv.num_blocks) & 0xffu;
-    if (bad && lane == 0) set_err(p.hdr, PA_ERRF_BAD_BLOCK_ID);
+    if (bad && lane == 0) flag(p.hdr, PA_ERRF_BAD_BLOCK_ID);
     if constexpr (DT == PA_KV_INT8) {
       const int key = k0t + (lane & 15) * 8;
       const uint4 u = sc_next;
@@ -911,6 +911,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   Work w;
   w.kvh = blockIdx.x % Hkv;
   const int rest = blockIdx.x / Hkv, split = rest % p.splits;
+  griddep_launch();   // (only the join follows, which waits for this grid)
   const TileOf to = find_tile(p, max_tiles - 1 - rest / p.splits, Gm::ROWS);   // the last tokens see most: first
   if (to.b < 0) return;
   if (warp == Gm::SMW) {
@@ -942,7 +943,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   const int capacity = (int)min((long long)p.stride * kBlock, 0x7fffffffLL);
   if (n < to.len || n > capacity) {
     if (tid == 0 && n != 0)
-      set_err(p.hdr, n < 0 ? PA_ERRF_NEG_LEN : n < to.len ? PA_ERRF_LEN_LT_QLEN : PA_ERRF_LEN_OVER_CAPACITY);
+      flag(p.hdr, n < 0 ? PA_ERRF_NEG_LEN : n < to.len ? PA_ERRF_LEN_LT_QLEN : PA_ERRF_LEN_OVER_CAPACITY);
     n = min(max(n, 0), capacity);
   }
   w.n = n;
@@ -1071,8 +1072,7 @@ cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
   const long long tiles = (long long)p.T * p.G / Gm::ROWS + p.B;
   const long long grid = tiles * p.kv.hkv * p.splits;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kern<<<(unsigned)grid, Gm::THREADS, Gm::SMEM, s>>>(p, (int)tiles);
-  return cudaGetLastError();
+  return launch_pdl(kern, (unsigned)grid, Gm::THREADS, Gm::SMEM, s, p, (int)tiles);
 }
 
 template <int DT, int D>
