@@ -347,15 +347,24 @@ __global__ void __launch_bounds__(kThreads, 3)
     it.part = rank;
     it.parts = nr;
     it.slot = -1;
-    it.pad = 0;
     len = L;
   } else {
     griddep_launch();   // the merge may start launching once every CTA has begun
     griddep_wait();     // the plan of this call is complete
+    // the item is requested with the count it is checked against (the grid has
+    // max_items CTAs), and holds the unit's key limit: one memory latency, not three
     const uint32_t num_items = p.hdr[HDR_NUM_ITEMS];
+    const int4 i0 = reinterpret_cast<const int4 *>(p.items + blockIdx.x)[0];
+    const int4 i1 = reinterpret_cast<const int4 *>(p.items + blockIdx.x)[1];
     if (blockIdx.x >= num_items) return;
-    it = p.items[blockIdx.x];
-    len = p.units[it.unit].len;
+    it.unit = i0.x;
+    it.kvh = i0.y;
+    it.blk_begin = i0.z;
+    it.blk_end = i0.w;
+    it.part = i1.x;
+    it.parts = i1.y;
+    it.slot = i1.z;
+    len = it.len = i1.w;
     if constexpr (SC)
       key_lo = key_range(p.sc, len - 1, len, p.sc.first_key ? __ldg(p.sc.first_key + it.unit) : 0, 0).lo;
   }

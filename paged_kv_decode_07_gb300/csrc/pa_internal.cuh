@@ -56,7 +56,8 @@ struct UnitInfo {      // int4 in the workspace
 
 struct WorkItem {      // two int4 in the workspace
   int unit, kvh, blk_begin, blk_end;
-  int part, parts, slot, pad;
+  int part, parts, slot;
+  int len;             // key limit of the unit (as in its UnitInfo)
 };
 
 // Score options as the kernels see them (pa_score; all zero: plain softmax).

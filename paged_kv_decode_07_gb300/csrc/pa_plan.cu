@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
     }
     const int chunk = (nblk + parts - 1) / parts;
     uint32_t e3 = 0;
-    int n = SC ? unit_len(p, u, e3) : 0;
+    int n = unit_len(p, u, e3);
     const int first = unit_first<SC>(p, u, n);
     WorkItem it;
     it.unit = u;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
     it.part = part;
     it.parts = parts;
     it.slot = parts > 1 ? slot_base + part : -1;
-    it.pad = 0;
+    it.len = n;
     p.items[j] = it;
   }
   if (tid == 0) {
