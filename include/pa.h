@@ -441,7 +441,8 @@ typedef struct pa_prefill_problem {
 } pa_prefill_problem;
 
 /* Workspace of pa_prefill (0 on invalid arguments): 256 bytes, more where the
- * chunks are too few to fill the GPU and the key axis is split. */
+ * chunks are too few to fill the GPU, or fill it several times and a little
+ * more (20 MB), and the key axis is split. */
 size_t pa_prefill_workspace_bytes(const pa_kv_cache *kv, const pa_prefill_problem *prob);
 int pa_prefill(const pa_kv_cache *kv, const pa_prefill_problem *prob, const pa_score *score,
                void *ws, size_t ws_bytes, pa_stream_t stream);

@@ -618,7 +618,7 @@ WoLayout wo_layout(const pa_kv_cache *kv, const pa_problem *p, const pa_wo *wo,
 
 // ---- ragged prefill
 struct PrefillLayout {
-  int splits;
+  int splits, tail;
   size_t part_lse, part_o, total;
 };
 
@@ -642,7 +642,14 @@ PrefillLayout prefill_layout(const pa_kv_cache *kv, const pa_prefill_problem *p)
                  ? prefill_splits(p->num_tokens, p->batch, kv->num_kv_heads,
                                   p->num_q_heads / kv->num_kv_heads, kv->head_dim, p->max_seq_len)
                  : 1;
-  const size_t rows = L.splits > 1 ? (size_t)L.splits * p->num_tokens * p->num_q_heads : 0;
+  const int G = p->num_q_heads / kv->num_kv_heads;
+  L.tail = L.splits == 1 && p->batch > 0 && p->num_tokens > 0
+               ? prefill_tail(p->num_tokens, p->batch, kv->num_kv_heads, G, kv->head_dim,
+                              p->max_seq_len, 0)
+               : 0;
+  const size_t rows = L.splits > 1 ? (size_t)L.splits * p->num_tokens * p->num_q_heads
+                      : L.tail > 0 ? (size_t)prefill_tail_rows(kv->head_dim)
+                                   : 0;
   L.part_lse = kHdrWords * 4;
   L.part_o = L.part_lse + up(rows * 4);
   L.total = L.part_o + up(rows * kv->head_dim * 4);
@@ -878,6 +885,10 @@ int pa_prefill(const pa_kv_cache *kv, const pa_prefill_problem *p, const pa_scor
   a.lse_out = p->lse_out;
   a.hdr = static_cast<uint32_t *>(ws);
   a.splits = L.splits;
+  // (the workspace is sized without the score options)
+  a.tail = L.tail > 0 && score && score->window > 0
+               ? prefill_tail(a.T, a.B, kv->num_kv_heads, a.G, kv->head_dim, p->max_seq_len, score->window)
+               : L.tail;
   a.part_lse = reinterpret_cast<float *>(w + L.part_lse);
   a.part_o = reinterpret_cast<float *>(w + L.part_o);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -135,9 +135,12 @@ struct PrefillParams {
   int out_fp32;
   float *lse_out;
   uint32_t *hdr;
-  int splits;               // key splits per row tile (1: outputs are written directly)
-  float *part_o;            // [splits][T][Hq][D], normalised partial outputs
-  float *part_lse;          // [splits][T][Hq]
+  int splits;               // key splits per row tile
+  int tail;                 // SMs, where the tiles of a last round may be split (splits 1), or 0
+  // normalised partial outputs [..][D] and their lse: [splits][T][Hq], or
+  // [tail tile][piece][row of the tile]
+  float *part_o;
+  float *part_lse;
 };
 
 // Norm, rotation and cache write of new tokens (pa_rope_append).

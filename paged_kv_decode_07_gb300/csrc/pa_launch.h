@@ -31,6 +31,8 @@ cudaError_t launch_append(const KvView &kv, const void *k_new, const void *v_new
 cudaError_t launch_rope(RopeParams p, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s);
 int prefill_splits(int T, int B, int Hkv, int G, int D, int max_seq_len);
+int prefill_tail(int T, int B, int Hkv, int G, int D, int max_seq_len, int window);
+long long prefill_tail_rows(int D);
 cudaError_t launch_gather(const KvView &kv, const int *tables, int stride, const int *seq_lens,
                           int B, int max_len, float *k_out, float *v_out, uint32_t *hdr,
                           cudaStream_t s);

@@ -25,20 +25,40 @@ __device__ __forceinline__ void flag(uint32_t *hdr, uint32_t bits) {
   set_err(hdr, bits);
 }
 
-// the sequence and row tile of tile index `tile` (tiles of all sequences in
-// order, `per` tokens each): every thread of a warp gets the answer
-struct TileOf {
-  // sequence (-1: none), tile in it, its query rows' start and count, its keys
-  int b, first, start, len, n;
+// One CTA's share of the batch: a row tile of a sequence and kv head, and which
+// of how many pieces of its keys.  The tiles of all sequences are counted in
+// order (rows_per_tile rows each) and taken from the last: the last tokens of a
+// prompt see most.  Pieces: all tiles in p.splits (few tiles), or, where the
+// tiles fill the GPU several times and then a little more, those of the last
+// round (p.tail: SMs) in as many pieces as make it a full round of short ones.
+struct Share {
+  int b;                      // sequence, -1: nothing to do
+  int first, start, len, n;   // tile in it, its query rows' start and count, its keys
+  int kvh, piece, pieces;
+  int tail;                   // place among the tiles of the last round, -1: not one
 };
-__device__ __forceinline__ TileOf find_tile(const PrefillParams &p, int tile, int rows_per_tile) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
+struct Round {
+  int tail, pieces;           // tiles in pieces at the end, pieces of each
+};
+__device__ __forceinline__ Round last_round(int total, int sms) {
+  Round r = {0, 1};
+  const int rem = sms > 0 ? total % sms : 0;
+  if (total > sms && rem > 0 && 2 * rem <= sms) {
+    r.tail = rem;
+    r.pieces = min(16, sms / rem);
+  }
+  return r;
+}
+
+// every thread of a warp gets the answer; `index`: of the CTA, or, in the join,
+// of a tail tile (join = true)
+__device__ __forceinline__ Share find_share(const PrefillParams &p, int index, int rows_per_tile, bool join) {
+  const int lane = threadIdx.x & 31, Hkv = p.kv.hkv;
   uint32_t err = 0;
-  TileOf r = {-1, 0, 0, 0, 0};
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
+  int start = 0, len = 0, keys = 0, inc = 0, n = 0;
+  auto scan = [&](int b0) {   // this lane's sequence, and the tiles up to it (inclusive)
     const int b = b0 + lane;
-    int start = 0, len = 0, keys = 0;
+    start = len = keys = 0;
     if (b < p.B) {
       const int s0 = __ldg(p.q_starts + b), s1 = __ldg(p.q_starts + b + 1);
       keys = __ldg(p.seq_lens + b);
@@ -47,13 +67,46 @@ __device__ __forceinline__ TileOf find_tile(const PrefillParams &p, int tile, in
       if (start != s0 || end != s1) err = 1;
       len = end - start;
     }
-    const int n = (int)(((long long)len * p.G + rows_per_tile - 1) / rows_per_tile);
-    int inc = n;
+    n = (int)(((long long)len * p.G + rows_per_tile - 1) / rows_per_tile);
+    inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
+  };
+  Share r = {-1, 0, 0, 0, 0, 0, 0, 1, -1};
+  int tiles = 0;   // at most rows / rows_per_tile + B: the host bounds them by 2^30
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    scan(b0);
+    tiles += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (err && !join) flag(p.hdr, PA_ERRF_BAD_Q_START);
+  const int total = tiles * Hkv;
+  const Round last = last_round(total, p.tail);
+  int t = index;   // tile and kv head
+  if (join) {
+    if (index >= last.tail) return r;
+    t = total - last.tail + index;
+    r.tail = index;
+    r.pieces = last.pieces;
+  } else if (p.splits > 1) {
+    r.piece = index % p.splits;
+    r.pieces = p.splits;
+    t = index / p.splits;
+  } else if (last.tail > 0 && index >= total - last.tail) {
+    const int x = index - (total - last.tail);
+    r.tail = x / last.pieces;
+    r.piece = x % last.pieces;
+    r.pieces = last.pieces;
+    t = total - last.tail + r.tail;
+  }
+  if (t >= total) return r;
+  r.kvh = t % Hkv;
+  const int tile = tiles - 1 - t / Hkv;
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    if (p.B > 32) scan(b0);
     const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > tile);
     if (hit) {
       const int l = __ffs(hit) - 1;
@@ -66,33 +119,26 @@ __device__ __forceinline__ TileOf find_tile(const PrefillParams &p, int tile, in
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (err) flag(p.hdr, PA_ERRF_BAD_Q_START);
   return r;
 }
 
-// joins the key splits of every row of the batch's sequences: one warp a row
+// out = sum_s w_s o_s / sum_s w_s of one row over `parts` partial rows
+// `pitch` rows apart, w_s = exp(lse_s - max); one warp a row
 template <int D>
-__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p) {
-  griddep_wait();   // the splits are complete
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const long long rows = (long long)p.T * p.Hq;
-  if (row >= rows) return;
-  const int t = (int)(row / p.Hq);
-  const int lo = min(max(__ldg(p.q_starts), 0), p.T), hi = min(max(__ldg(p.q_starts + p.B), 0), p.T);
-  if (t < lo || t >= hi) return;   // rows of no sequence stay as they were
+__device__ __forceinline__ void join_row(const PrefillParams &p, size_t part, size_t pitch, int parts,
+                                         size_t row, int lane) {
   float M = kNegInf;
-  for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.part_lse[s * rows + row]);
+  for (int s = 0; s < parts; ++s) M = fmaxf(M, p.part_lse[part + s * pitch]);
   float sum = 0.f, acc[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
   if (M != kNegInf)
-    for (int s = 0; s < p.splits; ++s) {
-      const float ls = p.part_lse[s * rows + row];
+    for (int s = 0; s < parts; ++s) {
+      const float ls = p.part_lse[part + s * pitch];
       if (ls == kNegInf) continue;
       const float w = expf(ls - M);
       sum += w;
-      const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (s * rows + row) * D);
+      const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (part + s * pitch) * D);
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
         const float4 x = __ldcs(src + i * 32 + lane);
@@ -105,7 +151,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < D / 128; ++i) {
-    const size_t at = (size_t)row * D + (i * 32 + lane) * 4;
+    const size_t at = row * D + (i * 32 + lane) * 4;
     const float x[4] = {acc[4 * i] * inv, acc[4 * i + 1] * inv, acc[4 * i + 2] * inv, acc[4 * i + 3] * inv};
     if (p.out_fp32)
       *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
@@ -116,6 +162,34 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p
   if (lane == 0 && p.lse_out) p.lse_out[row] = sum > 0.f ? M + logf(sum) : kNegInf;
 }
 
+// all rows in p.splits pieces
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p) {
+  griddep_wait();   // the pieces are complete
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long rows = (long long)p.T * p.Hq;
+  if (row >= rows) return;
+  const int t = (int)(row / p.Hq);
+  const int lo = min(max(__ldg(p.q_starts), 0), p.T), hi = min(max(__ldg(p.q_starts + p.B), 0), p.T);
+  if (t < lo || t >= hi) return;   // rows of no sequence stay as they were
+  join_row<D>(p, (size_t)row, (size_t)rows, p.splits, (size_t)row, threadIdx.x & 31);
+}
+
+// the tiles of the last round, eight rows at a time over all CTAs
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_tail_kernel(const PrefillParams p) {
+  constexpr int ROWS = D == 128 ? 256 : 128, STEPS = ROWS / 8;
+  griddep_wait();
+  for (int u = blockIdx.x;; u += gridDim.x) {
+    const int tail = u / STEPS, r = u % STEPS * 8 + (threadIdx.x >> 5);
+    const Share sh = find_share(p, tail, ROWS, true);
+    if (sh.b < 0) return;   // past the last round's tiles (or there are none)
+    const int flat = sh.first * ROWS + r;
+    if (flat >= sh.len * p.G) continue;
+    const size_t row = (size_t)(sh.start + flat / p.G) * p.Hq + sh.kvh * p.G + flat % p.G;
+    join_row<D>(p, (size_t)tail * sh.pieces * ROWS + r, ROWS, sh.pieces, row, threadIdx.x & 31);
+  }
+}
 
 }  // namespace pf
 }  // namespace pa

@@ -549,7 +549,7 @@ __device__ __forceinline__ float2 tanh_unit(float2 u) {
 // costs the others registers)
 template <int DT, int D, bool CAP, bool BIAS>
 __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c,
-                             uint32_t tmem, int split, int r_lo, int r_hi, int r_pos, bool live,
+                             uint32_t tmem, bool partial, int r_lo, int r_hi, int r_pos, bool live,
                              size_t r_out, float slope) {
   using Gm = PGeo<DT, D>;
   constexpr int NC = Gm::NC;
@@ -863,7 +863,6 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   const float inv = l > 0.f ? vg / l : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
   const int d0 = hf * Gm::NO;
-  const size_t orow = p.splits > 1 ? (size_t)split * p.T * p.Hq + r_out : r_out;
 #pragma unroll 1
   for (int ch = 0; ch < Gm::NO; ch += 16) {
     float o[16];
@@ -876,13 +875,13 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
-    if (p.splits > 1 || p.out_fp32) {
-      float4 *dst = reinterpret_cast<float4 *>((p.splits > 1 ? p.part_o : static_cast<float *>(p.out)) +
-                                               orow * D + d0 + ch);
+    if (partial || p.out_fp32) {
+      float4 *dst = reinterpret_cast<float4 *>((partial ? p.part_o : static_cast<float *>(p.out)) +
+                                               r_out * D + d0 + ch);
 #pragma unroll
       for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     } else {
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + orow * D + d0 + ch);
+      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + r_out * D + d0 + ch);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
@@ -890,10 +889,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     }
   }
   if (live && d0 == 0) {
-    if (p.splits > 1)
-      p.part_lse[orow] = lse;
+    if (partial)
+      p.part_lse[r_out] = lse;
     else if (p.lse_out)
-      p.lse_out[orow] = lse;
+      p.lse_out[r_out] = lse;
   }
 }
 
@@ -901,18 +900,16 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 
 template <int DT, int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
-    prefill_umma_kernel(const PrefillParams p, int max_tiles) {
+    prefill_umma_kernel(const PrefillParams p) {
   using Gm = PGeo<DT, D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ PCtl c;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int Hkv = p.kv.hkv, G = p.G;
+  const int G = p.G;
   Work w;
-  w.kvh = blockIdx.x % Hkv;
-  const int rest = blockIdx.x / Hkv, split = rest % p.splits;
-  griddep_launch();   // (only the join follows, which waits for this grid)
-  const TileOf to = find_tile(p, max_tiles - 1 - rest / p.splits, Gm::ROWS);   // the last tokens see most: first
+  griddep_launch();   // (only a join follows, which waits for this grid)
+  const Share to = find_share(p, blockIdx.x, Gm::ROWS, false);
   if (to.b < 0) return;
   if (warp == Gm::SMW) {
     tmem_alloc(&c.tmem, 512);
@@ -934,6 +931,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     fence_mbar_init();
   }
   w.b = to.b;
+  w.kvh = to.kvh;
   w.start = to.start;
   w.len = to.len;
   w.row0 = to.first * Gm::ROWS;
@@ -984,7 +982,12 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       r_lo = kr.lo;
       r_hi = kr.hi;
     }
+    // the row of the output, or of the pieces' partial ones
     r_out = (size_t)(w.start + tok) * p.Hq + head;
+    if (to.tail >= 0)
+      r_out = ((size_t)to.tail * to.pieces + to.piece) * Gm::ROWS + r;
+    else if (to.pieces > 1)
+      r_out += (size_t)to.piece * p.T * p.Hq;
     const bool sees = r_hi > r_lo;
     const int lo = __reduce_min_sync(0xffffffffu, sees ? r_lo : 0x7fffffff);
     const int hi = __reduce_max_sync(0xffffffffu, sees ? r_hi : 0);
@@ -1008,9 +1011,9 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   {
     const int t0 = w.see_lo < w.see_hi ? w.see_lo / kKeys : 0;
     const int t1 = w.see_lo < w.see_hi ? (w.see_hi + kKeys - 1) / kKeys : 0;
-    const int per = (t1 - t0 + p.splits - 1) / p.splits;
-    w.kt0 = t0 + min(t1 - t0, split * per);
-    w.ntiles = t0 + min(t1 - t0, (split + 1) * per) - w.kt0;
+    const int per = (t1 - t0 + to.pieces - 1) / to.pieces;
+    w.kt0 = t0 + min(t1 - t0, to.piece * per);
+    w.ntiles = t0 + min(t1 - t0, (to.piece + 1) * per) - w.kt0;
   }
   if (warp < Gm::SMW) {
 #pragma unroll
@@ -1033,7 +1036,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_SM>();
     // the second row tile's groups have nothing to do when it is empty
     if (warp < 8 || w.nrows > 128)
-      role_softmax<DT, D, CAP, BIAS>(p, w, smem, c, tmem, split, r_lo, r_hi, r_pos, live, r_out, slope);
+      role_softmax<DT, D, CAP, BIAS>(p, w, smem, c, tmem, to.pieces > 1, r_lo, r_hi, r_pos, live, r_out, slope);
   } else if (warp < Gm::SMW + 4) {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_MMA>();
     if (warp < Gm::SMW + Gm::MT)
@@ -1068,11 +1071,12 @@ cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if ((fa.numRegs + 7) / 8 * 8 != Gm::LAUNCH_REGS) return cudaErrorInvalidDeviceFunction;
   }
-  // every sequence has at most one tile that is not full
+  // every sequence has at most one tile that is not full; the pieces of a last
+  // round are at most one per SM
   const long long tiles = (long long)p.T * p.G / Gm::ROWS + p.B;
-  const long long grid = tiles * p.kv.hkv * p.splits;
+  const long long grid = tiles * p.kv.hkv * p.splits + p.tail;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(kern, (unsigned)grid, Gm::THREADS, Gm::SMEM, s, p, (int)tiles);
+  return launch_pdl(kern, (unsigned)grid, Gm::THREADS, Gm::SMEM, s, p);
 }
 
 template <int DT, int D>

@@ -109,6 +109,28 @@ def test_few_rows_over_a_long_cache(fmt):
     check(fmt, [40, 1], [5000, 3333], 2, 2, 128, slopes=slopes(4), window=2500)
 
 
+@pytest.mark.parametrize("fmt,D,hkv,G,new,lens", [
+    ("bf16", 256, 8, 8, [320], [8300]),            # 160 row tiles: eight in a last round of pieces
+    ("bf16", 128, 8, 8, [637, 3], [8250, 300]),    # 160 + 8
+    ("int8", 256, 4, 6, [411, 0, 420], [411, 20, 8500]),   # ragged: 80 + 80
+    ("nvfp4", 256, 1, 8, [1, 2500], [8300, 12600])])
+def test_last_round_of_tiles_in_pieces(fmt, D, hkv, G, new, lens):
+    """A little more row tiles than SMs: those of the last round are split and
+    joined, rows of no sequence stay as they were."""
+    kv, q, starts, tables, sl = build(fmt, new, lens, hkv, G, D)
+    T = sum(new)
+    qq = torch.cat((q, q[:3]))
+    out = torch.full((T + 3, hkv * G, D), 7.0, device=DEV)
+    sc = pa.Score(softcap=20.0, window=8200)
+    out, lse, ws = pa.prefill(kv, qq, starts, tables, sl, D ** -0.5, score=sc, out=out, return_lse=True,
+                              max_seq_len=max(lens))
+    assert pa.read_error(ws) == 0 and (out[T:] == 7.0).all()
+    ref, rl, bound = S.reference(vals(kv), q, new, lens, tables, D ** -0.5, softcap=20.0, window=8200,
+                                 eps_p=EPS_P[fmt], v_unit=kv.v_scale if fmt == "int8" else None)
+    S.within(out[:T], ref, bound)
+    S.lse_within(lse[:T], rl)
+
+
 def test_padded_and_empty_sequences_and_rows_behind_the_last():
     new, lens = [5, 0, 9, 0], [5, 40, 60, 0]
     kv, q, starts, tables, sl = build("bf16", new, lens, 2, 4, 128)
