@@ -282,6 +282,15 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // CL = false: one CTA per planned work item (partials merged by the merge
 // kernel).  CL = true: the single-launch variant for small problems -- no
 // planner and no merge kernel: cluster i handles (sequence i / Hkv, kv head
@@ -857,83 +866,120 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   __syncthreads();
 
-  // ---- merge the warps and write (rows h < R)
+  // ---- merge the warps and write (rows h < R): the warps' factors and the
+  // sum once per row, then four dims a thread (formed per element, they were
+  // most of the instructions of a short item)
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.0f;
-  const int G = p.G;
-  for (int idx = threadIdx.x; idx < R * D; idx += kThreads) {
-    const int h = idx / D, d = idx % D;
+  const int G = p.G, tid = threadIdx.x;
+  __shared__ float s_f[kWarps][8], s_L[8];
+  auto row_of = [&](int h) { return ((size_t)b * Q + qi) * p.Hq + (size_t)kvh * G + h; };
+  if (tid < R) {
+    const int h = tid;
     float M = kNegInf;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
-    float L = 0.f, acc = 0.f;
+    float L = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float mw = s_m[w][h];
       const float f = (mw == kNegInf) ? 0.f : exp2f(mw - M);
       L += f * s_l[w][h];
-      acc += f * reinterpret_cast<const float *>(smem + w * Gm::WARP_BYTES)[h * D + d];
+      s_f[w][h] = f;
     }
-    const float out = L > 0.f ? acc / L * vg : 0.f;
+    s_L[h] = L;
     const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : kNegInf;
-    if constexpr (CL) {   // this CTA's partial, for the cluster merge below
-      float *mo = reinterpret_cast<float *>(smem + kWarps * Gm::WARP_BYTES);
-      mo[h * D + d] = out;
-      if (d == 0) mo[8 * D + h] = lse;
+    if constexpr (CL) {
+      reinterpret_cast<float *>(smem + kWarps * Gm::WARP_BYTES)[8 * D + h] = lse;
     } else if (it.parts <= 1) {
-      const size_t row = ((size_t)b * Q + qi) * p.Hq + (size_t)kvh * G + h;
-      if (p.out_fp32)
-        reinterpret_cast<float *>(p.out)[row * D + d] = out;
-      else
-        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * D + d] = __float2bfloat16_rn(out);
-      if (d == 0 && p.lse_out) p.lse_out[row] = lse;
+      if (p.lse_out) p.lse_out[row_of(h)] = lse;
     } else {
-      const size_t prow = ((size_t)it.slot * Hkv + kvh) * p.R + h;
-      p.part_o[prow * D + d] = out;
-      if (d == 0) p.part_lse[prow] = lse;
+      p.part_lse[((size_t)it.slot * Hkv + kvh) * p.R + h] = lse;
+    }
+  }
+  __syncthreads();
+  auto store4 = [&](size_t row, int d, const float4 &v) {
+    if (p.out_fp32)
+      *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + row * D + d) = v;
+    else
+      *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + row * D + d) =
+          make_uint2(f2_to_bf2(v.x, v.y), f2_to_bf2(v.z, v.w));
+  };
+  for (int idx = tid; idx < R * (D / 4); idx += kThreads) {
+    const int h = idx / (D / 4), d = idx % (D / 4) * 4;
+    const float L = s_L[h];
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = s_f[w][h];
+      const float4 o4 = *reinterpret_cast<const float4 *>(
+          reinterpret_cast<const float *>(smem + w * Gm::WARP_BYTES) + h * D + d);
+      acc[0] += f * o4.x;
+      acc[1] += f * o4.y;
+      acc[2] += f * o4.z;
+      acc[3] += f * o4.w;
+    }
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (L > 0.f) v = make_float4(acc[0] / L * vg, acc[1] / L * vg, acc[2] / L * vg, acc[3] / L * vg);
+    if constexpr (CL) {   // this CTA's partial, for the cluster merge below
+      *reinterpret_cast<float4 *>(smem + kWarps * Gm::WARP_BYTES + (h * D + d) * 4) = v;
+    } else if (it.parts <= 1) {
+      store4(row_of(h), d, v);
+    } else {
+      *reinterpret_cast<float4 *>(p.part_o + (((size_t)it.slot * Hkv + kvh) * p.R + h) * D + d) = v;
     }
   }
   if constexpr (CL) {
     // LSE merge of the cluster's partials: this CTA takes head-dim slice
-    // [d0, d1) of every row
+    // [d0, d0 + per) of every row, four dims a thread
+    __shared__ float s_cw[kMaxCluster][8], s_csum[8];
     cluster_sync_all();
     const int rank = (int)cluster_rank(), nr = (int)cluster_size();
-    const int per = (D + nr - 1) / nr, d0 = rank * per, d1 = min(D, d0 + per);
+    const int per4 = (D / 4 + nr - 1) / nr, q0 = rank * per4, nq = max(0, min(D / 4, q0 + per4) - q0);
     const uint32_t mo = smem_u32(smem + kWarps * Gm::WARP_BYTES);
-    for (int idx = threadIdx.x; idx < R * per; idx += kThreads) {
-      const int h = idx / per, d = d0 + idx % per;
-      if (d >= d1) continue;
-      // all 2 * nr remote loads are issued before any result is used (an
-      // empty partial holds o = 0 and lse = -inf, both defined)
-      float lj[kMaxCluster], oj[kMaxCluster];
+    if (tid < R) {
+      // all remote loads are issued before any result is used (an empty
+      // partial holds o = 0 and lse = -inf, both defined)
+      const int h = tid;
+      float lj[kMaxCluster];
 #pragma unroll
-      for (int j = 0; j < kMaxCluster; ++j) {
-        if (j < nr) {
-          lj[j] = ld_cluster_f32(map_rank(mo + (uint32_t)(8 * D + h) * 4, (uint32_t)j));
-          oj[j] = ld_cluster_f32(map_rank(mo + (uint32_t)(h * D + d) * 4, (uint32_t)j));
-        }
-      }
+      for (int j = 0; j < kMaxCluster; ++j)
+        if (j < nr) lj[j] = ld_cluster_f32(map_rank(mo + (uint32_t)(8 * D + h) * 4, (uint32_t)j));
       float M = kNegInf;
 #pragma unroll
       for (int j = 0; j < kMaxCluster; ++j)
         if (j < nr) M = fmaxf(M, lj[j]);
-      float acc = 0.f, wsum = 0.f;
-      if (M != kNegInf) {
+      float wsum = 0.f;
 #pragma unroll
-        for (int j = 0; j < kMaxCluster; ++j) {
-          if (j < nr) {
-            const float w = lj[j] == kNegInf ? 0.f : __expf(lj[j] - M);
-            acc += w * oj[j];
-            wsum += w;
-          }
+      for (int j = 0; j < kMaxCluster; ++j)
+        if (j < nr) {
+          const float w = lj[j] == kNegInf ? 0.f : __expf(lj[j] - M);
+          s_cw[j][h] = w;
+          wsum += w;
         }
-      }
-      const float out = wsum > 0.f ? acc / wsum : 0.f;
-      const size_t row = ((size_t)b * Q + qi) * p.Hq + (size_t)kvh * G + h;
-      if (p.out_fp32)
-        reinterpret_cast<float *>(p.out)[row * D + d] = out;
-      else
-        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * D + d] = __float2bfloat16_rn(out);
-      if (d == 0 && p.lse_out) p.lse_out[row] = wsum > 0.f ? M + __logf(wsum) : kNegInf;
+      s_csum[h] = wsum;
+      if (rank == 0 && p.lse_out) p.lse_out[row_of(h)] = wsum > 0.f ? M + __logf(wsum) : kNegInf;
+    }
+    __syncthreads();
+    for (int idx = tid; idx < R * nq; idx += kThreads) {
+      const int h = idx / nq, d = (q0 + idx % nq) * 4;
+      float4 oj[kMaxCluster];
+#pragma unroll
+      for (int j = 0; j < kMaxCluster; ++j)
+        if (j < nr) oj[j] = ld_cluster_f4(map_rank(mo + (uint32_t)(h * D + d) * 4, (uint32_t)j));
+      const float wsum = s_csum[h];
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kMaxCluster; ++j)
+        if (j < nr) {
+          const float w = s_cw[j][h];
+          acc[0] += w * oj[j].x;
+          acc[1] += w * oj[j].y;
+          acc[2] += w * oj[j].z;
+          acc[3] += w * oj[j].w;
+        }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wsum > 0.f) v = make_float4(acc[0] / wsum, acc[1] / wsum, acc[2] / wsum, acc[3] / wsum);
+      store4(row_of(h), d, v);
     }
     cluster_sync_all();   // no CTA leaves while another still reads its partial
   }
