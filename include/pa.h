@@ -413,7 +413,9 @@ typedef struct pa_score {
 
 /* Decode (q_len 1) with score options: arguments, split plan, outputs and
  * flags as pa_decode; a window (or first_key) also shortens what is read.
- * opt->kernel: 0, 2 or 5 (else PA_ERR_UNSUPPORTED). */
+ * opt->kernel: 0, 2 or 5 (else PA_ERR_UNSUPPORTED); auto mode runs single-launch
+ * also for sequences of at most 128 keys in any number, and for at most 1,024
+ * keys (counting a window's keys only) up to three CTAs per SM. */
 int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_score *score,
                      const pa_options *opt, void *ws, size_t ws_bytes, pa_stream_t stream);
 

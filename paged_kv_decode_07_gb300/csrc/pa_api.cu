@@ -180,6 +180,11 @@ constexpr int kItemCostVerify = 32;
 constexpr int kClusterMax = 8;
 constexpr int kClusterBlocksPerCta = 8;
 constexpr int kClusterMaxCtas = 148;
+// scored decode: clusters of one CTA always (64 sequences x 4 heads of 64 keys:
+// 9.3 us against 15.4 planned; 512 sequences 45 against 59), larger ones while
+// their CTAs run at once, three per SM (28 x 400 keys, 448 CTAs: 17.7 against
+// 20.0 us; 64 x 400, 1,024 CTAs, would take 29.9 against 23.9)
+constexpr int kScoredClusterCtas = 3 * 152;
 constexpr size_t kAlign = 256;
 
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -382,7 +387,8 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   if (kernel == 0 && use_tc && !dense && !verify && Q == 1 && !extra_err &&
       !(o && (o->split_blocks > 0 || o->target_items > 0)) &&
       maxblk_all <= kClusterMax * kClusterBlocksPerCta &&
-      (long long)p->batch * kv->num_kv_heads * cluster <= kClusterMaxCtas)
+      ((long long)p->batch * kv->num_kv_heads * cluster <= kClusterMaxCtas ||
+       (sc && (cluster == 1 || (long long)p->batch * kv->num_kv_heads * cluster <= kScoredClusterCtas))))
     single = true;
   // the expired-wait test mode is built into the tensor-core decode kernel only
   if ((test_flags & PA_TEST_EXPIRE_WAIT) && !(use_tc && !dense && !umma)) return PA_ERR_UNSUPPORTED;
