@@ -546,8 +546,15 @@ __device__ __forceinline__ float2 tanh_unit(float2 u) {
 }
 
 // CAP, BIAS: whether scores are capped and biased (kernels of their own: either
-// costs the others registers)
-template <int DT, int D, bool CAP, bool BIAS>
+// costs the others registers).  FIX: capped scores lie in [-cap, cap], so 2^score
+// can be taken as it is, without a maximum, where fp32 and bf16 hold it and its
+// sums: cap * log2 e <= kFixedCap = 80, that is weights of 2^+-80, sums of up to
+// 2^30 of them, and values up to 2^17 without overflow.  (fp16 weights could not;
+// a bias has no bound.)  No pair of warps then has to agree on a maximum, no O is
+// rescaled (eight ragged chunks, heads of 128: 283 -> 266 us).
+constexpr float kFixedCap = 80.f;
+
+template <int DT, int D, bool CAP, bool BIAS, bool FIX>
 __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c,
                              uint32_t tmem, bool partial, int r_lo, int r_hi, int r_pos, bool live,
                              size_t r_out, float slope) {
@@ -596,7 +603,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   };
   [[maybe_unused]] uint4 sc_next = make_uint4(0, 0, 0, 0);
   if constexpr (DT == PA_KV_INT8) sc_next = row_scales(0, id_next);
-  float m = kNegInf, l = 0.f;
+  float m = FIX ? 0.f : kNegInf, l = 0.f;
+  // FIX: the way capped scores are formed (1, 2: the polynomials, 3: the
+  // formula), moved on when a product leaves the polynomial's interval
+  [[maybe_unused]] int mode = fabsf(fu) >= 0x1p-16f ? 1 : 2;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int buf = D == 128 ? rt : (j & 1);
@@ -679,6 +689,75 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 #pragma unroll
       for (int ch = 0; ch < NC; ch += 32) ld_wait(s + ch);
     };
+    if constexpr (FIX) {
+      float2 l2 = make_float2(0.f, 0.f);
+      if (none) {
+        const uint32_t z[16] = {};
+        tmem_st16(S, z);
+        tmem_st16(S + 16, z);
+      } else {
+        if (!dense) form();
+        load();
+        // scores over the products, which stay in tensor memory until the
+        // weights are written: read again where the polynomial did not hold
+        auto each = [&](auto &&score) {
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) {
+            const float2 y = score(make_float2(s[i], s[i + 1]));
+            s[i] = y.x;
+            s[i + 1] = y.y;
+          }
+        };
+        float v0 = 0.f, v1 = 0.f;   // largest squares
+        if (dense && mode == 1) {
+          each([&](float2 x) {
+            const float2 v = fmul2(x, x);
+            v0 = fmaxf(v0, v.x);
+            v1 = fmaxf(v1, v.y);
+            float2 h = ffma2(v, f2_of(small.c3), f2_of(small.c2));
+            h = ffma2(v, h, f2_of(small.c1));
+            h = ffma2(v, h, f2_of(small.c0));
+            return fmul2(x, h);
+          });
+          if (!__all_sync(0xffffffffu, fmaxf(v0, v1) * (fu * fu) <= kSmallU * kSmallU)) {
+            mode = 2;
+            load();
+          }
+        }
+        if (dense && mode == 2) {
+          v0 = v1 = 0.f;
+          each([&](float2 x) {
+            const float2 u = fmul2(x, f2_of(fu));
+            v0 = fmaxf(v0, fabsf(u.x));
+            v1 = fmaxf(v1, fabsf(u.y));
+            return fmul2(tanh_unit(u), f2_of(p.sc.cap_log2));
+          });
+          if (!__all_sync(0xffffffffu, fmaxf(v0, v1) <= 1.f)) {
+            mode = 3;
+            load();
+          }
+        }
+        if (dense && mode == 3)
+          each([&](float2 x) { return make_float2(capped(x.x * f, p.sc.cap_log2), capped(x.y * f, p.sc.cap_log2)); });
+#pragma unroll
+        for (int ch = 0; ch < NC; ch += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 a = make_float2(ex2_approx(s[ch + i]), ex2_approx(s[ch + i + 1]));
+            l2 = fadd2(l2, a);
+            pk[i / 2] = tc::f2_to_bf2(a.x, a.y);
+          }
+          tmem_st16(S + ch / 2, pk);
+        }
+      }
+      l += l2.x + l2.y;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.pready[buf]);
+      continue;
+    }
     float mx = kNegInf;      // this thread's largest score of the tile (log2 units)
     float fs = 1.f;          // score = fs * s
     int poly = 0;            // score = cap_log2 * tanh(fu * s), by either polynomial
@@ -898,7 +977,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 
 // --------------------------------------------------------------------- kernel
 
-template <int DT, int D, bool CAP, bool BIAS>
+template <int DT, int D, bool CAP, bool BIAS, bool FIX>
 __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     prefill_umma_kernel(const PrefillParams p) {
   using Gm = PGeo<DT, D>;
@@ -1036,7 +1115,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_SM>();
     // the second row tile's groups have nothing to do when it is empty
     if (warp < 8 || w.nrows > 128)
-      role_softmax<DT, D, CAP, BIAS>(p, w, smem, c, tmem, to.pieces > 1, r_lo, r_hi, r_pos, live, r_out, slope);
+      role_softmax<DT, D, CAP, BIAS, FIX>(p, w, smem, c, tmem, to.pieces > 1, r_lo, r_hi, r_pos, live, r_out, slope);
   } else if (warp < Gm::SMW + 4) {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_MMA>();
     if (warp < Gm::SMW + Gm::MT)
@@ -1057,10 +1136,10 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   }
 }
 
-template <int DT, int D, bool CAP, bool BIAS>
+template <int DT, int D, bool CAP, bool BIAS, bool FIX = false>
 cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
   using Gm = PGeo<DT, D>;
-  auto kern = prefill_umma_kernel<DT, D, CAP, BIAS>;
+  auto kern = prefill_umma_kernel<DT, D, CAP, BIAS, FIX>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
   if (e != cudaSuccess) return e;
   if constexpr (Gm::THREADS > 512) {
@@ -1081,6 +1160,9 @@ cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
 
 template <int DT, int D>
 cudaError_t launch_umma(const PrefillParams &p, cudaStream_t s) {
+  if constexpr (DT == PA_KV_BF16)
+    if (p.sc.cap_log2 != 0.f && p.sc.cap_log2 <= kFixedCap && !p.sc.slopes)
+      return launch_one<DT, D, true, false, true>(p, s);
   if (p.sc.cap_log2 != 0.f)
     return p.sc.slopes ? launch_one<DT, D, true, true>(p, s) : launch_one<DT, D, true, false>(p, s);
   return p.sc.slopes ? launch_one<DT, D, false, true>(p, s) : launch_one<DT, D, false, false>(p, s);
