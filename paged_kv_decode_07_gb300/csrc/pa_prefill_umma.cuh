@@ -941,7 +941,18 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
   const float inv = l > 0.f ? vg / l : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
-  const int d0 = hf * Gm::NO;
+  // The tile's MMAs are complete, so its shared memory is free: the output goes through it (16-byte pieces, swizzled by row) and leaves in whole
+  // rows.  (Stored from here, a row per lane, each instruction touched 32 lines:
+  // 6,000 cycles for a tile of 128 x 256.)
+  // A bf16 tile takes the place of its own queries; fp32 rows reach into what the
+  // other row tile's MMAs read.
+  const bool wide = partial || p.out_fp32;
+  if (D == 128 && wide && n > 0 && w.nrows > 128) {
+    wait_p(&c.odone[rt ^ 1], 0, c, p.hdr);
+    __syncwarp();
+  }
+  const int per_row = wide ? D / 4 : D / 8;   // pieces
+  auto piece_at = [&](int r, int k) { return smem + ((size_t)r * per_row + (k ^ (r & 7))) * 16; };
 #pragma unroll 1
   for (int ch = 0; ch < Gm::NO; ch += 16) {
     float o[16];
@@ -951,23 +962,32 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] = 0.f;
     }
-    if (!live) continue;
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
-    if (partial || p.out_fp32) {
-      float4 *dst = reinterpret_cast<float4 *>((partial ? p.part_o : static_cast<float *>(p.out)) +
-                                               r_out * D + d0 + ch);
+    const int d = hf * Gm::NO + ch;
+    if (wide) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4 *>(piece_at(row, d / 4 + i)) =
+            make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     } else {
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + r_out * D + d0 + ch);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                            pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+        *reinterpret_cast<uint4 *>(piece_at(row, d / 8 + i)) =
+            make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                       pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
     }
   }
-  if (live && d0 == 0) {
+  named_sync(pair, 64);   // both halves of the rows are there
+  uint4 *const dst = static_cast<uint4 *>(partial ? static_cast<void *>(p.part_o) : p.out);
+#pragma unroll 1
+  for (int i = lane; i < 16 * per_row; i += 32) {   // 16 of the pair's 32 rows each
+    const int q = hf * 16 + i / per_row, k = i % per_row;
+    const size_t to = __shfl_sync(0xffffffffu, r_out, q);
+    if (__shfl_sync(0xffffffffu, (int)live, q))
+      dst[to * per_row + k] = *reinterpret_cast<const uint4 *>(piece_at((row & ~31) + q, k));
+  }
+  if (live && hf == 0) {
     if (partial)
       p.part_lse[r_out] = lse;
     else if (p.lse_out)
@@ -1041,23 +1061,26 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   size_t r_out = 0;
   float slope = 0.f;
   if (warp < Gm::SMW) {
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH;
-      int tok, head;
-      split_row(q, tok, head);
-      qv[i] = make_uint4(0, 0, 0, 0);
-      if (q < w.nrows)
-        qv[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.start + tok) * p.Hq + head) * D) + k);
-    }
+    // (what the ranges need is requested before the queries: they would queue up)
     const int r = (tid >> 8) * 128 + (tid & 127);
     live = r < w.nrows;
     int tok, head;
     split_row(live ? r : 0, tok, head);
+    const int first = p.sc.first_key ? __ldg(p.sc.first_key + w.start + tok) : 0;
+    const int prefix = p.sc.prefix ? __ldg(p.sc.prefix + w.b) : 0;
+    if (p.sc.slopes) slope = __ldg(p.sc.slopes + head) * 1.4426950408889634f;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH;
+      int qt, qh;
+      split_row(q, qt, qh);
+      qv[i] = make_uint4(0, 0, 0, 0);
+      if (q < w.nrows)
+        qv[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.start + qt) * p.Hq + qh) * D) + k);
+    }
     r_pos = n - w.len + tok;
     if (live) {
-      const KeyRange kr = key_range(p.sc, r_pos, n, p.sc.first_key ? __ldg(p.sc.first_key + w.start + tok) : 0,
-                                    p.sc.prefix ? __ldg(p.sc.prefix + w.b) : 0);
+      const KeyRange kr = key_range(p.sc, r_pos, n, first, prefix);
       r_lo = kr.lo;
       r_hi = kr.hi;
     }
@@ -1074,7 +1097,6 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       c.lo[warp] = lo;
       c.hi[warp] = hi;
     }
-    if (p.sc.slopes) slope = __ldg(p.sc.slopes + head) * 1.4426950408889634f;
   }
   tc_fence_before();
   __syncthreads();
