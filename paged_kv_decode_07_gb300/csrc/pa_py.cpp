@@ -14,6 +14,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/pa.h"
@@ -48,7 +49,16 @@ bool opt(PyObject *o, const Tensor *&t, at::ScalarType dt, at::IntArrayRef shape
   t = tensor(o);
   return is(t, dt, shape, dev);
 }
+bool is_workspace(const Tensor *t, int dev) {
+  return t && t->is_cuda() && t->device().index() == dev && t->is_contiguous();
+}
 void *ptr(const Tensor *t) { return t ? t->data_ptr() : nullptr; }
+
+// one of the cache's arrays: its shape and element size, whatever the bytes are called
+bool is_pool(const Tensor *t, at::IntArrayRef shape, size_t bytes, int dev) {
+  return t && t->is_cuda() && t->device().index() == dev && t->sizes() == shape && t->itemsize() == bytes &&
+         t->is_contiguous();
+}
 
 // the KV cache's eight fields from args[0 ..]; the device index, or -1
 int cache(PyObject *const *a, pa_kv_cache &kv) {
@@ -68,6 +78,16 @@ int cache(PyObject *const *a, pa_kv_cache &kv) {
   kv.k_global_scale = (float)PyFloat_AsDouble(a[6]);
   kv.v_global_scale = (float)PyFloat_AsDouble(a[7]);
   const int dev = k->device().index();
+  const int64_t pages[4] = {k->size(0), k->size(1), kv.block_size, k->size(3)};
+  const size_t bytes = kv.dtype == PA_KV_BF16 ? 2 : 1;
+  if (!is_pool(k, pages, bytes, dev) || !is_pool(v, pages, bytes, dev)) return -1;
+  if (kv.dtype == PA_KV_INT8 && (!is_pool(ks, {pages[0], pages[1], pages[2]}, 2, dev) ||
+                                 !is_pool(vs, {pages[0], pages[1], pages[2]}, 2, dev)))
+    return -1;
+  if (kv.dtype == PA_KV_NVFP4) {
+    const int64_t blocks[4] = {pages[0], pages[1], pages[2], pages[3] / 8};
+    if (!is_pool(ks, blocks, 1, dev) || !is_pool(vs, blocks, 1, dev)) return -1;
+  }
   return c10::cuda::current_device() == dev ? dev : -1;
 }
 
@@ -107,14 +127,12 @@ bool output(PyObject *o, Tensor &out, at::IntArrayRef shape, bool fp32, const Te
   return true;
 }
 
+// torch's exceptions (out of memory, ..) become Python's
 template <typename F>
 PyObject *guarded(F &&f) {
-  try {
-    return f();
-  } catch (const std::exception &e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
+  HANDLE_TH_ERRORS
+  return f();
+  END_HANDLE_TH_ERRORS
 }
 
 PyObject *refused() {
@@ -150,7 +168,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       out = *o;
     }
     const Tensor *ws = a[20] == Py_None ? nullptr : tensor(a[20]);
-    if (a[20] != Py_None && (!ws || !ws->is_cuda() || ws->nbytes() < 256)) return refused();
+    if (a[20] != Py_None && (!is_workspace(ws, dev) || ws->nbytes() < 256)) return refused();
     pa_rope r;
     r.num_tokens = (int32_t)T;
     r.num_q_heads = (int32_t)H;
@@ -185,7 +203,7 @@ int with_workspace(PyObject *arg, Tensor &ws, const Tensor &like, C &&call, N &&
   int st = PA_ERR_WORKSPACE_TOO_SMALL;
   if (arg != Py_None) {
     const Tensor *t = tensor(arg);
-    if (!t || !t->is_cuda() || t->device() != like.device()) {
+    if (!is_workspace(t, like.device().index())) {
       ok = false;
       return 0;
     }

@@ -490,6 +490,27 @@ def _need(t, name, dtype, shape, idx, strided=False):
                              f"got strides {st}")
 
 
+def _need_cache(kv, idx):
+    """The cache's arrays: one shape and element size (whatever the bytes are called)."""
+    if idx < 0:
+        raise ValueError("the KV cache must be on a CUDA device")
+    k = kv.k_cache
+    pages = (k.shape[0], k.shape[1], kv.block_size, k.shape[3])
+    size = 2 if kv.dtype == "bf16" else 1
+    arrays = [("k_cache", k, pages, size), ("v_cache", kv.v_cache, pages, size)]
+    if kv.dtype == "int8":
+        arrays += [("k_scale", kv.k_scale, pages[:3], 2), ("v_scale", kv.v_scale, pages[:3], 2)]
+    elif kv.dtype == "nvfp4":
+        blocks = pages[:3] + (pages[3] // 8,)
+        arrays += [("k_scale", kv.k_scale, blocks, 1), ("v_scale", kv.v_scale, blocks, 1)]
+    for name, t, shape, size in arrays:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor: got {type(t).__name__}")
+        if t.shape != shape or t.element_size() != size or t.get_device() != idx or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {list(shape)} of {size}-byte elements on "
+                             f"cuda:{idx}: got {t.dtype} {list(t.shape)} on {t.device}")
+
+
 def _need_out(out, shape, idx):
     if out is not None:
         if not isinstance(out, torch.Tensor) or out.dtype not in (_F32, _BF16):
@@ -498,16 +519,15 @@ def _need_out(out, shape, idx):
 
 
 def _need_workspace(ws, idx):
-    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != idx or ws.nbytes < 256):
-        raise ValueError(f"workspace must be a tensor of at least 256 bytes on cuda:{idx}")
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != idx or
+                           not ws.is_contiguous() or ws.nbytes < 256):
+        raise ValueError(f"workspace must be a contiguous tensor of at least 256 bytes on cuda:{idx}")
 
 
 def _elsewhere(idx, stream):
     """A context for a call that the extension declined although its tensors
     are as they should be: its stream or its device is not the current one
     (outputs are then allocated there too)."""
-    if idx < 0:
-        raise ValueError("the KV cache must be on a CUDA device")
     if stream is not None:
         if stream.device.index != idx:
             raise ValueError(f"stream is on {stream.device}, the KV cache on cuda:{idx}")
@@ -552,6 +572,7 @@ def rope_append(kv: KvCache, q, k, v, positions, slot_mapping, inv_freq, *, inte
     if q_out is not None:
         _need(q_out, "q_out", _BF16, (T, Hq, D), idx, True)
     _need_workspace(workspace, idx)
+    _need_cache(kv, idx)
     with _elsewhere(idx, stream):
         return rope_append(kv, q, k, v, positions, slot_mapping, inv_freq, interleaved=interleaved,
                            attn_factor=attn_factor, q_norm=q_norm, k_norm=k_norm, eps=eps,
@@ -610,6 +631,7 @@ def decode_scored(kv: KvCache, q, block_tables, seq_lens, softmax_scale, *, scor
     _need_out(out, (B, 1, Hq, D), idx)
     sc._need(Hq, B, B, idx)
     _need_workspace(workspace, idx)
+    _need_cache(kv, idx)
     with _elsewhere(idx, stream):
         return decode_scored(kv, q, block_tables, seq_lens, softmax_scale, score=score, out=out,
                              out_fp32=out_fp32, return_lse=return_lse, max_seq_len=max_seq_len,
@@ -647,6 +669,7 @@ def prefill(kv: KvCache, q, q_starts, block_tables, seq_lens, softmax_scale, *, 
     _need_out(out, (T, Hq, D), idx)
     sc._need(Hq, T, B, idx)
     _need_workspace(workspace, idx)
+    _need_cache(kv, idx)
     with _elsewhere(idx, stream):
         return prefill(kv, q, q_starts, block_tables, seq_lens, softmax_scale, score=score, out=out,
                        out_fp32=out_fp32, return_lse=return_lse, max_seq_len=max_seq_len,
