@@ -34,12 +34,14 @@ int prefill_splits(int T, int B, int Hkv, int G, int D, int max_seq_len) {
 // Where there may be more row tiles than SMs, the tiles of a last round that
 // fills at most half of them are split over the others (768 tiles of 224 to
 // 256 key tiles, six rounds of which the last had eight tiles: 2.33 -> 1.99
-// ms; half as long, FP8: 619 -> 579 us).  Not where the tiles differ much (chunks of over half the keys they
-// see: the longest first already even out) or are short (below 64 key tiles the pieces and their join cost what they save).
+// ms; half as long, FP8: 619 -> 579 us).  Not where the tiles differ much
+// (chunks of over half the keys they see: the longest first already even out),
+// are short (below 64 key tiles the pieces and their join cost what they save),
+// or come from more than 32 sequences (whose tiles are not counted).
 int prefill_tail(int T, int B, int Hkv, int G, int D, int max_seq_len, int window) {
   long long span = max_seq_len;   // keys a row sees at most
   if (window > 0 && window < span) span = window;
-  if (span < 64 * 128 || 2LL * T > span * B) return 0;
+  if (span < 64 * 128 || 2LL * T > span * B || B > 32) return 0;
   return most_tiles(T, B, Hkv, G, D) > kSms ? kSms : 0;
 }
 // partial rows of such a round

@@ -50,38 +50,73 @@ __device__ __forceinline__ Round last_round(int total, int sms) {
   return r;
 }
 
+// More than 32 sequences: sequence b's tiles are given the places from
+// q_starts[b] * G / rows + b on, of which there are enough (and at most one too
+// many), so that a search finds a place's sequence (in two loads for 1,024
+// sequences, three for 32,768) without the counts of those before it.  CTA 0
+// looks at all starts.
+__device__ __forceinline__ Share search_share(const PrefillParams &p, int index, int rows_per_tile) {
+  const int lane = threadIdx.x & 31, Hkv = p.kv.hkv;
+  Share r = {-1, 0, 0, 0, 0, 0, 0, 1, -1};
+  auto start = [&](int b) { return min(max(__ldg(p.q_starts + b), 0), p.T); };
+  auto place = [&](int b) { return (int)((long long)start(b) * p.G / rows_per_tile) + b; };
+  if (index == 0) {
+    bool bad = false;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      const int s0 = __ldg(p.q_starts + b), s1 = __ldg(p.q_starts + b + 1);
+      bad = bad || s0 < 0 || s1 < s0 || s1 > p.T;
+    }
+    if (bad) flag(p.hdr, PA_ERRF_BAD_Q_START);
+  }
+  const int total = place(p.B);   // at most rows / rows_per_tile + B
+  const int t = index / p.splits, at = total - 1 - t / Hkv;
+  r.piece = index % p.splits;
+  r.pieces = p.splits;
+  r.kvh = t % Hkv;
+  if (at < 0) return r;
+  int lo = 0, hi = p.B;   // the last sequence of [lo, hi) that starts at or before `at`
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, b < hi && place(b) <= at);
+    lo += (31 - __clz((int)(le | 1u))) * step;
+    hi = min(hi, lo + step);
+  }
+  const int first = at - place(lo), s0 = start(lo), len = max(start(lo + 1) - s0, 0);
+  if (first < 0 || (long long)first * rows_per_tile >= (long long)len * p.G) return r;
+  r.b = lo;
+  r.first = first;
+  r.start = s0;
+  r.len = len;
+  r.n = __ldg(p.seq_lens + lo);
+  return r;
+}
+
 // every thread of a warp gets the answer; `index`: of the CTA, or, in the join,
 // of a tail tile (join = true)
 __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, int rows_per_tile, bool join) {
+  if (p.B > 32) return search_share(p, index, rows_per_tile);   // (there is no tail then)
   const int lane = threadIdx.x & 31, Hkv = p.kv.hkv;
-  uint32_t err = 0;
-  int start = 0, len = 0, keys = 0, inc = 0, n = 0;
-  auto scan = [&](int b0) {   // this lane's sequence, and the tiles up to it (inclusive)
-    const int b = b0 + lane;
-    start = len = keys = 0;
-    if (b < p.B) {
-      const int s0 = __ldg(p.q_starts + b), s1 = __ldg(p.q_starts + b + 1);
-      keys = __ldg(p.seq_lens + b);
-      start = min(max(s0, 0), p.T);
-      const int end = min(max(s1, start), p.T);
-      if (start != s0 || end != s1) err = 1;
-      len = end - start;
-    }
-    n = (int)(((long long)len * p.G + rows_per_tile - 1) / rows_per_tile);
-    inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-  };
-  Share r = {-1, 0, 0, 0, 0, 0, 0, 1, -1};
-  int tiles = 0;   // at most rows / rows_per_tile + B: the host bounds them by 2^30
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    scan(b0);
-    tiles += __shfl_sync(0xffffffffu, inc, 31);
+  // this lane's sequence, and the tiles up to it (inclusive)
+  int start = 0, len = 0, keys = 0;
+  if (lane < p.B) {
+    const int s0 = __ldg(p.q_starts + lane), s1 = __ldg(p.q_starts + lane + 1);
+    keys = __ldg(p.seq_lens + lane);
+    start = min(max(s0, 0), p.T);
+    const int end = min(max(s1, start), p.T);
+    if ((start != s0 || end != s1) && !join) flag(p.hdr, PA_ERRF_BAD_Q_START);
+    len = end - start;
   }
-  if (err && !join) flag(p.hdr, PA_ERRF_BAD_Q_START);
+  const int n = (int)(((long long)len * p.G + rows_per_tile - 1) / rows_per_tile);
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  Share r = {-1, 0, 0, 0, 0, 0, 0, 1, -1};
+  // at most rows / rows_per_tile + B: the host bounds them by 2^30 (descending
+  // starts count rows more than once, each sequence at most T)
+  const int tiles = __shfl_sync(0xffffffffu, inc, 31);
   const int total = tiles * Hkv;
   const Round last = last_round(total, p.tail);
   int t = index;   // tile and kv head
@@ -104,21 +139,12 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
   if (t >= total) return r;
   r.kvh = t % Hkv;
   const int tile = tiles - 1 - t / Hkv;
-  int before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    if (p.B > 32) scan(b0);
-    const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > tile);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      r.b = b0 + l;
-      r.first = tile - (before + __shfl_sync(0xffffffffu, inc - n, l));
-      r.start = __shfl_sync(0xffffffffu, start, l);
-      r.len = __shfl_sync(0xffffffffu, len, l);
-      r.n = __shfl_sync(0xffffffffu, keys, l);
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, inc, 31);
-  }
+  const int l = __ffs(__ballot_sync(0xffffffffu, inc > tile)) - 1;
+  r.b = l;
+  r.first = tile - __shfl_sync(0xffffffffu, inc - n, l);
+  r.start = __shfl_sync(0xffffffffu, start, l);
+  r.len = __shfl_sync(0xffffffffu, len, l);
+  r.n = __shfl_sync(0xffffffffu, keys, l);
   return r;
 }
 
