@@ -113,6 +113,10 @@ int tc_supported(int dtype, int D, int R) {
          (D == 128 || D == 256) && R >= 1 &&
          R <= 8 && (R == 1 || R % 2 == 0);
 }
+// the scored variants are built for every group size
+int scored_supported(int dtype, int D, int R) {
+  return R >= 1 && R <= kMaxG && tc_supported(dtype, D, 1);
+}
 
 cudaError_t launch_verify_int8(const AttnParams &p, int grid, cudaStream_t s);
 cudaError_t launch_verify_nvfp4(const AttnParams &p, int grid, cudaStream_t s);
@@ -315,8 +319,12 @@ ScoreView score_view(const pa_score *sc, float softmax_scale) {
   ScoreView v;
   std::memset(&v, 0, sizeof v);
   if (!sc) return v;
-  if (sc->softcap > 0.f) {
+  // (a cap above 1e18 changes no score that fp32 softmax could tell apart, and
+  // its log2 units would leave fp32's range; under a tiny one every score but 0
+  // is at the cap, and the factor must stay finite for that 0)
+  if (sc->softcap > 0.f && sc->softcap <= 1e18f) {
     v.cap_in = 2.0f * 1.4426950408889634f * softmax_scale / sc->softcap;
+    v.cap_in = std::min(1e30f, std::max(-1e30f, v.cap_in));
     v.cap_log2 = sc->softcap * 1.4426950408889634f;
   }
   v.slopes = sc->alibi_slopes;
@@ -341,7 +349,7 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   if (test_flags & ~PA_TEST_EXPIRE_WAIT) return PA_ERR_INVALID_ARG;
   // scored decode is built into the tensor-core decode kernel
   if (sc && (kernel == 1 || kernel == 3 || kernel == 4 || test_flags ||
-             !tc_supported(kv->dtype, kv->head_dim, p->num_q_heads / kv->num_kv_heads)))
+             !scored_supported(kv->dtype, kv->head_dim, p->num_q_heads / kv->num_kv_heads)))
     return PA_ERR_UNSUPPORTED;
   if (p->batch == 0) return PA_OK;
   const int G = p->num_q_heads / kv->num_kv_heads;
@@ -353,7 +361,7 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   const int Q = p->q_len;
   bool use_tc, dense = false, umma = false, single = false;
   if (kernel == 5) {
-    if (verify || Q != 1 || !tc_supported(kv->dtype, kv->head_dim, G) || extra_err)
+    if (verify || Q != 1 || (!sc && !tc_supported(kv->dtype, kv->head_dim, G)) || extra_err)
       return PA_ERR_UNSUPPORTED;
     use_tc = single = true;
   } else if (kernel == 4) {
@@ -361,14 +369,14 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
       return PA_ERR_UNSUPPORTED;
     use_tc = dense = umma = true;
   } else if (kernel == 2 || kernel == 3) {
-    if (!tc_supported(kv->dtype, kv->head_dim, G)) return PA_ERR_UNSUPPORTED;
+    if (!sc && !tc_supported(kv->dtype, kv->head_dim, G)) return PA_ERR_UNSUPPORTED;
     use_tc = true;
     dense = kernel == 2 && dense_supported(kv->dtype, kv->head_dim, Q, G);
   } else if (kernel == 1) {
     if (!simt_supported(kv->dtype, kv->head_dim, G)) return PA_ERR_UNSUPPORTED;
     use_tc = false;
   } else {
-    use_tc = tc_supported(kv->dtype, kv->head_dim, G);
+    use_tc = sc || tc_supported(kv->dtype, kv->head_dim, G);
     if (!use_tc && !simt_supported(kv->dtype, kv->head_dim, G)) return PA_ERR_UNSUPPORTED;
     dense = use_tc && dense_supported(kv->dtype, kv->head_dim, Q, G);
     // NVFP4 / FP8 verify: the tcgen05 kernel (4 x 64K keys, 8 queries: NVFP4
@@ -921,10 +929,9 @@ int pa_rope_append(const pa_kv_cache *kv, const pa_rope *r, void *ws, pa_stream_
         !aligned16(r->q_norm) || !aligned16(r->k_norm) || !aligned4(r->positions) ||
         !aligned4(r->inv_freq) || reinterpret_cast<uintptr_t>(r->slot_mapping) % 8 != 0)
       return PA_ERR_INVALID_ARG;
-    if (r->q_stride % 8 || r->k_stride % 8 || r->v_stride % 8 || r->q_out_stride % 8)
-      return PA_ERR_INVALID_ARG;
-    if (r->num_tokens > 1 && (r->q_out_stride < q_row || r->q_stride < 0 || r->k_stride < 0 ||
-                              r->v_stride < 0))
+    if (r->num_tokens > 1 &&
+        (r->q_stride % 8 || r->k_stride % 8 || r->v_stride % 8 || r->q_out_stride % 8 ||
+         r->q_out_stride < q_row || r->q_stride < 0 || r->k_stride < 0 || r->v_stride < 0))
       return PA_ERR_INVALID_ARG;
   }
   uint32_t *hdr = static_cast<uint32_t *>(ws);

@@ -608,9 +608,12 @@ __global__ void __launch_bounds__(kThreads, 3)
         sc[1] = sacc[1] * f0;
         sc[2] = sacc[2] * f1;
         sc[3] = sacc[3] * f1;
-        if (cap) {
+        if (cap && p.sc.cap_log2 <= kBigCap) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) sc[k] = capped(sc[k], p.sc.cap_log2);
+        } else if (cap) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[k] = capped_big(sc[k], p.sc.cap_log2);
         }
         const float d0 = (float)(len - 1 - tok0 - r), d1 = d0 - 8.f;   // distance to the query
         sc[0] = v0 ? fmaf(-slope[0], d0, sc[0]) : kNegInf;
@@ -982,6 +985,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       store4(row_of(h), d, v);
     }
     cluster_sync_all();   // no CTA leaves while another still reads its partial
+    if constexpr (SC) griddep_wait();   // nor before the header is cleared
   }
 }
 
@@ -1044,6 +1048,10 @@ cudaError_t launch_cluster_dtype(const AttnParams &p, int P, cudaStream_t s) {
   PA_TC_CASE(128, 1) PA_TC_CASE(128, 2) PA_TC_CASE(128, 4) PA_TC_CASE(128, 6)
   PA_TC_CASE(128, 8) PA_TC_CASE(256, 1) PA_TC_CASE(256, 2) PA_TC_CASE(256, 4)
   PA_TC_CASE(256, 6) PA_TC_CASE(256, 8)
+  if constexpr (SC) {
+    PA_TC_CASE(128, 3) PA_TC_CASE(128, 5) PA_TC_CASE(128, 7)
+    PA_TC_CASE(256, 3) PA_TC_CASE(256, 5) PA_TC_CASE(256, 7)
+  }
 #undef PA_TC_CASE
   return cudaErrorInvalidValue;
 }
@@ -1067,6 +1075,10 @@ int occupancy_dtype(int D, int R) {
   PA_TC_CASE(128, 1) PA_TC_CASE(128, 2) PA_TC_CASE(128, 4) PA_TC_CASE(128, 6)
   PA_TC_CASE(128, 8) PA_TC_CASE(256, 1) PA_TC_CASE(256, 2) PA_TC_CASE(256, 4)
   PA_TC_CASE(256, 6) PA_TC_CASE(256, 8)
+  if constexpr (SC) {
+    PA_TC_CASE(128, 3) PA_TC_CASE(128, 5) PA_TC_CASE(128, 7)
+    PA_TC_CASE(256, 3) PA_TC_CASE(256, 5) PA_TC_CASE(256, 7)
+  }
 #undef PA_TC_CASE
   return 0;
 }
@@ -1079,6 +1091,10 @@ cudaError_t launch_dtype(const AttnParams &p, int grid, cudaStream_t s) {
   PA_TC_CASE(128, 1) PA_TC_CASE(128, 2) PA_TC_CASE(128, 4) PA_TC_CASE(128, 6)
   PA_TC_CASE(128, 8) PA_TC_CASE(256, 1) PA_TC_CASE(256, 2) PA_TC_CASE(256, 4)
   PA_TC_CASE(256, 6) PA_TC_CASE(256, 8)
+  if constexpr (SC) {
+    PA_TC_CASE(128, 3) PA_TC_CASE(128, 5) PA_TC_CASE(128, 7)
+    PA_TC_CASE(256, 3) PA_TC_CASE(256, 5) PA_TC_CASE(256, 7)
+  }
 #undef PA_TC_CASE
   return cudaErrorInvalidValue;
 }

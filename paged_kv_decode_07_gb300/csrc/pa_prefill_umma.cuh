@@ -580,6 +580,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   // takes the other polynomial)
   const TanhSmall small = tanh_small_coefs(fu, p.sc.cap_log2);
   const float small_max = fu >= 0x1p-16f ? kSmallU : 0.f;
+  const bool big_cap = p.sc.cap_log2 > kBigCap;
   float *const wsc = reinterpret_cast<float *>(smem + Gm::OFF_SC) + (tid >> 5) * 2 * kKeys;
 
   // the tile's page ids, one page in each of lanes 0-7 (again in 8-15, ..)
@@ -661,7 +662,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
         }
         if constexpr (CAP) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = capped(x[i], p.sc.cap_log2);
+          for (int i = 0; i < 16; ++i) x[i] = FIX || !big_cap ? capped(x[i], p.sc.cap_log2) : capped_big(x[i], p.sc.cap_log2);
         }
         if constexpr (BIAS) {
           const float far = (float)(r_pos - k0 - ch);
@@ -1009,7 +1010,10 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   Work w;
   griddep_launch();   // (only a join follows, which waits for this grid)
   const Share to = find_share(p, blockIdx.x, Gm::ROWS, false);
-  if (to.b < 0) return;
+  if (to.b < 0) {
+    griddep_wait();   // the grid does not end before its header is cleared
+    return;
+  }
   if (warp == Gm::SMW) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
@@ -1155,6 +1159,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   if (warp == Gm::SMW) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+    griddep_wait();   // the grid does not end before its header is cleared
   }
 }
 

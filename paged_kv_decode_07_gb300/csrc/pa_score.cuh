@@ -46,4 +46,15 @@ __device__ __forceinline__ float capped(float y, float cap_log2) {
   return fmaf(-2.f * cap_log2, score_rcp(1.f + score_ex2(y)), cap_log2);
 }
 
+// Under a cap above some 180 that error reaches 2^-13 of a score unit, so there
+// scores below 0.4 cap come from a polynomial instead (see TanhSmall in
+// pa_prefill_umma.cuh), whose error is relative to the score.
+constexpr float kBigCap = 256.f;   // times log2 e
+__device__ __forceinline__ float capped_big(float y, float cap_log2) {
+  const float u = y * 0.34657359027997264f, v = u * u;
+  if (fabsf(u) > 0.4f) return capped(y, cap_log2);
+  const float h = fmaf(v, fmaf(v, fmaf(v, -0.0475493483f, 0.132708743f), -0.333313555f), 0.999999881f);
+  return cap_log2 * (u * h);
+}
+
 }  // namespace pa

@@ -196,6 +196,53 @@ def test_scores_far_beyond_the_cap():
         assert ((out.double() - ref).abs() <= (2.0 ** -8 + 2 * (400 * 2.0 ** -18 + 2.0 ** -14)) * big).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("cap", [1e6, 1e15, 1e30])
+def test_caps_far_above_the_scores_leave_them(fmt, cap):
+    """cap tanh(s / cap) differs from s by s^3 / (3 cap^2): below 1e-5 for |s| < 300."""
+    for bias in (None, slopes(4)):
+        kv, q, starts, tables, sl = build(fmt, [70, 200], [400, 200], 2, 2, 128)
+        sc = pa.Score(softcap=cap, slopes=bias)
+        out, ws = pa.prefill(kv, q, starts, tables, sl, 0.1, score=sc, out_fp32=True, max_seq_len=400)
+        ref, _, bound = S.reference(vals(kv), q, [70, 200], [400, 200], tables, 0.1, slopes=bias, eps_p=EPS_P[fmt],
+                                    v_unit=kv.v_scale if fmt == "int8" else None)
+        S.within(out, ref, bound + 2e-5 * vals(kv)[1].abs().max())
+
+
+def test_tiny_cap_averages_the_keys():
+    """Every score is at most the cap: equal weights, also for a product of 0."""
+    for fmt in ("bf16", "fp8"):
+        kv, q, starts, tables, sl = build(fmt, [70, 3], [400, 200], 2, 2, 128)
+        q[5, 1] = 0
+        out, ws = pa.prefill(kv, q, starts, tables, sl, 0.1, score=pa.Score(softcap=1e-40), out_fp32=True, max_seq_len=400)
+        ref, _, bound = S.reference(vals(kv), q * 0, [70, 3], [400, 200], tables, 0.1, eps_p=EPS_P[fmt])
+        S.within(out, ref, bound)
+
+
+@pytest.mark.parametrize("hkv,G,B,most", [(1, 8, 33, 150), (2, 3, 300, 40), (1, 1, 1100, 3)])
+def test_many_sequences(hkv, G, B, most):
+    """More than 32: chunks of 0 to `most` tokens over 0 to 60 earlier keys; rows
+    before the first and behind the last sequence stay as they were."""
+    r = torch.Generator().manual_seed(B)
+    new = [int(x) for x in torch.randint(0, most + 1, (B,), generator=r)]
+    lens = [m + int(x) for m, x in zip(new, torch.randint(0, 61, (B,), generator=r))]
+    kv, q, starts, tables, sl = build("bf16", new, lens, hkv, G, 128)
+    T = sum(new)
+    qq = torch.cat((q[:300], q, q[:3]))
+    k = len(qq) - T - 3   # rows before the first
+    out = torch.full((len(qq), hkv * G, 128), 7.0, device=DEV)
+    out, lse, ws = pa.prefill(kv, qq, starts + k, tables, sl, 0.1, out=out, return_lse=True, max_seq_len=max(lens))
+    assert pa.read_error(ws) == 0
+    ref, rl, bound = S.reference(vals(kv), q, new, lens, tables, 0.1)
+    S.within(out[k:k + T], ref, bound)
+    S.lse_within(lse[k:k + T], rl)
+    assert (out[:k] == 7.0).all() and (out[k + T:] == 7.0).all()
+    wild = starts.clone()
+    wild[-2] = T + 5
+    _, ws = pa.prefill(kv, q, wild, tables, sl, 0.1, max_seq_len=max(lens))
+    assert pa.read_error(ws) & pa.PA_ERRF_BAD_Q_START
+
+
 def test_bad_block_ids_lengths_and_starts_are_flagged():
     kv, q, starts, tables, sl = build("bf16", [20, 30], [120, 64], 2, 2, 128)
     bad = tables.clone()

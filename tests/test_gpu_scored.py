@@ -72,10 +72,43 @@ def test_single_launch_decode(fmt, opt):
     check(fmt, lens, 1, 6, 256, kernel=5, **options(opt, lens, 6))
 
 
-@pytest.mark.parametrize("G", [1, 2, 4, 6, 8])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
 def test_group_sizes(G):
     check("bf16", [700, 40], 3, G, 256, softcap=20.0, slopes=torch.linspace(0.01, 0.05, 3 * G, device=DEV))
     check("nvfp4", [2700, 40], 1, G, 128, softcap=20.0, slopes=torch.linspace(0.01, 0.05, G, device=DEV))
+
+
+@pytest.mark.parametrize("fmt,G,D", [("int8", 3, 256), ("fp8", 5, 128), ("nvfp4", 7, 256), ("bf16", 5, 256)])
+def test_odd_groups_split_and_single_launch(fmt, G, D):
+    o = dict(softcap=20.0, slopes=torch.linspace(0.01, 0.05, 2 * G, device=DEV), window=1800)
+    check(fmt, [2700, 40, 1], 2, G, D, **o)
+    check(fmt, [700, 40, 1], 2, G, D, kernel=5, **o)
+
+
+@pytest.mark.parametrize("cap", [300.0, 1e6, 1e15, 1e30])
+@pytest.mark.parametrize("kernel", [2, 5])
+def test_caps_far_above_the_scores_leave_them(cap, kernel):
+    """|s| < 15 here (unit queries, keys of 128 dims: norms of 11.3 +- 0.7):
+    cap tanh(s / cap) differs from s by s^3 / (3 cap^2), 1.3e-2 at cap = 300 (bounded
+    as a score's error, twice that of A) and below 2e-9 for the others."""
+    kv, q, tables, sl = build("bf16", [700, 40], 2, 4, 128)
+    q = torch.nn.functional.normalize(q.float(), dim=-1).bfloat16()
+    out, _ = pa.decode_scored(kv, q, tables, sl, 1.0, score=pa.Score(softcap=cap), out_fp32=True, max_seq_len=700,
+                              kernel=kernel)
+    ref, _, bound = S.reference(vals(kv), q[:, 0], [1, 1], [700, 40], tables, 1.0, eps_p=EPS_P["bf16"])
+    if cap < 1e4:
+        A = vals(kv)[1].abs().max()
+        bound = bound + 2 * 1.3e-2 * A
+    S.within(out[:, 0], ref, bound)
+
+
+def test_tiny_cap_averages_the_keys():
+    """Every score is at most the cap: equal weights, also for a product of 0."""
+    kv, q, tables, sl = build("bf16", [300, 40], 2, 4, 128)
+    q[0, 0, 1] = 0
+    out, _ = pa.decode_scored(kv, q, tables, sl, 0.1, score=pa.Score(softcap=1e-40), out_fp32=True, max_seq_len=300)
+    ref, _, bound = S.reference(vals(kv), q[:, 0] * 0, [1, 1], [300, 40], tables, 0.1, eps_p=EPS_P["bf16"])
+    S.within(out[:, 0], ref, bound)
 
 
 @pytest.mark.parametrize("fmt", FMTS)

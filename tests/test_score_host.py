@@ -102,7 +102,7 @@ def test_score_refusals(L, score):
 
 
 @pytest.mark.parametrize("kernel,G,status", [(1, 6, pa.PA_ERR_UNSUPPORTED), (3, 6, pa.PA_ERR_UNSUPPORTED),
-                                             (4, 6, pa.PA_ERR_UNSUPPORTED), (0, 3, pa.PA_ERR_UNSUPPORTED),
+                                             (4, 6, pa.PA_ERR_UNSUPPORTED), (0, 9, pa.PA_ERR_UNSUPPORTED),
                                              (9, 6, pa.PA_ERR_INVALID_ARG)])
 def test_decode_scored_refusals(L, kernel, G, status):
     p = pa._Problem(2, 4 * G, 1, FAKE, FAKE, 8, FAKE, 100, 0.06, FAKE, 0, None)
