@@ -981,7 +981,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   }
   named_sync(pair, 64);   // both halves of the rows are there
   uint4 *const dst = static_cast<uint4 *>(partial ? static_cast<void *>(p.part_o) : p.out);
-#pragma unroll 1
+#pragma unroll 4
   for (int i = lane; i < 16 * per_row; i += 32) {   // 16 of the pair's 32 rows each
     const int q = hf * 16 + i / per_row, k = i % per_row;
     const size_t to = __shfl_sync(0xffffffffu, r_out, q);
@@ -1056,16 +1056,12 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     tok = tok0 + q;
     head = w.kvh * G + x - q * G;
   };
-  // ---- the queries are requested, the rows' key ranges found, and the copies
-  // may begin while the queries are on their way
-  constexpr int CH = D / 8, NT = Gm::SMW * 32, NQ = Gm::ROWS * CH / NT;
-  uint4 qv[NQ];
+  // ---- the rows' key ranges, and then the copies and the queries
   int r_lo = 0, r_hi = 0, r_pos = 0;
   bool live = false;
   size_t r_out = 0;
   float slope = 0.f;
   if (warp < Gm::SMW) {
-    // (what the ranges need is requested before the queries: they would queue up)
     const int r = (tid >> 8) * 128 + (tid & 127);
     live = r < w.nrows;
     int tok, head;
@@ -1073,15 +1069,6 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     const int first = p.sc.first_key ? __ldg(p.sc.first_key + w.start + tok) : 0;
     const int prefix = p.sc.prefix ? __ldg(p.sc.prefix + w.b) : 0;
     if (p.sc.slopes) slope = __ldg(p.sc.slopes + head) * 1.4426950408889634f;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH;
-      int qt, qh;
-      split_row(q, qt, qh);
-      qv[i] = make_uint4(0, 0, 0, 0);
-      if (q < w.nrows)
-        qv[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.start + qt) * p.Hq + qh) * D) + k);
-    }
     r_pos = n - w.len + tok;
     if (live) {
       const KeyRange kr = key_range(p.sc, r_pos, n, first, prefix);
@@ -1121,6 +1108,17 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     w.ntiles = t0 + min(t1 - t0, (to.piece + 1) * per) - w.kt0;
   }
   if (warp < Gm::SMW) {
+    constexpr int CH = D / 8, NT = Gm::SMW * 32, NQ = Gm::ROWS * CH / NT;
+    uint4 qv[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH;
+      int qt, qh;
+      split_row(q, qt, qh);
+      qv[i] = make_uint4(0, 0, 0, 0);
+      if (q < w.nrows)
+        qv[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.start + qt) * p.Hq + qh) * D) + k);
+    }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int q = (i * NT + tid) / CH, k = (i * NT + tid) % CH, r2 = q & 127;
