@@ -952,8 +952,8 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     wait_p(&c.odone[rt ^ 1], 0, c, p.hdr);
     __syncwarp();
   }
-  const int per_row = wide ? D / 4 : D / 8;   // pieces
-  auto piece_at = [&](int r, int k) { return smem + ((size_t)r * per_row + (k ^ (r & 7))) * 16; };
+  const int sh = (D == 128 ? 4 : 5) + (wide ? 1 : 0), per_row = 1 << sh;   // pieces
+  auto piece_at = [&](int r, int k) { return smem + (((r << sh) + (k ^ (r & 7))) << 4); };
 #pragma unroll 1
   for (int ch = 0; ch < Gm::NO; ch += 16) {
     float o[16];
@@ -983,10 +983,10 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   uint4 *const dst = static_cast<uint4 *>(partial ? static_cast<void *>(p.part_o) : p.out);
 #pragma unroll 4
   for (int i = lane; i < 16 * per_row; i += 32) {   // 16 of the pair's 32 rows each
-    const int q = hf * 16 + i / per_row, k = i % per_row;
+    const int q = hf * 16 + (i >> sh), k = i & (per_row - 1);
     const size_t to = __shfl_sync(0xffffffffu, r_out, q);
     if (__shfl_sync(0xffffffffu, (int)live, q))
-      dst[to * per_row + k] = *reinterpret_cast<const uint4 *>(piece_at((row & ~31) + q, k));
+      dst[(to << sh) + k] = *reinterpret_cast<const uint4 *>(piece_at((row & ~31) + q, k));
   }
   if (live && hf == 0) {
     if (partial)
