@@ -391,7 +391,12 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
   constexpr bool FP4 = DT == PA_KV_NVFP4;
   constexpr int IT = FP4 ? 2 : 4, LPR = FP4 ? 4 : 8, RPI = 128 / LPR;   // loads per half unit
   constexpr int ROW = FP4 ? D / 2 : D;
-  const int sub = t % LPR, r0 = t / LPR;
+  // lane: place in the row and row.  Eight neighbouring lanes write to one chunk,
+  // pieces 2 (or 4) apart of 2 (or 4) neighbouring rows, which the swizzle puts
+  // into different banks (a row's lanes side by side met in pairs: 128 KB of
+  // stores a tile then took as long as its MMAs)
+  const int sub = FP4 ? (t & 1) | ((t >> 3) & 1) << 1 : (t & 3) | ((t >> 3) & 1) << 2;
+  const int r0 = FP4 ? ((t >> 1) & 3) | (t >> 4) << 2 : ((t >> 2) & 1) | (t >> 4) << 1;
   const uint32_t ubase = smem_u32(smem + Gm::OFF_U);
   uint4 code[IT], next[IT];
   uint32_t sc[FP4 ? IT : 1], next_sc[FP4 ? IT : 1];
