@@ -639,7 +639,8 @@ struct PrefillLayout {
 int check_prefill_sizes(const pa_kv_cache *kv, const pa_prefill_problem *p) {
   if (!p || p->batch < 0 || p->num_tokens < 0 || p->max_seq_len < 0) return PA_ERR_INVALID_ARG;
   if (p->num_q_heads < 1 || p->num_q_heads % kv->num_kv_heads) return PA_ERR_INVALID_ARG;
-  if (p->num_q_heads / kv->num_kv_heads > kMaxG) return PA_ERR_UNSUPPORTED;
+  // (a page of keys is addressed in 32 bits)
+  if (p->num_q_heads / kv->num_kv_heads > kMaxG || kv->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   if (!std::isfinite(p->softmax_scale)) return PA_ERR_INVALID_ARG;
   if (p->batch > 0 && (p->block_table_stride < 1 || p->block_table_stride > (1 << 26)))
     return PA_ERR_INVALID_ARG;

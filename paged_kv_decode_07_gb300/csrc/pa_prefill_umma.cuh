@@ -401,27 +401,39 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
   uint4 code[IT], next[IT];
   uint32_t sc[FP4 ? IT : 1], next_sc[FP4 ? IT : 1];
   int id[2 * IT], id_next[2 * IT];
+  // bytes between pages, and this thread's place in one
+  const uint32_t page = (uint32_t)p.kv.hkv * kBlock * ROW, spage = (uint32_t)p.kv.hkv * kBlock * (D / 16);
+  const uint32_t row0 = (uint32_t)w.kvh * kBlock + (r0 & (kBlock - 1));
+  const size_t off = (size_t)row0 * ROW + h * (ROW * 128 / D) + sub * 16;
+  const size_t soff = (size_t)row0 * (D / 16) + h * 8 + sub * 2;
+  const uint8_t *const kbase = static_cast<const uint8_t *>(p.kv.k) + off;
+  const uint8_t *const vbase = static_cast<const uint8_t *>(p.kv.v) + off;
+  const uint8_t *const ksbase = static_cast<const uint8_t *>(p.kv.ks) + soff;
+  const uint8_t *const vsbase = static_cast<const uint8_t *>(p.kv.vs) + soff;
   auto ids = [&](const Order<D> &o, int (&d)[2 * IT]) {   // -1: nothing of this thread's row is read
     const int k0 = (w.kt0 + o.j) * kKeys;
+    const int *const at = w.trow + (k0 + r0) / kBlock;
+    if (!o.done() && k0 >= w.see_lo && k0 + kKeys <= w.see_hi) {
 #pragma unroll
-    for (int i = 0; i < 2 * IT; ++i) {
-      const int key = k0 + i * RPI + r0;
-      d[i] = !o.done() && key >= w.see_lo && key < w.see_hi ? __ldg(w.trow + key / kBlock) : -1;
+      for (int i = 0; i < 2 * IT; ++i) d[i] = __ldg(at + i * (RPI / kBlock));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * IT; ++i) {
+        const int key = k0 + i * RPI + r0;
+        d[i] = !o.done() && key >= w.see_lo && key < w.see_hi ? __ldg(at + i * (RPI / kBlock)) : -1;
+      }
     }
   };
   auto load = [&](bool is_v, int half) {
-    const uint8_t *base = static_cast<const uint8_t *>(is_v ? p.kv.v : p.kv.k);
-    const uint8_t *sbase = static_cast<const uint8_t *>(is_v ? p.kv.vs : p.kv.ks);
+    const uint8_t *const base = is_v ? vbase : kbase, *const sbase = is_v ? vsbase : ksbase;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       next[i] = make_uint4(0, 0, 0, 0);
       if constexpr (FP4) next_sc[i] = 0;
-      const int pg = id[half * IT + i];
-      if ((uint32_t)pg < (uint32_t)p.kv.num_blocks) {
-        const size_t row = ((size_t)pg * p.kv.hkv + w.kvh) * kBlock + ((i * RPI + r0) & (kBlock - 1));
-        next[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ROW + h * (ROW * 128 / D)) + sub);
-        if constexpr (FP4)
-          next_sc[i] = __ldg(reinterpret_cast<const uint16_t *>(sbase + row * (D / 16) + h * 8) + sub);
+      const uint32_t pg = (uint32_t)id[half * IT + i];
+      if (pg < (uint32_t)p.kv.num_blocks) {
+        next[i] = __ldg(reinterpret_cast<const uint4 *>(base + (uint64_t)pg * page));
+        if constexpr (FP4) next_sc[i] = __ldg(reinterpret_cast<const uint16_t *>(sbase + (uint64_t)pg * spage));
       }
     }
   };
@@ -787,10 +799,12 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 #pragma unroll
           for (int i = 0; i < NC; i += 4) {
             const float4 k = *reinterpret_cast<const float4 *>(ksc + i);
-            s[i] *= k.x;
-            s[i + 1] *= k.y;
-            s[i + 2] *= k.z;
-            s[i + 3] *= k.w;
+            const float2 a = fmul2(make_float2(s[i], s[i + 1]), make_float2(k.x, k.y));
+            const float2 b = fmul2(make_float2(s[i + 2], s[i + 3]), make_float2(k.z, k.w));
+            s[i] = a.x;
+            s[i + 1] = a.y;
+            s[i + 2] = b.x;
+            s[i + 3] = b.y;
           }
         }
       }

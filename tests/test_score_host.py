@@ -89,6 +89,10 @@ def test_prefill_refusals(L, kw, status):
     assert prefill(L, **kw) == status
 
 
+def test_prefill_refuses_too_many_heads(L):
+    assert prefill(L, kv=kv_struct(hkv=65536), num_q_heads=65536) == pa.PA_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("score", [
     pa._Score(-1.0, 0, None, None, None), pa._Score(math.nan, 0, None, None, None),
     pa._Score(math.inf, 0, None, None, None), pa._Score(0.0, -1, None, None, None),
