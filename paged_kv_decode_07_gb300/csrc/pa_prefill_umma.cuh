@@ -86,8 +86,9 @@ struct PGeo {
 
 struct PCtl {
   uint64_t full[5], empty[5];   // units
-  uint64_t sfull[2];            // S ready
-  uint64_t pready[2];           // P written
+  // S ready, P written: by S buffer (0 and 1: D = 128 has one a row tile), or, where
+  // the halves take turns, by row tile and half
+  uint64_t sfull[4], pready[4];
   // D = 128: the last PV of each row tile.  D = 256: PV of the even and of the
   // odd tiles; S of tile j complete means PV of j - 2 complete, so a wait for
   // tile j - 1 or j is never two phases ahead of its barrier.
@@ -188,15 +189,21 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
 }
 
 // D = 128: a warp per row tile issues, so that one's waits and commits (some
-// 200 cycles each, as long as three MMAs) pass under the other's MMAs.  D =
+// 200 cycles each, as long as three MMAs) pass under the other's MMAs.  Tensor
+// memory holds one S of a row tile; where no maximum ties its two halves (64
+// keys, one softmax group each) together (FIX below), they take turns: the
+// products of one half's next keys follow that half's weights while the other
+// is at its softmax (eight ragged chunks: 253 -> 209 us; with a running maximum
+// the halves would wait for each other, 257 -> 327 us for one chunk of 8192
+// keys).  D =
 // 256: one warp, in the order that lets the products of tile j + 2 follow the
 // weights of tile j in their columns without a wait (a second warp for P V
 // would have to wait for each tile's completion: 390 against 358 us where the
 // tensor pipe is all that runs).
-template <int DT, int D>
+template <int DT, int D, bool TURNS>
 __device__ void role_mma(int t, int n, int nm, uint8_t *smem, PCtl &c, uint32_t *hdr, uint32_t tmem) {
   using Gm = PGeo<DT, D>;
-  constexpr uint32_t IQK = idesc_pf(!Gm::QUANT, 128, false);
+  constexpr uint32_t IQK = idesc_pf(!Gm::QUANT, TURNS ? 64 : 128, false);
   constexpr uint32_t IPV = idesc_pf(!Gm::QUANT, 128, true);
   const uint32_t lead = elect_one();
   wait_p(&c.qfull, 0, c, hdr);
@@ -213,35 +220,76 @@ __device__ void role_mma(int t, int n, int nm, uint8_t *smem, PCtl &c, uint32_t 
     wait_p(full(i), fpar(i), c, hdr);
     landed();
   };
-  // S(buffer) (+)= Q tile t, dims 128 h .. + 127, times K unit i
-  auto qk = [&](uint32_t i, int t, int h, uint32_t buf) {
-    const uint64_t kb = dK + (uint64_t)((i % Gm::NU) * (kUnitBytes >> 4));
+  // S(buffer x) (+)= Q (of row tile t), dims 128 h .. + 127, times K unit i.  TURNS:
+  // half x of row tile t's S = Q times half x of K unit i
+  auto qk = [&](uint32_t i, int h, uint32_t x) {
+    const uint64_t kb = dK + (uint64_t)((i % Gm::NU) * (kUnitBytes >> 4) + (TURNS ? x * (64 * 128 >> 4) : 0));
     const uint64_t qb = dQ + (uint64_t)((t * (128 * D * 2) + h * kUnitBytes) >> 4);
+    const uint32_t to = tmem + (TURNS ? t * 128 + x * 64 : x * 128);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       const uint64_t off = (uint64_t)(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
-      mma_ss_if(lead, tmem + buf * 128, qb + off, kb + off, IQK, (h > 0 || ks > 0) ? 1u : 0u);
+      mma_ss_if(lead, to, qb + off, kb + off, IQK, (h > 0 || ks > 0) ? 1u : 0u);
     }
   };
-  // O (+)= P(buffer) times V unit i; P sits in two runs of 32 columns, one in
-  // each softmax group's half of S
-  auto pv = [&](uint32_t i, uint32_t o, uint32_t buf, bool first) {
+  // O (+)= P(buffer) times V unit i, keys 16 k0 .. 16 k1 - 1; P sits in two runs of
+  // 32 columns, one in each softmax group's half of S
+  auto pv = [&](uint32_t i, uint32_t o, uint32_t buf, bool first, int k0, int k1) {
     const uint64_t vb = dV + (uint64_t)((i % Gm::NU) * (kUnitBytes >> 4));
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
+    for (int ks = k0; ks < k1; ++ks)
       mma_ts_if(lead, o, tmem + buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
-                vb + (uint64_t)((ks * 2048) >> 4), IPV, (!first || ks > 0) ? 1u : 0u);
+                vb + (uint64_t)((ks * 2048) >> 4), IPV, (!first || ks > k0) ? 1u : 0u);
   };
-  if constexpr (D == 128) {
+  if constexpr (TURNS) {
     if (t >= nm) n = 0;
     if (n > 0) {
       wait_full(0);
-      qk(0, t, 0, t);
-      commit_if(lead, &c.sfull[t]);
+      qk(0, 0, 0);
+      commit_if(lead, &c.sfull[2 * t]);
+      qk(0, 0, 1);
+      commit_if(lead, &c.sfull[2 * t + 1]);
       commit_if(lead, &c.empty[0]);
     }
     for (int j = 0; j < n; ++j) {
       // the checks of a tile's V, next K and weights are issued together
+      const uint32_t uv = 2 * j + 1, uk = 2 * j + 2;
+      const bool more = j + 1 < n;
+      const bool rp = mbar_test(&c.pready[2 * t], j & 1);
+      const bool rv = mbar_test(full(uv), fpar(uv));
+      const bool rk = !more || mbar_test(full(uk), fpar(uk));
+      if (!rv) wait_slow(full(uv), fpar(uv), c, hdr);
+      if (!rp) wait_slow(&c.pready[2 * t], j & 1, c, hdr);
+      landed();
+      pv(uv, tmem + Gm::COL_O + t * 128, t, j == 0, 0, 4);
+      if (more) {
+        if (!rk) {
+          wait_slow(full(uk), fpar(uk), c, hdr);
+          landed();
+        }
+        qk(uk, 0, 0);
+        commit_if(lead, &c.sfull[2 * t]);
+      }
+      wait_p(&c.pready[2 * t + 1], j & 1, c, hdr);
+      tc_fence_after();
+      pv(uv, tmem + Gm::COL_O + t * 128, t, false, 4, 8);
+      commit_if(lead, &c.empty[uv % Gm::NU]);
+      if (more) {
+        qk(uk, 0, 1);
+        commit_if(lead, &c.sfull[2 * t + 1]);
+        commit_if(lead, &c.empty[uk % Gm::NU]);
+      }
+    }
+    if (n > 0) commit_if(lead, &c.odone[t]);
+  } else if constexpr (D == 128) {
+    if (t >= nm) n = 0;
+    if (n > 0) {
+      wait_full(0);
+      qk(0, 0, t);
+      commit_if(lead, &c.sfull[t]);
+      commit_if(lead, &c.empty[0]);
+    }
+    for (int j = 0; j < n; ++j) {
       const uint32_t uv = 2 * j + 1, uk = 2 * j + 2;
       const bool more = j + 1 < n;
       const bool rp = mbar_test(&c.pready[t], j & 1);
@@ -250,14 +298,14 @@ __device__ void role_mma(int t, int n, int nm, uint8_t *smem, PCtl &c, uint32_t 
       if (!rv) wait_slow(full(uv), fpar(uv), c, hdr);
       if (!rp) wait_slow(&c.pready[t], j & 1, c, hdr);
       landed();
-      pv(uv, tmem + Gm::COL_O + t * 128, t, j == 0);
+      pv(uv, tmem + Gm::COL_O + t * 128, t, j == 0, 0, 8);
       commit_if(lead, &c.empty[uv % Gm::NU]);
       if (!more) break;
       if (!rk) {
         wait_slow(full(uk), fpar(uk), c, hdr);
         landed();
       }
-      qk(uk, t, 0, t);
+      qk(uk, 0, t);
       commit_if(lead, &c.sfull[t]);
       commit_if(lead, &c.empty[uk % Gm::NU]);
     }
@@ -267,7 +315,7 @@ __device__ void role_mma(int t, int n, int nm, uint8_t *smem, PCtl &c, uint32_t 
     auto tile_qk = [&](int j) {
       for (int h = 0; h < Gm::H; ++h, ++u) {
         wait_full(u);
-        qk(u, 0, h, j & 1);
+        qk(u, h, j & 1);
         commit_if(lead, &c.empty[u % Gm::NU]);
       }
       commit_if(lead, &c.sfull[j & 1]);
@@ -282,7 +330,7 @@ __device__ void role_mma(int t, int n, int nm, uint8_t *smem, PCtl &c, uint32_t 
       landed();
       for (int h = 0; h < Gm::H; ++h, ++u) {
         if (h > 0) wait_full(u);
-        pv(u, tmem + Gm::COL_O + h * 128, j & 1, j == 0);
+        pv(u, tmem + Gm::COL_O + h * 128, j & 1, j == 0, 0, 8);
         commit_if(lead, &c.empty[u % Gm::NU]);
       }
       commit_if(lead, &c.odone[j & 1]);
@@ -577,6 +625,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
                              size_t r_out, float slope) {
   using Gm = PGeo<DT, D>;
   constexpr int NC = Gm::NC;
+  constexpr bool TURNS = FIX && D == 128;
   // row tile `rt`, half `hf` of its columns; a pair of warps shares 32 rows
   const int tid = threadIdx.x, hf = (tid >> 7) & 1, rt = tid >> 8, wq = (tid >> 5) & 3, lane = tid & 31;
   const int row = rt * 128 + (tid & 127), pair = 1 + rt * 4 + wq;
@@ -627,7 +676,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   [[maybe_unused]] int mode = fabsf(fu) >= 0x1p-16f ? 1 : 2;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
-    const int buf = D == 128 ? rt : (j & 1);
+    const int buf = D == 128 ? rt : (j & 1), turn = TURNS ? 2 * rt + hf : buf;
     const uint32_t par = D == 128 ? (j & 1) : ((j >> 1) & 1);
     const int k0t = (w.kt0 + j) * kKeys;              // the tile's first key
     const int k0 = k0t + hf * NC;                     // this thread's
@@ -655,7 +704,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       d[1] = make_float4(x[4], x[5], x[6], x[7]);
       __syncwarp();
     }
-    wait_p(&c.sfull[buf], par, c, p.hdr);
+    wait_p(&c.sfull[turn], par, c, p.hdr);
     __syncwarp();
     tc_fence_after();
     const uint32_t S = tmem + lane_off + buf * 128 + hf * NC;
@@ -773,7 +822,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c.pready[buf]);
+      if (lane == 0) mbar_arrive(&c.pready[turn]);
       continue;
     }
     float mx = kNegInf;      // this thread's largest score of the tile (log2 units)
@@ -940,7 +989,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c.pready[buf]);
+      if (lane == 0) mbar_arrive(&c.pready[turn]);
     }
   }
   // ---- the sum, the last PV, the output
@@ -1042,11 +1091,11 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       // D = 128: both row tiles use a unit; D = 256: one MMA warp does
       mbar_init(&c.empty[i], D == 128 && to.len * G - to.first * Gm::ROWS > 128 ? 2 : 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&c.sfull[i], 1);
-      mbar_init(&c.pready[i], 8);   // softmax warps of a row tile
-      mbar_init(&c.odone[i], 1);
+      mbar_init(&c.pready[i], FIX && D == 128 ? 4 : 8);   // a group's, or both groups' warps
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&c.odone[i], 1);
     mbar_init(&c.qfull, Gm::SMW);
     mbar_init(&c.done, Gm::MT);
     c.abort = 0;
@@ -1162,7 +1211,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   } else if (warp < Gm::SMW + 4) {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_MMA>();
     if (warp < Gm::SMW + Gm::MT)
-      role_mma<DT, D>(warp - Gm::SMW, __shfl_sync(0xffffffffu, w.ntiles, 0), __shfl_sync(0xffffffffu, w.nrows > 128 ? 2 : 1, 0),
+      role_mma<DT, D, FIX && D == 128>(warp - Gm::SMW, __shfl_sync(0xffffffffu, w.ntiles, 0), __shfl_sync(0xffffffffu, w.nrows > 128 ? 2 : 1, 0),
                       smem, c, p.hdr, __shfl_sync(0xffffffffu, tmem, 0));
   } else {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_COPY>();
