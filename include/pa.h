@@ -94,7 +94,8 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_INT8 = 1, PA_KV_NVFP4 = 2, PA_KV_FP8 = 3 } 
 #define PA_ERRF_BAD_SLOT          0x40u /* pa_append_kv, pa_rope_append: slot outside
                                            [-1, 16 * num_blocks): row skipped */
 #define PA_ERRF_BAD_Q_START       0x80u /* pa_prefill: q_starts descending or outside
-                                           [0, num_tokens]: clamped */
+                                           [0, num_tokens]: clamped; the rows of the
+                                           sequences concerned are unspecified */
 
 /* The paged KV pool.  block_size must be 16; head_dim 128 or 256. */
 typedef struct pa_kv_cache {
@@ -401,9 +402,12 @@ int pa_rope_frequencies(int32_t rot_dim, double base, int32_t kind, double facto
  *                    t >= first_key[query], and (window > 0) t > p - window
  * first_key separates documents packed into one sequence; a query that sees
  * no key has output 0 and lse -inf.  Keys hidden from every query of a
- * sequence's chunk are never read. */
+ * sequence's chunk are never used, whatever their slots hold; keys that some
+ * queries of a chunk see and others do not (later tokens of a prompt, other
+ * documents) have weight 0 for the others, so their values must be finite, as
+ * in any product with a masked softmax. */
 typedef struct pa_score {
-  float softcap;               /* 0: none; else > 0 and finite */
+  float softcap;               /* 0: none; else > 0 and finite (above 1e18: none) */
   int32_t window;              /* 0: none; else the last `window` keys up to the query's own */
   const float *alibi_slopes;   /* fp32 [num_q_heads], or NULL */
   const int32_t *first_key;    /* int32, one per query token: [num_tokens] (pa_prefill) or
@@ -413,7 +417,7 @@ typedef struct pa_score {
 
 /* Decode (q_len 1) with score options: arguments, split plan, outputs and
  * flags as pa_decode; a window (or first_key) also shortens what is read.
- * opt->kernel: 0, 2 or 5 (else PA_ERR_UNSUPPORTED); auto mode runs single-launch
+ * Any Hq / Hkv up to 8.  opt->kernel: 0, 2 or 5 (else PA_ERR_UNSUPPORTED); auto mode runs single-launch
  * also for sequences of at most 128 keys in any number, and for at most 1,024
  * keys (counting a window's keys only) up to three CTAs per SM. */
 int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_score *score,
@@ -425,7 +429,12 @@ int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_sco
  * the row i of q_len is at position p = seq_lens[b] - q_len + i and sees the
  * keys t <= p, subject to `score`.  Rows of q before q_starts[0] or from
  * q_starts[batch] on are neither read nor written.  Any Hq / Hkv up to 8,
- * any chunk length from one token. */
+ * any chunk length from one token; at most 65,535 kv heads.
+ * Weights meet the values rounded to bf16 (bf16 cache) or fp16 (the others, as
+ * the queries do then: |q| up to 65,504, below 2^-14 with fewer bits; int8: the
+ * row's scale is in the weight, so |v| up to 32,000).  Scores capped at 55 or
+ * less over a bf16 cache take |v| up to 2^17: their weights are not relative to
+ * the row's largest. */
 typedef struct pa_prefill_problem {
   int32_t batch;               /* B >= 0 */
   int32_t num_q_heads;         /* Hq, a multiple of num_kv_heads; Hq / Hkv <= 8 */

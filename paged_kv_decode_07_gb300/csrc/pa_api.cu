@@ -494,6 +494,7 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   if (sc) {
     pp.window = sc->window;
     pp.first_key = sc->first_key;
+    pp.scored = 1;
   }
 
   AttnParams ap;

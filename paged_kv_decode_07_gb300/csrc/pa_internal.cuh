@@ -118,6 +118,7 @@ struct PlanParams {
   // planned (window, first_key); 0 / null otherwise
   int window;
   const int *first_key;
+  int scored;
 };
 
 // A ragged batch of prompt chunks over the paged cache (pa_prefill).

@@ -15,9 +15,9 @@
 // target_items)) unless fixed by the caller; when every sequence has the
 // same length, W then grows until the item count is a whole number of
 // rounds of the attention kernel's resident CTAs (the number of rounds from
-// a cost model: a round costs its items' blocks plus a fixed cost per item).  parts_u = ceil(nblk_u /
-// W); blocks are split evenly, ceil(nblk_u / parts_u) per part (never
-// empty).
+// a cost model: a round costs its items' blocks plus a fixed cost per item).
+// parts_u = ceil(nblk_u / W); blocks are split evenly, ceil(nblk_u / parts_u)
+// per part (never empty).
 // Items of multi-part units come first (they are about W blocks each), then
 // the single-part ones (shorter), a longest-first order for the hardware's
 // in-order CTA dispatch.
@@ -197,7 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
       // completely, with parts_k = the most partitions per unit that fit k
       // rounds, the partitions take the k of least k * (nb / parts_k + c).
       const int nb = s_gmax;
-      if (p.resident > 0 && nb > 0 && s_gmin == nb) {
+      // (scored: a window makes most lengths equal, but for a block by where it
+      // starts and the sequences it does not fill: 16 windows of 2048 keys 37.4 ->
+      // 28.2 us a call, 64 of 4096, some not filled, 98.7 -> 97.0)
+      const bool even = SC ? 8 * s_total >= 7ull * NG * nb : s_gmin == nb;
+      if (p.resident > 0 && nb > 0 && even) {
         const long long per = (long long)NG * GS * p.hkv;   // items per partition index
         const long long items0 = per * ((nb + W - 1) / W);
         // at most 64 rounds are weighed: past that a partial round costs
@@ -335,6 +339,139 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
   }
 }
 
+// The same plan for scored decode of up to 1024 sequences, a thread each: the
+// kernel above is one straight run of cold instructions and a dozen barriers,
+// 11.4 us by itself, and the attention waits for it (32 int8 sequences of 1K to
+// 32K keys: 119 -> 113 us a call; 64 windows of 4096 keys: 97.0 -> 93.3).
+// One read of the lengths, two barriers for the sums and the scan, then every
+// warp writes the items of sequences of its own.
+__global__ void __launch_bounds__(kThreads, 1) plan_scored_kernel(PlanParams p) {
+  __shared__ uint32_t s_sum[32], s_err[32];
+  __shared__ int s_max[32], s_a[32], s_b[32];
+  __shared__ int s_nblk[kThreads], s_first[kThreads], s_len[kThreads], s_parts[kThreads], s_at[kThreads];
+  griddep_launch();   // the attention kernel may launch now; it waits for this grid to finish
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, NG = p.B;
+  int n = 0, first = 0;
+  uint32_t err = 0;
+  if (tid < NG) {
+    n = unit_len(p, tid, err);
+    first = unit_first<true>(p, tid, n);
+  }
+  const int nblk = (n + kBlock - 1) / kBlock - first;
+  {
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, (uint32_t)nblk);   // below 2^31: 32 of 2^26
+    const int hi = __reduce_max_sync(0xffffffffu, nblk);
+    const uint32_t e = __reduce_or_sync(0xffffffffu, err);
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_max[warp] = hi;
+      s_err[warp] = e;
+    }
+  }
+  __syncthreads();
+  // every warp: the totals, and the blocks of a partition (as in plan_kernel)
+  unsigned long long total = s_sum[lane];
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int nb = __reduce_max_sync(0xffffffffu, s_max[lane]);
+  err = __reduce_or_sync(0xffffffffu, s_err[lane]);
+  int W, round = 0;
+  if (p.split_blocks > 0) {
+    W = p.split_blocks;
+  } else {
+    const unsigned long long work = total * (unsigned)p.hkv;
+    W = (int)min((work + p.target_items - 1) / p.target_items, 1ull << 30);
+    W = max(W, max(p.min_split_blocks, 1));
+    if (p.resident > 0 && nb > 0 && 8 * total >= 7ull * NG * nb) {
+      const long long per = (long long)NG * p.hkv, items0 = per * ((nb + W - 1) / W);
+      const int kmax = (int)min(items0 / p.resident, 64LL);
+      unsigned long long best = ~0ull;   // cost, k - 1 below it
+      int best_w = 0;
+      for (int k = lane + 1; k <= kmax; k += 32) {
+        const int parts = (int)((long long)k * p.resident / per);
+        if (parts < 1) continue;
+        const int wk = (nb + parts - 1) / parts;
+        const unsigned long long t = (unsigned long long)k * (unsigned)(wk + p.item_cost) << 6 | (unsigned)(k - 1);
+        if (t < best) {
+          best = t;
+          best_w = wk;
+        }
+      }
+      unsigned long long least = best;
+      for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+      if (least != ~0ull) {
+        const uint32_t who = __ballot_sync(0xffffffffu, best == least);
+        W = max(W, __shfl_sync(0xffffffffu, best_w, __ffs(who) - 1));
+        round = p.resident;
+      }
+    }
+  }
+  const int parts = nblk ? (nblk + W - 1) / W : 0;
+  // slots of the sequences in several parts, and how many are in one
+  const int a = parts > 1 ? parts : 0, b = parts == 1;
+  int ia = a, ib = b;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int xa = __shfl_up_sync(0xffffffffu, ia, o), xb = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ia += xa;
+      ib += xb;
+    }
+  }
+  if (lane == 31) {
+    s_a[warp] = ia;
+    s_b[warp] = ib;
+  }
+  __syncthreads();
+  int wa = s_a[lane], wb = s_b[lane];   // inclusive over the warps
+  for (int o = 1; o < 32; o <<= 1) {
+    const int xa = __shfl_up_sync(0xffffffffu, wa, o), xb = __shfl_up_sync(0xffffffffu, wb, o);
+    if (lane >= o) {
+      wa += xa;
+      wb += xb;
+    }
+  }
+  const int slots = __shfl_sync(0xffffffffu, wa, 31), singles = __shfl_sync(0xffffffffu, wb, 31);
+  const int before_a = warp ? __shfl_sync(0xffffffffu, wa, warp - 1) : 0;
+  const int before_b = warp ? __shfl_sync(0xffffffffu, wb, warp - 1) : 0;
+  const int slot = before_a + ia - a, single = before_b + ib - b;
+  const bool fits = (long long)(slots + singles) * p.hkv <= p.max_items && slots <= p.max_slots;
+  if (tid < NG) {
+    UnitInfo ui;
+    ui.parts = parts;
+    ui.slot_base = parts > 1 ? slot : -1;
+    ui.nblk = nblk;
+    ui.len = n;
+    p.units[tid] = ui;
+  }
+  s_nblk[tid] = nblk;
+  s_first[tid] = first;
+  s_len[tid] = n;
+  s_parts[tid] = parts;
+  s_at[tid] = parts > 1 ? slot : slots + single;   // times hkv: the first item
+  __syncthreads();
+  if (fits) {
+    // 32 / NG warps a sequence where there are few
+    const int wpg = max(1, 32 / max(NG, 1));
+    for (int g = warp / wpg; g < NG; g += 32 / wpg) {
+      const int np = s_parts[g], blocks = s_nblk[g], at = s_at[g];
+      if (np == 0) continue;
+      const int chunk = (blocks + np - 1) / np, lo = s_first[g], hi = lo + blocks;
+      for (int j = (warp % wpg) * 32 + lane; j < np * p.hkv; j += wpg * 32) {
+        const int part = j / p.hkv;
+        int4 *const it = reinterpret_cast<int4 *>(p.items + (size_t)at * p.hkv + j);
+        it[0] = make_int4(g, j - part * p.hkv, lo + part * chunk, min(hi, lo + (part + 1) * chunk));
+        it[1] = make_int4(part, np, np > 1 ? at + part : -1, s_len[g]);
+      }
+    }
+  }
+  if (tid == 0) {
+    p.hdr[HDR_ERR] = err | (p.extra_err ? *p.extra_err : 0u) | (fits ? 0u : PA_ERRF_PLAN_OVERFLOW);
+    p.hdr[HDR_NUM_ITEMS] = fits ? (uint32_t)((slots + singles) * p.hkv) : 0u;
+    p.hdr[HDR_SPLIT] = (uint32_t)W;
+    p.hdr[HDR_NUM_SLOTS] = (uint32_t)slots;
+    p.hdr[HDR_ROUND] = (uint32_t)round;
+  }
+}
+
 }  // namespace
 
 // clears the header of a call that has no plan; its attention kernel is
@@ -350,7 +487,9 @@ cudaError_t launch_clear(uint32_t *hdr, cudaStream_t s) {
 }
 
 cudaError_t launch_plan(const PlanParams &pp, cudaStream_t s) {
-  if (pp.window > 0 || pp.first_key)
+  if (pp.scored && pp.B <= kThreads)
+    plan_scored_kernel<<<1, kThreads, 0, s>>>(pp);
+  else if (pp.window > 0 || pp.first_key)
     plan_kernel<true><<<1, kThreads, 0, s>>>(pp);
   else
     plan_kernel<false><<<1, kThreads, 0, s>>>(pp);

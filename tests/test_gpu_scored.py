@@ -111,6 +111,34 @@ def test_tiny_cap_averages_the_keys():
     S.within(out[:, 0], ref, bound)
 
 
+@pytest.mark.parametrize("B,most", [(1, 9000), (3, 5000), (40, 1500), (1024, 90), (1100, 90)])
+def test_plans_of_few_and_many_sequences(B, most):
+    """Lengths of 0 to `most`; windows and documents leave some sequences a few
+    blocks, some one, some none."""
+    r = torch.Generator().manual_seed(B)
+    lens = [int(x) for x in torch.randint(0, most + 1, (B,), generator=r)]
+    lens[0] = most
+    first = torch.tensor([n if i % 7 == 3 else max(0, n - 200 * (i % 5)) for i, n in enumerate(lens)],
+                         dtype=torch.int32, device=DEV)
+    check("bf16", lens, 2, 4, 128, kernel=2)
+    check("fp8", lens, 2, 2, 128, kernel=2, window=1000, softcap=20.0)
+    check("bf16", lens, 1, 4, 128, kernel=2, window=500, first_key=first)
+
+
+def test_equal_windows_fill_whole_rounds():
+    """64 windows of 64 or 65 blocks, four of them not filled: items of one size in
+    whole rounds of the resident CTAs; the header says which rule was taken."""
+    lens = [3000 + 13 * i for i in range(60)] + [900, 1000, 17, 700]
+    kv, q, tables, sl = build("fp8", lens, 4, 2, 128)
+    out, lse, ws = pa.decode_scored(kv, q, tables, sl, 0.1, score=pa.Score(window=1024), out_fp32=True, return_lse=True,
+                                    max_seq_len=max(lens), kernel=2)
+    ref, rl, bound = S.reference(vals(kv), q[:, 0], [1] * 64, lens, tables, 0.1, window=1024, eps_p=EPS_P["fp8"])
+    S.within(out[:, 0], ref, bound)
+    S.lse_within(lse[:, 0], rl)
+    _, items, W, _, resident = ws[:20].view(torch.int32).tolist()
+    assert resident > 0 and W > 8 and items <= max(resident, 256 * -(-65 // W))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_long_cache_with_window(fmt):
     check(fmt, [40000, 17, 9001], 2, 4, 256, window=1025, softcap=50.0)
