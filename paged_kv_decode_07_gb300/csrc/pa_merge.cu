@@ -170,6 +170,80 @@ __global__ void __launch_bounds__(kThreads) merge_plan_kernel(const AttnParams p
             p.out_fp32, (size_t)row * D, p.lse_out, row);
 }
 
+// Scored decode of many rows behind a window: a warp each, eight rows a CTA.  With
+// a CTA a row (above) such a batch is several rounds of CTAs that mostly wait (64
+// windows of 4096 keys, 1536 rows: 93.3 -> 90.4 us a call; of 1024 keys 43 -> 40).
+// A window bounds a row's partials (at least eight blocks each); without one they
+// may be hundreds, which a warp takes long over (32 sequences of 1K to 32K keys,
+// up to 60 partials: 113 -> 130 us).
+constexpr int kWarpRows = 256;         // rows from which it is taken,
+constexpr int kWarpWindow = 8192;      // and the window up to which
+// adds w_q o_q of up to 32 partials, lane q holding partial q's weight; eight are
+// on their way at once (an empty one may hold anything)
+template <int D>
+__device__ __forceinline__ void add_partials(const float *po, size_t pitch, int parts, float w, int lane,
+                                             float4 (&acc)[D / 128]) {
+#pragma unroll 1
+  for (int q0 = 0; q0 < parts; q0 += 8) {
+    float4 v[8][D / 128];
+    float wq[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int q = q0 + k;
+      wq[k] = __shfl_sync(0xffffffffu, w, q & 31);
+      if (q >= parts) wq[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (wq[k] != 0.f) v[k][i] = *reinterpret_cast<const float4 *>(po + q * pitch * D + (i * 32 + lane) * 4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        acc[i].x += wq[k] * v[k][i].x;
+        acc[i].y += wq[k] * v[k][i].y;
+        acc[i].z += wq[k] * v[k][i].z;
+        acc[i].w += wq[k] * v[k][i].w;
+      }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) merge_window_kernel(const AttnParams p) {
+  griddep_wait();   // the attention kernel's outputs and partials are complete
+  const int lane = threadIdx.x & 31, row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (row >= p.B * p.Hq) return;
+  const UnitInfo ui = p.units[row / p.Hq];
+  if (ui.parts == 1) return;   // written by the attention kernel
+  // a plan that did not fit the workspace must not read past the slots
+  const int parts = ui.slot_base >= 0 && ui.slot_base + ui.parts <= p.max_slots ? ui.parts : 0;
+  const size_t pitch = (size_t)p.kv.hkv * p.R;   // rows between a row's partials
+  const int hq = row % p.Hq;
+  const size_t prow = parts ? ((size_t)ui.slot_base * p.kv.hkv + hq / p.G) * p.R + hq % p.G : 0;
+  const float *po = p.part_o + prow * D, *pl = p.part_lse + prow;
+  float M = kNegInf, sum = 0.f;
+  for (int q = lane; q < parts; q += 32) M = fmaxf(M, pl[q * pitch]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float4 acc[D / 128] = {};
+  for (int q0 = 0; q0 < parts; q0 += 32) {
+    const float l = q0 + lane < parts ? pl[(q0 + lane) * pitch] : kNegInf;
+    const float w = l == kNegInf ? 0.f : __expf(l - M);
+    sum += w;
+    add_partials<D>(po + q0 * pitch * D, pitch, min(32, parts - q0), w, lane, acc);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 128; ++i)
+    store4(p.out, p.out_fp32, (size_t)row * D + (i * 32 + lane) * 4,
+           make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
+  if (p.lse_out && lane == 0) p.lse_out[row] = sum > 0.f ? M + __logf(sum) : kNegInf;
+}
+
 // public pa_merge: part_out [S, R, D], part_lse [S, R]
 __global__ void __launch_bounds__(kThreads)
     merge_dense_kernel(const float *po, const float *pl, int S, int R, int D, void *out,
@@ -185,6 +259,11 @@ cudaError_t launch_merge_plan(const AttnParams &p, cudaStream_t s) {
   const long long rows = (long long)p.B * p.Q * p.Hq;
   if (rows == 0) return cudaSuccess;
   if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (p.sc.window > 0 && p.sc.window <= kWarpWindow && rows >= kWarpRows) {
+    const unsigned grid = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+    return p.kv.D == 128 ? launch_pdl(merge_window_kernel<128>, grid, kThreads, 0, s, p)
+                         : launch_pdl(merge_window_kernel<256>, grid, kThreads, 0, s, p);
+  }
   return launch_pdl(merge_plan_kernel, (unsigned)rows, kThreads, 0, s, p);
 }
 

@@ -495,6 +495,8 @@ def _need_cache(kv, idx):
     if idx < 0:
         raise ValueError("the KV cache must be on a CUDA device")
     k = kv.k_cache
+    if k.dim() != 4:
+        raise ValueError(f"k_cache must have four dimensions: got {list(k.shape)}")
     pages = (k.shape[0], k.shape[1], kv.block_size, k.shape[3])
     size = 2 if kv.dtype == "bf16" else 1
     arrays = [("k_cache", k, pages, size), ("v_cache", kv.v_cache, pages, size)]

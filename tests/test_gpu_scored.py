@@ -125,6 +125,17 @@ def test_plans_of_few_and_many_sequences(B, most):
     check("bf16", lens, 1, 4, 128, kernel=2, window=500, first_key=first)
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_one_long_sequence_among_many(D):
+    """Rows of hundreds of partials beside rows of one, two and none."""
+    lens = [50] * 10 + [40000] + [300, 0, 260] * 10
+    check("bf16", lens, 2, 4, D, softcap=30.0)
+    check("fp8", lens, 2, 4, D, window=8000)    # 62 partials at most
+    first = torch.zeros(len(lens), dtype=torch.int32, device=DEV)
+    first[10] = 50000          # and the long one sees nothing
+    check("nvfp4", lens, 1, 7, D, first_key=first)
+
+
 def test_equal_windows_fill_whole_rounds():
     """64 windows of 64 or 65 blocks, four of them not filled: items of one size in
     whole rounds of the resident CTAs; the header says which rule was taken."""
@@ -222,3 +233,37 @@ def test_capture_and_replay_with_new_inputs(lens):
                                     first_key=first, eps_p=EPS_P["fp8"])
         S.within(out[:, 0], ref, bound)
         assert pa.read_error(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "nvfp4"])
+def test_wrong_caches_and_workspaces_are_refused_by_name(fmt):
+    kv, q, tables, sl = build(fmt, [300, 200], 2, 4, 128)
+    bad = [("v_cache", kv.v_cache[:, :1]), ("v_cache", kv.v_cache[:-1]), ("v_cache", kv.v_cache.cpu()),
+           ("v_cache", kv.v_cache.transpose(0, 1).contiguous().transpose(0, 1)), ("v_cache", kv.v_cache.float()),
+           ("k_cache", kv.k_cache[:, :, :8])]
+    if fmt != "bf16":
+        bad += [("k_scale", None), ("v_scale", kv.v_scale[:-1]), ("v_scale", kv.v_scale.float())]
+    for name, t in bad:
+        other = pa.KvCache(fmt, kv.k_cache, kv.v_cache, kv.k_scale, kv.v_scale, kv.k_global, kv.v_global)
+        setattr(other, name, t)
+        with pytest.raises(ValueError, match="cache|scale"):
+            pa.decode_scored(other, q, tables, sl, 0.1, max_seq_len=300)
+        starts = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+        with pytest.raises(ValueError, match="cache|scale"):
+            pa.prefill(other, q[:, 0], starts, tables, sl, 0.1, max_seq_len=300)
+    ws = torch.zeros((1 << 20, 2), dtype=torch.uint8, device=DEV)[:, 0]
+    with pytest.raises(ValueError, match="workspace"):
+        pa.decode_scored(kv, q, tables, sl, 0.1, max_seq_len=300, workspace=ws)
+
+
+def test_one_token_rows_of_any_pitch_are_rotated():
+    """With a single token no stride counts."""
+    kv, q, tables, sl = build("bf16", [300], 2, 4, 128)
+    x = torch.randn((1, 12 * 128 + 5), device=DEV).bfloat16()
+    views = [x[:, i * 128 * n0:][:, :n * 128].view(1, n, 128) for i, n0, n in ((0, 1, 8), (8, 1, 2), (10, 1, 2))]
+    pos = torch.tensor([7], dtype=torch.int32, device=DEV)
+    slot = torch.tensor([3], dtype=torch.int64, device=DEV)
+    inv, _ = pa.rope_frequencies(64, device=DEV)
+    a = pa.rope_append(kv, *views, pos, slot, inv)
+    b = pa.rope_append(kv, *(v.clone(memory_format=torch.contiguous_format) for v in views), pos, slot, inv)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
