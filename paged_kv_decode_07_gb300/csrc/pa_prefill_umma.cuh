@@ -80,8 +80,7 @@ struct PGeo {
   static constexpr int GROUPS = QUANT ? H : 1, CPW = 4 * GROUPS;
   static constexpr int THREADS = (SMW + 4 + CPW) * 32;
   // Registers per thread at launch, and after the split (not where 512 threads
-  // have 128 each): MMA group,
-  // copies or dequantisation, softmax groups
+  // have 128 each): MMA group, copies or dequantisation, softmax groups
   static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
   static constexpr int REG_MMA = 40, REG_COPY = QUANT ? 88 : 56;
   static constexpr int REG_SM =
@@ -441,9 +440,11 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
 
 // ------------------------------------------- other formats: codes to f16 units
 
-// 128 threads convert unit h of every tile, half a unit (64 keys) at a time; the codes of the next half are requested before the present
-// one is converted, so that their latency passes meanwhile.  int8 and FP8: 8 lanes per key row, 16 codes a lane; NVFP4: 4
-// lanes per row, 32 codes (two scale blocks) a lane.
+// 128 threads convert unit h of every tile, half a unit (64 keys) at a time; the
+// codes of the next half are requested before the present one is converted, so
+// that their latency passes meanwhile (a whole unit ahead was no faster: the
+// instructions are the bound).  int8 and FP8: 8 lanes per key row, 16 codes a
+// lane; NVFP4: 4 lanes per row, 32 codes (two scale blocks) a lane.
 template <int DT, int D>
 __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t, int h) {
   using Gm = PGeo<DT, D>;
@@ -627,7 +628,8 @@ __device__ __forceinline__ float2 tanh_unit(float2 u) {
 // sums: cap * log2 e <= kFixedCap = 80, that is weights of 2^+-80, sums of up to
 // 2^30 of them, and values up to 2^17 without overflow.  (fp16 weights could not;
 // a bias has no bound.)  No pair of warps then has to agree on a maximum, no O is
-// rescaled (eight ragged chunks, heads of 128: 283 -> 266 us).
+// rescaled (eight ragged chunks, heads of 128: 283 -> 266 us; and the halves of S
+// may then take turns, see role_mma).
 constexpr float kFixedCap = 80.f;
 
 template <int DT, int D, bool CAP, bool BIAS, bool FIX>
@@ -1030,11 +1032,11 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
   const float inv = l > 0.f ? vg / l : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
-  // The tile's MMAs are complete, so its shared memory is free: the output goes through it (16-byte pieces, swizzled by row) and leaves in whole
-  // rows.  (Stored from here, a row per lane, each instruction touched 32 lines:
-  // 6,000 cycles for a tile of 128 x 256.)
-  // A bf16 tile takes the place of its own queries; fp32 rows reach into what the
-  // other row tile's MMAs read.
+  // The tile's MMAs are complete, so its shared memory is free: the output goes
+  // through it (16-byte pieces, swizzled by row) and leaves in whole rows.  (Stored
+  // from here, a row per lane, each instruction touched 32 lines: 6,000 cycles for
+  // a tile of 128 x 256.)  A bf16 tile takes the place of its own queries; fp32 rows
+  // reach into what the other row tile's MMAs read.
   const bool wide = partial || p.out_fp32;
   if (D == 128 && wide && n > 0 && w.nrows > 128) {
     wait_p(&c.odone[rt ^ 1], 0, c, p.hdr);
