@@ -38,8 +38,8 @@
 // 210 us, 930 TFLOP/s).  Quantised caches: the instructions of dequantisation
 // and softmax together (8192 keys, heads of 256: FP8 525 us, NVFP4 552, int8 745
 // against bf16 380 to 410).  Short sequences: the 10,000 cycles until a CTA's
-// first weights and 5,000 of its output (four packed int8 prompts: 58 us for
-// 4.2 CTAs an SM).
+// first weights and 5,000 of its output (four packed int8 prompts: 58 us, 324
+// CTAs in three rounds).
 #pragma once
 
 #include "pa_prefill.cuh"
