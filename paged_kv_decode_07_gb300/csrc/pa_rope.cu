@@ -23,6 +23,10 @@
 // pair never leaves a thread, every access is 16 bytes, and a lane's eight
 // sines and cosines serve every head of its token.  rot is a multiple of 32,
 // so the 16-element scale blocks of NVFP4 sit in neighbouring lanes.
+//
+// Bound by HBM, reads and writes mixed: 8,191 tokens of 24 + 4 heads of 256 with
+// norms (268 MB) in 47.0 us, 5.7 TB/s or 0.84 of a pure copy; 32,768 tokens into an
+// FP8 cache (1.0 GB) in 178 us, 0.83.
 #include "pa_codec.cuh"
 #include "pa_launch.h"
 
@@ -193,7 +197,7 @@ __device__ __forceinline__ void encode_row(const KvView &kv, int which, size_t r
 
 // A token's rows are taken in steps of 32 / L heads of one kind: first the
 // queries, then the keys, then the values.  One warp takes a run of a token's
-// steps, the next one's rows on their way while it is at one.
+// steps, the next one's rows (or two's) on their way while it is at one.
 template <int DT, int D, bool IL>
 __global__ void __launch_bounds__(32, kRopeCtas) rope_kernel(const RopeParams p) {
   constexpr int L = D / 16, RPW = 32 / L;
@@ -239,7 +243,12 @@ __global__ void __launch_bounds__(32, kRopeCtas) rope_kernel(const RopeParams p)
     }
     return x;
   };
-  Step x0 = load(s0);
+  // bf16 caches, D = 256: two steps' rows on their way (8,191 tokens 48.3 -> 47.0 us,
+  // 32,768 173 -> 165).  The others have no registers for it (FP8 178 -> 266 us) or
+  // half the steps (D = 128: 49.2 -> 50.0 us).
+  constexpr bool TWO = DT == PA_KV_BF16 && D == 256;
+  Step x0 = load(s0), x1;
+  if constexpr (TWO) x1 = load(s0 + 1);
   // the angles of this lane's pairs, once for every head of the token
   float cs[8], sn[8];
   const int pos = __ldg(p.positions + t);
@@ -286,10 +295,20 @@ __global__ void __launch_bounds__(32, kRopeCtas) rope_kernel(const RopeParams p)
     encode_row<DT, D>(p.kv, st.kind == 2, row0 + (size_t)st.h * kBlock, ca, cb, x, st.live && keep);
   };
 #pragma unroll 1
-  for (int s = s0; s < s1; ++s) {
+  for (int s = s0; s < s1; s += TWO ? 2 : 1) {
     const Step y = x0;
-    if (s + 1 < s1) x0 = load(s + 1);
+    if constexpr (TWO)
+      x0 = load(s + 2);
+    else if (s + 1 < s1)
+      x0 = load(s + 1);
     finish(y);
+    if constexpr (TWO) {
+      if (s + 1 < s1) {
+        const Step z = x1;
+        x1 = load(s + 3);
+        finish(z);
+      }
+    }
   }
 }
 
