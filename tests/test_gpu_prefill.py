@@ -219,16 +219,18 @@ def test_tiny_cap_averages_the_keys():
         S.within(out, ref, bound)
 
 
-@pytest.mark.parametrize("hkv,G,B,most", [(1, 8, 33, 150), (2, 3, 300, 40), (1, 1, 1100, 3)])
-def test_many_sequences(hkv, G, B, most):
-    """More than 32: chunks of 0 to `most` tokens over 0 to 60 earlier keys; rows
-    before the first and behind the last sequence stay as they were."""
+@pytest.mark.parametrize("hkv,G,B,most,earlier", [(1, 8, 33, 150, 60), (2, 3, 300, 40, 60), (1, 1, 1100, 3, 60),
+                                                  (1, 2, 40, 3, 2000)])
+def test_many_sequences(hkv, G, B, most, earlier):
+    """More than 32: chunks of 0 to `most` tokens over 0 to `earlier` keys (2000: the
+    keys are split); rows before the first and behind the last sequence stay as
+    they were."""
     r = torch.Generator().manual_seed(B)
     new = [int(x) for x in torch.randint(0, most + 1, (B,), generator=r)]
-    lens = [m + int(x) for m, x in zip(new, torch.randint(0, 61, (B,), generator=r))]
+    lens = [m + int(x) for m, x in zip(new, torch.randint(0, earlier + 1, (B,), generator=r))]
     kv, q, starts, tables, sl = build("bf16", new, lens, hkv, G, 128)
     T = sum(new)
-    qq = torch.cat((q[:300], q, q[:3]))
+    qq = torch.cat((q[:min(T, 300)], q, q[:3]))
     k = len(qq) - T - 3   # rows before the first
     out = torch.full((len(qq), hkv * G, 128), 7.0, device=DEV)
     out, lse, ws = pa.prefill(kv, qq, starts + k, tables, sl, 0.1, out=out, return_lse=True, max_seq_len=max(lens))
