@@ -1028,14 +1028,17 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     wait_p(&c.odone[D == 128 ? rt : (n - 1) & 1], D == 128 ? 0 : ((n - 1) >> 1) & 1, c, p.hdr);
     __syncwarp();
     tc_fence_after();
+  } else {   // no product ever waited for the queries: other warps may still be storing them
+    wait_p(&c.qfull, 0, c, p.hdr);
+    __syncwarp();
   }
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
   const float inv = l > 0.f ? vg / l : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
-  // The tile's MMAs are complete, so its shared memory is free: the output goes
-  // through it (16-byte pieces, swizzled by row) and leaves in whole rows.  (Stored
-  // from here, a row per lane, each instruction touched 32 lines: 6,000 cycles for
-  // a tile of 128 x 256.)  A bf16 tile takes the place of its own queries; fp32 rows
+  // The tile's MMAs are complete (of a tile without keys: its queries are all there),
+  // so its shared memory is free: the output goes through it (16-byte pieces,
+  // swizzled by row) and leaves in whole rows.  (Stored from here, a row per lane,
+  // each instruction touched 32 lines: 6,000 cycles for a tile of 128 x 256.)  A bf16 tile takes the place of its own queries; fp32 rows
   // reach into what the other row tile's MMAs read.
   const bool wide = partial || p.out_fp32;
   if (D == 128 && wide && n > 0 && w.nrows > 128) {
