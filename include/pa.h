@@ -432,9 +432,10 @@ int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_sco
  * any chunk length from one token; at most 65,535 kv heads.
  * Weights meet the values rounded to bf16 (bf16 cache) or fp16 (the others, as
  * the queries do then: |q| up to 65,504, below 2^-14 with fewer bits; int8: the
- * row's scale is in the weight, so |v| up to 32,000).  Scores capped at 55 or
- * less over a bf16 cache take |v| up to 2^17: their weights are not relative to
- * the row's largest. */
+ * row's scale is in the weight, relative to the largest scale of 128 neighbouring
+ * keys: of any size, with fewer bits where weight and scale together are below
+ * 2^-14 of the largest).  Scores capped at 55 or less over a bf16 cache take |v| up
+ * to 2^17: their weights are not relative to the row's largest. */
 typedef struct pa_prefill_problem {
   int32_t batch;               /* B >= 0 */
   int32_t num_q_heads;         /* Hq, a multiple of num_kv_heads; Hq / Hkv <= 8 */

@@ -55,6 +55,18 @@ constexpr int kUnitBytes = 32768;    // [128 keys][128 dims] of 16-bit values
 constexpr int kChunkBytes = 16384;   // 64 dims of it
 constexpr float kLazy = 8.0f;        // log2 of how far a score may pass the running maximum
 
+// int8: a weight is multiplied by its value row's scale before it is rounded to
+// fp16, so values of 0.01 would meet weights in fp16's subnormals (scores of
+// deviation 2 over 8192 keys: 1 % off).  The weights are therefore taken 2^v times
+// as large, v such that the largest scale of a tile times 2^v lies in [2^0, 2^7):
+// weights of up to 2^kLazy then meet their scales below 2^15, and those of the
+// largest scale have all their bits down to 2^-14.  v is part of the exponent that
+// the running maximum is subtracted from, so sum and O both hold it, and moves, by
+// the rescale that a new maximum makes, only when a tile's largest scale leaves the
+// range.  (4096 tokens at 8192 keys, heads of 256: 750 -> 759 us.)
+constexpr int kScaleExp = 4, kScaleExpMax = 6;   // exponent of the largest scale when v moves, at most
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }   // |e| < 127
+
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   float2 d;
   asm("add.rn.f32x2 %0, %1, %2;"
@@ -683,6 +695,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   };
   [[maybe_unused]] uint4 sc_next = make_uint4(0, 0, 0, 0);
   if constexpr (DT == PA_KV_INT8) sc_next = row_scales(0, id_next);
+  [[maybe_unused]] int vexp = 0;   // int8: the power of two that all weights hold
   float m = FIX ? 0.f : kNegInf, l = 0.f;
   // FIX: the way capped scores are formed (1, 2: the polynomials, 3: the
   // formula), moved on when a product leaves the polynomial's interval
@@ -699,6 +712,17 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     if constexpr (DT == PA_KV_INT8) id_after = page_id(j + 2);
     const uint32_t bad = __ballot_sync(0xffffffffu, id < 0 || id >= p.kv.num_blocks) & 0xffu;
     if (bad && lane == 0) flag(p.hdr, PA_ERRF_BAD_BLOCK_ID);
+    [[maybe_unused]] uint32_t most = 0;   // int8: the tile's largest value scale
+    [[maybe_unused]] float vfix = 1.f;    // and what it changes the weights' power of two by
+    // (all warps of the CTA alike.  Here for heads of 128; for heads of 256 behind the
+    // scores, 759 us against 768; for heads of 128 that place took 671 against 638)
+    auto fit_scales = [&]() {
+      const int e = min((int)(most >> 23) - 127, 15);   // (an infinite scale needs no room)
+      if (most != 0 && (e + vexp < 0 || e + vexp > kScaleExpMax)) {
+        vfix = pow2(kScaleExp - e - vexp);
+        vexp = kScaleExp - e;
+      }
+    };
     if constexpr (DT == PA_KV_INT8) {
       const int key = k0t + (lane & 15) * 8;
       const uint4 u = sc_next;
@@ -711,6 +735,12 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
         x[2 * i] = key + 2 * i >= w.see_lo && key + 2 * i < w.see_hi ? y.x : 0.f;
         x[2 * i + 1] = key + 2 * i + 1 >= w.see_lo && key + 2 * i + 1 < w.see_hi ? y.y : 0.f;
       }
+      float top = fabsf(x[0]);
+#pragma unroll
+      for (int i = 1; i < 7; i += 2) top = fmaxf(fmaxf(fabsf(x[i]), fabsf(x[i + 1])), top);
+      top = fmaxf(top, fabsf(x[7]));
+      most = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(top));
+      if constexpr (D == 128) fit_scales();
       __syncwarp();
       float4 *d = reinterpret_cast<float4 *>(wsc + (lane >> 4) * kKeys + (lane & 15) * 8);
       d[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -927,8 +957,9 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
         mx = largest();
       }
     }
+    if constexpr (DT == PA_KV_INT8 && D == 256) fit_scales();
     // ---- the running maximum moves when some score passes it by 2^kLazy
-    if (named_sync_or(pair, 64, mx > m + kLazy)) {
+    if (named_sync_or(pair, 64, mx > m + kLazy || (DT == PA_KV_INT8 && vfix != 1.f))) {
       // with the row's other keys
       if (hf == 0) c.red[row] = mx;
       named_sync(pair, 64);
@@ -939,7 +970,8 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       named_sync(pair, 64);
       if (hf == 0) mx = c.red[row];
       const float mn = fmaxf(m, mx);
-      const float al = mn == kNegInf ? 1.f : ex2_approx(m - mn);
+      float al = mn == kNegInf ? 1.f : ex2_approx(m - mn);
+      if constexpr (DT == PA_KV_INT8) al *= vfix;
       m = mn;
       l *= al;
       if (j > 0) {
@@ -963,7 +995,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     }
     // ---- weights
     {
-      const float mu = m == kNegInf ? 0.f : m;
+      const float mu = (m == kNegInf ? 0.f : m) - (DT == PA_KV_INT8 ? (float)vexp : 0.f);
       const float2 nm = make_float2(-mu, -mu), ff = make_float2(fs, fs);
       const float2 uu = make_float2(fu, fu), cc = make_float2(p.sc.cap_log2, p.sc.cap_log2);
       float2 l2 = make_float2(0.f, 0.f);
@@ -1034,7 +1066,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   }
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
   const float inv = l > 0.f ? vg / l : 0.f;
-  const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+  const float lse = l > 0.f ? (m - (DT == PA_KV_INT8 ? (float)vexp : 0.f) + log2f(l)) * 0.69314718055994531f : kNegInf;
   // The tile's MMAs are complete (of a tile without keys: its queries are all there),
   // so its shared memory is free: the output goes through it (16-byte pieces,
   // swizzled by row) and leaves in whole rows.  (Stored from here, a row per lane,
