@@ -496,6 +496,17 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
   };
 
+  // int8: a weight is multiplied by its V row's scale before it is rounded to fp16,
+  // so weights hold 2^v, v such that the block's largest scale times it lies in
+  // [2^0, 2^7): below 2^15 with weights of up to 2^kRescale, and with all bits down to
+  // weights of 2^-14 (without it values of 0.001 met weights in fp16's subnormals:
+  // errors of 5 to 50 times the roundings').  v is part of the exponent (m_run is the
+  // maximum less v), so sums and outputs hold it alike, and moves with the rescale of a
+  // new maximum.  Two votes a block (16 sequences of 16K keys, heads of 128: 113.8 ->
+  // 114.9 us; the largest scale itself, by a reduction in every block, 115.9).
+  constexpr bool FIT = DT == PA_KV_INT8;
+  constexpr int kScaleExp = 4;                // exponent of the largest scale when v moves
+  float lim = kRescale, unit = 1.f;           // kRescale + v, 2^-v
   // ---- state: columns 2c, 2c+1 (query heads) of this lane
   float m_run[2] = {kNegInf, kNegInf};
   float l_run[2] = {0.f, 0.f};
@@ -632,8 +643,28 @@ __global__ void __launch_bounds__(kThreads, 3)
       // it by more than kRescale); only then is the column max reduced over
       // the 8 lanes that hold the column.
       float mx[2] = {fmaxf(sc[0], sc[2]), fmaxf(sc[1], sc[3])};
-      const bool need = (mx[0] > m_run[0] + kRescale) || (mx[1] > m_run[1] + kRescale);
-      if (__any_sync(0xffffffffu, need)) {
+      bool need = (mx[0] > m_run[0] + lim) || (mx[1] > m_run[1] + lim);
+      [[maybe_unused]] float vs0 = 0.f, vs1 = 0.f;   // V scales of this lane's tokens
+      bool fits = true;
+      if constexpr (FIT) {
+        vs0 = v0 ? fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r]) : 0.f;
+        vs1 = v1 ? fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r + 8]) : 0.f;
+        const float top = fmaxf(fabsf(vs0), fabsf(vs1));
+        need = need || top >= 128.f * unit;
+        fits = __any_sync(0xffffffffu, top >= unit);
+      }
+      if (__any_sync(0xffffffffu, need) || !fits) {
+        float shift = 0.f;   // of v
+        if constexpr (FIT) {
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(vs0), fabsf(vs1))));
+          const int e = min((int)(most >> 23) - 127, 15);   // (an infinite scale needs no room)
+          const float v = (float)(kScaleExp - e);
+          if (most != 0 && (__uint_as_float(most) >= 128.f * unit || !fits)) {
+            shift = kRescale + v - lim;
+            lim = kRescale + v;
+            unit = __int_as_float((127 + e - kScaleExp) << 23);
+          }
+        }
         float al[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -643,7 +674,11 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float mn = fmaxf(m_run[h], mx[h]);
+          float mn;
+          if constexpr (FIT)   // (lim holds the new v)
+            mn = fmaxf(m_run[h] - shift, mx[h] - (lim - kRescale));
+          else
+            mn = fmaxf(m_run[h], mx[h]);
           al[h] = (mn == kNegInf) ? 1.f : ex2f(m_run[h] - mn);
           m_run[h] = mn;
           l_run[h] *= al[h];
@@ -664,12 +699,10 @@ __global__ void __launch_bounds__(kThreads, 3)
       l_run[0] += pr[0] + pr[2];
       l_run[1] += pr[1] + pr[3];
       if constexpr (DT == PA_KV_INT8) {
-        const float vs0 = fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r]);
-        const float vs1 = fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r + 8]);
-        pr[0] = v0 ? pr[0] * vs0 : 0.f;
-        pr[1] = v0 ? pr[1] * vs0 : 0.f;
-        pr[2] = v1 ? pr[2] * vs1 : 0.f;
-        pr[3] = v1 ? pr[3] * vs1 : 0.f;
+        pr[0] *= vs0;
+        pr[1] *= vs0;
+        pr[2] *= vs1;
+        pr[3] *= vs1;
       }
       // ---- P^T fragment (tokens 2c, 2c+1 | 2c+8, 2c+9; column r): the lane
       // holds P[token r | r + 8][heads 2c, 2c+1], which is the row layout of

@@ -2,7 +2,7 @@
 
 A weight meets its value row's scale before it is rounded to fp16, normalised
 by a power of two that puts the largest scale M of the keys at hand (a tile of
-128) between 1 and 2^7.  Where the product
+128 in a prompt, a block of 16 in decode) between 1 and 2^7.  Where the product
 is below fp16's normal range its rounding is off by 2^-25 in those units, that
 is by 2^-25 M of the value's own, times the code: per key 2^-25 M |code|, over
 the weights' sum (the weights are relative to the row's largest, so it is at
@@ -14,6 +14,7 @@ import torch
 from paged_kv_decode_07_gb300 import pa
 from tests import score_helpers as S
 from tests import test_gpu_prefill as P
+from tests import test_gpu_scored as C
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -68,3 +69,19 @@ def test_prompts(kind, new, lens, hkv, G, D, opt):
                                  v_unit=unit(kv.v_scale, tables, lens, 128), **o)
     S.within(out, ref, bound, f"{kind} {new} {lens}")
     S.lse_within(lse, rl)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,hkv,G,D,kernel", [([8192, 17, 3000], 2, 4, 256, 2), ([32768], 1, 8, 128, 2),
+                                                 ([1000, 40], 2, 6, 256, 5), ([900, 1], 2, 3, 128, 5)])
+def test_scored_decode(kind, lens, hkv, G, D, kernel):
+    kv, q, tables, sl = C.build("int8", lens, hkv, G, D)
+    amplitudes(kv, tables, lens, kind)
+    for o in (dict(), dict(softcap=30.0, window=2000)):
+        out, lse, ws = pa.decode_scored(kv, q, tables, sl, D ** -0.5, score=pa.Score(**o), out_fp32=True,
+                                        return_lse=True, max_seq_len=max(lens), kernel=kernel)
+        assert pa.read_error(ws) == 0
+        ref, rl, bound = S.reference(C.vals(kv), q[:, 0], [1] * len(lens), lens, tables, D ** -0.5, eps_p=S.EPS_FP16,
+                                     v_unit=unit(kv.v_scale, tables, lens, 16), **o)
+        S.within(out[:, 0], ref, bound, f"{kind} {lens} {o}")
+        S.lse_within(lse[:, 0], rl)
