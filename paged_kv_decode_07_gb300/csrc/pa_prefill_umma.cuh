@@ -63,8 +63,10 @@ constexpr float kLazy = 8.0f;        // log2 of how far a score may pass the run
 // largest scale have all their bits down to 2^-14.  v is part of the exponent that
 // the running maximum is subtracted from, so sum and O both hold it, and moves, by
 // the rescale that a new maximum makes, only when a tile's largest scale leaves the
-// range.  (4096 tokens at 8192 keys, heads of 256: 750 -> 759 us.)
-constexpr int kScaleExp = 4, kScaleExpMax = 6;   // exponent of the largest scale when v moves, at most
+// range, which two votes tell.  (4096 tokens at 8192 keys: heads of 256 749 -> 752 us,
+// of 128 636 -> 640; with the largest scale itself, by a reduction in every tile, 759
+// and 638.)
+constexpr int kScaleExp = 4;   // exponent of the largest scale when v moves
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }   // |e| < 127
 
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
@@ -695,7 +697,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   };
   [[maybe_unused]] uint4 sc_next = make_uint4(0, 0, 0, 0);
   if constexpr (DT == PA_KV_INT8) sc_next = row_scales(0, id_next);
-  [[maybe_unused]] int vexp = 0;   // int8: the power of two that all weights hold
+  [[maybe_unused]] float vexp = 0.f, vunit = 1.f;   // int8: the weights hold 2^vexp = 1 / vunit
   float m = FIX ? 0.f : kNegInf, l = 0.f;
   // FIX: the way capped scores are formed (1, 2: the polynomials, 3: the
   // formula), moved on when a product leaves the polynomial's interval
@@ -712,17 +714,8 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     if constexpr (DT == PA_KV_INT8) id_after = page_id(j + 2);
     const uint32_t bad = __ballot_sync(0xffffffffu, id < 0 || id >= p.kv.num_blocks) & 0xffu;
     if (bad && lane == 0) flag(p.hdr, PA_ERRF_BAD_BLOCK_ID);
-    [[maybe_unused]] uint32_t most = 0;   // int8: the tile's largest value scale
-    [[maybe_unused]] float vfix = 1.f;    // and what it changes the weights' power of two by
-    // (all warps of the CTA alike.  Here for heads of 128; for heads of 256 behind the
-    // scores, 759 us against 768; for heads of 128 that place took 671 against 638)
-    auto fit_scales = [&]() {
-      const int e = min((int)(most >> 23) - 127, 15);   // (an infinite scale needs no room)
-      if (most != 0 && (e + vexp < 0 || e + vexp > kScaleExpMax)) {
-        vfix = pow2(kScaleExp - e - vexp);
-        vexp = kScaleExp - e;
-      }
-    };
+    [[maybe_unused]] float vtop = 0.f;   // int8: the largest of this lane's value scales
+    [[maybe_unused]] bool refit = false; // whether the tile's largest one leaves its range
     if constexpr (DT == PA_KV_INT8) {
       const int key = k0t + (lane & 15) * 8;
       const uint4 u = sc_next;
@@ -735,12 +728,11 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
         x[2 * i] = key + 2 * i >= w.see_lo && key + 2 * i < w.see_hi ? y.x : 0.f;
         x[2 * i + 1] = key + 2 * i + 1 >= w.see_lo && key + 2 * i + 1 < w.see_hi ? y.y : 0.f;
       }
-      float top = fabsf(x[0]);
+      vtop = fabsf(x[0]);
 #pragma unroll
-      for (int i = 1; i < 7; i += 2) top = fmaxf(fmaxf(fabsf(x[i]), fabsf(x[i + 1])), top);
-      top = fmaxf(top, fabsf(x[7]));
-      most = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(top));
-      if constexpr (D == 128) fit_scales();
+      for (int i = 1; i < 7; i += 2) vtop = fmaxf(fmaxf(fabsf(x[i]), fabsf(x[i + 1])), vtop);
+      vtop = lane < 16 ? 0.f : fmaxf(vtop, fabsf(x[7]));
+      refit = __any_sync(0xffffffffu, vtop >= 128.f * vunit) || !__any_sync(0xffffffffu, vtop >= vunit);
       __syncwarp();
       float4 *d = reinterpret_cast<float4 *>(wsc + (lane >> 4) * kKeys + (lane & 15) * 8);
       d[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -957,9 +949,8 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
         mx = largest();
       }
     }
-    if constexpr (DT == PA_KV_INT8 && D == 256) fit_scales();
     // ---- the running maximum moves when some score passes it by 2^kLazy
-    if (named_sync_or(pair, 64, mx > m + kLazy || (DT == PA_KV_INT8 && vfix != 1.f))) {
+    if (named_sync_or(pair, 64, mx > m + kLazy || refit)) {
       // with the row's other keys
       if (hf == 0) c.red[row] = mx;
       named_sync(pair, 64);
@@ -971,7 +962,15 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       if (hf == 0) mx = c.red[row];
       const float mn = fmaxf(m, mx);
       float al = mn == kNegInf ? 1.f : ex2_approx(m - mn);
-      if constexpr (DT == PA_KV_INT8) al *= vfix;
+      if constexpr (DT == PA_KV_INT8) {
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(vtop));
+        const int e = min((int)(most >> 23) - 127, 15);   // (an infinite scale needs no room)
+        if (refit && most != 0) {   // all warps of the CTA alike
+          al *= pow2(kScaleExp - e) * vunit;
+          vunit = pow2(e - kScaleExp);
+          vexp = (float)(kScaleExp - e);
+        }
+      }
       m = mn;
       l *= al;
       if (j > 0) {
@@ -995,7 +994,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     }
     // ---- weights
     {
-      const float mu = (m == kNegInf ? 0.f : m) - (DT == PA_KV_INT8 ? (float)vexp : 0.f);
+      const float mu = (m == kNegInf ? 0.f : m) - (DT == PA_KV_INT8 ? vexp : 0.f);
       const float2 nm = make_float2(-mu, -mu), ff = make_float2(fs, fs);
       const float2 uu = make_float2(fu, fu), cc = make_float2(p.sc.cap_log2, p.sc.cap_log2);
       float2 l2 = make_float2(0.f, 0.f);
@@ -1066,7 +1065,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   }
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
   const float inv = l > 0.f ? vg / l : 0.f;
-  const float lse = l > 0.f ? (m - (DT == PA_KV_INT8 ? (float)vexp : 0.f) + log2f(l)) * 0.69314718055994531f : kNegInf;
+  const float lse = l > 0.f ? (m - (DT == PA_KV_INT8 ? vexp : 0.f) + log2f(l)) * 0.69314718055994531f : kNegInf;
   // The tile's MMAs are complete (of a tile without keys: its queries are all there),
   // so its shared memory is free: the output goes through it (16-byte pieces,
   // swizzled by row) and leaves in whole rows.  (Stored from here, a row per lane,
