@@ -435,7 +435,8 @@ int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_sco
  * row's scale is in the weight, relative to the largest scale of 128 neighbouring
  * keys: of any size, with fewer bits where weight and scale together are below
  * 2^-14 of the largest).  Scores capped at 55 or less over a bf16 cache take |v| up
- * to 2^17: their weights are not relative to the row's largest. */
+ * to 2^17: their weights are not relative to the row's largest.
+ * A NaN in a query, or in a key or value that it sees, is in its output (and lse). */
 typedef struct pa_prefill_problem {
   int32_t batch;               /* B >= 0 */
   int32_t num_q_heads;         /* Hq, a multiple of num_kv_heads; Hq / Hkv <= 8 */

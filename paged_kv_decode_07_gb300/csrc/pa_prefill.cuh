@@ -158,23 +158,22 @@ __device__ __forceinline__ void join_row(const PrefillParams &p, size_t part, si
   float sum = 0.f, acc[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  if (M != kNegInf)
-    for (int s = 0; s < parts; ++s) {
-      const float ls = p.part_lse[part + s * pitch];
-      if (ls == kNegInf) continue;
-      const float w = expf(ls - M);
-      sum += w;
-      const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (part + s * pitch) * D);
+  for (int s = 0; s < parts; ++s) {
+    const float ls = p.part_lse[part + s * pitch];
+    if (ls == kNegInf) continue;
+    const float w = expf(ls - M);   // (a NaN among a part's scores is in its lse)
+    sum += w;
+    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (part + s * pitch) * D);
 #pragma unroll
-      for (int i = 0; i < D / 128; ++i) {
-        const float4 x = __ldcs(src + i * 32 + lane);
-        acc[4 * i] += w * x.x;
-        acc[4 * i + 1] += w * x.y;
-        acc[4 * i + 2] += w * x.z;
-        acc[4 * i + 3] += w * x.w;
-      }
+    for (int i = 0; i < D / 128; ++i) {
+      const float4 x = __ldcs(src + i * 32 + lane);
+      acc[4 * i] += w * x.x;
+      acc[4 * i + 1] += w * x.y;
+      acc[4 * i + 2] += w * x.z;
+      acc[4 * i + 3] += w * x.w;
     }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < D / 128; ++i) {
     const size_t at = row * D + (i * 32 + lane) * 4;
@@ -185,7 +184,7 @@ __device__ __forceinline__ void join_row(const PrefillParams &p, size_t part, si
       *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
           make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
   }
-  if (lane == 0 && p.lse_out) p.lse_out[row] = sum > 0.f ? M + logf(sum) : kNegInf;
+  if (lane == 0 && p.lse_out) p.lse_out[row] = sum != 0.f ? M + logf(sum) : kNegInf;
 }
 
 // all rows in p.splits pieces

@@ -1064,8 +1064,9 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
     __syncwarp();
   }
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.f;
-  const float inv = l > 0.f ? vg / l : 0.f;
-  const float lse = l > 0.f ? (m - (DT == PA_KV_INT8 ? vexp : 0.f) + log2f(l)) * 0.69314718055994531f : kNegInf;
+  // (a sum of 0: the row saw no key; a NaN among its scores is in the sum and goes on)
+  const float inv = l != 0.f ? vg / l : 0.f;
+  const float lse = l != 0.f ? (m - (DT == PA_KV_INT8 ? vexp : 0.f) + log2f(l)) * 0.69314718055994531f : kNegInf;
   // The tile's MMAs are complete (of a tile without keys: its queries are all there),
   // so its shared memory is free: the output goes through it (16-byte pieces,
   // swizzled by row) and leaves in whole rows.  (Stored from here, a row per lane,
@@ -1088,7 +1089,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
       for (int i = 0; i < 16; ++i) o[i] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = l > 0.f ? o[i] * inv : 0.f;
+    for (int i = 0; i < 16; ++i) o[i] = l != 0.f ? o[i] * inv : 0.f;
     const int d = hf * Gm::NO + ch;
     if (wide) {
 #pragma unroll
