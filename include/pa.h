@@ -405,7 +405,9 @@ int pa_rope_frequencies(int32_t rot_dim, double base, int32_t kind, double facto
  * sequence's chunk are never used, whatever their slots hold; keys that some
  * queries of a chunk see and others do not (later tokens of a prompt, other
  * documents) have weight 0 for the others, so their values must be finite, as
- * in any product with a masked softmax. */
+ * in any product with a masked softmax.  A NaN in a query, or in a key or value
+ * that it sees, is in its output (a NaN score in its lse too; pa_decode and
+ * pa_verify give such a row 0 and -inf). */
 typedef struct pa_score {
   float softcap;               /* 0: none; else > 0 and finite (above 1e18: none) */
   int32_t window;              /* 0: none; else the last `window` keys up to the query's own */
@@ -435,8 +437,7 @@ int pa_decode_scored(const pa_kv_cache *kv, const pa_problem *prob, const pa_sco
  * row's scale is in the weight, relative to the largest scale of 128 neighbouring
  * keys: of any size, with fewer bits where weight and scale together are below
  * 2^-14 of the largest).  Scores capped at 55 or less over a bf16 cache take |v| up
- * to 2^17: their weights are not relative to the row's largest.
- * A NaN in a query, or in a key or value that it sees, is in its output (and lse). */
+ * to 2^17: their weights are not relative to the row's largest. */
 typedef struct pa_prefill_problem {
   int32_t batch;               /* B >= 0 */
   int32_t num_q_heads;         /* Hq, a multiple of num_kv_heads; Hq / Hkv <= 8 */

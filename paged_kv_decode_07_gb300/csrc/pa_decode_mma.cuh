@@ -908,6 +908,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   const float vg = has_global_scale(DT) ? p.kv.vg : 1.0f;
   const int G = p.G, tid = threadIdx.x;
   __shared__ float s_f[kWarps][8], s_L[8];
+  // whether a row saw a key; scored: a NaN among its scores is in its sum and goes on
+  auto some = [](float sum) { return SC ? sum != 0.f : sum > 0.f; };
   auto row_of = [&](int h) { return ((size_t)b * Q + qi) * p.Hq + (size_t)kvh * G + h; };
   if (tid < R) {
     const int h = tid;
@@ -923,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       s_f[w][h] = f;
     }
     s_L[h] = L;
-    const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : kNegInf;
+    const float lse = some(L) ? (M + __log2f(L)) * 0.69314718055994531f : kNegInf;
     if constexpr (CL) {
       reinterpret_cast<float *>(smem + kWarps * Gm::WARP_BYTES)[8 * D + h] = lse;
     } else if (it.parts <= 1) {
@@ -955,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       acc[3] += f * o4.w;
     }
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (L > 0.f) v = make_float4(acc[0] / L * vg, acc[1] / L * vg, acc[2] / L * vg, acc[3] / L * vg);
+    if (some(L)) v = make_float4(acc[0] / L * vg, acc[1] / L * vg, acc[2] / L * vg, acc[3] / L * vg);
     if constexpr (CL) {   // this CTA's partial, for the cluster merge below
       *reinterpret_cast<float4 *>(smem + kWarps * Gm::WARP_BYTES + (h * D + d) * 4) = v;
     } else if (it.parts <= 1) {
@@ -993,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           wsum += w;
         }
       s_csum[h] = wsum;
-      if (rank == 0 && p.lse_out) p.lse_out[row_of(h)] = wsum > 0.f ? M + __logf(wsum) : kNegInf;
+      if (rank == 0 && p.lse_out) p.lse_out[row_of(h)] = some(wsum) ? M + __logf(wsum) : kNegInf;
     }
     __syncthreads();
     for (int idx = tid; idx < R * nq; idx += kThreads) {
@@ -1014,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           acc[3] += w * oj[j].w;
         }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (wsum > 0.f) v = make_float4(acc[0] / wsum, acc[1] / wsum, acc[2] / wsum, acc[3] / wsum);
+      if (some(wsum)) v = make_float4(acc[0] / wsum, acc[1] / wsum, acc[2] / wsum, acc[3] / wsum);
       store4(row_of(h), d, v);
     }
     cluster_sync_all();   // no CTA leaves while another still reads its partial

@@ -11,7 +11,13 @@
 namespace pa {
 namespace {
 
-
+// the larger one; NaN if either is (a NaN among a part's scores is in its lse, and
+// goes on to the row)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 
 __device__ __forceinline__ void store4(void *out, int out_fp32, size_t off, float4 v) {
   if (out_fp32) {
@@ -51,15 +57,15 @@ __device__ void merge_row(const float *po, size_t pstride, const float *pl, size
   for (int q = tid; q < parts; q += kThreads) {
     const float l = pl[(size_t)q * lstride];
     if (q < kChunk) s_l[q] = l;
-    M = fmaxf(M, l);
+    M = max_nan(M, l);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) s_red[warp] = M;
   __syncthreads();
   if (tid == 0) {
     float m = s_red[0];
-    for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_red[w]);
+    for (int w = 1; w < kThreads / 32; ++w) m = max_nan(m, s_red[w]);
     s_M = m;
   }
   __syncthreads();
@@ -224,9 +230,9 @@ __global__ void __launch_bounds__(kThreads) merge_window_kernel(const AttnParams
   const size_t prow = parts ? ((size_t)ui.slot_base * p.kv.hkv + hq / p.G) * p.R + hq % p.G : 0;
   const float *po = p.part_o + prow * D, *pl = p.part_lse + prow;
   float M = kNegInf, sum = 0.f;
-  for (int q = lane; q < parts; q += 32) M = fmaxf(M, pl[q * pitch]);
+  for (int q = lane; q < parts; q += 32) M = max_nan(M, pl[q * pitch]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
   float4 acc[D / 128] = {};
   for (int q0 = 0; q0 < parts; q0 += 32) {
     const float l = q0 + lane < parts ? pl[(q0 + lane) * pitch] : kNegInf;
@@ -236,12 +242,12 @@ __global__ void __launch_bounds__(kThreads) merge_window_kernel(const AttnParams
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < D / 128; ++i)
     store4(p.out, p.out_fp32, (size_t)row * D + (i * 32 + lane) * 4,
            make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
-  if (p.lse_out && lane == 0) p.lse_out[row] = sum > 0.f ? M + __logf(sum) : kNegInf;
+  if (p.lse_out && lane == 0) p.lse_out[row] = sum != 0.f ? M + __logf(sum) : kNegInf;
 }
 
 // public pa_merge: part_out [S, R, D], part_lse [S, R]

@@ -6,6 +6,7 @@ import torch
 from paged_kv_decode_07_gb300 import pa
 from tests import score_helpers as S
 from tests import test_gpu_prefill as P
+from tests import test_gpu_scored as C
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -76,3 +77,42 @@ def test_a_prompts_values(fmt, D, opt):
     bad = torch.zeros(out.shape, dtype=torch.bool, device=DEV)
     bad[:, :4, list(dims)] = True
     assert torch.equal(out.isnan(), bad)
+
+
+# planned and merged, merged by a warp a row (windows of many rows), one launch
+DECODES = [([3000, 40, 700], 2, 2, {}), ([2000] * 40, 2, 2, dict(window=1000)), ([900, 300], 1, 5, {}), ([60, 9], 2, 5, {})]
+
+
+@pytest.mark.parametrize("opt", ["plain", "cap", "both"])
+@pytest.mark.parametrize("fmt,G,D", [("bf16", 4, 128), ("bf16", 3, 256), ("int8", 4, 256), ("fp8", 8, 128), ("nvfp4", 2, 256)])
+@pytest.mark.parametrize("lens,hkv,kernel,extra", DECODES)
+def test_scored_decode(fmt, G, D, opt, lens, hkv, kernel, extra):
+    kv, q, tables, sl = C.build(fmt, lens, hkv, G, D)
+    o = dict(options(opt, hkv * G), **extra)
+    ref, rl, bound = S.reference(C.vals(kv), q[:, 0], [1] * len(lens), lens, tables, 0.1, eps_p=C.EPS_P[fmt],
+                                 v_unit=kv.v_scale.clone() if fmt == "int8" else None, **o)
+    # one query head of the last sequence, and a key of the first, of the last kv head
+    q[-1, 0, 0, 5] = NAN
+    at = lens[0] - 20
+    spoil_key(kv, int(tables[0, at // 16]), at % 16, hkv - 1)
+    out, lse, ws = pa.decode_scored(kv, q, tables, sl, 0.1, score=pa.Score(**o), out_fp32=True, return_lse=True,
+                                    max_seq_len=max(lens), kernel=kernel)
+    assert pa.read_error(ws) == 0
+    bad = torch.zeros(out.shape[:1] + out.shape[2:3], dtype=torch.bool, device=DEV)
+    bad[-1, 0] = True
+    bad[0, (hkv - 1) * G:] = True
+    assert out[:, 0][bad].isnan().all() and lse[:, 0][bad].isnan().all()
+    S.within(out[:, 0][~bad], ref[~bad], bound[~bad])
+    S.lse_within(lse[:, 0][~bad], rl[~bad])
+
+
+@pytest.mark.parametrize("kernel", [2, 5])
+def test_a_key_that_is_the_only_one_seen(kernel):
+    """Every part of the row is empty or NaN."""
+    lens = [700, 1]
+    kv, q, tables, sl = C.build("bf16", lens, 2, 4, 128)
+    for b, n in enumerate(lens):
+        kv.k_cache[int(tables[b, (n - 1) // 16]), :, (n - 1) % 16] = NAN
+    out, lse, _ = pa.decode_scored(kv, q, tables, sl, 0.1, score=pa.Score(window=1), return_lse=True, max_seq_len=700,
+                                   kernel=kernel)
+    assert out.isnan().all() and lse.isnan().all()
