@@ -58,7 +58,8 @@
  *     verify row with seq_len < q_len) never trap: the offending block is
  *     skipped or the length clamped, and a bit is set in the workspace
  *     header, which pa_read_error returns.  The flags describe the most
- *     recent pa_decode / pa_verify call that used the workspace.
+ *     recent pa_decode / pa_verify / pa_decode_scored / pa_prefill call
+ *     that used the workspace; one without sequences or tokens clears them.
  *   - seq_lens[b] = 0 marks a padded row: its outputs are 0 and lse -inf.
  */
 #ifndef PA_H_
@@ -406,8 +407,8 @@ int pa_rope_frequencies(int32_t rot_dim, double base, int32_t kind, double facto
  * queries of a chunk see and others do not (later tokens of a prompt, other
  * documents) have weight 0 for the others, so their values must be finite, as
  * in any product with a masked softmax.  A NaN in a query, or in a key or value
- * that it sees, is in its output (a NaN score in its lse too; pa_decode and
- * pa_verify give such a row 0 and -inf). */
+ * that it sees, is in its output (a NaN score in its lse too; pa_decode
+ * takes a row with one for a row that sees no key). */
 typedef struct pa_score {
   float softcap;               /* 0: none; else > 0 and finite (above 1e18: none) */
   int32_t window;              /* 0: none; else the last `window` keys up to the query's own */

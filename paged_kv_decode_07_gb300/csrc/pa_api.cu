@@ -334,6 +334,20 @@ ScoreView score_view(const pa_score *sc, float softmax_scale) {
   return v;
 }
 
+// The end of a call without sequences or tokens: the flags of its workspace, if it
+// has one, are its own.  (Such a call is allowed without a workspace, so what is
+// no memory that the device was given is left alone.)
+int nothing_to_do(void *ws, size_t ws_bytes, cudaStream_t s) {
+  cudaPointerAttributes at;
+  if (!ws || !aligned16(ws) || ws_bytes < kHdrWords * 4) return PA_OK;
+  if (cudaPointerGetAttributes(&at, ws) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return PA_OK;
+  }
+  if (at.type == cudaMemoryTypeUnregistered) return PA_OK;
+  return cudaMemsetAsync(ws, 0, 16, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 // sc: scored decode (pa_decode_scored), else null
 int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *o, void *ws,
                   size_t ws_bytes, cudaStream_t stream, bool verify,
@@ -351,7 +365,7 @@ int run_attention(const pa_kv_cache *kv, const pa_problem *p, const pa_options *
   if (sc && (kernel == 1 || kernel == 3 || kernel == 4 || test_flags ||
              !scored_supported(kv->dtype, kv->head_dim, p->num_q_heads / kv->num_kv_heads)))
     return PA_ERR_UNSUPPORTED;
-  if (p->batch == 0) return PA_OK;
+  if (p->batch == 0) return nothing_to_do(ws, ws_bytes, stream);
   const int G = p->num_q_heads / kv->num_kv_heads;
   // Kernel choice.  auto: tensor cores (the CUDA cores cannot issue the
   // 3,072 FMA per token and kv head, plus the quantised formats' dequant, at
@@ -873,7 +887,8 @@ int pa_prefill(const pa_kv_cache *kv, const pa_prefill_problem *p, const pa_scor
   if (st) return st;
   st = check_score(score);
   if (st) return st;
-  if (p->batch == 0 || p->num_tokens == 0) return PA_OK;
+  if (p->batch == 0 || p->num_tokens == 0)
+    return nothing_to_do(ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
   if (!p->q || !p->q_starts || !p->block_tables || !p->seq_lens || !p->out) return PA_ERR_INVALID_ARG;
   if (!aligned16(p->q) || !aligned16(p->out) || !aligned4(p->q_starts) ||
       !aligned4(p->block_tables) || !aligned4(p->seq_lens) || !aligned4(p->lse_out))
