@@ -122,6 +122,8 @@ struct PCtl {
   uint32_t tmem;
   int abort;
   int lo[16], hi[16];           // keys that some row of each softmax warp sees
+  int blind[16];                // GAPS: whether a token of the warp sees nothing, and
+  uint32_t seen[16][8];         // bit i: a row of the warp sees key i of the tile's own tokens
   float red[256];               // a row's maximum (at the end its sum), from one half to the other
 };
 
@@ -143,14 +145,49 @@ __device__ __forceinline__ void wait_p(uint64_t *bar, uint32_t parity, PCtl &c, 
   if (!mbar_test(bar, parity)) wait_slow(bar, parity, c, hdr);
 }
 
+static_assert(sizeof(PCtl) <= 2048, "PGeo::SMEM leaves 2 KB");
+
 // what every role knows of the CTA's work
 struct Work {
   int b, kvh, row0, nrows;   // sequence, kv head, first flat row, rows
   int start, len, n;         // query tokens' start and count, keys in the cache
   int see_lo, see_hi;        // keys that some row sees
+  int gap0;                  // see `seen`
   int kt0, ntiles;           // key tiles of this CTA
   const int *trow;
 };
+
+// GAPS: the caller gave first keys.  The keys from see_lo to see_hi are all seen by some
+// row, but for those of the tile's own tokens (at most 256, from key gap0 on) that see
+// nothing themselves, such as padding between packed documents: their slots may hold
+// anything, so they are filled with zeros like the keys outside.  (A row that sees
+// anything sees its own key or, up to a prefix, all from its first one on; keys before
+// the tile's tokens are seen by the row with the least first key.)  gap0 is 0x7fffffff
+// where every token sees something.  Kernels of their own: in one kernel with the
+// others it took 5 to 17 % from calls without first keys (packed documents of 700 keys,
+// int8, heads of 256: no change; of 4000, heads of 128: bf16 206 -> 214 us).
+template <bool GAPS, int SMW>
+__device__ __forceinline__ bool seen(const Work &w, const PCtl &c, int key) {
+  if constexpr (!GAPS) return true;
+  if (key < w.gap0) return true;
+  const uint32_t i = (uint32_t)(key - w.gap0);
+  if (i >= 256u) return true;
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int k = 0; k < SMW; ++k) any |= c.seen[k][i >> 5];
+  return (any >> (i & 31)) & 1u;
+}
+// bit i: key + i * step is seen, i < N
+template <bool GAPS, int SMW, int N>
+__device__ __forceinline__ uint32_t seen_mask(const Work &w, const PCtl &c, int key, int step) {
+  uint32_t m = 0xffffffffu;
+  if (GAPS && key + N * step > w.gap0) {
+#pragma unroll 1
+    for (int i = 0; i < N; ++i)
+      if (!seen<GAPS, SMW>(w, c, key + i * step)) m &= ~(1u << i);
+  }
+  return m;
+}
 
 // instruction descriptor (kind::f16, D fp32): bf16 or f16 operands, B K-major or MN-major
 __host__ __device__ constexpr uint32_t idesc_pf(bool bf16, int N, bool b_mn) {
@@ -388,7 +425,7 @@ __device__ __forceinline__ void copy_arrive(uint64_t *bar) {
 // holds must be zero).  A unit's barrier counts the threads' copies as they
 // land, so the whole ring is in flight; the MMA warps order their reads after
 // these generic-proxy writes by a proxy fence behind the wait.
-template <int D>
+template <int D, bool GAPS>
 __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t) {
   using Gm = PGeo<PA_KV_BF16, D>;
   // piece `piece` of rows r0, r0 + 8, ..: two rows of every page, 1 KB apart
@@ -422,6 +459,8 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
     bool dense = k0 >= w.see_lo && k0 + kKeys <= w.see_hi;
 #pragma unroll
     for (int g = 0; g < 8; ++g) dense = dense && (uint32_t)id[g] < (uint32_t)p.kv.num_blocks;
+    const uint32_t mask = seen_mask<GAPS, Gm::SMW, 16>(w, c, k0 + r0, 8);
+    if (GAPS) dense = dense && mask == 0xffffffffu;
 #pragma unroll
     for (int h = 0; h < Gm::H; ++h) {
       const int st = u % Gm::NU;
@@ -438,7 +477,8 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) {   // rows 8 i + r0: page i / 2
           const int g = id[i >> 1], key = k0 + i * 8 + r0;
-          const bool valid = (uint32_t)g < (uint32_t)p.kv.num_blocks && key >= w.see_lo && key < w.see_hi;
+          const bool valid = (uint32_t)g < (uint32_t)p.kv.num_blocks && key >= w.see_lo && key < w.see_hi &&
+                             (!GAPS || ((mask >> i) & 1));
           copy16z(dst + i * 1024, base + h * 256 + (valid ? (size_t)g * page + (i & 1) * (8 * D * 2) : 0), valid);
         }
       }
@@ -459,7 +499,7 @@ __device__ void role_copy(const PrefillParams &p, const Work &w, uint8_t *smem, 
 // that their latency passes meanwhile (a whole unit ahead was no faster: the
 // instructions are the bound).  int8 and FP8: 8 lanes per key row, 16 codes a
 // lane; NVFP4: 4 lanes per row, 32 codes (two scale blocks) a lane.
-template <int DT, int D>
+template <int DT, int D, bool GAPS>
 __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c, int t, int h) {
   using Gm = PGeo<DT, D>;
   constexpr bool FP4 = DT == PA_KV_NVFP4;
@@ -487,14 +527,15 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
   auto ids = [&](const Order<D> &o, int (&d)[2 * IT]) {   // -1: nothing of this thread's row is read
     const int k0 = (w.kt0 + o.j) * kKeys;
     const int *const at = w.trow + (k0 + r0) / kBlock;
-    if (!o.done() && k0 >= w.see_lo && k0 + kKeys <= w.see_hi) {
+    const uint32_t mask = seen_mask<GAPS, Gm::SMW, 2 * IT>(w, c, k0 + r0, RPI);
+    if (!o.done() && k0 >= w.see_lo && k0 + kKeys <= w.see_hi && (!GAPS || mask == 0xffffffffu)) {
 #pragma unroll
       for (int i = 0; i < 2 * IT; ++i) d[i] = __ldg(at + i * (RPI / kBlock));
     } else {
 #pragma unroll
       for (int i = 0; i < 2 * IT; ++i) {
         const int key = k0 + i * RPI + r0;
-        d[i] = !o.done() && key >= w.see_lo && key < w.see_hi ? __ldg(at + i * (RPI / kBlock)) : -1;
+        d[i] = !o.done() && key >= w.see_lo && key < w.see_hi && (!GAPS || ((mask >> i) & 1)) ? __ldg(at + i * (RPI / kBlock)) : -1;
       }
     }
   };
@@ -637,7 +678,7 @@ __device__ __forceinline__ float2 tanh_unit(float2 u) {
 }
 
 // CAP, BIAS: whether scores are capped and biased (kernels of their own: either
-// costs the others registers).  FIX: capped scores lie in [-cap, cap], so 2^score
+// costs the others registers).  GAPS: see `seen`.  FIX: capped scores lie in [-cap, cap], so 2^score
 // can be taken as it is, without a maximum, where fp32 and bf16 hold it and its
 // sums: cap * log2 e <= kFixedCap = 80, that is weights of 2^+-80, sums of up to
 // 2^30 of them, and values up to 2^17 without overflow.  (fp16 weights could not;
@@ -646,7 +687,7 @@ __device__ __forceinline__ float2 tanh_unit(float2 u) {
 // may then take turns, see role_mma).
 constexpr float kFixedCap = 80.f;
 
-template <int DT, int D, bool CAP, bool BIAS, bool FIX>
+template <int DT, int D, bool CAP, bool BIAS, bool FIX, bool GAPS>
 __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *smem, PCtl &c,
                              uint32_t tmem, bool partial, int r_lo, int r_hi, int r_pos, bool live,
                              size_t r_out, float slope) {
@@ -727,6 +768,11 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
         const float2 y = h2u_to_f2(h2[i]);
         x[2 * i] = key + 2 * i >= w.see_lo && key + 2 * i < w.see_hi ? y.x : 0.f;
         x[2 * i + 1] = key + 2 * i + 1 >= w.see_lo && key + 2 * i + 1 < w.see_hi ? y.y : 0.f;
+      }
+      if (GAPS && k0t + kKeys > w.gap0) {
+        const uint32_t mask = seen_mask<GAPS, Gm::SMW, 8>(w, c, key, 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (mask >> i) & 1 ? x[i] : 0.f;
       }
       vtop = fabsf(x[0]);
 #pragma unroll
@@ -1123,7 +1169,7 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
 
 // --------------------------------------------------------------------- kernel
 
-template <int DT, int D, bool CAP, bool BIAS, bool FIX>
+template <int DT, int D, bool CAP, bool BIAS, bool FIX, bool GAPS>
 __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     prefill_umma_kernel(const PrefillParams p) {
   using Gm = PGeo<DT, D>;
@@ -1213,6 +1259,17 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
       c.lo[warp] = lo;
       c.hi[warp] = hi;
     }
+    if constexpr (GAPS) {
+      const int blind = __any_sync(0xffffffffu, live && !sees && r_pos >= 0);
+      if (lane == 0) c.blind[warp] = blind;
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {   // (a range's ends are below 2^31, tok0's position above -2^30)
+        const long long at = (long long)(n - w.len + tok0) + 32 * i;
+        const int x = (int)min(max(r_lo - at, 0LL), 32LL), y = (int)min(max(r_hi - at, 0LL), 32LL);
+        const uint32_t any = __reduce_or_sync(0xffffffffu, y > x ? (0xffffffffu >> (32 - (y - x))) << x : 0u);
+        if (lane == 0) c.seen[warp][i] = any;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1225,6 +1282,10 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     w.see_lo = min(w.see_lo, c.lo[i]);
     w.see_hi = max(w.see_hi, c.hi[i]);
   }
+  w.gap0 = 0x7fffffff;
+  if constexpr (GAPS)
+    for (int i = 0; i < Gm::SMW; ++i)
+      if (c.blind[i]) w.gap0 = n - w.len + tok0;
   {
     const int t0 = w.see_lo < w.see_hi ? w.see_lo / kKeys : 0;
     const int t1 = w.see_lo < w.see_hi ? (w.see_hi + kKeys - 1) / kKeys : 0;
@@ -1264,7 +1325,7 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_SM>();
     // the second row tile's groups have nothing to do when it is empty
     if (warp < 8 || w.nrows > 128)
-      role_softmax<DT, D, CAP, BIAS, FIX>(p, w, smem, c, tmem, to.pieces > 1, r_lo, r_hi, r_pos, live, r_out, slope);
+      role_softmax<DT, D, CAP, BIAS, FIX, GAPS>(p, w, smem, c, tmem, to.pieces > 1, r_lo, r_hi, r_pos, live, r_out, slope);
   } else if (warp < Gm::SMW + 4) {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_MMA>();
     if (warp < Gm::SMW + Gm::MT)
@@ -1273,9 +1334,9 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   } else {
     if constexpr (REGS) setmaxnreg_to<Gm::LAUNCH_REGS, Gm::REG_COPY>();
     if constexpr (Gm::QUANT)
-      role_dequant<DT, D>(p, w, smem, c, (tid - (Gm::SMW + 4) * 32) & 127, (warp - Gm::SMW - 4) >> 2);
+      role_dequant<DT, D, GAPS>(p, w, smem, c, (tid - (Gm::SMW + 4) * 32) & 127, (warp - Gm::SMW - 4) >> 2);
     else
-      role_copy<D>(p, w, smem, c, tid - (Gm::SMW + 4) * 32);
+      role_copy<D, GAPS>(p, w, smem, c, tid - (Gm::SMW + 4) * 32);
   }
   tc_fence_before();
   __syncthreads();
@@ -1286,10 +1347,10 @@ __global__ void __launch_bounds__(PGeo<DT, D>::THREADS, 1)
   }
 }
 
-template <int DT, int D, bool CAP, bool BIAS, bool FIX = false>
-cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
+template <int DT, int D, bool CAP, bool BIAS, bool FIX, bool GAPS>
+cudaError_t launch_kernel(const PrefillParams &p, cudaStream_t s) {
   using Gm = PGeo<DT, D>;
-  auto kern = prefill_umma_kernel<DT, D, CAP, BIAS, FIX>;
+  auto kern = prefill_umma_kernel<DT, D, CAP, BIAS, FIX, GAPS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
   if (e != cudaSuccess) return e;
   if constexpr (Gm::THREADS > 512) {
@@ -1306,6 +1367,12 @@ cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
   const long long grid = tiles * p.kv.hkv * p.splits + p.tail;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(kern, (unsigned)grid, Gm::THREADS, Gm::SMEM, s, p);
+}
+
+template <int DT, int D, bool CAP, bool BIAS, bool FIX = false>
+cudaError_t launch_one(const PrefillParams &p, cudaStream_t s) {
+  return p.sc.first_key ? launch_kernel<DT, D, CAP, BIAS, FIX, true>(p, s)
+                        : launch_kernel<DT, D, CAP, BIAS, FIX, false>(p, s);
 }
 
 template <int DT, int D>
