@@ -72,6 +72,9 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 4 : 2)
   using Gm = Geo<DT, NT>;
   constexpr int NSTAGE = Gm::NSTAGE, ROW = Gm::ROW, SROW = Gm::SROW, NC = Gm::NC, EPO = Gm::EPO;
   constexpr float kRescale = 8.0f;
+  [[maybe_unused]] constexpr int kScaleExp = 4;   // int8: exponent of the largest V scale when v moves
+  float lim = kRescale;                           // kRescale + v
+  [[maybe_unused]] float unit = 1.f;              // 2^-v
 
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -306,17 +309,40 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 4 : 2)
       // the lane's own scores decide whether the running max must move; only
       // then is the column max reduced over the 8 lanes holding the column
       mx[k] = fmaxf(sc[k][0], sc[k][1]);
-      need |= mx[k] > m_run[k] + kRescale;
+      need |= mx[k] > m_run[k] + lim;
+    }
+    // int8: the weights hold 2^v, so that they keep their bits beside the value rows'
+    // scales (as in the decode kernel; 4 sequences of 64K keys, 8 queries: 333 -> 340 us,
+    // 32 of 4K, 4 queries: 186 -> 185)
+    float vs0 = 1.f, vs1 = 1.f;
+    [[maybe_unused]] bool fits = true;
+    if constexpr (DT == PA_KV_INT8) {
+      vs0 = (valid && r < nvalid) ? fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r]) : 0.f;
+      vs1 = (valid && r + 8 < nvalid) ? fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r + 8])
+                                      : 0.f;
+      const float top = fmaxf(fabsf(vs0), fabsf(vs1));
+      fits = __any_sync(0xffffffffu, top >= unit);
+      need |= top >= 128.f * unit || !fits;
     }
     const bool any_need = __syncthreads_or(need);   // B2
     if (any_need) {
+      float shift = 0.f;
+      if constexpr (DT == PA_KV_INT8) {
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(vs0), fabsf(vs1))));
+        if (most != 0 && (!fits || __uint_as_float(most) >= 128.f * unit)) {   // all warps of the CTA alike
+          const int e = min((int)(most >> 23) - 127, 15);
+          shift = kRescale + (float)(kScaleExp - e) - lim;
+          lim = kRescale + (float)(kScaleExp - e);
+          unit = __int_as_float((127 + e - kScaleExp) << 23);
+        }
+      }
 #pragma unroll
       for (int k = 0; k < EPO; ++k) {
         float v = mx[k];
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float mn = fmaxf(m_run[k], v);
+        const float mn = DT == PA_KV_INT8 ? fmaxf(m_run[k] - shift, v - (lim - kRescale)) : fmaxf(m_run[k], v);
         const float al = (mn == kNegInf) ? 1.f : ex2f(m_run[k] - mn);
         m_run[k] = mn;
         l_run[k] *= al;
@@ -327,12 +353,6 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 4 : 2)
     // 4c'+{0,1}, token 2c'+8+{0,1} at slot 4c'+2+{0,1}
     {
       const int slot0 = (r >> 1) * 4 + (r & 1), slot1 = slot0 + 2;
-      float vs0 = 1.f, vs1 = 1.f;
-      if constexpr (DT == PA_KV_INT8) {
-        vs0 = (valid && r < nvalid) ? fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r]) : 0.f;
-        vs1 = (valid && r + 8 < nvalid) ? fp16_bits_to_f(reinterpret_cast<const uint16_t *>(sVs)[r + 8])
-                                        : 0.f;
-      }
 #pragma unroll
       for (int k = 0; k < EPO; ++k) {
         const float p0 = sc[k][0] == kNegInf ? 0.f : ex2f(sc[k][0] - m_run[k]);

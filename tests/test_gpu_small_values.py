@@ -85,3 +85,17 @@ def test_scored_decode(kind, lens, hkv, G, D, kernel):
                                      v_unit=unit(kv.v_scale, tables, lens, 16), **o)
         S.within(out[:, 0], ref, bound, f"{kind} {lens} {o}")
         S.lse_within(lse[:, 0], rl)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,lens,hkv,G,D", [(4, [8192, 17, 3000], 2, 4, 256), (8, [5000, 900], 1, 6, 256), (3, [4000, 40], 2, 4, 128)])
+def test_verify(kind, m, lens, hkv, G, D):
+    kv, q, starts, tables, sl = P.build("int8", [m] * len(lens), lens, hkv, G, D)
+    amplitudes(kv, tables, lens, kind)
+    out, lse, ws = pa.verify(kv, q.view(len(lens), m, hkv * G, D), tables, sl, D ** -0.5, out_fp32=True, return_lse=True,
+                             max_seq_len=max(lens))
+    assert pa.read_error(ws) == 0
+    ref, rl, bound = S.reference(P.vals(kv), q, [m] * len(lens), lens, tables, D ** -0.5, eps_p=S.EPS_FP16,
+                                 v_unit=unit(kv.v_scale, tables, lens, 16))
+    S.within(out.view(ref.shape), ref, bound, f"{kind} {lens}")
+    S.lse_within(lse.view(rl.shape), rl)
