@@ -14,7 +14,9 @@ cudaError_t launch_prefill_fp8_d128(const PrefillParams &p, cudaStream_t s);
 cudaError_t launch_prefill_fp8_d256(const PrefillParams &p, cudaStream_t s);
 
 namespace {
-constexpr int kSms = 152;   // CTAs at once: one per SM
+// CTAs at once: one per SM of this GPU.  (Another count would only split the work
+// worse: pieces, their workspace and their join go by this number alone.)
+constexpr int kSms = 152;
 int rows_of(int D) { return D == 128 ? 256 : 128; }
 long long most_tiles(int T, int B, int Hkv, int G, int D) {
   return ((long long)T * G / rows_of(D) + B) * Hkv;

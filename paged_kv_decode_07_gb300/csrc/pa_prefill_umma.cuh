@@ -8,6 +8,10 @@
 //   O [128 x D] += P [128 x 128] . V       A = P in tensor memory, B = V
 // with the running maximum m moved only when a score passes it by 2^8 (the
 // rescale of O is then rare), and one division by the sum at the end.
+// P is rounded once, to bf16 (bf16 cache) or fp16: against 64 bits the outputs are off
+// by 0.0023 (bf16, relative to their norm) where the rounding of the output alone makes
+// 0.0017.  The decode kernel's pair of bf16 weights would double P V's products, in the
+// kernel that the tensor pipe and its operands bound.
 //
 // K and V tiles arrive in a ring of 32 KB units [128 keys x 128 dims], used
 // as they lie: K is K-major, V MN-major.  A warpgroup of its own fills them:
@@ -31,13 +35,13 @@
 // Hand-offs are mbarriers; every wait is capped (see wait_slow).
 //
 // What bounds it (one chunk of 4096 tokens at 32768 keys, 24 heads on 4 of 256,
-// bf16, capped: 1.88 to 2.0 ms by the power the chip may draw, 1550 to 1650
-// TFLOP/s): a tile's MMAs take 2048 cycles and shared memory 2500 (192 KB of
+// bf16, capped: 1.80 to 2.12 ms by the power the chip may draw, 2.12 in calls back to
+// back, 1460 to 1720 TFLOP/s): a tile's MMAs take 2048 cycles and shared memory 2500 (192 KB of
 // operands and 128 KB of copies at 128 bytes a cycle), a tile 2750.  D = 128:
 // the softmax of capped scores (eight ragged chunks behind a window of 4096:
 // 210 us, 930 TFLOP/s).  Quantised caches: the instructions of dequantisation
-// and softmax together (8192 keys, heads of 256: FP8 525 us, NVFP4 552, int8 745
-// against bf16 380 to 410).  Short sequences: the 10,000 cycles until a CTA's
+// and softmax together (4096 tokens at 8192 keys, heads of 256, capped: FP8 521 us,
+// NVFP4 553, int8 745 against bf16 397).  Short sequences: the 10,000 cycles until a CTA's
 // first weights and 5,000 of its output (four packed int8 prompts: 58 us, 324
 // CTAs in three rounds).
 #pragma once
