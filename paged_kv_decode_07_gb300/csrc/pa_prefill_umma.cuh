@@ -36,14 +36,13 @@
 //
 // What bounds it (one chunk of 4096 tokens at 32768 keys, 24 heads on 4 of 256,
 // bf16, capped: 1.80 to 2.12 ms by the power the chip may draw, 2.12 in calls back to
-// back, 1460 to 1720 TFLOP/s): a tile's MMAs take 2048 cycles and shared memory 2500 (192 KB of
-// operands and 128 KB of copies at 128 bytes a cycle), a tile 2750.  D = 128:
-// the softmax of capped scores (eight ragged chunks behind a window of 4096:
-// 210 us, 930 TFLOP/s).  Quantised caches: the instructions of dequantisation
-// and softmax together (4096 tokens at 8192 keys, heads of 256, capped: FP8 521 us,
-// NVFP4 553, int8 745 against bf16 397).  Short sequences: the 10,000 cycles until a CTA's
-// first weights and 5,000 of its output (four packed int8 prompts: 58 us, 324
-// CTAs in three rounds).
+// back, 1460 to 1720 TFLOP/s): a tile's MMAs take 2048 cycles and shared memory 2500
+// (192 KB of operands and 128 KB of copies at 128 bytes a cycle), a tile 2750.  D = 128:
+// the softmax of capped scores (eight ragged chunks behind a window of 4096: 210 us,
+// 930 TFLOP/s).  Quantised caches: the instructions of dequantisation and softmax
+// together (4096 tokens at 8192 keys, heads of 256, capped: FP8 521 us, NVFP4 553, int8
+// 745 against bf16 397).  Short sequences: the 10,000 cycles until a CTA's first weights
+// and 5,000 of its output (four packed int8 prompts: 59 us, 324 CTAs in three rounds).
 #pragma once
 
 #include "pa_prefill.cuh"
@@ -539,7 +538,8 @@ __device__ void role_dequant(const PrefillParams &p, const Work &w, uint8_t *sme
 #pragma unroll
       for (int i = 0; i < 2 * IT; ++i) {
         const int key = k0 + i * RPI + r0;
-        d[i] = !o.done() && key >= w.see_lo && key < w.see_hi && (!GAPS || ((mask >> i) & 1)) ? __ldg(at + i * (RPI / kBlock)) : -1;
+        const bool read = !o.done() && key >= w.see_lo && key < w.see_hi && (!GAPS || ((mask >> i) & 1));
+        d[i] = read ? __ldg(at + i * (RPI / kBlock)) : -1;
       }
     }
   };
@@ -682,7 +682,8 @@ __device__ __forceinline__ float2 tanh_unit(float2 u) {
 }
 
 // CAP, BIAS: whether scores are capped and biased (kernels of their own: either
-// costs the others registers).  GAPS: see `seen`.  FIX: capped scores lie in [-cap, cap], so 2^score
+// costs the others registers).  GAPS: see `seen`.
+// FIX: capped scores lie in [-cap, cap], so 2^score
 // can be taken as it is, without a maximum, where fp32 and bf16 hold it and its
 // sums: cap * log2 e <= kFixedCap = 80, that is weights of 2^+-80, sums of up to
 // 2^30 of them, and values up to 2^17 without overflow.  (fp16 weights could not;
@@ -1120,8 +1121,9 @@ __device__ void role_softmax(const PrefillParams &p, const Work &w, uint8_t *sme
   // The tile's MMAs are complete (of a tile without keys: its queries are all there),
   // so its shared memory is free: the output goes through it (16-byte pieces,
   // swizzled by row) and leaves in whole rows.  (Stored from here, a row per lane,
-  // each instruction touched 32 lines: 6,000 cycles for a tile of 128 x 256.)  A bf16 tile takes the place of its own queries; fp32 rows
-  // reach into what the other row tile's MMAs read.
+  // each instruction touched 32 lines: 6,000 cycles for a tile of 128 x 256.)  A bf16
+  // tile takes the place of its own queries; fp32 rows reach into what the other row
+  // tile's MMAs read.
   const bool wide = partial || p.out_fp32;
   if (D == 128 && wide && n > 0 && w.nrows > 128) {
     wait_p(&c.odone[rt ^ 1], 0, c, p.hdr);
