@@ -58,7 +58,8 @@
  *     verify row with seq_len < q_len) never trap: the offending block is
  *     skipped or the length clamped, and a bit is set in the workspace
  *     header, which pa_read_error returns.  The flags describe the most
- *     recent pa_decode / pa_verify / pa_decode_scored / pa_prefill call
+ *     recent pa_decode / pa_verify / pa_decode_scored / pa_prefill /
+ *     pa_latent_prefill / pa_latent_decode call
  *     that used the workspace; one without sequences or tokens clears them.
  *   - seq_lens[b] = 0 marks a padded row: its outputs are 0 and lse -inf.
  */
@@ -92,11 +93,12 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_INT8 = 1, PA_KV_NVFP4 = 2, PA_KV_FP8 = 3 } 
 #define PA_ERRF_LEN_LT_QLEN       0x8u  /* verify: 0 < seq_len < q_len: rows with no key get 0 */
 #define PA_ERRF_WAIT_TIMEOUT      0x10u /* an in-kernel wait hit its iteration cap: outputs invalid */
 #define PA_ERRF_PLAN_OVERFLOW     0x20u /* the split plan did not fit the workspace: nothing computed */
-#define PA_ERRF_BAD_SLOT          0x40u /* pa_append_kv, pa_rope_append: slot outside
+#define PA_ERRF_BAD_SLOT          0x40u /* pa_append_kv, pa_rope_append, pa_latent_append: slot outside
                                            [-1, 16 * num_blocks): row skipped */
-#define PA_ERRF_BAD_Q_START       0x80u /* pa_prefill: q_starts descending or outside
-                                           [0, num_tokens]: clamped; the rows of the
-                                           sequences concerned are unspecified */
+#define PA_ERRF_BAD_Q_START       0x80u /* pa_prefill, pa_latent_prefill, pa_latent_gather:
+                                           starts descending or outside their rows:
+                                           clamped; the rows of the sequences concerned
+                                           are unspecified */
 
 /* The paged KV pool.  block_size must be 16; head_dim 128 or 256. */
 typedef struct pa_kv_cache {
@@ -461,6 +463,152 @@ typedef struct pa_prefill_problem {
 size_t pa_prefill_workspace_bytes(const pa_kv_cache *kv, const pa_prefill_problem *prob);
 int pa_prefill(const pa_kv_cache *kv, const pa_prefill_problem *prob, const pa_score *score,
                void *ws, size_t ws_bytes, pa_stream_t stream);
+
+/* ---- Latent attention: the keys and values of all heads of a token come
+ * from one shared row, a latent of 512 values c and a rotated part of 64 r.
+ * Head h has keys [W_K(h) c, r] (128 + 64 dims) and values W_V(h) c (128).
+ *   expanded (pa_latent_prefill): W_K c and W_V c are formed for every key and
+ *            head, 192 + 128 products a query-key pair and head: prompts.
+ *   absorbed (pa_latent_decode): <q, W_K c> = <W_K^T q, c>, so W_K goes into
+ *            the query once and W_V onto the attention's output; every head
+ *            reads the cached rows themselves, 576 + 512 products a pair, one
+ *            row of memory for all heads: single tokens and verify steps.
+ * Formats: PA_KV_BF16: latent bf16 [NB, 16, 512], rope bf16 [NB, 16, 64].
+ *          PA_KV_FP8:  latent uint8 [NB, 16, 512], FP8-E4M3 codes; rope bf16;
+ *                      a value of either part is the stored one times
+ *                      global_scale.
+ * Blocks, tables, flags and errors as in the other entry points. */
+typedef struct pa_latent_cache {
+  int32_t dtype;          /* PA_KV_BF16 or PA_KV_FP8 */
+  int32_t num_blocks;
+  int32_t block_size;     /* 16 */
+  int32_t latent_dim;     /* 512 */
+  int32_t rope_dim;       /* 64 */
+  const void *latent;
+  const void *rope;
+  float global_scale;     /* (host) FP8; ignored otherwise */
+} pa_latent_cache;
+
+/* Cache write of new tokens, the step between the projections and the
+ * attention.  In fp32, per token:
+ *   latent  c_d <- c_d * norm_d / sqrt(mean_d(c_d^2) + eps)   (norm given)
+ *   rope    pairs turned by position * inv_freq[i], i < 32, and scaled by
+ *           attn_factor, as in pa_rope_append; so is q's row of every head
+ *           (the 64 rotated dims of its query)
+ * and one rounding: q_out to bf16; the cache's values over global_scale (FP8:
+ * as IEEE quotients, codes as pa_append_kv writes them, rope to bf16; a scale
+ * <= 0 writes zeros).  slot_mapping as in pa_append_kv; the queries of a
+ * padded row are written.  Rows are contiguous, any distance apart (multiples
+ * of 8 elements), so that they can be slices of a projection or of the query
+ * that pa_latent_decode reads; q_out may be q itself (same pointer and
+ * strides), else it must not overlap the inputs. */
+typedef struct pa_latent_new {
+  int32_t num_tokens;           /* T >= 0 */
+  int32_t num_q_heads;          /* Hq >= 0 (0: no queries) */
+  const void *latent;           /* bf16 [T, 512] */
+  const void *rope;             /* bf16 [T, 64] */
+  const void *q;                /* bf16 [T, Hq, 64] */
+  void *q_out;                  /* bf16 [T, Hq, 64] */
+  int64_t latent_stride;        /* elements between tokens */
+  int64_t rope_stride;
+  int64_t q_stride, q_head_stride;
+  int64_t q_out_stride, q_out_head_stride;
+  const int32_t *positions;     /* int32 [T] */
+  const int64_t *slot_mapping;  /* int64 [T], distinct */
+  int32_t interleaved;
+  const float *inv_freq;        /* fp32 [32] */
+  float attn_factor;
+  const void *norm;             /* bf16 [512], or NULL */
+  float eps;                    /* >= 0 */
+} pa_latent_new;
+
+/* The cache's arrays are written.  ws: NULL, or >= 256 bytes whose header
+ * receives the flags (PA_ERRF_BAD_SLOT). */
+int pa_latent_append(const pa_latent_cache *kv, const pa_latent_new *in, void *ws,
+                     pa_stream_t stream);
+
+/* Cached rows of a ragged batch as bf16 rows (FP8: the product with the scale
+ * rounded once), the input of the expansion by W_K and W_V: row starts[b] + i,
+ * below starts[b + 1], is token first[b] + i of sequence b (first NULL: 0).
+ * starts: int32 [batch + 1], ascending, within [0, num_rows].  Rows outside
+ * are left as they are; those of a bad block id, or of a token before 0 or
+ * past the table's capacity, are 0 (flags PA_ERRF_BAD_BLOCK_ID,
+ * PA_ERRF_NEG_LEN, PA_ERRF_LEN_OVER_CAPACITY; PA_ERRF_BAD_Q_START for
+ * `starts`).  latent_out bf16 [num_rows, 512], rope_out bf16 [num_rows, 64].
+ * ws: NULL, or >= 256 bytes whose header receives the flags. */
+int pa_latent_gather(const pa_latent_cache *kv, const int32_t *block_tables,
+                     int32_t block_table_stride, const int32_t *starts, const int32_t *first,
+                     int32_t batch, int32_t num_rows, void *latent_out, void *rope_out, void *ws,
+                     pa_stream_t stream);
+
+/* The expanded form over a ragged batch: sequence b owns the query rows
+ * q_starts[b] .. q_starts[b + 1] - 1 (m of them) and the key rows kv_starts[b]
+ * .. kv_starts[b + 1] - 1 (n).  Head h of query i and key t:
+ *   s = softmax_scale * (<q[0..127], k_nope> + <q[128..191], k_rope>)
+ * causal: key t is visible iff t <= n - m + i (the last query at the last
+ * key); else every key is (a part of a long context, say: pa_merge joins such
+ * parts by their lse).  A query that sees no key has output 0 and lse -inf
+ * (m > n > 0 sets PA_ERRF_LEN_LT_QLEN when causal).  Query rows of no sequence
+ * are neither read nor written.  A NaN in a query, or in a key or value that
+ * it sees, is in its output; keys that other queries of a sequence see and it
+ * does not have weight 0, so their values must be finite; rows of other
+ * sequences may hold anything.  Weights meet the values rounded to bf16.
+ * Rows of q, k_nope, k_rope and v are contiguous; tokens and heads lie any
+ * distance apart (positive multiples of 8 elements). */
+typedef struct pa_latent_prefill_problem {
+  int32_t batch;               /* B >= 0 */
+  int32_t num_heads;           /* H >= 1 */
+  int32_t num_tokens;          /* rows of q */
+  int32_t num_keys;            /* rows of k and v */
+  const void *q;               /* bf16 [num_tokens, H, 192] */
+  const void *k_nope;          /* bf16 [num_keys, H, 128] */
+  const void *k_rope;          /* bf16 [num_keys, 64], shared by the heads */
+  const void *v;               /* bf16 [num_keys, H, 128] */
+  int64_t q_stride, q_head_stride;      /* elements */
+  int64_t k_stride, k_head_stride;
+  int64_t k_rope_stride;
+  int64_t v_stride, v_head_stride;
+  const int32_t *q_starts;     /* int32 [B + 1], ascending, within [0, num_tokens] */
+  const int32_t *kv_starts;    /* int32 [B + 1], ascending, within [0, num_keys] */
+  int32_t causal;
+  float softmax_scale;
+  void *out;                   /* bf16 (or fp32 if out_fp32) [num_tokens, H, 128] */
+  int32_t out_fp32;
+  float *lse_out;              /* optional fp32 [num_tokens, H] natural-log LSE, or NULL */
+} pa_latent_prefill_problem;
+
+size_t pa_latent_prefill_workspace_bytes(const pa_latent_prefill_problem *prob);
+int pa_latent_prefill(const pa_latent_prefill_problem *prob, void *ws, size_t ws_bytes,
+                      pa_stream_t stream);
+
+/* The absorbed form over the paged cache: query i of q_len (the last tokens of
+ * its sequence) and head h
+ *   s_t = softmax_scale * (<q[0..511], c_t> + <q[512..575], r_t>),
+ *         t < seq_lens[b] - q_len + 1 + i
+ *   out = sum_t softmax(s)_t c_t                       (512 values)
+ * seq_lens, flags and padded rows as in pa_verify; keys of a bad block id are
+ * skipped.  Weights meet the latents rounded to bf16 (bf16 cache) or fp16
+ * (FP8, as the queries and the stored rotated parts do then: up to 65,504,
+ * below 2^-14 with fewer bits).  Keys that some tokens of a verify step see
+ * and others do not must be finite; slots past seq_lens may hold anything. */
+typedef struct pa_latent_problem {
+  int32_t batch;               /* B >= 0 */
+  int32_t num_heads;           /* H, 1..128 */
+  int32_t q_len;               /* 1..16 */
+  const void *q;               /* bf16 [B, q_len, H, 576] */
+  const int32_t *block_tables; /* int32 [B, block_table_stride] */
+  int32_t block_table_stride;
+  const int32_t *seq_lens;     /* int32 [B], the q_len new tokens included; 0 = padded row */
+  int32_t max_seq_len;         /* (host) upper bound of seq_lens, sizes the workspace */
+  float softmax_scale;
+  void *out;                   /* bf16 (or fp32 if out_fp32) [B, q_len, H, 512] */
+  int32_t out_fp32;
+  float *lse_out;              /* optional fp32 [B, q_len, H] natural-log LSE, or NULL */
+} pa_latent_problem;
+
+size_t pa_latent_decode_workspace_bytes(const pa_latent_cache *kv, const pa_latent_problem *prob);
+int pa_latent_decode(const pa_latent_cache *kv, const pa_latent_problem *prob, void *ws,
+                     size_t ws_bytes, pa_stream_t stream);
 
 /* Copies the device error flags (PA_ERRF_*) of the last call that used ws
  * to *host_flags (host).  Synchronises `stream`. */

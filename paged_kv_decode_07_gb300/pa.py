@@ -4,8 +4,9 @@ Every step of the attention runs in libpa.so's CUDA kernels; this module
 only turns torch tensors into pointers and sizes, picks the current CUDA
 stream, and allocates outputs / workspace with torch when the caller does
 not pass them.  There is no fallback: if libpa.so is missing or a call
-fails, it raises.  rope_append, prefill and decode_scored do the same in the
-extension _pa_py (csrc/pa_py.cpp); here only what it declines is looked at:
+fails, it raises.  rope_append, prefill, decode_scored and the latent_ calls
+do the same in the extension _pa_py (csrc/pa_py.cpp); here only what it
+declines is looked at:
 arguments to refuse by name, another stream, another device.
 """
 from __future__ import annotations
@@ -49,7 +50,9 @@ EXPORTED = ("pa_workspace_bytes", "pa_decode", "pa_verify", "pa_merge", "pa_dequ
             "pa_append_kv", "pa_block_means", "pa_sparse_workspace_bytes", "pa_decode_sparse",
             "pa_decode_wo_workspace_bytes", "pa_decode_wo",
             "pa_rope_append", "pa_rope_frequencies", "pa_decode_scored",
-            "pa_prefill_workspace_bytes", "pa_prefill",
+            "pa_prefill_workspace_bytes", "pa_prefill", "pa_latent_append", "pa_latent_gather",
+            "pa_latent_prefill_workspace_bytes", "pa_latent_prefill",
+            "pa_latent_decode_workspace_bytes", "pa_latent_decode",
             "pa_read_error", "pa_status_string", "pa_version")
 
 
@@ -116,6 +119,48 @@ class _Prefill(ctypes.Structure):
                 ("lse_out", ctypes.c_void_p)]
 
 
+class _LatentCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("latent", ctypes.c_void_p),
+                ("rope", ctypes.c_void_p), ("global_scale", ctypes.c_float)]
+
+
+class _LatentNew(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("latent", ctypes.c_void_p), ("rope", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("latent_stride", ctypes.c_int64),
+                ("rope_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("q_out_head_stride", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("slot_mapping", ctypes.c_void_p), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("attn_factor", ctypes.c_float),
+                ("norm", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class _LatentPrefill(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("num_tokens", ctypes.c_int32), ("num_keys", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("k_nope", ctypes.c_void_p), ("k_rope", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("k_rope_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("q_starts", ctypes.c_void_p), ("kv_starts", ctypes.c_void_p),
+                ("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("out", ctypes.c_void_p), ("out_fp32", ctypes.c_int32),
+                ("lse_out", ctypes.c_void_p)]
+
+
+class _LatentProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("q_len", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("block_tables", ctypes.c_void_p), ("block_table_stride", ctypes.c_int32),
+                ("seq_lens", ctypes.c_void_p), ("max_seq_len", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("out", ctypes.c_void_p),
+                ("out_fp32", ctypes.c_int32), ("lse_out", ctypes.c_void_p)]
+
+
 class _Options(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("split_blocks", ctypes.c_int32),
                 ("target_items", ctypes.c_int32), ("event_begin", ctypes.c_void_p),
@@ -170,6 +215,18 @@ def lib():
         L.pa_prefill_workspace_bytes.argtypes = [P, P]
         L.pa_prefill.restype = ctypes.c_int
         L.pa_prefill.argtypes = [P, P, P, P, ctypes.c_size_t, P]
+        L.pa_latent_append.restype = ctypes.c_int
+        L.pa_latent_append.argtypes = [P, P, P, P]
+        L.pa_latent_gather.restype = ctypes.c_int
+        L.pa_latent_gather.argtypes = [P, P, i32, P, P, i32, i32, P, P, P, P]
+        L.pa_latent_prefill_workspace_bytes.restype = ctypes.c_size_t
+        L.pa_latent_prefill_workspace_bytes.argtypes = [P]
+        L.pa_latent_prefill.restype = ctypes.c_int
+        L.pa_latent_prefill.argtypes = [P, P, ctypes.c_size_t, P]
+        L.pa_latent_decode_workspace_bytes.restype = ctypes.c_size_t
+        L.pa_latent_decode_workspace_bytes.argtypes = [P, P]
+        L.pa_latent_decode.restype = ctypes.c_int
+        L.pa_latent_decode.argtypes = [P, P, P, ctypes.c_size_t, P]
         L.pa_append_kv.restype = ctypes.c_int
         L.pa_append_kv.argtypes = [P, P, P, i32, P, P, P]
         L.pa_read_error.restype = ctypes.c_int
@@ -196,7 +253,9 @@ def _fast():
         loader.exec_module(ext)
         ext.entry_points(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "pa_rope_append", "pa_prefill", "pa_prefill_workspace_bytes", "pa_decode_scored",
-            "pa_workspace_bytes")))
+            "pa_workspace_bytes", "pa_latent_append", "pa_latent_gather", "pa_latent_prefill",
+            "pa_latent_prefill_workspace_bytes", "pa_latent_decode",
+            "pa_latent_decode_workspace_bytes")))
         _ext = ext
     return _ext
 
@@ -532,7 +591,7 @@ def _elsewhere(idx, stream):
     (outputs are then allocated there too)."""
     if stream is not None:
         if stream.device.index != idx:
-            raise ValueError(f"stream is on {stream.device}, the KV cache on cuda:{idx}")
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{idx}")
         return torch.cuda.stream(stream)
     if torch.cuda.current_device() != idx:
         return torch.cuda.device(idx)
@@ -676,6 +735,184 @@ def prefill(kv: KvCache, q, q_starts, block_tables, seq_lens, softmax_scale, *, 
         return prefill(kv, q, q_starts, block_tables, seq_lens, softmax_scale, score=score, out=out,
                        out_fp32=out_fp32, return_lse=return_lse, max_seq_len=max_seq_len,
                        workspace=workspace)
+
+
+@dataclass
+class LatentCache:
+    """The paged cache of latent attention: one row a token for all heads.
+
+    dtype "bf16": latent bf16 [NB, 16, 512], rope bf16 [NB, 16, 64]; "fp8":
+    latent uint8 (E4M3 codes), rope bf16, a value being the stored one times
+    scale in both."""
+    dtype: str
+    latent: torch.Tensor
+    rope: torch.Tensor
+    scale: float = 1.0
+    block_size: int = 16
+
+    def struct(self) -> _LatentCache:
+        return _LatentCache(DTYPE_CODES[self.dtype], int(self.latent.shape[0]), self.block_size,
+                            int(self.latent.shape[2]), int(self.rope.shape[2]), _ptr(self.latent),
+                            _ptr(self.rope), float(self.scale))
+
+    def _need(self, idx):
+        if idx < 0:
+            raise ValueError("the latent cache must be on a CUDA device")
+        c, r = self.latent, self.rope
+        if c.dim() != 3 or r.dim() != 3:
+            raise ValueError(f"latent and rope must have three dimensions: got {list(c.shape)}, {list(r.shape)}")
+        size = 2 if self.dtype == "bf16" else 1
+        shape = (c.shape[0], self.block_size, c.shape[2])
+        if c.shape != shape or c.element_size() != size or not c.is_contiguous():
+            raise ValueError(f"latent must be contiguous {list(shape)} of {size}-byte elements: got {c.dtype} "
+                             f"{list(c.shape)}")
+        _need(r, "rope", _BF16, (c.shape[0], self.block_size, r.shape[2]), idx)
+
+
+def _need_strided(t, name, shape, idx):
+    """bf16, the last dim contiguous, the others any distance apart."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor: got {type(t).__name__}")
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != idx or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {_BF16} {list(shape)} on cuda:{idx} with contiguous rows: got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}, strides {t.stride()}")
+
+
+def latent_append(kv: LatentCache, latent, rope, positions, slot_mapping, inv_freq, *, q=None, q_out=None,
+                  interleaved=False, attn_factor=1.0, norm=None, eps=1e-6, workspace=None, stream=None):
+    """RMS norm (norm bf16 [512], optional) of the new tokens' latents,
+    position rotation of their rotated parts and of the queries', and the
+    write into the cache (in place), in one pass.
+
+    latent bf16 [T, 512], rope bf16 [T, 64], q bf16 [T, Hq, 64] (None: no
+    queries): rows contiguous, any distance apart (slices of projections).
+    positions int32 [T]; slot_mapping int64 [T] (-1 = padded row); inv_freq
+    fp32 [32] (rope_frequencies(64)).  Returns the turned queries, in q_out if
+    given: q itself, or the last 64 dims of latent_decode's query."""
+    if stream is None:
+        r = (_ext or _fast()).latent_append(
+            DTYPE_CODES[kv.dtype], kv.block_size, kv.latent, kv.rope, kv.scale, latent, rope, positions,
+            slot_mapping, inv_freq, q, q_out, interleaved, attn_factor, norm, eps, workspace)
+        if r is True:
+            return None
+        if type(r) is int:
+            raise PaError("pa_latent_append", r)
+        if r is not None:
+            return r
+    idx = kv.latent.get_device()
+    kv._need(idx)
+    T, dims, half = latent.shape[0], kv.latent.shape[2], kv.rope.shape[2]
+    _need_strided(latent, "latent", (T, dims), idx)
+    _need_strided(rope, "rope", (T, half), idx)
+    _need(positions, "positions", _I32, (T,), idx)
+    _need(slot_mapping, "slot_mapping", _I64, (T,), idx)
+    _need(inv_freq, "inv_freq", _F32, (half // 2,), idx)
+    if norm is not None:
+        _need(norm, "norm", _BF16, (dims,), idx)
+    if q is not None:
+        _need_strided(q, "q", (T, q.shape[1], half), idx)
+        if q_out is not None:
+            _need_strided(q_out, "q_out", tuple(q.shape), idx)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _need_workspace(workspace, idx)
+    with _elsewhere(idx, stream):
+        return latent_append(kv, latent, rope, positions, slot_mapping, inv_freq, q=q, q_out=q_out,
+                             interleaved=interleaved, attn_factor=attn_factor, norm=norm, eps=eps,
+                             workspace=workspace)
+
+
+def latent_gather(kv: LatentCache, block_tables, starts, num_rows: int, *, first=None, latent_out=None,
+                  rope_out=None, workspace=None, stream=None):
+    """Cached rows as bf16 (latent [num_rows, 512], rope [num_rows, 64]): rows
+    starts[b] .. starts[b + 1] - 1 (starts int32 [B + 1]) are sequence b's
+    tokens from first[b] on (first int32 [B]; None: 0).  Rows of no sequence
+    are left as they are."""
+    if stream is None:
+        r = (_ext or _fast()).latent_gather(
+            DTYPE_CODES[kv.dtype], kv.block_size, kv.latent, kv.rope, kv.scale, block_tables, starts, num_rows,
+            first, latent_out, rope_out, workspace)
+        if type(r) is int:
+            raise PaError("pa_latent_gather", r)
+        if r is not None:
+            return r
+    idx = kv.latent.get_device()
+    kv._need(idx)
+    B = block_tables.shape[0]
+    _need(block_tables, "block_tables", _I32, (B, block_tables.shape[1]), idx)
+    _need(starts, "starts", _I32, (B + 1,), idx)
+    if first is not None:
+        _need(first, "first", _I32, (B,), idx)
+    for t, name, d in ((latent_out, "latent_out", kv.latent.shape[2]), (rope_out, "rope_out", kv.rope.shape[2])):
+        if t is not None:
+            _need(t, name, _BF16, (num_rows, d), idx)
+    _need_workspace(workspace, idx)
+    with _elsewhere(idx, stream):
+        return latent_gather(kv, block_tables, starts, num_rows, first=first, latent_out=latent_out,
+                             rope_out=rope_out, workspace=workspace)
+
+
+def latent_prefill(q, k_nope, k_rope, v, q_starts, kv_starts, softmax_scale, *, causal=True, out=None,
+                   out_fp32=False, return_lse=False, workspace=None, stream=None):
+    """The expanded form of latent attention over a ragged batch.
+
+    q bf16 [T, H, 192] (128 dims and the 64 rotated ones), k_nope bf16 [N, H,
+    128], k_rope bf16 [N, 64] (shared by the heads), v bf16 [N, H, 128]: rows
+    contiguous, any distance apart.  Sequence b owns the query rows from
+    q_starts[b] and the key rows from kv_starts[b] (int32 [B + 1]); causal: its
+    last query is at its last key, else every query sees every key.  Returns
+    (out [T, H, 128], [lse [T, H],] workspace); rows of no sequence are left
+    as they are.  A workspace that is too small is replaced."""
+    if stream is None:
+        r = (_ext or _fast()).latent_prefill(q, k_nope, k_rope, v, q_starts, kv_starts, softmax_scale, causal,
+                                             out, out_fp32, return_lse, workspace)
+        if type(r) is int:
+            raise PaError("pa_latent_prefill", r)
+        if r is not None:
+            return r
+    idx = q.get_device()
+    if idx < 0:
+        raise ValueError("q must be on a CUDA device")
+    T, H, N, B = q.shape[0], q.shape[1], k_nope.shape[0], q_starts.shape[0] - 1
+    _need_strided(q, "q", (T, H, 192), idx)
+    _need_strided(k_nope, "k_nope", (N, H, 128), idx)
+    _need_strided(k_rope, "k_rope", (N, 64), idx)
+    _need_strided(v, "v", (N, H, 128), idx)
+    _need(q_starts, "q_starts", _I32, (B + 1,), idx)
+    _need(kv_starts, "kv_starts", _I32, (B + 1,), idx)
+    _need_out(out, (T, H, 128), idx)
+    _need_workspace(workspace, idx)
+    with _elsewhere(idx, stream):
+        return latent_prefill(q, k_nope, k_rope, v, q_starts, kv_starts, softmax_scale, causal=causal, out=out,
+                              out_fp32=out_fp32, return_lse=return_lse, workspace=workspace)
+
+
+def latent_decode(kv: LatentCache, q, block_tables, seq_lens, softmax_scale, *, out=None, out_fp32=False,
+                  return_lse=False, max_seq_len=None, workspace=None, stream=None):
+    """The absorbed form of latent attention over the paged cache: q bf16 [B,
+    Q, H, 576] (the query times W_K, 512 dims, beside its 64 rotated ones) of
+    the last Q tokens of each sequence, causal among them -> (out [B, Q, H,
+    512], [lse,] workspace).  A workspace that is too small is replaced."""
+    if stream is None:
+        r = (_ext or _fast()).latent_decode(
+            DTYPE_CODES[kv.dtype], kv.block_size, kv.latent, kv.rope, kv.scale, q, block_tables, seq_lens,
+            softmax_scale, out, out_fp32, return_lse, max_seq_len, workspace)
+        if type(r) is int:
+            raise PaError("pa_latent_decode", r)
+        if r is not None:
+            return r
+    idx = kv.latent.get_device()
+    kv._need(idx)
+    B, Q, H, _ = q.shape
+    dims = int(kv.latent.shape[2])
+    _need(q, "q", _BF16, (B, Q, H, dims + kv.rope.shape[2]), idx)
+    _need(block_tables, "block_tables", _I32, (B, block_tables.shape[1]), idx)
+    _need(seq_lens, "seq_lens", _I32, (B,), idx)
+    _need_out(out, (B, Q, H, dims), idx)
+    _need_workspace(workspace, idx)
+    with _elsewhere(idx, stream):
+        return latent_decode(kv, q, block_tables, seq_lens, softmax_scale, out=out, out_fp32=out_fp32,
+                             return_lse=return_lse, max_seq_len=max_seq_len, workspace=workspace)
 
 
 def read_error(workspace: torch.Tensor, stream=None) -> int:
