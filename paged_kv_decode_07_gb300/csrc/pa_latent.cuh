@@ -71,7 +71,23 @@ struct AbsorbedParams {
   int out_fp32;
   float *lse_out;
   uint32_t *hdr;
+  // work: see DecodePlan
+  int R, RG, S, workers;
+  int *starts;                        // [B + 1] tiles of the sequences before
+  float *part_o;                      // [2 * workers][S][R][512]
+  float *part_lse;                    // [2 * workers][S][R]
 };
+
+// The rows (token, head) of a sequence in RG groups of R, one CTA each; S groups
+// walk the same keys side by side (a worker), RG / S such sets one after another.
+// The key tiles of all sets of all sequences are one list, of which every worker
+// takes an equal run.
+constexpr int kTileKeys = 64;
+constexpr int kMaxRows = 64;
+struct DecodePlan {
+  int R, RG, S, workers;
+};
+DecodePlan plan_latent_decode(int B, int Q, int H, int max_seq_len);
 
 cudaError_t launch_latent_append(const LatentAppendParams &p, cudaStream_t s);
 cudaError_t launch_latent_gather(const LatentGatherParams &p, cudaStream_t s);

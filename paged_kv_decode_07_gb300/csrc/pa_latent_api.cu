@@ -71,6 +71,23 @@ int check_decode(const pa_latent_problem *p) {
   return PA_OK;
 }
 
+struct DecodeLayout {
+  DecodePlan plan;
+  size_t starts, part_lse, part_o, total;
+};
+
+DecodeLayout decode_layout(const pa_latent_problem *p) {
+  DecodeLayout L;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  L.plan = plan_latent_decode(p->batch, p->q_len, p->num_heads, p->max_seq_len);
+  const size_t rows = (size_t)2 * L.plan.workers * L.plan.S * L.plan.R;
+  L.starts = kHdrWords * 4;
+  L.part_lse = L.starts + up(((size_t)p->batch + 1) * 4);
+  L.part_o = L.part_lse + up(rows * 4);
+  L.total = L.part_o + rows * kLatent * 4;
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -210,7 +227,7 @@ int pa_latent_prefill(const pa_latent_prefill_problem *p, void *ws, size_t ws_by
 }
 
 size_t pa_latent_decode_workspace_bytes(const pa_latent_cache *kv, const pa_latent_problem *p) {
-  return check_cache(kv) == PA_OK && check_decode(p) == PA_OK ? kHdrWords * 4 : 0;
+  return check_cache(kv) == PA_OK && check_decode(p) == PA_OK ? decode_layout(p).total : 0;
 }
 
 int pa_latent_decode(const pa_latent_cache *kv, const pa_latent_problem *p, void *ws, size_t ws_bytes,
@@ -226,7 +243,9 @@ int pa_latent_decode(const pa_latent_cache *kv, const pa_latent_problem *p, void
       !aligned4(p->lse_out))
     return PA_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws)) return PA_ERR_INVALID_ARG;
-  if (ws_bytes < pa_latent_decode_workspace_bytes(kv, p)) return PA_ERR_WORKSPACE_TOO_SMALL;
+  const DecodeLayout L = decode_layout(p);
+  if (ws_bytes < L.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t *w = static_cast<uint8_t *>(ws);
   AbsorbedParams a;
   std::memset(&a, 0, sizeof a);
   a.kv = view_of(kv);
@@ -242,6 +261,13 @@ int pa_latent_decode(const pa_latent_cache *kv, const pa_latent_problem *p, void
   a.out_fp32 = p->out_fp32 ? 1 : 0;
   a.lse_out = p->lse_out;
   a.hdr = static_cast<uint32_t *>(ws);
+  a.R = L.plan.R;
+  a.RG = L.plan.RG;
+  a.S = L.plan.S;
+  a.workers = L.plan.workers;
+  a.starts = reinterpret_cast<int *>(w + L.starts);
+  a.part_lse = reinterpret_cast<float *>(w + L.part_lse);
+  a.part_o = reinterpret_cast<float *>(w + L.part_o);
   if (launch_clear(a.hdr, s) != cudaSuccess) return PA_ERR_CUDA;
   return launch_latent_decode(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
