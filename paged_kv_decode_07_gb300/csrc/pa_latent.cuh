@@ -82,7 +82,6 @@ struct AbsorbedParams {
 // walk the same keys side by side (a worker), RG / S such sets one after another.
 // The key tiles of all sets of all sequences are one list, of which every worker
 // takes an equal run.
-constexpr int kTileKeys = 64;
 constexpr int kMaxRows = 64;
 struct DecodePlan {
   int R, RG, S, workers;
