@@ -1,73 +1,497 @@
 // pa_latent_prefill.cu -- the expanded form of latent attention over a ragged
-// batch, the simplest kernel: a warp per (token, head), one key after another
-// with the running maximum and sum of the softmax.
-#include "pa_latent.cuh"
+// batch, on the 5th-generation tensor cores (tcgen05.mma, accumulators in tensor
+// memory).
+//
+// A CTA takes 256 query tokens of one head, two row tiles of 128 that share every
+// key tile of 128 keys; in fp32 accumulation:
+//   S [128 x 128] = Q [128 x 192] . K^T    K = the head's 128 dims and the shared 64
+//   P = exp2(S * scale - m)                softmax threads, half a row each
+//   O [128 x 128] += P [128 x 128] . V     P in tensor memory, over S
+// with the running maximum m moved only when a score passes it by 2^8 (the rescale
+// of O is then rare) and one division by the sum at the end.  P is rounded once, to
+// bf16.  While one row tile is at its softmax the products of the other run.
+//
+// Q, K and V arrive by tiled copies in units [128 rows][64 dims] (128-byte rows,
+// swizzled) that both products read as they lie: three units of K, then two of V a
+// tile, in a ring of eight.
+//
+// Roles: four softmax groups (two a row tile, 64 of a tile's keys each), a warp per
+// row tile that issues its products, a warp that copies.  Hand-offs are mbarriers;
+// waits are capped.
+#include "pa_latent_umma.cuh"
 
 namespace pa {
 namespace lat {
 namespace {
 
-__global__ void __launch_bounds__(256) prefill_kernel(const ExpandedParams p) {
+constexpr int kRows = 256;                  // query tokens a CTA
+constexpr int kKeys = 128;                  // keys a tile
+constexpr uint32_t kUnit = 128 * 128;       // bytes of a unit
+constexpr int kUnits = 8;                   // ring
+constexpr int kPerTile = 5;                 // units of a tile: three of K, two of V
+constexpr uint32_t kOffRing = 2 * 3 * kUnit;
+constexpr uint32_t kSmem = kOffRing + kUnits * kUnit + 1024;
+constexpr int kThreads = 640;
+constexpr int kLaunchRegs = 96, kRegCtl = 40, kRegSoft = 104;   // 5 groups: 40 + 4 * 104 <= 5 * 96
+static_assert(kRegCtl + 4 * kRegSoft <= 5 * kLaunchRegs && kLaunchRegs == 65536 / kThreads / 8 * 8, "register split");
+constexpr float kLazy = 8.0f;               // log2 of how far a score may pass the running maximum
+constexpr uint32_t kColO = 256;             // S of the two row tiles, then their O
+
+struct PCtl {
+  uint64_t full[kUnits], empty[kUnits];
+  uint64_t qfull[2], sfull[2], pready[2], odone[2], done;
+  uint32_t tmem;
+  int abort;
+  float red[kRows];                         // a row's maximum (at the end its sum), from one half to the other
+};
+static_assert(sizeof(PCtl) <= 2048 && kSmem + 2048 <= 227 * 1024, "shared memory");
+
+// A CTA's share: 256 tokens of a sequence, a head.  Sequence b's tiles are given
+// the places from q_starts[b] / 256 + b on, of which there are enough (and at most one
+// too many), so that a search finds a place's sequence without the counts of those
+// before it.  Places are taken from the last: the last tokens of a prompt see most.
+struct Share {
+  int b, head, start, len, first;           // b < 0: nothing to do; first token of the tile
+  int key0, n;                              // the sequence's key rows
+};
+__device__ __forceinline__ Share find_share(const ExpandedParams &p, int index) {
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)p.T * p.H) return;
-  const int t = (int)(row / p.H), h = (int)(row % p.H);
-  auto qs = [&](int b) { return min(max(__ldg(p.q_starts + b), 0), p.T); };
-  if (row == 0)
-    for (int b = lane; b < p.B; b += 32) {
+  auto start = [&](int b) { return min(max(__ldg(p.q_starts + b), 0), p.T); };
+  auto place = [&](int b) { return start(b) / kRows + b; };
+  if (index == 0) {
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
       const int a = __ldg(p.q_starts + b), e = __ldg(p.q_starts + b + 1);
       const int c = __ldg(p.kv_starts + b), d = __ldg(p.kv_starts + b + 1);
-      if (a < 0 || e < a || e > p.T || c < 0 || d < c || d > p.N) set_err(p.hdr, PA_ERRF_BAD_Q_START);
-      else if (p.causal && d > c && e - a > d - c) set_err(p.hdr, PA_ERRF_LEN_LT_QLEN);
+      if (a < 0 || e < a || e > p.T || c < 0 || d < c || d > p.N) flag(p.hdr, PA_ERRF_BAD_Q_START);
+      else if (p.causal && d > c && e - a > d - c) flag(p.hdr, PA_ERRF_LEN_LT_QLEN);
     }
-  if (t < qs(0) || t >= qs(p.B)) return;
-  int lo = 0, hi = p.B;
+  }
+  Share r = {-1, index % p.H, 0, 0, 0, 0, 0};
+  const int at = place(p.B) - 1 - index / p.H;
+  if (at < 0) return r;
+  int lo = 0, hi = p.B;                     // the last sequence of [lo, hi) that starts at or before `at`
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (qs(mid) <= t) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, b < hi && place(b) <= at);
+    lo += (31 - __clz((int)(le | 1u))) * step;
+    hi = min(hi, lo + step);
   }
-  const int k0 = min(max(__ldg(p.kv_starts + lo), 0), p.N), k1 = min(max(__ldg(p.kv_starts + lo + 1), k0), p.N);
-  const int n = k1 - k0, m = qs(lo + 1) - qs(lo), i = t - qs(lo);
-  const int see = p.causal ? min(max(n - m + 1 + i, 0), n) : n;
-  const __nv_bfloat16 *q = p.q + (size_t)t * p.q_stride + (size_t)h * p.q_head;
-  float qv[6], o[4] = {}, top = kNegInf, sum = 0.f;
+  r.start = start(lo);
+  r.len = max(start(lo + 1) - r.start, 0);
+  const long long first = (long long)(at - place(lo)) * kRows;
+  if (first < 0 || first >= r.len) return r;
+  r.b = lo;
+  r.first = (int)first;
+  r.key0 = min(max(__ldg(p.kv_starts + lo), 0), p.N);
+  r.n = min(max(__ldg(p.kv_starts + lo + 1), r.key0), p.N) - r.key0;
+  return r;
+}
+
+struct Work {
+  int nrows, n;                             // rows of the CTA, keys of the sequence
+  int tiles[2];                             // key tiles of each row tile
+  int row_tiles;
+};
+
+// ------------------------------------------------------------------- products
+
+// row tile t; tiles that only the other one sees: their units are given back
+__device__ void role_mma(const ExpandedParams &p, int t, int n, int all, int keys, uint8_t *smem, PCtl &c, uint32_t tmem) {
+  constexpr uint32_t IQK = idesc_of(true, 128, 128, false, false), IPV = idesc_of(true, 128, 64, false, true);
+  const uint32_t lead = elect_one();
+  const uint64_t dQ = sdesc(smem_u32(smem + t * 3 * kUnit), 16, 1024);
+  const uint64_t dU = sdesc(smem_u32(smem + kOffRing), 16, 1024);
+  const uint32_t S = tmem + t * 128, O = tmem + kColO + t * 128;
+  auto full = [&](uint32_t u) { wait_cap(&c.full[u % kUnits], (u / kUnits) & 1, &c.abort, p.hdr); };
+  auto qk = [&](int j) {
 #pragma unroll
-  for (int d = 0; d < 6; ++d) qv[d] = __bfloat162float(q[d * 32 + lane]);
-  for (int k = 0; k < see; ++k) {
-    const __nv_bfloat16 *kn = p.kn + (size_t)(k0 + k) * p.k_stride + (size_t)h * p.k_head;
-    const __nv_bfloat16 *kr = p.kr + (size_t)(k0 + k) * p.kr_stride;
-    const __nv_bfloat16 *v = p.v + (size_t)(k0 + k) * p.v_stride + (size_t)h * p.v_head;
-    float s = 0.f;
+    for (int ch = 0; ch < 3; ++ch) {
+      const uint32_t u = kPerTile * j + ch;
+      full(u);
+      tc_fence_after();
+      const uint64_t kb = dU + (uint64_t)((u % kUnits) * (kUnit >> 4)), qb = dQ + (uint64_t)(ch * (kUnit >> 4));
 #pragma unroll
-    for (int d = 0; d < 4; ++d) s += qv[d] * __bfloat162float(kn[d * 32 + lane]);
-#pragma unroll
-    for (int d = 0; d < 2; ++d) s += qv[4 + d] * __bfloat162float(kr[d * 32 + lane]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale_log2;
-    const float mn = fmaxf(top, s), al = mn == kNegInf ? 1.f : exp2f(top - mn);
-    const float w = exp2f(s - (mn == kNegInf ? 0.f : mn));
-    top = mn;
-    sum = sum * al + w;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) o[d] = o[d] * al + w * __bfloat162float(v[d * 32 + lane]);
+      for (int ks = 0; ks < 4; ++ks)
+        mma_ss_if(lead, S, qb + (uint64_t)((ks * 32) >> 4), kb + (uint64_t)((ks * 32) >> 4), IQK, ch + ks > 0 ? 1u : 0u);
+      commit_if(lead, &c.empty[u % kUnits]);
+    }
+    commit_if(lead, &c.sfull[t]);
+  };
+  if (n > 0) {
+    wait_cap(&c.qfull[t], 0, &c.abort, p.hdr);
+    qk(0);
   }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int steps = min(8, (keys - j * kKeys + 15) / 16);   // (the last tile's rows past the sequence are not read)
+    const uint32_t u = kPerTile * j + 3;
+    full(u);
+    full(u + 1);
+    wait_cap(&c.pready[t], j & 1, &c.abort, p.hdr);
+    tc_fence_after();
+    // P sits in two runs of 32 columns, one in each softmax group's half of S
+    if (steps == 8) {
 #pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const size_t at = (size_t)row * kV + d * 32 + lane;
-    if (p.out_fp32) static_cast<float *>(p.out)[at] = o[d] * inv;
-    else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o[d] * inv);
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t vb = dU + (uint64_t)(((u + h) % kUnits) * (kUnit >> 4));
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts_if(lead, O + h * 64, S + (ks >> 2) * 64 + (ks & 3) * 8, vb + (uint64_t)((ks * 2048) >> 4), IPV,
+                    j > 0 || ks > 0 ? 1u : 0u);
+        commit_if(lead, &c.empty[(u + h) % kUnits]);
+      }
+    } else {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t vb = dU + (uint64_t)(((u + h) % kUnits) * (kUnit >> 4));
+#pragma unroll 1
+        for (int ks = 0; ks < steps; ++ks)
+          mma_ts_if(lead, O + h * 64, S + (ks >> 2) * 64 + (ks & 3) * 8, vb + (uint64_t)((ks * 2048) >> 4), IPV,
+                    j > 0 || ks > 0 ? 1u : 0u);
+        commit_if(lead, &c.empty[(u + h) % kUnits]);
+      }
+    }
+    if (j + 1 < n) qk(j + 1);
   }
-  if (p.lse_out && lane == 0) p.lse_out[row] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : kNegInf;
+  if (n > 0) commit_if(lead, &c.odone[t]);
+#pragma unroll 1
+  for (uint32_t u = kPerTile * n; u < (uint32_t)(kPerTile * all); ++u) {
+    full(u);                                // (in order: an arrival belongs to its own fill)
+    commit_if(lead, &c.empty[u % kUnits]);
+  }
+  commit_if(lead, &c.done);                 // tensor memory is released only after every product completes
+  drain_wait(&c.done, 0);
+  __syncwarp();
+}
+
+// --------------------------------------------------------------------- copies
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// one lane; rows past the sequence are its neighbours' (or zeros past the tensor)
+__device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
+                                          const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, int row_tiles,
+                                          int all, uint8_t *smem, PCtl &c) {
+  for (int t = 0; t < row_tiles; ++t) {
+    mbar_arrive_expect_tx(&c.qfull[t], 3 * kUnit);
+    for (int ch = 0; ch < 3; ++ch)
+      tma_3d(smem_u32(smem + (t * 3 + ch) * kUnit), mq, ch * 64, sh.head, sh.start + sh.first + t * 128, &c.qfull[t]);
+  }
+  uint32_t u = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (int j = 0; j < all && ok; ++j) {
+    const int key = sh.key0 + j * kKeys;
+#pragma unroll 1
+    for (int i = 0; i < kPerTile; ++i, ++u) {
+      const uint32_t st = u % kUnits;
+      if (u >= kUnits && !wait_cap(&c.empty[st], (u / kUnits - 1) & 1, &c.abort, p.hdr)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = smem_u32(smem + kOffRing + st * kUnit);
+      mbar_arrive_expect_tx(&c.full[st], kUnit);
+      if (i < 2) tma_3d(dst, mk, i * 64, sh.head, key, &c.full[st]);
+      else if (i == 2) tma_2d(dst, mr, 0, key, &c.full[st]);
+      else tma_3d(dst, mv, (i - 3) * 64, sh.head, key, &c.full[st]);
+    }
+  }
+  // nothing lands after the CTA's end
+  for (int t = 0; t < row_tiles; ++t) drain_wait(&c.qfull[t], 0);
+  for (uint32_t k = u > kUnits ? u - kUnits : 0; k < u; ++k) drain_wait(&c.full[k % kUnits], (k / kUnits) & 1);
+}
+
+// -------------------------------------------------------------------- softmax
+
+__device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Work &w, uint8_t *smem, PCtl &c,
+                             uint32_t tmem) {
+  constexpr int NC = 64;                    // S columns a thread, and O columns
+  // row tile rt, half hf of its columns; a pair of warps shares 32 rows
+  const int tid = threadIdx.x, hf = (tid >> 7) & 1, rt = tid >> 8, wq = (tid >> 5) & 3, lane = tid & 31;
+  const int row = rt * 128 + (tid & 127), pair = 1 + rt * 4 + wq;
+  const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+  const uint32_t S = tmem + lane_off + rt * 128 + hf * NC, O = tmem + lane_off + kColO + rt * 128 + hf * NC;
+  const int n = w.tiles[rt];
+  const bool live = row < w.nrows;
+  // keys that this thread's row sees; that some, and that every row of the warp sees
+  int see = 0;
+  if (live) see = p.causal ? min(max(w.n - sh.len + sh.first + row + 1, 0), w.n) : w.n;
+  const int some = __reduce_max_sync(0xffffffffu, see);
+  const int every = __reduce_min_sync(0xffffffffu, live ? see : 0x7fffffff);
+  const float f = p.scale_log2;
+  float m = kNegInf, l = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int k0 = j * kKeys + hf * NC;
+    wait_cap(&c.sfull[rt], j & 1, &c.abort, p.hdr);
+    __syncwarp();
+    tc_fence_after();
+    const bool none = k0 >= some;
+    float s[NC], mx = kNegInf, fs = f;
+    if (!none) {
+      pf::ld32_issue(S, s);
+      pf::ld32_issue(S + 32, s + 32);
+      pf::ld_wait(s);
+      pf::ld_wait(s + 32);
+      if (!(f > 0.f)) {                     // (the products' order is turned around)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) s[i] *= f;
+        fs = 1.f;
+      }
+      if (k0 + NC > every) {
+        const int lim = see - k0;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) s[i] = i < lim ? s[i] : kNegInf;
+      }
+      float x0 = s[0], x1 = s[1];
+#pragma unroll
+      for (int i = 2; i < NC; i += 2) {
+        x0 = fmaxf(x0, s[i]);
+        x1 = fmaxf(x1, s[i + 1]);
+      }
+      mx = fmaxf(x0, x1) * fs;
+    }
+    // ---- the running maximum moves when some score passes it by 2^kLazy
+    if (named_sync_or(pair, 64, mx > m + kLazy)) {
+      // with the row's other keys
+      if (hf == 0) c.red[row] = mx;
+      named_sync(pair, 64);
+      if (hf == 1) {
+        mx = fmaxf(mx, c.red[row]);
+        c.red[row] = mx;
+      }
+      named_sync(pair, 64);
+      if (hf == 0) mx = c.red[row];
+      const float mn = fmaxf(m, mx);
+      const float al = mn == kNegInf ? 1.f : ex2_approx(m - mn);
+      m = mn;
+      l *= al;
+      if (j > 0) {                          // (S of this tile complete: so is the product before it)
+#pragma unroll 1
+        for (int ch = 0; ch < NC; ch += 16) {
+          float o[16];
+          tmem_ld16(O + ch, o);
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(o[i] * al);
+          tmem_st16(O + ch, v);
+        }
+        tmem_st_wait();
+      }
+    }
+    // ---- weights
+    if (none) {
+      const uint32_t z[16] = {};
+      tmem_st16(S, z);
+      tmem_st16(S + 16, z);
+    } else {
+      const float mu = m == kNegInf ? 0.f : m;
+      const float2 nm = make_float2(-mu, -mu), ff = make_float2(fs, fs);
+      float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int ch = 0; ch < NC; ch += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 y = ffma2(make_float2(s[ch + i], s[ch + i + 1]), ff, nm);
+          const float2 a = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          l2 = pf::fadd2(l2, a);
+          pk[i / 2] = tc::f2_to_bf2(a.x, a.y);
+        }
+        tmem_st16(S + ch / 2, pk);
+      }
+      l += l2.x + l2.y;
+    }
+    // The last tile's rows past the sequence are its neighbour's, who may hold
+    // anything: zeros, for a zero weight times them must be zero (up to the 16 that
+    // a step of the product takes)
+    const int valid = w.n - j * kKeys;
+    if (valid < kKeys && (valid & 15)) {
+      const uint32_t u = kPerTile * j + 3;
+      for (int h = 0; h < 2; ++h) wait_cap(&c.full[(u + h) % kUnits], ((u + h) / kUnits) & 1, &c.abort, p.hdr);
+      const int r = valid + (tid & 15);     // 16 rows of eight pieces, in two units
+      if (r < ((valid + 15) & ~15))
+        sts_u4(smem_u32(smem + kOffRing + ((u + ((tid >> 7) & 1)) % kUnits) * kUnit) + r * 128 + ((tid >> 4) & 7) * 16, 0, 0, 0, 0);
+      fence_async_smem();
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.pready[rt]);
+  }
+  // ---- the sum, the last product, the output
+  named_sync(pair, 64);                     // the other warp has read the last maximum
+  if (hf == 0) c.red[row] = l;
+  named_sync(pair, 64);
+  if (hf == 1) {
+    l += c.red[row];
+    c.red[row] = l;
+  }
+  named_sync(pair, 64);
+  if (hf == 0) l = c.red[row];
+  // the queries' place takes the output: their copy has landed, and no product reads them
+  wait_cap(&c.qfull[rt], 0, &c.abort, p.hdr);
+  if (n > 0) wait_cap(&c.odone[rt], 0, &c.abort, p.hdr);
+  // (fp32 rows reach into what the other row tile's products read)
+  if (p.out_fp32 && w.row_tiles > 1) {
+    wait_cap(&c.qfull[rt ^ 1], 0, &c.abort, p.hdr);
+    if (w.tiles[rt ^ 1] > 0) wait_cap(&c.odone[rt ^ 1], 0, &c.abort, p.hdr);
+  }
+  __syncwarp();
+  tc_fence_after();
+  const float inv = l != 0.f ? 1.f / l : 0.f;   // (0: the row saw no key; a NaN among its scores goes on)
+  const long long r_out = (long long)(sh.start + sh.first + row) * p.H + sh.head;
+  // through shared memory, 16-byte pieces swizzled by row, to leave in whole rows
+  const int shift = p.out_fp32 ? 5 : 4;         // pieces a row
+  uint8_t *const base = p.out_fp32 ? smem + rt * 65536 : smem + rt * 3 * kUnit;
+  auto piece_at = [&](int r, int k) { return base + (((r << shift) + (k ^ (r & 7))) << 4); };
+  const int r = tid & 127;
+#pragma unroll 1
+  for (int ch = 0; ch < NC; ch += 16) {
+    float o[16];
+    if (n > 0) {
+      tmem_ld16(O + ch, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = l != 0.f ? o[i] * inv : 0.f;
+    const int d = hf * NC + ch;
+    if (p.out_fp32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4 *>(piece_at(r, d / 4 + i)) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint4 *>(piece_at(r, d / 8 + i)) =
+            make_uint4(tc::f2_to_bf2(o[8 * i], o[8 * i + 1]), tc::f2_to_bf2(o[8 * i + 2], o[8 * i + 3]),
+                       tc::f2_to_bf2(o[8 * i + 4], o[8 * i + 5]), tc::f2_to_bf2(o[8 * i + 6], o[8 * i + 7]));
+    }
+  }
+  named_sync(pair, 64);                     // both halves of the rows are there
+  uint4 *const dst = static_cast<uint4 *>(p.out);
+#pragma unroll 4
+  for (int i = lane; i < 16 << shift; i += 32) {   // 16 of the pair's 32 rows each
+    const int q = wq * 32 + hf * 16 + (i >> shift), k = i & ((1 << shift) - 1);
+    if (rt * 128 + q < w.nrows) {
+      const long long to = (long long)(sh.start + sh.first + rt * 128 + q) * p.H + sh.head;
+      dst[(to << shift) + k] = *reinterpret_cast<const uint4 *>(piece_at(q, k));
+    }
+  }
+  if (live && hf == 0 && p.lse_out) p.lse_out[r_out] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prefill_kernel(const ExpandedParams p, const __grid_constant__ CUtensorMap mq,
+                          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mr,
+                          const __grid_constant__ CUtensorMap mv) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  __shared__ PCtl c;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  griddep_launch();
+  const Share sh = find_share(p, blockIdx.x);
+  if (sh.b < 0) {
+    griddep_wait();                         // the grid does not end before its header is cleared
+    return;
+  }
+  Work w;
+  w.nrows = min(kRows, sh.len - sh.first);
+  w.n = sh.n;
+  w.row_tiles = w.nrows > 128 ? 2 : 1;
+  int all = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(t * 128 + 127, w.nrows - 1);   // row of the row tile that sees most
+    const int see = p.causal ? min(max(sh.n - sh.len + sh.first + last + 1, 0), sh.n) : sh.n;
+    w.tiles[t] = t < w.row_tiles ? (see + kKeys - 1) / kKeys : 0;
+    all = max(all, w.tiles[t]);
+  }
+  if (warp == 16) {
+    tmem_alloc(&c.tmem, 512);
+    tmem_relinquish();
+  } else if (tid == 0) {
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&c.full[i], 1);
+      mbar_init(&c.empty[i], w.row_tiles);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.qfull[i], 1);
+      mbar_init(&c.sfull[i], 1);
+      mbar_init(&c.pready[i], 8);
+      mbar_init(&c.odone[i], 1);
+    }
+    mbar_init(&c.done, w.row_tiles);
+    c.abort = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
+  if (warp < 16) {
+    setmaxnreg_to<kLaunchRegs, kRegSoft>();
+    if (warp < 8 * w.row_tiles) role_softmax(p, sh, w, smem, c, tmem);
+  } else {
+    setmaxnreg_to<kLaunchRegs, kRegCtl>();
+    if (warp < 16 + w.row_tiles) {
+      const int t = warp - 16;
+      role_mma(p, t, __shfl_sync(0xffffffffu, w.tiles[t & 1], 0), __shfl_sync(0xffffffffu, all, 0),
+               __shfl_sync(0xffffffffu, w.n, 0), smem, c, tmem);
+    } else if (tid == 18 * 32) {
+      role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, all, smem, c);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+    griddep_wait();                         // the grid does not end before its header is cleared
+  }
+}
+
+// rows [count][heads][dims] of 64-value units, 128 rows of one head a copy
+bool map_heads(CUtensorMap *m, const void *base, int dims, int heads, int count, long long head, long long stride) {
+  const uint64_t d[3] = {(uint64_t)dims, (uint64_t)heads, (uint64_t)count};
+  // (a single head's, or row's, distance is not the caller's to give)
+  const uint64_t s[2] = {heads > 1 ? (uint64_t)head * 2 : (uint64_t)dims * 2, count > 1 ? (uint64_t)stride * 2 : (uint64_t)dims * 2};
+  const uint32_t b[3] = {64, 1, 128};
+  return make_map(m, base, 3, d, s, b);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_prefill(const ExpandedParams &p, cudaStream_t s) {
-  prefill_kernel<<<(unsigned)(((long long)p.T * p.H + 7) / 8), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  CUtensorMap mq, mk, mr, mv;
+  const int keys = p.N > 0 ? p.N : 1;       // (without keys nothing is copied)
+  const void *kn = p.N > 0 ? p.kn : p.q, *kr = p.N > 0 ? p.kr : p.q, *v = p.N > 0 ? p.v : p.q;
+  const uint64_t dr[2] = {kRope, (uint64_t)keys}, sr[1] = {keys > 1 ? (uint64_t)p.kr_stride * 2 : kRope * 2};
+  const uint32_t br[2] = {kRope, 128};
+  if (!map_heads(&mq, p.q, kQk, p.H, p.T, p.q_head, p.q_stride) ||
+      !map_heads(&mk, kn, kNope, p.H, keys, p.k_head, p.k_stride) || !make_map(&mr, kr, 2, dr, sr, br) ||
+      !map_heads(&mv, v, kV, p.H, keys, p.v_head, p.v_stride))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  // the register split starts from kLaunchRegs (allocated in eights): a build that
+  // gave the kernel another count is refused, never launched
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, latent_prefill_kernel);
+  if (e != cudaSuccess) return e;
+  if ((fa.numRegs + 7) / 8 * 8 != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+  const long long grid = ((long long)p.T / kRows + p.B) * p.H;   // every sequence has at most one tile that is not full
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(latent_prefill_kernel, (unsigned)grid, kThreads, kSmem, s, p, mq, mk, mr, mv);
 }
 
 }  // namespace lat
