@@ -35,13 +35,14 @@ constexpr int kThreads = 640;
 constexpr int kLaunchRegs = 96, kRegCtl = 40, kRegSoft = 104;   // 5 groups: 40 + 4 * 104 <= 5 * 96
 static_assert(kRegCtl + 4 * kRegSoft <= 5 * kLaunchRegs && kLaunchRegs == 65536 / kThreads / 8 * 8, "register split");
 constexpr float kLazy = 8.0f;               // log2 of how far a score may pass the running maximum
+constexpr float kMost = 0x1p32f;            // first pass: sum of 64 weights up to which a row goes on
 constexpr uint32_t kColO = 256;             // S of the two row tiles, then their O
 
 struct PCtl {
   uint64_t full[kUnits], empty[kUnits];
   uint64_t qfull[2], sfull[2], pready[2], odone[2], done;
   uint32_t tmem;
-  int abort;
+  int abort, again;                         // again: a weight of the first pass passed kMost
   float red[kRows];                         // a row's maximum (at the end its sum), from one half to the other
 };
 static_assert(sizeof(PCtl) <= 2048 && kSmem + 2048 <= 227 * 1024, "shared memory");
@@ -95,8 +96,12 @@ struct Work {
 
 // ------------------------------------------------------------------- products
 
-// row tile t; tiles that only the other one sees: their units are given back
-__device__ void role_mma(const ExpandedParams &p, int t, int n, int all, int keys, uint8_t *smem, PCtl &c, uint32_t tmem) {
+// Row tile t; tiles that only the other one sees: their units are given back.
+// S of the two row tiles takes turns, row tile 0 first: left alone they run in step,
+// both at their products and then both at their softmax (5,500 cycles a pair of
+// tiles, of which the products take 2,570).  `n0`: key tiles of row tile 0 (0: there
+// is no other row tile).
+__device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all, int keys, uint8_t *smem, PCtl &c, uint32_t tmem) {
   constexpr uint32_t IQK = idesc_of(true, 128, 128, false, false), IPV = idesc_of(true, 128, 64, false, true);
   const uint32_t lead = elect_one();
   const uint64_t dQ = sdesc(smem_u32(smem + t * 3 * kUnit), 16, 1024);
@@ -104,6 +109,8 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int all, int key
   const uint32_t S = tmem + t * 128, O = tmem + kColO + t * 128;
   auto full = [&](uint32_t u) { wait_cap(&c.full[u % kUnits], (u / kUnits) & 1, &c.abort, p.hdr); };
   auto qk = [&](int j) {
+    if (t == 1 && j < n0) wait_cap(&c.sfull[0], j & 1, &c.abort, p.hdr);
+    if (t == 0 && n0 > 0 && j > 0) wait_cap(&c.sfull[1], (j - 1) & 1, &c.abort, p.hdr);
 #pragma unroll
     for (int ch = 0; ch < 3; ++ch) {
       const uint32_t u = kPerTile * j + ch;
@@ -209,6 +216,11 @@ __device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtenso
 
 // -------------------------------------------------------------------- softmax
 
+// FIX: weights relative to the row's maximum over its first tile, whatever follows.
+// bf16 and fp32 hold 2^+-126, so a later score may well pass it; where 64 weights sum
+// to more than 2^32 the CTA takes a second pass with a running maximum.  (With one,
+// the two warps of a row agree on it in every tile: 1,475 cycles from S to the weights.)
+template <bool FIX>
 __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Work &w, uint8_t *smem, PCtl &c,
                              uint32_t tmem) {
   constexpr int NC = 64;                    // S columns a thread, and O columns
@@ -224,8 +236,9 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   if (live) see = p.causal ? min(max(w.n - sh.len + sh.first + row + 1, 0), w.n) : w.n;
   const int some = __reduce_max_sync(0xffffffffu, see);
   const int every = __reduce_min_sync(0xffffffffu, live ? see : 0x7fffffff);
-  const float f = p.scale_log2;
+  const float f = p.scale_log2, fs = f > 0.f ? f : 1.f;   // score = fs * s
   float m = kNegInf, l = 0.f;
+  bool over = false;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int k0 = j * kKeys + hf * NC;
@@ -233,7 +246,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     __syncwarp();
     tc_fence_after();
     const bool none = k0 >= some;
-    float s[NC], mx = kNegInf, fs = f;
+    float s[NC];
     if (!none) {
       pf::ld32_issue(S, s);
       pf::ld32_issue(S + 32, s + 32);
@@ -242,47 +255,51 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
       if (!(f > 0.f)) {                     // (the products' order is turned around)
 #pragma unroll
         for (int i = 0; i < NC; ++i) s[i] *= f;
-        fs = 1.f;
       }
       if (k0 + NC > every) {
         const int lim = see - k0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) s[i] = i < lim ? s[i] : kNegInf;
       }
-      float x0 = s[0], x1 = s[1];
-#pragma unroll
-      for (int i = 2; i < NC; i += 2) {
-        x0 = fmaxf(x0, s[i]);
-        x1 = fmaxf(x1, s[i + 1]);
-      }
-      mx = fmaxf(x0, x1) * fs;
     }
-    // ---- the running maximum moves when some score passes it by 2^kLazy
-    if (named_sync_or(pair, 64, mx > m + kLazy)) {
-      // with the row's other keys
-      if (hf == 0) c.red[row] = mx;
-      named_sync(pair, 64);
-      if (hf == 1) {
-        mx = fmaxf(mx, c.red[row]);
-        c.red[row] = mx;
-      }
-      named_sync(pair, 64);
-      if (hf == 0) mx = c.red[row];
-      const float mn = fmaxf(m, mx);
-      const float al = mn == kNegInf ? 1.f : ex2_approx(m - mn);
-      m = mn;
-      l *= al;
-      if (j > 0) {                          // (S of this tile complete: so is the product before it)
-#pragma unroll 1
-        for (int ch = 0; ch < NC; ch += 16) {
-          float o[16];
-          tmem_ld16(O + ch, o);
-          uint32_t v[16];
+    if (!FIX || j == 0) {
+      float mx = kNegInf;
+      if (!none) {
+        float x0 = s[0], x1 = s[1];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(o[i] * al);
-          tmem_st16(O + ch, v);
+        for (int i = 2; i < NC; i += 2) {
+          x0 = fmaxf(x0, s[i]);
+          x1 = fmaxf(x1, s[i + 1]);
         }
-        tmem_st_wait();
+        mx = fmaxf(x0, x1) * fs;
+      }
+      // ---- the running maximum moves when some score passes it by 2^kLazy
+      if (named_sync_or(pair, 64, mx > m + kLazy)) {
+        // with the row's other keys
+        if (hf == 0) c.red[row] = mx;
+        named_sync(pair, 64);
+        if (hf == 1) {
+          mx = fmaxf(mx, c.red[row]);
+          c.red[row] = mx;
+        }
+        named_sync(pair, 64);
+        if (hf == 0) mx = c.red[row];
+        const float mn = fmaxf(m, mx);
+        const float al = mn == kNegInf ? 1.f : ex2_approx(m - mn);
+        m = mn;
+        l *= al;
+        if (j > 0) {                        // (S of this tile complete: so is the product before it)
+#pragma unroll 1
+          for (int ch = 0; ch < NC; ch += 16) {
+            float o[16];
+            tmem_ld16(O + ch, o);
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(o[i] * al);
+            tmem_st16(O + ch, v);
+          }
+          tmem_st_wait();
+        }
       }
     }
     // ---- weights
@@ -306,7 +323,9 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
         }
         tmem_st16(S + ch / 2, pk);
       }
-      l += l2.x + l2.y;
+      const float add = l2.x + l2.y;
+      l += add;
+      if (FIX) over = over || add > kMost;
     }
     // The last tile's rows past the sequence are its neighbour's, who may hold
     // anything: zeros, for a zero weight times them must be zero (up to the 16 that
@@ -325,6 +344,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.pready[rt]);
   }
+  if (FIX && over && live) c.again = 1;
   // ---- the sum, the last product, the output
   named_sync(pair, 64);                     // the other warp has read the last maximum
   if (hf == 0) c.red[row] = l;
@@ -389,6 +409,27 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   if (live && hf == 0 && p.lse_out) p.lse_out[r_out] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
 }
 
+__device__ __forceinline__ void init_barriers(PCtl &c, int row_tiles) {
+  for (int i = 0; i < kUnits; ++i) {
+    mbar_init(&c.full[i], 1);
+    mbar_init(&c.empty[i], row_tiles);
+  }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&c.qfull[i], 1);
+    mbar_init(&c.sfull[i], 1);
+    mbar_init(&c.pready[i], 8);
+    mbar_init(&c.odone[i], 1);
+  }
+  mbar_init(&c.done, row_tiles);
+  c.again = 0;
+  fence_mbar_init();
+}
+// the barriers' memory is given back, to be initialised anew
+__device__ __forceinline__ void drop_barriers(PCtl &c) {
+  for (uint64_t *b = c.full; b <= &c.done; ++b)
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const ExpandedParams p, const __grid_constant__ CUtensorMap mq,
                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mr,
@@ -419,42 +460,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
   } else if (tid == 0) {
-    for (int i = 0; i < kUnits; ++i) {
-      mbar_init(&c.full[i], 1);
-      mbar_init(&c.empty[i], w.row_tiles);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.qfull[i], 1);
-      mbar_init(&c.sfull[i], 1);
-      mbar_init(&c.pready[i], 8);
-      mbar_init(&c.odone[i], 1);
-    }
-    mbar_init(&c.done, w.row_tiles);
+    init_barriers(c, w.row_tiles);
     c.abort = 0;
-    fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
+  // between the passes: every role is at its end; the barriers begin anew
+  auto once_more = [&]() {
+    tc_fence_before();
+    fence_async_smem();                     // (the queries come again to where the output was)
+    __syncthreads();
+    tc_fence_after();
+    const bool again = *reinterpret_cast<volatile int *>(&c.again) && !*reinterpret_cast<volatile int *>(&c.abort);
+    __syncthreads();
+    if (again) {
+      if (tid == 0) {
+        drop_barriers(c);
+        init_barriers(c, w.row_tiles);
+      }
+      __syncthreads();
+    }
+    return again;
+  };
   if (warp < 16) {
     setmaxnreg_to<kLaunchRegs, kRegSoft>();
-    if (warp < 8 * w.row_tiles) role_softmax(p, sh, w, smem, c, tmem);
+    if (warp < 8 * w.row_tiles) role_softmax<true>(p, sh, w, smem, c, tmem);
+    if (once_more()) {
+      if (warp < 8 * w.row_tiles) role_softmax<false>(p, sh, w, smem, c, tmem);
+      once_more();
+    }
   } else {
     setmaxnreg_to<kLaunchRegs, kRegCtl>();
-    if (warp < 16 + w.row_tiles) {
-      const int t = warp - 16;
-      role_mma(p, t, __shfl_sync(0xffffffffu, w.tiles[t & 1], 0), __shfl_sync(0xffffffffu, all, 0),
-               __shfl_sync(0xffffffffu, w.n, 0), smem, c, tmem);
-    } else if (tid == 18 * 32) {
-      role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, all, smem, c);
-    }
-    __syncwarp();
+    const int t = warp - 16;
+    bool again;
+    do {
+      if (t < w.row_tiles)
+        role_mma(p, t, __shfl_sync(0xffffffffu, w.tiles[t & 1], 0),
+                 __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, all, 0),
+                 __shfl_sync(0xffffffffu, w.n, 0), smem, c, tmem);
+      else if (tid == 18 * 32)
+        role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, all, smem, c);
+      __syncwarp();
+      again = once_more();
+    } while (again);
   }
-  tc_fence_before();
-  __syncthreads();
   if (warp == 16) {
-    tc_fence_after();
     tmem_dealloc(tmem, 512);
     griddep_wait();                         // the grid does not end before its header is cleared
   }

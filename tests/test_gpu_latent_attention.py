@@ -335,3 +335,43 @@ def test_a_prompt_and_its_next_tokens(fmt):
     # rounded on the way: expanded keys and values or absorbed queries (2^-8 of sums of unit size, in the
     # scores times |q| ~ 14 and the scale 0.07: below 2^-6 a score), the gathered rows (2^-8)
     assert ((got - want).abs() <= bound + 2.0 ** -4).all()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_prefill_increasing_scores(sign):
+    """Keys aligned with the queries and ever longer: scores pass the first tile's by hundreds (the second pass with
+    a running maximum), in one sequence of two and for one head of two."""
+    new, keys, H = [300, 40], [1300, 700], 2
+    q, kn, kr, v = prefill_case(new, keys, H)
+    u = torch.randn(128, device=DEV, generator=torch.Generator(DEV).manual_seed(9))
+    q[:300, 1, :128] = u.bfloat16()
+    kn[:1300, 1] = (sign * u * (torch.arange(1300, device=DEV) / 100.0 - 3)[:, None]).bfloat16()
+    o, lse, ws = pa.latent_prefill(q, kn, kr, v, L.starts_of(new), L.starts_of(keys), SCALE * sign, out_fp32=True,
+                                   return_lse=True)
+    ref, rl, bound = L.prefill_reference(q, kn, kr, v, new, keys, SCALE * sign)
+    L.within(o, ref, bound)
+    L.lse_within(lse, rl, most=0.1)   # sums |q k| of thousands: 2^-16 of them
+    ob, _ = pa.latent_prefill(q, kn, kr, v, L.starts_of(new), L.starts_of(keys), SCALE * sign, workspace=ws)
+    assert torch.equal(ob, o.bfloat16()) and pa.read_error(ws) == 0
+
+
+def test_prefill_negative_and_zero_scale():
+    new, keys, H = [129, 5], [200, 300], 2
+    q, kn, kr, v = prefill_case(new, keys, H)
+    for scale in (-SCALE, 0.0):
+        o, lse, _ = pa.latent_prefill(q, kn, kr, v, L.starts_of(new), L.starts_of(keys), scale, out_fp32=True,
+                                      return_lse=True)
+        ref, rl, bound = L.prefill_reference(q, kn, kr, v, new, keys, scale)
+        L.within(o, ref, bound)
+        L.lse_within(lse, rl)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_decode_negative_and_zero_scale(fmt):
+    lens = [129, 5]
+    kv, vals, q, tables, sl = decode_case(fmt, lens, 2, 20)
+    for scale in (-SCALE, 0.0):
+        o, lse, _ = pa.latent_decode(kv, q, tables, sl, scale, out_fp32=True, return_lse=True)
+        ref, rl, bound = L.decode_reference(fmt, vals, q, lens, tables, scale)
+        L.within(o, ref, bound)
+        L.lse_within(lse, rl)
