@@ -57,6 +57,9 @@ struct ExpandedParams {
   int out_fp32;
   float *lse_out;
   uint32_t *hdr;
+  // partial outputs of items in pieces: [item][piece][256][128] and their lse, or null
+  float *part_o;
+  float *part_lse;
 };
 
 struct AbsorbedParams {
@@ -90,6 +93,7 @@ DecodePlan plan_latent_decode(int B, int Q, int H, int max_seq_len);
 
 cudaError_t launch_latent_append(const LatentAppendParams &p, cudaStream_t s);
 cudaError_t launch_latent_gather(const LatentGatherParams &p, cudaStream_t s);
+long long latent_prefill_parts(int B, int H, int T, int N);
 cudaError_t launch_latent_prefill(const ExpandedParams &p, cudaStream_t s);
 cudaError_t launch_latent_decode(const AbsorbedParams &p, cudaStream_t s);
 

@@ -177,7 +177,8 @@ int pa_latent_gather(const pa_latent_cache *kv, const int32_t *block_tables, int
 }
 
 size_t pa_latent_prefill_workspace_bytes(const pa_latent_prefill_problem *p) {
-  return check_prefill(p) == PA_OK ? kHdrWords * 4 : 0;
+  if (check_prefill(p) != PA_OK) return 0;
+  return kHdrWords * 4 + (size_t)latent_prefill_parts(p->batch, p->num_heads, p->num_tokens, p->num_keys) * (kV + 1) * 4;
 }
 
 int pa_latent_prefill(const pa_latent_prefill_problem *p, void *ws, size_t ws_bytes, pa_stream_t stream) {
@@ -222,6 +223,10 @@ int pa_latent_prefill(const pa_latent_prefill_problem *p, void *ws, size_t ws_by
   a.out_fp32 = p->out_fp32 ? 1 : 0;
   a.lse_out = p->lse_out;
   a.hdr = static_cast<uint32_t *>(ws);
+  if (const long long rows = latent_prefill_parts(p->batch, p->num_heads, p->num_tokens, p->num_keys)) {
+    a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHdrWords * 4);
+    a.part_lse = a.part_o + rows * kV;
+  }
   if (launch_clear(a.hdr, s) != cudaSuccess) return PA_ERR_CUDA;
   return launch_latent_prefill(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

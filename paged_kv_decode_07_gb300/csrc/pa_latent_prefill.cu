@@ -32,7 +32,7 @@ constexpr int kPerTile = 5;                 // units of a tile: three of K, two 
 constexpr uint32_t kOffRing = 2 * 3 * kUnit;
 constexpr uint32_t kSmem = kOffRing + kUnits * kUnit + 1024;
 constexpr int kThreads = 640;
-constexpr int kLaunchRegs = 96, kRegCtl = 40, kRegSoft = 104;   // 5 groups: 40 + 4 * 104 <= 5 * 96
+constexpr int kLaunchRegs = 96, kRegCtl = 64, kRegSoft = 104;   // 5 groups: 40 + 4 * 104 <= 5 * 96
 static_assert(kRegCtl + 4 * kRegSoft <= 5 * kLaunchRegs && kLaunchRegs == 65536 / kThreads / 8 * 8, "register split");
 constexpr float kLazy = 8.0f;               // log2 of how far a score may pass the running maximum
 constexpr float kMost = 0x1p32f;            // first pass: sum of 64 weights up to which a row goes on
@@ -47,27 +47,56 @@ struct PCtl {
 };
 static_assert(sizeof(PCtl) <= 2048 && kSmem + 2048 <= 227 * 1024, "shared memory");
 
-// A CTA's share: 256 tokens of a sequence, a head.  Sequence b's tiles are given
-// the places from q_starts[b] / 256 + b on, of which there are enough (and at most one
-// too many), so that a search finds a place's sequence without the counts of those
-// before it.  Places are taken from the last: the last tokens of a prompt see most.
+// CTAs at once: one per SM of this GPU (another count would only split the work worse)
+constexpr int kSms = 152;
+constexpr int kMinTiles = 8;                // key tiles of a piece at least
+
+// Long sequences: heads go in groups of just so many that the tiles of a group fill the
+// GPU, so that the keys of few heads are in use at a time and stay in L2 for all their
+// tiles (4,096 tokens over 16,384 keys of 32 heads, 268 MB of keys and values: 801 ->
+// 785 us).  Short ones: all heads of a tile first, which puts the longest items of the
+// whole batch first (eight chunks of up to 4,096 keys: 181 us in groups, 170).
+__device__ __forceinline__ int heads_at_once(int tiles) { return tiles < kSms ? (kSms + tiles - 1) / max(tiles, 1) : 1; }
+
+// A CTA's share: 256 tokens of a sequence (a tile), a head, and a piece of its keys.
+// Tiles are counted over all sequences and taken from the last: the last tokens of a
+// prompt see most.
 struct Share {
   int b, head, start, len, first;           // b < 0: nothing to do; first token of the tile
   int key0, n;                              // the sequence's key rows
+  int item, piece, pieces, most;            // place among the items in pieces (-1: not one); most pieces of one
 };
-__device__ __forceinline__ Share find_share(const ExpandedParams &p, int index) {
+// Items (tile, head) that are taken in pieces: all, where they fill less than half of
+// the SMs; those of a last round that fills at most half of them, in as many as make it
+// a full round of short ones (512 items, three rounds and 56: 831 -> 797 us).
+struct Split {
+  int items, pieces;
+};
+__device__ __forceinline__ Split split_of(int items, bool on) {
+  const int rem = items < kSms ? items : items % kSms;
+  if (!on || rem == 0 || 2 * rem > kSms) return {0, 1};
+  return {rem, min(16, kSms / rem)};
+}
+// key tiles that the last token of a tile sees, and the pieces that they make
+__device__ __forceinline__ int tiles_of(const ExpandedParams &p, const Share &s, int last) {
+  return ((p.causal ? min(max(s.n - s.len + last + 1, 0), s.n) : s.n) + kKeys - 1) / kKeys;
+}
+__device__ __forceinline__ int pieces_of(const ExpandedParams &p, const Share &s, int pieces) {
+  return max(1, min(pieces, tiles_of(p, s, min(s.first + kRows, s.len) - 1) / kMinTiles));
+}
+__device__ __forceinline__ void keys_of(const ExpandedParams &p, Share &r) {
+  r.key0 = min(max(__ldg(p.kv_starts + r.b), 0), p.N);
+  r.n = min(max(__ldg(p.kv_starts + r.b + 1), r.key0), p.N) - r.key0;
+}
+
+// More than 32 sequences: sequence b's tiles are given the places from q_starts[b] /
+// 256 + b on, of which there are enough (and at most one too many), so that a search
+// finds a place's sequence without the counts of those before it.
+__device__ __forceinline__ Share search_share(const ExpandedParams &p, int index) {
   const int lane = threadIdx.x & 31;
   auto start = [&](int b) { return min(max(__ldg(p.q_starts + b), 0), p.T); };
   auto place = [&](int b) { return start(b) / kRows + b; };
-  if (index == 0) {
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-      const int a = __ldg(p.q_starts + b), e = __ldg(p.q_starts + b + 1);
-      const int c = __ldg(p.kv_starts + b), d = __ldg(p.kv_starts + b + 1);
-      if (a < 0 || e < a || e > p.T || c < 0 || d < c || d > p.N) flag(p.hdr, PA_ERRF_BAD_Q_START);
-      else if (p.causal && d > c && e - a > d - c) flag(p.hdr, PA_ERRF_LEN_LT_QLEN);
-    }
-  }
-  Share r = {-1, index % p.H, 0, 0, 0, 0, 0};
+  Share r = {-1, index % p.H, 0, 0, 0, 0, 0, -1, 0, 1, 1};
   const int at = place(p.B) - 1 - index / p.H;
   if (at < 0) return r;
   int lo = 0, hi = p.B;                     // the last sequence of [lo, hi) that starts at or before `at`
@@ -83,15 +112,79 @@ __device__ __forceinline__ Share find_share(const ExpandedParams &p, int index) 
   if (first < 0 || first >= r.len) return r;
   r.b = lo;
   r.first = (int)first;
-  r.key0 = min(max(__ldg(p.kv_starts + lo), 0), p.N);
-  r.n = min(max(__ldg(p.kv_starts + lo + 1), r.key0), p.N) - r.key0;
+  keys_of(p, r);
   return r;
 }
 
+// every thread of a warp gets the answer; `index`: of the CTA, or, in the join, of an
+// item in pieces
+__device__ __forceinline__ Share find_share(const ExpandedParams &p, int index, bool join) {
+  if (!join && index == 0) {
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      const int a = __ldg(p.q_starts + b), e = __ldg(p.q_starts + b + 1);
+      const int c = __ldg(p.kv_starts + b), d = __ldg(p.kv_starts + b + 1);
+      if (a < 0 || e < a || e > p.T || c < 0 || d < c || d > p.N) flag(p.hdr, PA_ERRF_BAD_Q_START);
+      else if (p.causal && d > c && e - a > d - c) flag(p.hdr, PA_ERRF_LEN_LT_QLEN);
+    }
+  }
+  if (p.B > 32) return search_share(p, index);   // (nothing is in pieces then)
+  const int lane = threadIdx.x & 31;
+  int start = 0, len = 0;                   // this lane's sequence, and the tiles up to it
+  if (lane < p.B) {
+    start = min(max(__ldg(p.q_starts + lane), 0), p.T);
+    len = max(min(max(__ldg(p.q_starts + lane + 1), 0), p.T) - start, 0);
+  }
+  const int n = (len + kRows - 1) / kRows;
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  const int tiles = __shfl_sync(0xffffffffu, inc, 31), items = tiles * p.H;
+  const Split sp = split_of(items, p.part_o != nullptr);
+  Share r = {-1, 0, 0, 0, 0, 0, 0, -1, 0, 1, sp.pieces};
+  int t = index;
+  if (join) {
+    if (index >= sp.items) return r;
+    t = items - sp.items + index;
+    r.item = index;
+    r.pieces = sp.pieces;
+  } else if (sp.items > 0 && index >= items - sp.items) {
+    const int x = index - (items - sp.items);
+    r.item = x / sp.pieces;
+    r.piece = x % sp.pieces;
+    r.pieces = sp.pieces;
+    t = items - sp.items + r.item;
+  }
+  if (t >= items) return r;
+  const int heads = p.part_o ? heads_at_once(tiles) : p.H, group = t / (heads * tiles), i = t % (heads * tiles);
+  const int of = min(heads, p.H - group * heads), tile = tiles - 1 - i / of;
+  r.head = group * heads + i % of;
+  const int l = __ffs(__ballot_sync(0xffffffffu, inc > tile)) - 1;
+  r.start = __shfl_sync(0xffffffffu, start, l);
+  r.len = __shfl_sync(0xffffffffu, len, l);
+  r.first = (tile - __shfl_sync(0xffffffffu, inc - n, l)) * kRows;
+  r.b = l;
+  keys_of(p, r);
+  if (r.item >= 0) {
+    r.pieces = pieces_of(p, r, sp.pieces);
+    if (r.pieces == 1) r.item = -1;
+    if (r.piece >= r.pieces) r.b = -1;
+  }
+  return r;
+}
+// row of a piece's partial output
+__device__ __forceinline__ size_t part_row(const Share &s, int row) {
+  return ((size_t)s.item * s.most + s.piece) * kRows + row;
+}
+
 struct Work {
-  int nrows, n;                             // rows of the CTA, keys of the sequence
+  int nrows;                                // rows of the CTA
+  int kt0, keys;                            // its first key tile; keys from there on
   int tiles[2];                             // key tiles of each row tile
   int row_tiles;
+  size_t part;                              // first row among the partial outputs
 };
 
 // ------------------------------------------------------------------- products
@@ -184,7 +277,7 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
 // one lane; rows past the sequence are its neighbours' (or zeros past the tensor)
 __device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
                                           const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, int row_tiles,
-                                          int all, uint8_t *smem, PCtl &c) {
+                                          int kt0, int all, uint8_t *smem, PCtl &c) {
   for (int t = 0; t < row_tiles; ++t) {
     mbar_arrive_expect_tx(&c.qfull[t], 3 * kUnit);
     for (int ch = 0; ch < 3; ++ch)
@@ -194,7 +287,7 @@ __device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtenso
   bool ok = true;
 #pragma unroll 1
   for (int j = 0; j < all && ok; ++j) {
-    const int key = sh.key0 + j * kKeys;
+    const int key = sh.key0 + (kt0 + j) * kKeys;
 #pragma unroll 1
     for (int i = 0; i < kPerTile; ++i, ++u) {
       const uint32_t st = u % kUnits;
@@ -219,7 +312,8 @@ __device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtenso
 // FIX: weights relative to the row's maximum over its first tile, whatever follows.
 // bf16 and fp32 hold 2^+-126, so a later score may well pass it; where 64 weights sum
 // to more than 2^32 the CTA takes a second pass with a running maximum.  (With one,
-// the two warps of a row agree on it in every tile: 1,475 cycles from S to the weights.)
+// the two warps of a row agree on it in every tile: 4,096 tokens over 16,384 keys 970 us
+// instead of 857.)
 template <bool FIX>
 __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Work &w, uint8_t *smem, PCtl &c,
                              uint32_t tmem) {
@@ -233,7 +327,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   const bool live = row < w.nrows;
   // keys that this thread's row sees; that some, and that every row of the warp sees
   int see = 0;
-  if (live) see = p.causal ? min(max(w.n - sh.len + sh.first + row + 1, 0), w.n) : w.n;
+  if (live) see = (p.causal ? min(max(sh.n - sh.len + sh.first + row + 1, 0), sh.n) : sh.n) - w.kt0 * kKeys;   // (from the first tile on)
   const int some = __reduce_max_sync(0xffffffffu, see);
   const int every = __reduce_min_sync(0xffffffffu, live ? see : 0x7fffffff);
   const float f = p.scale_log2, fs = f > 0.f ? f : 1.f;   // score = fs * s
@@ -246,32 +340,36 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     __syncwarp();
     tc_fence_after();
     const bool none = k0 >= some;
-    float s[NC];
-    if (!none) {
-      pf::ld32_issue(S, s);
-      pf::ld32_issue(S + 32, s + 32);
+    // 32 columns: products (or, where the factor is not positive, which turns their
+    // order around, scores), hidden keys at -inf
+    auto load = [&](int ch, float *s) {
+      pf::ld32_issue(S + ch, s);
       pf::ld_wait(s);
-      pf::ld_wait(s + 32);
-      if (!(f > 0.f)) {                     // (the products' order is turned around)
+      if (!(f > 0.f)) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) s[i] *= f;
+        for (int i = 0; i < 32; ++i) s[i] *= f;
       }
       if (k0 + NC > every) {
-        const int lim = see - k0;
+        const int lim = see - k0 - ch;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) s[i] = i < lim ? s[i] : kNegInf;
+        for (int i = 0; i < 32; ++i) s[i] = i < lim ? s[i] : kNegInf;
       }
-    }
+    };
     if (!FIX || j == 0) {
       float mx = kNegInf;
       if (!none) {
-        float x0 = s[0], x1 = s[1];
+#pragma unroll 1
+        for (int ch = 0; ch < NC; ch += 32) {
+          float s[32];
+          load(ch, s);
+          float x0 = s[0], x1 = s[1];
 #pragma unroll
-        for (int i = 2; i < NC; i += 2) {
-          x0 = fmaxf(x0, s[i]);
-          x1 = fmaxf(x1, s[i + 1]);
+          for (int i = 2; i < 32; i += 2) {
+            x0 = fmaxf(x0, s[i]);
+            x1 = fmaxf(x1, s[i + 1]);
+          }
+          mx = fmaxf(mx, fmaxf(x0, x1) * fs);
         }
-        mx = fmaxf(x0, x1) * fs;
       }
       // ---- the running maximum moves when some score passes it by 2^kLazy
       if (named_sync_or(pair, 64, mx > m + kLazy)) {
@@ -310,27 +408,32 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     } else {
       const float mu = m == kNegInf ? 0.f : m;
       const float2 nm = make_float2(-mu, -mu), ff = make_float2(fs, fs);
-      float2 l2 = make_float2(0.f, 0.f);
+      float2 l2 = make_float2(0.f, 0.f), l3 = l2;
 #pragma unroll
       for (int ch = 0; ch < NC; ch += 32) {
+        float s[32];
+        load(ch, s);
         uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 y = ffma2(make_float2(s[ch + i], s[ch + i + 1]), ff, nm);
+        for (int i = 0; i < 32; i += 4) {
+          const float2 y = ffma2(make_float2(s[i], s[i + 1]), ff, nm), z = ffma2(make_float2(s[i + 2], s[i + 3]), ff, nm);
           const float2 a = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          const float2 b = make_float2(ex2_approx(z.x), ex2_approx(z.y));
           l2 = pf::fadd2(l2, a);
+          l3 = pf::fadd2(l3, b);
           pk[i / 2] = tc::f2_to_bf2(a.x, a.y);
+          pk[i / 2 + 1] = tc::f2_to_bf2(b.x, b.y);
         }
-        tmem_st16(S + ch / 2, pk);
+        tmem_st16(S + ch / 2, pk);          // (over columns that have been read)
       }
-      const float add = l2.x + l2.y;
+      const float add = (l2.x + l2.y) + (l3.x + l3.y);
       l += add;
       if (FIX) over = over || add > kMost;
     }
     // The last tile's rows past the sequence are its neighbour's, who may hold
     // anything: zeros, for a zero weight times them must be zero (up to the 16 that
     // a step of the product takes)
-    const int valid = w.n - j * kKeys;
+    const int valid = w.keys - j * kKeys;
     if (valid < kKeys && (valid & 15)) {
       const uint32_t u = kPerTile * j + 3;
       for (int h = 0; h < 2; ++h) wait_cap(&c.full[(u + h) % kUnits], ((u + h) / kUnits) & 1, &c.abort, p.hdr);
@@ -358,18 +461,21 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   // the queries' place takes the output: their copy has landed, and no product reads them
   wait_cap(&c.qfull[rt], 0, &c.abort, p.hdr);
   if (n > 0) wait_cap(&c.odone[rt], 0, &c.abort, p.hdr);
+  const bool partial = sh.item >= 0, wide = partial || p.out_fp32;
   // (fp32 rows reach into what the other row tile's products read)
-  if (p.out_fp32 && w.row_tiles > 1) {
+  if (wide && w.row_tiles > 1) {
     wait_cap(&c.qfull[rt ^ 1], 0, &c.abort, p.hdr);
     if (w.tiles[rt ^ 1] > 0) wait_cap(&c.odone[rt ^ 1], 0, &c.abort, p.hdr);
   }
   __syncwarp();
   tc_fence_after();
   const float inv = l != 0.f ? 1.f / l : 0.f;   // (0: the row saw no key; a NaN among its scores goes on)
-  const long long r_out = (long long)(sh.start + sh.first + row) * p.H + sh.head;
+  auto row_out = [&](int r) {
+    return partial ? w.part + r : (size_t)(sh.start + sh.first + r) * p.H + sh.head;
+  };
   // through shared memory, 16-byte pieces swizzled by row, to leave in whole rows
-  const int shift = p.out_fp32 ? 5 : 4;         // pieces a row
-  uint8_t *const base = p.out_fp32 ? smem + rt * 65536 : smem + rt * 3 * kUnit;
+  const int shift = wide ? 5 : 4;               // pieces a row
+  uint8_t *const base = wide ? smem + rt * 65536 : smem + rt * 3 * kUnit;
   auto piece_at = [&](int r, int k) { return base + (((r << shift) + (k ^ (r & 7))) << 4); };
   const int r = tid & 127;
 #pragma unroll 1
@@ -384,7 +490,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = l != 0.f ? o[i] * inv : 0.f;
     const int d = hf * NC + ch;
-    if (p.out_fp32) {
+    if (wide) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4 *>(piece_at(r, d / 4 + i)) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -397,16 +503,14 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     }
   }
   named_sync(pair, 64);                     // both halves of the rows are there
-  uint4 *const dst = static_cast<uint4 *>(p.out);
+  uint4 *const dst = static_cast<uint4 *>(partial ? static_cast<void *>(p.part_o) : p.out);
 #pragma unroll 4
   for (int i = lane; i < 16 << shift; i += 32) {   // 16 of the pair's 32 rows each
     const int q = wq * 32 + hf * 16 + (i >> shift), k = i & ((1 << shift) - 1);
-    if (rt * 128 + q < w.nrows) {
-      const long long to = (long long)(sh.start + sh.first + rt * 128 + q) * p.H + sh.head;
-      dst[(to << shift) + k] = *reinterpret_cast<const uint4 *>(piece_at(q, k));
-    }
+    if (rt * 128 + q < w.nrows) dst[(row_out(rt * 128 + q) << shift) + k] = *reinterpret_cast<const uint4 *>(piece_at(q, k));
   }
-  if (live && hf == 0 && p.lse_out) p.lse_out[r_out] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+  float *const lse = partial ? p.part_lse : p.lse_out;
+  if (live && hf == 0 && lse) lse[row_out(row)] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
 }
 
 __device__ __forceinline__ void init_barriers(PCtl &c, int row_tiles) {
@@ -439,23 +543,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ PCtl c;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   griddep_launch();
-  const Share sh = find_share(p, blockIdx.x);
+  const Share sh = find_share(p, blockIdx.x, false);
   if (sh.b < 0) {
     griddep_wait();                         // the grid does not end before its header is cleared
     return;
   }
   Work w;
   w.nrows = min(kRows, sh.len - sh.first);
-  w.n = sh.n;
   w.row_tiles = w.nrows > 128 ? 2 : 1;
-  int all = 0;
+  int all = tiles_of(p, sh, sh.first + w.nrows - 1);
+  const int per = (all + sh.pieces - 1) / sh.pieces;
+  w.kt0 = min(all, sh.piece * per);
+  const int end = min(all, w.kt0 + per);
+  all = end - w.kt0;
+  w.keys = sh.n - w.kt0 * kKeys;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int last = min(t * 128 + 127, w.nrows - 1);   // row of the row tile that sees most
-    const int see = p.causal ? min(max(sh.n - sh.len + sh.first + last + 1, 0), sh.n) : sh.n;
-    w.tiles[t] = t < w.row_tiles ? (see + kKeys - 1) / kKeys : 0;
-    all = max(all, w.tiles[t]);
-  }
+  for (int t = 0; t < 2; ++t)
+    w.tiles[t] = t < w.row_tiles ? max(min(tiles_of(p, sh, sh.first + min(t * 128 + 127, w.nrows - 1)), end) - w.kt0, 0) : 0;
+  w.part = sh.item >= 0 ? part_row(sh, 0) : 0;
   if (warp == 16) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
@@ -499,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t < w.row_tiles)
         role_mma(p, t, __shfl_sync(0xffffffffu, w.tiles[t & 1], 0),
                  __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, all, 0),
-                 __shfl_sync(0xffffffffu, w.n, 0), smem, c, tmem);
+                 __shfl_sync(0xffffffffu, w.keys, 0), smem, c, tmem);
       else if (tid == 18 * 32)
-        role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, all, smem, c);
+        role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, w.kt0, all, smem, c);
       __syncwarp();
       again = once_more();
     } while (again);
@@ -509,6 +614,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 16) {
     tmem_dealloc(tmem, 512);
     griddep_wait();                         // the grid does not end before its header is cleared
+  }
+}
+
+// out = sum_s w_s o_s / sum_s w_s over the pieces of an item's rows, w_s = exp(lse_s -
+// max); a warp a row, eight rows a CTA
+__global__ void __launch_bounds__(256) latent_prefill_join_kernel(const ExpandedParams p) {
+  constexpr int STEPS = kRows / 8;
+  griddep_wait();                           // the pieces are complete
+  const int lane = threadIdx.x & 31;
+  for (int u = blockIdx.x;; u += gridDim.x) {
+    Share sh = find_share(p, u / STEPS, true);
+    if (sh.b < 0) return;                   // past the items in pieces (or there are none)
+    const int r = u % STEPS * 8 + (threadIdx.x >> 5);
+    if (sh.item < 0 || sh.first + r >= sh.len) continue;
+    const size_t part = part_row(sh, r);
+    float M = kNegInf, sum = 0.f;
+    for (int k = 0; k < sh.pieces; ++k) M = fmaxf(M, p.part_lse[part + k * kRows]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < sh.pieces; ++k) {
+      const float ls = p.part_lse[part + k * kRows];
+      if (ls == kNegInf) continue;
+      const float wt = expf(ls - M);        // (a NaN among a piece's scores is in its lse)
+      sum += wt;
+      const float4 x = __ldcs(reinterpret_cast<const float4 *>(p.part_o + (part + k * kRows) * kV) + lane);
+      acc.x += wt * x.x;
+      acc.y += wt * x.y;
+      acc.z += wt * x.z;
+      acc.w += wt * x.w;
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const size_t row = (size_t)(sh.start + sh.first + r) * p.H + sh.head;
+    if (p.out_fp32)
+      reinterpret_cast<float4 *>(p.out)[row * 32 + lane] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else
+      reinterpret_cast<uint2 *>(p.out)[row * 32 + lane] =
+          make_uint2(tc::f2_to_bf2(acc.x * inv, acc.y * inv), tc::f2_to_bf2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse_out) p.lse_out[row] = sum != 0.f ? M + logf(sum) : kNegInf;
   }
 }
 
@@ -522,6 +664,15 @@ bool map_heads(CUtensorMap *m, const void *base, int dims, int heads, int count,
 }
 
 }  // namespace
+
+// Partial rows that a call may need: none where items have no keys for two pieces, or
+// fill the GPU and are short (below 64 key tiles the pieces and their join cost what they
+// save: eight chunks of up to 4,096 keys 169 -> 178 us).
+long long latent_prefill_parts(int B, int H, int T, int N) {
+  const bool few = 2 * ((long long)T / kRows + B) * H <= kSms;
+  const long long least = few ? 2 * kMinTiles : 64;
+  return B > 0 && B <= 32 && N / B >= least * kKeys ? (long long)kSms * kRows : 0;
+}
 
 cudaError_t launch_latent_prefill(const ExpandedParams &p, cudaStream_t s) {
   CUtensorMap mq, mk, mr, mv;
@@ -541,9 +692,12 @@ cudaError_t launch_latent_prefill(const ExpandedParams &p, cudaStream_t s) {
   e = cudaFuncGetAttributes(&fa, latent_prefill_kernel);
   if (e != cudaSuccess) return e;
   if ((fa.numRegs + 7) / 8 * 8 != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
-  const long long grid = ((long long)p.T / kRows + p.B) * p.H;   // every sequence has at most one tile that is not full
+  // every sequence has at most one tile that is not full; pieces are at most one an SM
+  const long long grid = ((long long)p.T / kRows + p.B) * p.H + (p.part_o ? kSms : 0);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(latent_prefill_kernel, (unsigned)grid, kThreads, kSmem, s, p, mq, mk, mr, mv);
+  e = launch_pdl(latent_prefill_kernel, (unsigned)grid, kThreads, kSmem, s, p, mq, mk, mr, mv);
+  if (e != cudaSuccess || !p.part_o) return e;
+  return launch_pdl(latent_prefill_join_kernel, 4 * kSms, 256, 0, s, p);
 }
 
 }  // namespace lat

@@ -375,3 +375,23 @@ def test_decode_negative_and_zero_scale(fmt):
         ref, rl, bound = L.decode_reference(fmt, vals, q, lens, tables, scale)
         L.within(o, ref, bound)
         L.lse_within(lse, rl)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,keys,H", [([10], [9000], 3),            # few tiles: all in pieces
+                                        ([300, 5, 0, 130], [5000, 40, 0, 2100], 4),
+                                        ([2300], [2600], 16),         # a round and a little more: the last in pieces
+                                        ([260] * 20, [1100] * 20, 4)])
+def test_prefill_pieces(new, keys, H, causal):
+    check_prefill(new, keys, H, causal)
+
+
+def test_prefill_pieces_that_see_nothing_and_hold_anything():
+    """Pieces of a causal tile that its first rows do not see, beside neighbours of NaN."""
+    m, n, H = 256, 4090, 2
+    q, kn, kr, v = prefill_case([m], [n], H, extra_k=200)
+    kn[n:], v[n:], kr[n:] = math.nan, math.nan, math.nan
+    o, lse, _ = pa.latent_prefill(q, kn, kr, v, L.starts_of([m]), L.starts_of([n]), SCALE, out_fp32=True, return_lse=True)
+    ref, rl, bound = L.prefill_reference(q, kn, kr, v, [m], [n], SCALE)
+    L.within(o, ref, bound + 2.0 ** -20)
+    L.lse_within(lse, rl)
