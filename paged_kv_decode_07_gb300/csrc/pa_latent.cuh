@@ -75,7 +75,8 @@ struct AbsorbedParams {
   float *lse_out;
   uint32_t *hdr;
   // work: see DecodePlan
-  int R, RG, S, workers;
+  int R, RG, S, workers, least;       // least: tiles of a run
+  uint32_t *flags;                    // [workers * S]
   int *starts;                        // [B + 1] tiles of the sequences before
   float *part_o;                      // [2 * workers][S][R][512]
   float *part_lse;                    // [2 * workers][S][R]
@@ -87,7 +88,7 @@ struct AbsorbedParams {
 // takes an equal run.
 constexpr int kMaxRows = 64;
 struct DecodePlan {
-  int R, RG, S, workers;
+  int R, RG, S, workers, least;
 };
 DecodePlan plan_latent_decode(int B, int Q, int H, int max_seq_len);
 

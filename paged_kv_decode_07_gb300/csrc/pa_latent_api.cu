@@ -73,7 +73,7 @@ int check_decode(const pa_latent_problem *p) {
 
 struct DecodeLayout {
   DecodePlan plan;
-  size_t starts, part_lse, part_o, total;
+  size_t flags, starts, part_lse, part_o, total;
 };
 
 DecodeLayout decode_layout(const pa_latent_problem *p) {
@@ -81,7 +81,8 @@ DecodeLayout decode_layout(const pa_latent_problem *p) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   L.plan = plan_latent_decode(p->batch, p->q_len, p->num_heads, p->max_seq_len);
   const size_t rows = (size_t)2 * L.plan.workers * L.plan.S * L.plan.R;
-  L.starts = kHdrWords * 4;
+  L.flags = kHdrWords * 4;
+  L.starts = L.flags + up((size_t)L.plan.workers * L.plan.S * 4);
   L.part_lse = L.starts + up(((size_t)p->batch + 1) * 4);
   L.part_o = L.part_lse + up(rows * 4);
   L.total = L.part_o + rows * kLatent * 4;
@@ -270,10 +271,11 @@ int pa_latent_decode(const pa_latent_cache *kv, const pa_latent_problem *p, void
   a.RG = L.plan.RG;
   a.S = L.plan.S;
   a.workers = L.plan.workers;
+  a.least = L.plan.least;
+  a.flags = reinterpret_cast<uint32_t *>(w + L.flags);
   a.starts = reinterpret_cast<int *>(w + L.starts);
   a.part_lse = reinterpret_cast<float *>(w + L.part_lse);
   a.part_o = reinterpret_cast<float *>(w + L.part_o);
-  if (launch_clear(a.hdr, s) != cudaSuccess) return PA_ERR_CUDA;
   return launch_latent_decode(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

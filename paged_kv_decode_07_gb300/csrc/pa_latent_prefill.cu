@@ -528,12 +528,6 @@ __device__ __forceinline__ void init_barriers(PCtl &c, int row_tiles) {
   c.again = 0;
   fence_mbar_init();
 }
-// the barriers' memory is given back, to be initialised anew
-__device__ __forceinline__ void drop_barriers(PCtl &c) {
-  for (uint64_t *b = c.full; b <= &c.done; ++b)
-    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const ExpandedParams p, const __grid_constant__ CUtensorMap mq,
                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mr,
@@ -582,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (again) {
       if (tid == 0) {
-        drop_barriers(c);
+        drop_barriers(c.full, &c.done);
         init_barriers(c, w.row_tiles);
       }
       __syncthreads();

@@ -34,6 +34,12 @@ __device__ __forceinline__ bool wait_cap(uint64_t *bar, uint32_t parity, int *ab
   return mbar_test(bar, parity) || wait_long(bar, parity, abort, hdr);
 }
 
+// the memory of the barriers first .. last is given back, to be initialised anew
+__device__ __forceinline__ void drop_barriers(uint64_t *first, uint64_t *last) {
+  for (uint64_t *b = first; b <= last; ++b)
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+
 // tiled copies global -> shared, completion on an mbarrier
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
   asm volatile(

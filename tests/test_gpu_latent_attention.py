@@ -395,3 +395,24 @@ def test_prefill_pieces_that_see_nothing_and_hold_anything():
     ref, rl, bound = L.prefill_reference(q, kn, kr, v, [m], [n], SCALE)
     L.within(o, ref, bound + 2.0 ** -20)
     L.lse_within(lse, rl)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("Q,H", [(1, 16), (1, 24), (2, 64), (1, 128)])
+def test_decode_scores_far_past_the_first_tile(fmt, Q, H):
+    """Some rows of some sequences: a worker goes over its run again."""
+    lens = [900, 40, 7000]
+    kv, _, q, tables, sl = decode_case(fmt, lens, Q, H)
+    u = torch.randn(512, device=DEV, generator=torch.Generator(DEV).manual_seed(5))
+    n = lens[2]
+    t = torch.arange(n, device=DEV)
+    k = u * (t / 700.0)[:, None]
+    kv.latent[tables[2, t // 16].long(), t % 16] = (k.bfloat16() if fmt == "bf16" else
+                                                    (k * 8).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    q[2, :, ::3, :512] = u.bfloat16()
+    rows, scale = L.values(fmt, kv.latent, kv.rope, kv.scale)
+    o, lse, ws = pa.latent_decode(kv, q, tables, sl, SCALE, out_fp32=True, return_lse=True)
+    ref, rl, bound = L.decode_reference(fmt, (torch.nan_to_num(rows), scale), q, lens, tables, SCALE)
+    L.within(o, ref, bound)
+    L.lse_within(lse, rl, most=0.5)   # sums |q k| * scale of up to 30,000: 2^-16 of them
+    assert pa.read_error(ws) == 0
