@@ -33,6 +33,7 @@ namespace pa {
 namespace lat {
 namespace {
 
+constexpr int kAhead = 6;                                 // FP8: tiles that L2 is asked for ahead
 constexpr uint32_t kBarSoft = 1;                          // named barrier of the softmax warps
 
 template <bool FP8, int N>
@@ -56,13 +57,13 @@ struct Geo {
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t sfull[2], pready[2], odone[2];   // of even and odd tiles
+  uint64_t sfull[2], sread[2], pready[2], odone[2];   // of even and odd tiles
   uint64_t qfull, qready, qfree, done;
   uint32_t tmem, flags;
   int abort, again;                     // again: a weight passed kMost
   Run run;
   uint32_t dead[kMaxStages];            // bit j: page j of the tile has a bad id
-  float fac[kMaxRows];                  // at the end of a piece a row's 1 / sum
+  alignas(16) float fac[kMaxRows];      // at the end of a piece a row's 1 / sum
 };
 static_assert(sizeof(Ctl) <= 2048, "Geo::SMEM leaves 2 KB");
 
@@ -70,8 +71,9 @@ static_assert(sizeof(Ctl) <= 2048, "Geo::SMEM leaves 2 KB");
 
 // A warp for each product: between a commit and the next product of the same warp
 // lie some 350 cycles of barrier latencies, which pass under the other's products.
-// S of a tile waits for its copy and for the weights of the tile before last, whose
-// buffer it takes.  SAFE: every piece twice, its first time for the maximum alone.
+// S of a tile waits for its copy and until the scores of the tile before last, whose
+// buffer it takes, have been read (not for their weights: 1,390 cycles a tile of 64
+// rows).  SAFE: every piece twice, its first time for the maximum alone.
 template <bool FP8, int N, bool SAFE>
 __device__ void role_scores(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uint32_t tmem) {
   using G = Geo<FP8, N>;
@@ -88,9 +90,9 @@ __device__ void role_scores(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uint
 #pragma unroll 1
     for (int k = 0; k < n; ++k, ++g) {
       const uint32_t st = g % G::NS;
-      const bool rp = g < 2 || mbar_test(&c.pready[g & 1], ((g >> 1) - 1) & 1);
+      const bool rs = g < 2 || mbar_test(&c.sread[g & 1], ((g >> 1) - 1) & 1);
       const bool rk = mbar_test(&c.full[st], (g / G::NS) & 1);
-      if (!rp) wait_long(&c.pready[g & 1], ((g >> 1) - 1) & 1, &c.abort, &c.flags);
+      if (!rs) wait_long(&c.sread[g & 1], ((g >> 1) - 1) & 1, &c.abort, &c.flags);
       if (!rk) wait_long(&c.full[st], (g / G::NS) & 1, &c.abort, &c.flags);
       tc_fence_after();
       const uint64_t at = (uint64_t)(st * (G::STAGE >> 4));
@@ -195,93 +197,136 @@ __device__ __forceinline__ void role_copy(const AbsorbedParams &p, const CUtenso
 
 // ------------------------------------------------- FP8: codes to f16 (exact)
 
-// 256 threads, 32 lanes a key row (16 codes each), eight rows apart; then the
-// rotated parts, eight lanes a row.  The next tile's codes are requested before the
-// present one's are converted.
+// The tiles of the worker's run, one after another, page ids two at a time (-1: nothing
+// to read; `dead`: bit j, page j has a bad id).
+template <int TK, bool SAFE>
+struct Tiles {
+  Piece<TK> x;
+  int tile, again;
+  bool more;
+  __device__ __forceinline__ Tiles(const AbsorbedParams &p, const Run &r) : x(r), again(SAFE ? 1 : 0) {
+    more = x.next(p);
+    tile = x.t0;
+  }
+  __device__ __forceinline__ void next(const AbsorbedParams &p) {
+    if (!more || ++tile < x.t1) return;
+    if (again > 0) {
+      --again;
+    } else {
+      more = x.next(p);
+      again = SAFE ? 1 : 0;
+    }
+    tile = x.t0;
+  }
+};
+struct Pages {
+  int id[2];
+  uint32_t dead;
+};
+
+// Two groups of 128 threads take turns at the tiles, so that one's codes are on their
+// way while the other's are converted; the ids of a group's next tile are read a tile
+// before its codes are asked for, and L2 is asked for the pages of tiles that come
+// later.  A warp takes eight rows of a chunk of 64 dims at a time, four lanes a row: the
+// swizzle then spreads its 16-byte stores over all banks.  (One group of 256 threads, a
+// row a warp, ids and codes in one step: 2,350 cycles a tile, 64 sequences of 128 heads
+// 173 us.)
 template <int N, bool SAFE>
-__device__ __forceinline__ void role_dequant(const AbsorbedParams &p, uint8_t *stages, Ctl &c, int t) {
+__device__ __forceinline__ void role_dequant(const AbsorbedParams &p, uint8_t *stages, Ctl &c, int sub, int t) {
   using G = Geo<true, N>;
-  constexpr int RI = G::TK / 8, RR = G::TK / 32;   // rows of codes, pieces of rotated parts a thread
-  const int lane = t & 31, w = t >> 5;
+  constexpr int TK = G::TK;
+  const int lane = t & 31, grp = t >> 7, u = t & 127, w = u >> 5;
+  auto page_ids = [&](const Tiles<TK, SAFE> &x) {
+    Pages d = {{-1, -1}, 0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int key = x.tile * TK + j * kBlock;
+      if (x.more && key < x.x.n) {
+        d.id[j] = __ldg(p.tables + (size_t)x.x.b * p.stride + key / kBlock);
+        if ((uint32_t)d.id[j] >= (uint32_t)p.kv.num_blocks) {
+          d.dead |= 1u << j;
+          d.id[j] = -1;
+        }
+      }
+    }
+    return d;
+  };
+  // pages of a tile that comes later, into L2 (by one of the CTAs that read them)
+  auto ahead = [&](const Tiles<TK, SAFE> &x) {
+    const int tile = x.tile + kAhead, key = tile * TK + u * kBlock;
+    if (u >= G::PG || !x.more || tile >= x.x.t1 || key >= x.x.n || (p.S > 1 && tile % p.S != sub)) return;
+    const uint32_t id = __ldg(p.tables + (size_t)x.x.b * p.stride + key / kBlock);
+    if (id >= (uint32_t)p.kv.num_blocks) return;
+    prefetch_l2(static_cast<const uint8_t *>(p.kv.latent) + (size_t)id * kBlock * kLatent, kBlock * kLatent);
+    prefetch_l2(static_cast<const uint8_t *>(p.kv.rope) + (size_t)id * kBlock * kRope * 2, kBlock * kRope * 2);
+  };
   struct Raw {
-    uint4 code[RI], rr[RR];
-    uint32_t dead;
+    uint4 code[8], rr[2];
   };
-  auto load = [&](const Piece<G::TK> &x, int tile, Raw &v) {
-    const int *row = p.tables + (size_t)x.b * p.stride;
-    const int k0 = tile * G::TK;
-    int id[G::PG];
-    v.dead = 0;
+  const uint32_t row = lane >> 2, at_row = row * kLatent + (lane & 3) * 16;
+  auto load = [&](const Pages &d, Raw &v) {
 #pragma unroll
-    for (int j = 0; j < G::PG; ++j) {
-      const int key = k0 + j * kBlock;
-      id[j] = key < x.n ? __ldg(row + key / kBlock) : -1;
-      if ((uint32_t)id[j] >= (uint32_t)p.kv.num_blocks) {
-        if (key < x.n) v.dead |= 1u << j;
-        id[j] = -1;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < RI; ++i) {   // row w + 8 i, in page i / 2
+    for (int i = 0; i < 8; ++i) {   // row group i / 2, chunk 4 (i % 2) + w
+      const int pg = d.id[i >> 2];
       v.code[i] = make_uint4(0, 0, 0, 0);
-      if (id[i >> 1] >= 0)
+      if (pg >= 0)
         v.code[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.kv.latent) +
-                                                          ((size_t)id[i >> 1] * kBlock + (i & 1) * 8 + w) * kLatent) + lane);
+                                                          (size_t)pg * (kBlock * kLatent) + ((i >> 1) & 1) * (8 * kLatent) +
+                                                          at_row + ((i & 1) * 4 + w) * 64));
     }
 #pragma unroll
-    for (int i = 0; i < RR; ++i) {   // row t / 8 + 32 i
-      const int pg = t < 128 ? id[2 * i] : id[2 * i + 1];
+    for (int i = 0; i < 2; ++i) {   // row u / 8 of page i
       v.rr[i] = make_uint4(0, 0, 0, 0);
-      if (pg >= 0)
+      if (d.id[i] >= 0)
         v.rr[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.kv.rope) +
-                                                        ((size_t)pg * kBlock + ((t >> 3) & 15)) * kRope) + (t & 7));
+                                                        ((size_t)d.id[i] * kBlock + (u >> 3)) * kRope) + (u & 7));
     }
   };
-  uint32_t g = 0;
-  Piece<G::TK> x(c.run);
-  Raw raw;
-  bool more = x.next(p);
-  int tile = x.t0, again = SAFE ? 1 : 0;   // times that the piece comes again
-  if (more) load(x, tile, raw);
+  Tiles<TK, SAFE> x(p, c.run);      // the tile whose ids are read
+  for (int i = 0; i < grp; ++i) x.next(p);
+  Pages now = page_ids(x);          // of the tile whose codes are asked for
+  bool more = x.more;
+  Raw v, raw;
+  load(now, raw);
+  x.next(p);
+  x.next(p);
+  Pages then = page_ids(x);
+  uint32_t g = grp;
   while (more) {
-    const Raw v = raw;
-    if (++tile == x.t1) {
-      if (again > 0) {
-        --again;
-      } else {
-        more = x.next(p);
-        again = SAFE ? 1 : 0;
-      }
-      tile = x.t0;
-    }
-    if (more) load(x, tile, raw);
+    v = raw;
+    const uint32_t dead = now.dead;
+    now = then;
+    more = x.more;
+    load(now, raw);
+    ahead(x);
+    x.next(p);
+    x.next(p);
+    then = page_ids(x);
     const uint32_t st = g % G::NS;
     if (g >= G::NS) wait_cap(&c.empty[st], (g / G::NS - 1) & 1, &c.abort, &c.flags);
     const uint32_t dst = smem_u32(stages + st * G::STAGE);
-    // the row's place in its group of eight is w: group i, chunk lane / 4
 #pragma unroll
-    for (int i = 0; i < RI; ++i) {
+    for (int i = 0; i < 8; ++i) {
       uint32_t h[8];
       e4m3x16(v.code[i], h);
-      const uint32_t at = dst + i * 8192 + (lane >> 2) * 1024 + w * 128;
-      const uint32_t p0 = 2 * (lane & 3);
-      sts_u4(at + ((p0 ^ w) << 4), h[0], h[1], h[2], h[3]);
-      sts_u4(at + (((p0 + 1) ^ w) << 4), h[4], h[5], h[6], h[7]);
+      const uint32_t at = dst + (i >> 1) * 8192 + ((i & 1) * 4 + w) * 1024 + row * 128, p0 = 2 * (lane & 3);
+      sts_u4(at + ((p0 ^ row) << 4), h[0], h[1], h[2], h[3]);
+      sts_u4(at + (((p0 + 1) ^ row) << 4), h[4], h[5], h[6], h[7]);
     }
 #pragma unroll
-    for (int i = 0; i < RR; ++i) {
-      const int r = (t >> 3) + 32 * i;
+    for (int i = 0; i < 2; ++i) {
+      const int r = (u >> 3) + 16 * i;
       const uint4 h = bf16x8_to_h(v.rr[i]);
-      sts_u4(dst + G::LAT + r * 128 + (((t & 7) ^ (r & 7)) << 4), h.x, h.y, h.z, h.w);
+      sts_u4(dst + G::LAT + r * 128 + (((u & 7) ^ (r & 7)) << 4), h.x, h.y, h.z, h.w);
     }
-    if (t == 0) {
-      c.dead[st] = v.dead;
-      if (v.dead) set_err(&c.flags, PA_ERRF_BAD_BLOCK_ID);
+    if (u == 0) {
+      c.dead[st] = dead;
+      if (dead) set_err(&c.flags, PA_ERRF_BAD_BLOCK_ID);
     }
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.full[st]);
-    ++g;
+    g += 2;
   }
 }
 
@@ -382,10 +427,13 @@ __device__ void role_softmax(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uin
       __syncwarp();
       tc_fence_after();
       const uint32_t dead = *reinterpret_cast<const volatile uint32_t *>(&c.dead[st]);
-      float s[RPT][8];
+      float s[RPT][8], v[16];
       if (act) {
-        float v[16];
         tmem_ld_16(tmem + lane_off + G::COL_S + (g & 1) * TK, v);
+        tc_fence_before();
+      }
+      if (lane == 0) mbar_arrive(&c.sread[g & 1]);
+      if (act) {
 #pragma unroll
         for (int a = 0; a < RPT; ++a) {
 #pragma unroll
@@ -474,7 +522,7 @@ __device__ void role_softmax(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uin
     wait_cap(&c.odone[(g - 1) & 1], ((g - 1) >> 1) & 1, &c.abort, &c.flags);
     named_sync(kBarSoft, 128);
     tc_fence_after();
-    write_rows<N>(p, tmem + lane_off + G::COL_O, N, 4, 0, c.fac, rows, whole, r_out, slot, w, lane);
+    write_rows<N>(p, tmem + lane_off + G::COL_O, c.fac, rows, whole, r_out, slot, w, lane);
     tc_fence_before();
     named_sync(kBarSoft, 128);   // every warp has read O and the factors
   }
@@ -486,11 +534,12 @@ template <bool FP8, int N>
 __device__ __forceinline__ void init_barriers(Ctl &c) {
   using G = Geo<FP8, N>;
   for (int i = 0; i < G::NS; ++i) {
-    mbar_init(&c.full[i], FP8 ? G::FWARPS : G::PG);
+    mbar_init(&c.full[i], FP8 ? G::FWARPS / 2 : G::PG);
     mbar_init(&c.empty[i], 1);
   }
   for (int i = 0; i < 2; ++i) {
     mbar_init(&c.sfull[i], 1);
+    mbar_init(&c.sread[i], 4);
     mbar_init(&c.pready[i], 4);
     mbar_init(&c.odone[i], 1);
   }
@@ -515,7 +564,7 @@ __device__ void run_roles(const AbsorbedParams &p, const CUtensorMap *mq, const 
     if ((threadIdx.x & 31) == 0) role_query<FP8, N>(p, mq, smem, c, sub);
     __syncwarp();
   } else if (warp < G::WARP_F + G::FWARPS) {
-    if constexpr (FP8) role_dequant<N, SAFE>(p, smem + G::OFF_K, c, (int)threadIdx.x - G::WARP_F * 32);
+    if constexpr (FP8) role_dequant<N, SAFE>(p, smem + G::OFF_K, c, sub, (int)threadIdx.x - G::WARP_F * 32);
     else role_copy<N, SAFE>(p, mc, mr, smem + G::OFF_K, c);
   }
 }
