@@ -17,6 +17,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const AbsorbedParams p
   const int all = p.Q * p.H, row = blockIdx.x, b = row / all, r = row % all;
   const int tid = threadIdx.x, lane = tid & 31;
   const int grp = p.RG == 1 ? 0 : r / p.R, sets = p.RG / p.S;
+  griddep_launch();                     // (a call that follows may set itself up)
   griddep_wait();                       // the pieces are complete
   if (row == 0 && tid < 32) {
     uint32_t bits = 0;

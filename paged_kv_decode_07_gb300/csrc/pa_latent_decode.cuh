@@ -216,15 +216,14 @@ inline bool cache_maps(const AbsorbedParams &p, CUtensorMap *mc, CUtensorMap *mr
   const uint32_t br[2] = {kRope, kBlock};
   return make_map(mc, p.kv.latent, 4, dc, sc, bc) && make_map(mr, p.kv.rope, 2, dr, sr, br);
 }
-// the queries' rows, 64 dims of `rows` of them a copy
+// the queries' rows as [9 chunks of 64 dims][rows][64 dims], all chunks of `rows` rows a copy
 inline bool query_map(const AbsorbedParams &p, CUtensorMap *mq, uint32_t rows) {
-  const uint64_t dims[2] = {(uint64_t)kRow, (uint64_t)p.B * p.Q * p.H}, strides[1] = {kRow * 2};
-  const uint32_t box[2] = {64, rows};
-  return make_map(mq, p.q, 2, dims, strides, box);
+  const uint64_t dims[3] = {64, (uint64_t)p.B * p.Q * p.H, 9}, strides[2] = {kRow * 2, 128};
+  const uint32_t box[3] = {64, rows, 9};
+  return make_map(mq, p.q, 3, dims, strides, box);
 }
 
-cudaError_t launch_latent_rows(const AbsorbedParams &p, cudaStream_t s);    // R <= 32 rows a CTA
-cudaError_t launch_latent_pairs(const AbsorbedParams &p, cudaStream_t s);   // R <= 64 rows a CTA, CTAs in pairs
+cudaError_t launch_latent_rows(const AbsorbedParams &p, cudaStream_t s);
 
 }  // namespace lat
 }  // namespace pa

@@ -266,14 +266,6 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all,
 
 // --------------------------------------------------------------------- copies
 
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // one lane; rows past the sequence are its neighbours' (or zeros past the tensor)
 __device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
                                           const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, int row_tiles,

@@ -343,8 +343,7 @@ __device__ __forceinline__ void role_query(const AbsorbedParams &p, const CUtens
     int rows;
     const long long r0 = group_row(p, x, sub, rows);
     mbar_arrive_expect_tx(&c.qfull, G::QBYTES);   // (rows past the group are its neighbour's, or zeros)
-#pragma unroll 1
-    for (int ch = 0; ch < 9; ++ch) tma_2d(smem_u32(smem + ch * G::QCHUNK), mq, ch * 64, (int)r0, &c.qfull);
+    tma_3d(smem_u32(smem), mq, 0, (int)r0, 0, &c.qfull);
     ++piece;
   }
   if (piece > 0) drain_wait(&c.qfull, (piece - 1) & 1);
@@ -593,8 +592,9 @@ __global__ void __launch_bounds__(Geo<FP8, N>::THREADS, 1)
     prefetch_map(&mr);
   }
   if (tid == 0) c.flags = 0;
-  __syncthreads();
   tc_fence_before();
+  __syncthreads();
+  griddep_wait();     // (nothing of the call was read before; what ran earlier is complete)
   find_run<G::TK>(p, c.run, &c.flags, worker, blockIdx.x == 0);
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
@@ -628,8 +628,7 @@ cudaError_t launch_n(const AbsorbedParams &p, cudaStream_t s) {
   auto kern = latent_rows_kernel<FP8, N>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(p.workers * p.S), G::THREADS, G::SMEM, s>>>(p, mq, mc, mr);
-  return cudaGetLastError();
+  return launch_pdl(kern, (unsigned)(p.workers * p.S), G::THREADS, G::SMEM, s, p, mq, mc, mr);
 }
 
 }  // namespace
