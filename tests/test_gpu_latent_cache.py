@@ -209,3 +209,12 @@ def test_gather_flags():
     assert flags([0, 16, 32], [0, 1]) == pa.PA_ERRF_LEN_OVER_CAPACITY
     assert flags([0, 16, 40]) & pa.PA_ERRF_BAD_Q_START
     assert flags([0, 20, 10]) & pa.PA_ERRF_BAD_Q_START
+
+
+def test_append_queries_with_the_heads_outermost():
+    rows, q, slots, kv, w, pos, inv = make("bf16", 21, 6, True, True)
+    want = pa.latent_append(kv, rows[:, :512], rows[:, 512:], pos, slots, inv, q=q)
+    turned_ = q.transpose(0, 1).contiguous().transpose(0, 1)
+    out = torch.empty((6, 21, 64), device=DEV, dtype=torch.bfloat16).transpose(0, 1)
+    got = pa.latent_append(kv, rows[:, :512], rows[:, 512:], pos, slots, inv, q=turned_, q_out=out)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(got, want)
