@@ -392,6 +392,8 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
         }
       }
     }
+    // (a first tile of scores of -inf: nothing to go by, while other keys may follow)
+    if (FIX && j == 0) over = m == kNegInf && see > 0;
     // ---- weights
     if (none) {
       const uint32_t z[16] = {};

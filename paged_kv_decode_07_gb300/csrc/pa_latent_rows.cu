@@ -458,6 +458,8 @@ __device__ void role_softmax(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uin
             for (int i = 0; i < 8; ++i) y = fmaxf(y, s[a][i]);
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
             m[a] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+            // (nothing to go by, bad pages or scores of -inf, while other keys may follow)
+            if (!SAFE) over = over || (m[a] == kNegInf && row + 8 * a < rows && k0 < see[a]);
           }
         }
         if (!SAFE || k >= 0) {

@@ -416,3 +416,82 @@ def test_decode_scores_far_past_the_first_tile(fmt, Q, H):
     L.within(o, ref, bound)
     L.lse_within(lse, rl, most=0.5)   # sums |q k| * scale of up to 30,000: 2^-16 of them
     assert pa.read_error(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("Q,H", [(5, 128), (16, 128), (16, 100)])
+def test_verify_many_groups(fmt, Q, H):
+    """More than eight groups of rows: several sets of them walk the keys one after another."""
+    check_decode(fmt, [Q + 3, 130, 0, 1500], Q, H)
+
+
+@pytest.mark.parametrize("H", [1, 3])
+def test_prefill_heads_before_tokens(H):
+    """Queries, keys and values with the heads outermost, and a single head with strides of its own."""
+    new, keys = [150, 3], [200, 90]
+    q, kn, kr, v = prefill_case(new, keys, H, packed=False)
+    qs, ks = L.starts_of(new), L.starts_of(keys)
+    want, _ = pa.latent_prefill(q, kn, kr, v, qs, ks, SCALE)
+    if H == 1:
+        def turn(x):
+            return torch.as_strided(x, x.shape, (x.stride(0), 24, 1))
+    else:
+        def turn(x):
+            return x.transpose(0, 1).contiguous().transpose(0, 1)
+    got, _ = pa.latent_prefill(turn(q), turn(kn), kr, turn(v), qs, ks, SCALE)
+    assert torch.equal(got, want)
+
+
+def test_prefill_one_token_of_one_key():
+    q, kn, kr, v = prefill_case([1], [1], 2)
+    o, _ = pa.latent_prefill(q[:, :1], kn[:, :1], kr, v[:, :1], L.starts_of([1]), L.starts_of([1]), SCALE)
+    assert torch.equal(o, v[:, :1])
+
+
+def test_two_workspaces_at_once():
+    """Two calls on two streams with a workspace each."""
+    kv, _, q, tables, sl = decode_case("bf16", [3000, 800], 1, 40)
+    kv2, _, q2, tables2, sl2 = decode_case("fp8", [5000, 70], 1, 128, seed=4)
+    want, want2 = pa.latent_decode(kv, q, tables, sl, SCALE)[0], pa.latent_decode(kv2, q2, tables2, sl2, SCALE)[0]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        x, _ = pa.latent_decode(kv, q, tables, sl, SCALE, stream=a)
+        y, _ = pa.latent_decode(kv2, q2, tables2, sl2, SCALE, stream=b)
+    torch.cuda.synchronize()
+    assert torch.equal(x, want) and torch.equal(y, want2)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("Q,H", [(1, 24), (2, 60)])
+def test_bad_first_pages_before_low_scores(fmt, Q, H):
+    """The first tile of a piece gives no maximum; the keys after it all score about -460."""
+    lens = [200, 90]
+    kv, vals, q, tables, sl = decode_case(fmt, lens, Q, H)
+    one = torch.tensor(4.0 if fmt == "bf16" else 32.0, device=DEV)
+    kv.latent[..., 0] = one.bfloat16() if fmt == "bf16" else one.to(torch.float8_e4m3fn).view(torch.uint8)
+    vals[0][..., 0] = one.double()
+    q[..., 0] = -1600.0
+    tables[0, :2] = 1 << 30
+    tables[1, 0] = -1
+    o, lse, ws = pa.latent_decode(kv, q, tables, sl, SCALE, out_fp32=True, return_lse=True)
+    ref, rl, bound = L.decode_reference(fmt, vals, q, lens, tables, SCALE)
+    L.within(o, ref, bound)
+    L.lse_within(lse, rl, most=0.02)   # sums |q k| * scale of about 600: 2^-16 of them
+    assert (lse < -300).all() and pa.read_error(ws) == pa.PA_ERRF_BAD_BLOCK_ID
+
+
+@pytest.mark.parametrize("n,at", [(300, 0), (2100, 0), (2100, 1024)])
+def test_prefill_first_tile_of_minus_infinity(n, at):
+    """128 keys score -inf, the first tile of a piece; the others about -460."""
+    H = 2
+    q, kn, kr, v = prefill_case([150], [n], H)
+    q[..., 0] = 800.0
+    kn[..., 0] = -8.0
+    kn[at:at + 128, :, 0] = -math.inf
+    o, lse, _ = pa.latent_prefill(q, kn, kr, v, L.starts_of([150]), L.starts_of([n]), SCALE, causal=False, out_fp32=True,
+                                  return_lse=True)
+    left = torch.cat((torch.arange(at), torch.arange(at + 128, n))).to(DEV)
+    ref, rl, bound = L.prefill_reference(q, kn[left], kr[left], v[left], [150], [n - 128], SCALE, causal=False)
+    L.within(o, ref, bound)
+    L.lse_within(lse, rl, most=0.02)   # sums |q k| * scale of about 500: 2^-16 of them
