@@ -68,6 +68,9 @@ int check_decode(const pa_latent_problem *p) {
   if (!std::isfinite(p->softmax_scale)) return PA_ERR_INVALID_ARG;
   if (p->batch > 0 && (p->block_table_stride < 1 || p->block_table_stride > (1 << 26))) return PA_ERR_INVALID_ARG;
   if ((long long)p->batch * p->q_len * p->num_heads > (1LL << 27)) return PA_ERR_UNSUPPORTED;
+  // the key tiles of a call are counted in 32 bits
+  const DecodePlan d = plan_latent_decode(p->batch, p->q_len, p->num_heads, p->max_seq_len);
+  if (p->batch > 0 && (p->block_table_stride + 1LL) / 2 * p->batch * (d.RG / d.S) >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 

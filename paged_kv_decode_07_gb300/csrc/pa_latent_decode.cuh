@@ -29,7 +29,7 @@ __device__ __forceinline__ int keys_of(const AbsorbedParams &p, int b) {
 }
 template <int TK>
 __device__ __forceinline__ int tiles_of(int n) { return n / TK + (n % TK != 0); }
-// Tiles a worker takes.  (Their number is held in 32 bits: 2^31 tiles would be 79 TB.)
+// Tiles a worker takes.  (All of them are fewer than 2^31: the host sees to it.)
 __device__ __forceinline__ uint32_t run_of(const AbsorbedParams &p, uint32_t total) {
   const uint32_t w = (uint32_t)p.workers;
   return max(total / w + (total % w != 0), (uint32_t)p.least);

@@ -166,3 +166,14 @@ def test_the_binding_names_what_it_refuses():
     with pytest.raises(ValueError, match="CUDA device"):
         pa.latent_prefill(torch.zeros((2, 4, 192), dtype=bf), torch.zeros((2, 4, 128), dtype=bf), rows[:, 512:],
                           torch.zeros((2, 4, 128), dtype=bf), ints, ints, 0.1)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=64, block_table_stride=1 << 26), UNSUP),                           # 2^31 tiles of 32 keys
+    (dict(batch=63, block_table_stride=1 << 26), pa.PA_ERR_WORKSPACE_TOO_SMALL),
+    (dict(batch=16, block_table_stride=1 << 26, num_heads=128, q_len=16), UNSUP),   # four sets of groups
+    (dict(batch=15, block_table_stride=1 << 26, num_heads=128, q_len=16), pa.PA_ERR_WORKSPACE_TOO_SMALL),
+])
+def test_decode_tiles_fit_32_bits(L, kw, status):
+    assert L.pa_latent_decode(ref(cache()), ref(problem(**kw)), FAKE, 256, None) == status
+    assert (L.pa_latent_decode_workspace_bytes(ref(cache()), ref(problem(**kw))) == 0) == (status == UNSUP)
