@@ -1,5 +1,5 @@
-// pa_latent_decode.cuh -- what the two kernels of the absorbed form share: the
-// worker's run of key tiles, conversion of FP8 rows, the tensor maps of the cache.
+// pa_latent_decode.cuh -- the parts of the absorbed form: a worker's run of key tiles and
+// its pieces, conversion of FP8 rows, the write of the output, the tensor maps.
 #pragma once
 
 #include "pa_latent_umma.cuh"

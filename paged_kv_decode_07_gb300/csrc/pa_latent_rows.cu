@@ -1,19 +1,20 @@
 // pa_latent_rows.cu -- the absorbed form of latent attention over the paged cache, up to
-// 32 rows a CTA, on the 5th-generation tensor cores (tcgen05.mma, accumulators in
+// 64 rows a CTA, on the 5th-generation tensor cores (tcgen05.mma, accumulators in
 // tensor memory).
 //
-// A row is one (token, head) of a sequence; the R <= 32 rows of a group share every
-// key.  Per tile of 32 keys, in fp32 accumulation:
-//   S [128 x 32] = Q [128 x 576] . K^T             A = Q in tensor memory (32 rows used)
+// A row is one (token, head) of a sequence; the N = 16, 32 or 64 rows of a group share
+// every key.  Per tile of 32 keys, in fp32 accumulation:
+//   S [N x 32] = Q [N x 576] . K^T                 A = Q in tensor memory
 //   P = exp2(S * scale - m)                        to shared memory, 16 bits
 //   O^T [512 x N] += C^T [512 x 32] . P^T [32 x N] A = the same tile, MN-major
 // A cached row is key and value at once, so a tile is brought in once and read by
 // both products as it lies.  With the latent dims on the instruction's M side the
-// output takes 4 N columns of tensor memory (N = 16 or 32 rows) instead of 512, which
-// leaves room for the queries: read from there they cost shared memory nothing (from
-// shared memory, where the instruction takes 64 rows at least, 74 KB a tile of 37 KB:
-// 32 sequences of 1K to 32K keys, 24 heads, 75 us instead of ROWS).  P is rounded once,
-// to bf16 (bf16 cache) or fp16.
+// output takes 4 N columns of tensor memory instead of 512, which leaves room for the
+// queries: read from there they cost shared memory nothing (from shared memory, where
+// the instruction takes 64 rows at least, 74 KB a tile of 37 KB; 32 sequences of 1K to
+// 32K keys, 24 heads: 76 us, 70 with them here and without a running maximum).  Of 64
+// rows' queries the last three chunks of 64 dims stay in shared memory: O takes half of
+// tensor memory then.  P is rounded once, to bf16 (bf16 cache) or fp16.
 //
 // A 16-token page lies in shared memory as [2 row groups][8 chunks of 64 dims][8
 // rows][128 bytes], swizzled: one four-dimensional tiled copy a page (and one of its
@@ -23,10 +24,15 @@
 // pieces of a sequence that several workers share are joined by their log-sum-exp
 // in a second kernel.
 //
-// Roles: four softmax warps (8 rows each; they also put the queries into tensor memory
-// and write the output), a warp for each product, one that copies queries, one that
-// copies pages or, FP8, eight that turn codes into f16 (exact).  Hand-offs are
-// mbarriers; waits are capped.
+// What bounds it.  16 or 32 rows: HBM, 1,415 cycles a tile and SM (32 sequences of 1K to
+// 32K keys, 24 heads: 67 us with the join, 49 at the copy's rate; the rest is the first
+// copies and the pieces' ends).  64 rows: shared memory; a tile's operands take 1,195
+// cycles to read, of 1,285 (8 verify tokens at 4 x 64K keys, 24 heads: 125 us), and with an
+// FP8 cache its conversion 600 more (64 sequences, 128 heads: 141 us).
+//
+// Roles: four softmax warps (they also put the queries into tensor memory and write the
+// output), a warp for each product, one that copies queries, one that copies pages or,
+// FP8, eight that turn codes into f16 (exact).  Hand-offs are mbarriers; waits are capped.
 #include "pa_latent_decode.cuh"
 
 namespace pa {
@@ -635,6 +641,9 @@ cudaError_t launch_n(const AbsorbedParams &p, cudaStream_t s) {
 
 }  // namespace
 
+// The fewest columns that hold the rows: a step of 16 of the score product takes 16.6
+// cycles for 16 or 32 rows and 24.7 (or, from tensor memory, 16.6) for 64, one of the output's
+// four blocks 39.7, 40.7 and 48.8, and a softmax warp has 4, 8 or 16 rows.
 cudaError_t launch_latent_rows(const AbsorbedParams &p, cudaStream_t s) {
   const bool fp8 = p.kv.dtype == PA_KV_FP8;
   if (p.R <= 16) return fp8 ? launch_n<true, 16>(p, s) : launch_n<false, 16>(p, s);

@@ -6,8 +6,8 @@ weights and A = sum p |v|:
   * each weight is rounded once before it meets a value: relative eps_p (bf16
     2^-8, fp16 2^-11), so A * eps_p; an fp16 weight below 2^-14 is off by up to
     2^-25 instead, and weights are relative to a maximum that the row's largest
-    passes by 2^8 at most and that it reaches up to that factor: + 2^-25 *
-    sum |stored value| of the keys seen, over a sum of at least 1;
+    score reaches or passes, never misses: + 2^-25 * sum |stored value| of the
+    keys seen, over a sum of at least 1;
   * a score off by d changes the output by at most 2 d A.  A score's products
     are added in at most 36 matrix steps (576 dims), each off by 2^-22 of its
     sum at most: 36 * 2^-22 < 2^-16 of S, the largest sum |q k| * scale of the
