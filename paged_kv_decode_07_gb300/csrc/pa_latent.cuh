@@ -57,6 +57,7 @@ struct ExpandedParams {
   int out_fp32;
   float *lse_out;
   uint32_t *hdr;
+  int shares;                         // places of the kernel's list of work
   // partial outputs of items in pieces: [item][piece][256][128] and their lse, or null
   float *part_o;
   float *part_lse;

@@ -16,10 +16,13 @@
 // swizzled) that both products read as they lie: three units of K, then two of V a
 // tile, in a ring of eight.
 //
-// What bounds it.  4,096 tokens over 16,384 keys, 32 heads: 794 us, 1,510 TFLOP/s of 1,908
+// A CTA a SM takes one item after another, the longest first, from a counter (with a CTA
+// an item, in the order of the tiles: eight chunks 170 us, now 160; 4,096 tokens 790, now 772).
+//
+// What bounds it.  4,096 tokens over 16,384 keys, 32 heads: 772 us, 1,550 TFLOP/s of 1,908
 // measured for a library product; the tensor pipe is busy 72 % of the active cycles, and
 // power counts when sustained.  Eight chunks of up to 2,048 tokens over up to 4,096 keys:
-// 170 us of 97; of a CTA's 20,000 to 40,000 cycles 12,000 are its start and end.
+// 160 us of 97; of an item's 20,000 to 110,000 cycles 16,000 are around its tiles.
 //
 // Roles: four softmax groups (two a row tile, 64 of a tile's keys each), a warp per
 // row tile that issues its products, a warp that copies.  Hand-offs are mbarriers;
@@ -44,11 +47,20 @@ constexpr float kLazy = 8.0f;               // log2 of how far a score may pass 
 constexpr float kMost = 0x1p32f;            // first pass: sum of 64 weights up to which a row goes on
 constexpr uint32_t kColO = 256;             // S of the two row tiles, then their O
 
+// A CTA's share: 256 tokens of a sequence (a tile), a head, and a piece of its keys.
+// Tiles of all sequences are taken by their number of keys, the most first (32 sequences
+// at most; of more, from the last sequence on): what is left to the end is short.
+struct Share {
+  int b, head, start, len, first;           // b < 0: nothing to do; first token of the tile
+  int key0, n;                              // the sequence's key rows
+  int item, piece, pieces, most;            // place among the items in pieces (-1: not one); most pieces of one
+};
 struct PCtl {
   uint64_t full[kUnits], empty[kUnits];
   uint64_t qfull[2], sfull[2], pready[2], odone[2], done;
   uint32_t tmem;
-  int abort, again;                         // again: a weight of the first pass passed kMost
+  int abort, again[2];                      // again: a weight of the first pass passed kMost (by passes in turn)
+  Share item[2];                            // of even and odd turns of the CTA
   float red[kRows];                         // a row's maximum (at the end its sum), from one half to the other
 };
 static_assert(sizeof(PCtl) <= 2048 && kSmem + 2048 <= 227 * 1024, "shared memory");
@@ -64,14 +76,6 @@ constexpr int kMinTiles = 8;                // key tiles of a piece at least
 // whole batch first (eight chunks of up to 4,096 keys: 181 us in groups, 170).
 __device__ __forceinline__ int heads_at_once(int tiles) { return tiles < kSms ? (kSms + tiles - 1) / max(tiles, 1) : 1; }
 
-// A CTA's share: 256 tokens of a sequence (a tile), a head, and a piece of its keys.
-// Tiles are counted over all sequences and taken from the last: the last tokens of a
-// prompt see most.
-struct Share {
-  int b, head, start, len, first;           // b < 0: nothing to do; first token of the tile
-  int key0, n;                              // the sequence's key rows
-  int item, piece, pieces, most;            // place among the items in pieces (-1: not one); most pieces of one
-};
 // Items (tile, head) that are taken in pieces: all, where they fill less than half of
 // the SMs; those of a last round that fills at most half of them, in as many as make it
 // a full round of short ones (512 items, three rounds and 56: 831 -> 797 us).
@@ -122,32 +126,29 @@ __device__ __forceinline__ Share search_share(const ExpandedParams &p, int index
   return r;
 }
 
-// every thread of a warp gets the answer; `index`: of the CTA, or, in the join, of an
+__device__ __forceinline__ void check_starts(const ExpandedParams &p) {
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int a = __ldg(p.q_starts + b), e = __ldg(p.q_starts + b + 1);
+    const int c = __ldg(p.kv_starts + b), d = __ldg(p.kv_starts + b + 1);
+    if (a < 0 || e < a || e > p.T || c < 0 || d < c || d > p.N) flag(p.hdr, PA_ERRF_BAD_Q_START);
+    else if (p.causal && d > c && e - a > d - c) flag(p.hdr, PA_ERRF_LEN_LT_QLEN);
+  }
+}
+
+// every thread of a warp gets the answer; `index`: of the share, or, in the join, of an
 // item in pieces
 __device__ __forceinline__ Share find_share(const ExpandedParams &p, int index, bool join) {
-  if (!join && index == 0) {
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-      const int a = __ldg(p.q_starts + b), e = __ldg(p.q_starts + b + 1);
-      const int c = __ldg(p.kv_starts + b), d = __ldg(p.kv_starts + b + 1);
-      if (a < 0 || e < a || e > p.T || c < 0 || d < c || d > p.N) flag(p.hdr, PA_ERRF_BAD_Q_START);
-      else if (p.causal && d > c && e - a > d - c) flag(p.hdr, PA_ERRF_LEN_LT_QLEN);
-    }
-  }
   if (p.B > 32) return search_share(p, index);   // (nothing is in pieces then)
   const int lane = threadIdx.x & 31;
-  int start = 0, len = 0;                   // this lane's sequence, and the tiles up to it
+  int start = 0, len = 0, key0 = 0, keys = 0;   // this lane's sequence
   if (lane < p.B) {
     start = min(max(__ldg(p.q_starts + lane), 0), p.T);
     len = max(min(max(__ldg(p.q_starts + lane + 1), 0), p.T) - start, 0);
+    key0 = min(max(__ldg(p.kv_starts + lane), 0), p.N);
+    keys = min(max(__ldg(p.kv_starts + lane + 1), key0), p.N) - key0;
   }
   const int n = (len + kRows - 1) / kRows;
-  int inc = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  const int tiles = __shfl_sync(0xffffffffu, inc, 31), items = tiles * p.H;
+  const int tiles = __reduce_add_sync(0xffffffffu, n), items = tiles * p.H;
   const Split sp = split_of(items, p.part_o != nullptr);
   Share r = {-1, 0, 0, 0, 0, 0, 0, -1, 0, 1, sp.pieces};
   int t = index;
@@ -165,14 +166,38 @@ __device__ __forceinline__ Share find_share(const ExpandedParams &p, int index, 
   }
   if (t >= items) return r;
   const int heads = p.part_o ? heads_at_once(tiles) : p.H, group = t / (heads * tiles), i = t % (heads * tiles);
-  const int of = min(heads, p.H - group * heads), tile = tiles - 1 - i / of;
+  const int of = min(heads, p.H - group * heads), rank = i / of;
   r.head = group * heads + i % of;
-  const int l = __ffs(__ballot_sync(0xffffffffu, inc > tile)) - 1;
+  // the tile of this rank, by its key tiles, the most first: of a sequence the last `v or
+  // more` tiles are known at once
+  auto at_least = [&](int v) {
+    const int need = (v - 1) * kKeys + 1;   // keys that some token of the tile has to see
+    if (v <= 0) return n;
+    if (keys < need) return 0;
+    const int last = p.causal ? need - (keys - len) : 0;   // tokens up to the first one that does
+    return n - (last > 0 && n > 0 ? (last + kRows - 1) / kRows - 1 : 0);
+  };
+  int v = 0, over = (__reduce_max_sync(0xffffffffu, keys) + kKeys - 1) / kKeys + 1;   // v: more than `rank` have so many
+  while (over - v > 1) {
+    const int mid = (v + over) / 2;
+    if ((int)__reduce_add_sync(0xffffffffu, at_least(mid)) > rank) v = mid;
+    else over = mid;
+  }
+  const int here = at_least(v), mine = here - at_least(v + 1);
+  const int before = __reduce_add_sync(0xffffffffu, here - mine);   // tiles that have more
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  const int l = __ffs(__ballot_sync(0xffffffffu, inc > rank - before)) - 1;
   r.start = __shfl_sync(0xffffffffu, start, l);
   r.len = __shfl_sync(0xffffffffu, len, l);
-  r.first = (tile - __shfl_sync(0xffffffffu, inc - n, l)) * kRows;
+  r.key0 = __shfl_sync(0xffffffffu, key0, l);
+  r.n = __shfl_sync(0xffffffffu, keys, l);
+  r.first = (__shfl_sync(0xffffffffu, n - here - (inc - mine), l) + rank - before) * kRows;
   r.b = l;
-  keys_of(p, r);
   if (r.item >= 0) {
     r.pieces = pieces_of(p, r, sp.pieces);
     if (r.pieces == 1) r.item = -1;
@@ -190,8 +215,24 @@ struct Work {
   int kt0, keys;                            // its first key tile; keys from there on
   int tiles[2];                             // key tiles of each row tile
   int row_tiles;
+  int all;                                  // the most
   size_t part;                              // first row among the partial outputs
 };
+__device__ __forceinline__ Work work_of(const ExpandedParams &p, const Share &sh) {
+  Work w;
+  w.nrows = min(kRows, sh.len - sh.first);
+  w.row_tiles = w.nrows > 128 ? 2 : 1;
+  const int all = tiles_of(p, sh, sh.first + w.nrows - 1), per = (all + sh.pieces - 1) / sh.pieces;
+  w.kt0 = min(all, sh.piece * per);
+  const int end = min(all, w.kt0 + per);
+  w.all = end - w.kt0;
+  w.keys = sh.n - w.kt0 * kKeys;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    w.tiles[t] = t < w.row_tiles ? max(min(tiles_of(p, sh, sh.first + min(t * 128 + 127, w.nrows - 1)), end) - w.kt0, 0) : 0;
+  w.part = sh.item >= 0 ? part_row(sh, 0) : 0;
+  return w;
+}
 
 // ------------------------------------------------------------------- products
 
@@ -272,8 +313,9 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all,
 
 // --------------------------------------------------------------------- copies
 
-// one lane; rows past the sequence are its neighbours' (or zeros past the tensor)
-__device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
+// one lane; rows past the sequence are its neighbours' (or zeros past the tensor); gives
+// the number of units
+__device__ __forceinline__ uint32_t role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
                                           const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, int row_tiles,
                                           int kt0, int all, uint8_t *smem, PCtl &c) {
   for (int t = 0; t < row_tiles; ++t) {
@@ -300,9 +342,30 @@ __device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtenso
       else tma_3d(dst, mv, (i - 3) * 64, sh.head, key, &c.full[st]);
     }
   }
-  // nothing lands after the CTA's end
+  return u;
+}
+// nothing lands after the item's end
+__device__ __forceinline__ void copy_end(uint32_t u, int row_tiles, PCtl &c) {
   for (int t = 0; t < row_tiles; ++t) drain_wait(&c.qfull[t], 0);
   for (uint32_t k = u > kUnits ? u - kUnits : 0; k < u; ++k) drain_wait(&c.full[k % kUnits], (k / kUnits) & 1);
+}
+
+__device__ __forceinline__ int take_index(const ExpandedParams &p) {
+  griddep_wait();                           // the counter is cleared
+  int x = 0;
+  if ((threadIdx.x & 31) == 0) x = (int)min(atomicAdd(p.hdr + HDR_NUM_ITEMS, 1u), 0x3fffffffu);
+  return __shfl_sync(0xffffffffu, x, 0) + (int)gridDim.x;
+}
+// A warp: the first share from `index` on that has work, taking further ones from the
+// counter (cleared with the header); b < 0: there is none.
+__device__ __forceinline__ Share take(const ExpandedParams &p, int index) {
+  for (;;) {
+    Share r = {-1, 0, 0, 0, 0, 0, 0, -1, 0, 1, 1};
+    if (index >= p.shares) return r;
+    r = find_share(p, index, false);
+    if (r.b >= 0) return r;
+    index = take_index(p);
+  }
 }
 
 // -------------------------------------------------------------------- softmax
@@ -314,7 +377,7 @@ __device__ __forceinline__ void role_copy(const ExpandedParams &p, const CUtenso
 // instead of 857.)
 template <bool FIX>
 __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Work &w, uint8_t *smem, PCtl &c,
-                             uint32_t tmem) {
+                             uint32_t tmem, int pass) {
   constexpr int NC = 64;                    // S columns a thread, and O columns
   // row tile rt, half hf of its columns; a pair of warps shares 32 rows
   const int tid = threadIdx.x, hf = (tid >> 7) & 1, rt = tid >> 8, wq = (tid >> 5) & 3, lane = tid & 31;
@@ -447,7 +510,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.pready[rt]);
   }
-  if (FIX && over && live) c.again = 1;
+  if (FIX && over && live) c.again[pass & 1] = 1;
   // ---- the sum, the last product, the output
   named_sync(pair, 64);                     // the other warp has read the last maximum
   if (hf == 0) c.red[row] = l;
@@ -513,21 +576,25 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   if (live && hf == 0 && lse) lse[row_out(row)] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
 }
 
-__device__ __forceinline__ void init_barriers(PCtl &c, int row_tiles) {
-  for (int i = 0; i < kUnits; ++i) {
-    mbar_init(&c.full[i], 1);
-    mbar_init(&c.empty[i], row_tiles);
+// a warp: lane i the i-th barrier; `anew`: they have been in use
+constexpr int kBars = 2 * kUnits + 9;
+__device__ __forceinline__ void init_barriers(PCtl &c, int row_tiles, bool anew) {
+  static_assert(offsetof(PCtl, done) == (kBars - 1) * 8 && kBars <= 32, "a lane a barrier");
+  const int i = threadIdx.x & 31;
+  if (i < kBars) {
+    const bool both = (i >= kUnits && i < 2 * kUnits) || i == kBars - 1;   // empty, done: an arrival a row tile
+    if (anew) drop_barriers(c.full + i, c.full + i);
+    mbar_init(c.full + i, both ? row_tiles : i == 2 * kUnits + 4 || i == 2 * kUnits + 5 ? 8 : 1);   // (pready: eight)
+    fence_mbar_init();
   }
-  for (int i = 0; i < 2; ++i) {
-    mbar_init(&c.qfull[i], 1);
-    mbar_init(&c.sfull[i], 1);
-    mbar_init(&c.pready[i], 8);
-    mbar_init(&c.odone[i], 1);
-  }
-  mbar_init(&c.done, row_tiles);
-  c.again = 0;
-  fence_mbar_init();
+  __syncwarp();
 }
+__device__ __forceinline__ void prefetch_maps(const CUtensorMap *a, const CUtensorMap *b, const CUtensorMap *c,
+                                              const CUtensorMap *d) {
+  for (const CUtensorMap *m : {a, b, c, d})
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const ExpandedParams p, const __grid_constant__ CUtensorMap mq,
                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mr,
@@ -535,75 +602,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ PCtl c;
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   griddep_launch();
-  const Share sh = find_share(p, blockIdx.x, false);
-  if (sh.b < 0) {
-    griddep_wait();                         // the grid does not end before its header is cleared
-    return;
-  }
-  Work w;
-  w.nrows = min(kRows, sh.len - sh.first);
-  w.row_tiles = w.nrows > 128 ? 2 : 1;
-  int all = tiles_of(p, sh, sh.first + w.nrows - 1);
-  const int per = (all + sh.pieces - 1) / sh.pieces;
-  w.kt0 = min(all, sh.piece * per);
-  const int end = min(all, w.kt0 + per);
-  all = end - w.kt0;
-  w.keys = sh.n - w.kt0 * kKeys;
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-    w.tiles[t] = t < w.row_tiles ? max(min(tiles_of(p, sh, sh.first + min(t * 128 + 127, w.nrows - 1)), end) - w.kt0, 0) : 0;
-  w.part = sh.item >= 0 ? part_row(sh, 0) : 0;
+  if (blockIdx.x == 0) check_starts(p);
   if (warp == 16) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
-  } else if (tid == 0) {
-    init_barriers(c, w.row_tiles);
-    c.abort = 0;
+  } else if (warp == 18) {
+    if (lane == 0) prefetch_maps(&mq, &mk, &mr, &mv);
+    const Share sh = take(p, blockIdx.x);
+    init_barriers(c, sh.len - sh.first > 128 ? 2 : 1, false);
+    if (lane == 0) {
+      c.item[0] = sh;
+      c.abort = c.again[0] = c.again[1] = 0;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
-  // between the passes: every role is at its end; the barriers begin anew
-  auto once_more = [&]() {
+  // Every role is at its end; the barriers begin anew: for a second pass (true), or for the
+  // next item.
+  int pass = 0;
+  auto once_more = [&](int turn) {
     tc_fence_before();
     fence_async_smem();                     // (the queries come again to where the output was)
     __syncthreads();
     tc_fence_after();
-    const bool again = *reinterpret_cast<volatile int *>(&c.again) && !*reinterpret_cast<volatile int *>(&c.abort);
-    __syncthreads();
-    if (again) {
-      if (tid == 0) {
-        drop_barriers(c.full, &c.done);
-        init_barriers(c, w.row_tiles);
+    const bool abort = *reinterpret_cast<volatile int *>(&c.abort);
+    const bool again = *reinterpret_cast<volatile int *>(&c.again[pass & 1]) && !abort;
+    ++pass;
+    if (warp == 0) {
+      Share &sh = c.item[again ? turn & 1 : (turn + 1) & 1];
+      if (sh.b >= 0) init_barriers(c, sh.len - sh.first > 128 ? 2 : 1, true);
+      if (lane == 0) {
+        c.again[pass & 1] = 0;
+        if (abort) sh.b = -1;
       }
-      __syncthreads();
     }
+    __syncthreads();
     return again;
   };
+  auto item = [&](int turn, Share &sh) {
+    sh = c.item[turn & 1];
+    return sh.b >= 0;
+  };
+  Share sh;
   if (warp < 16) {
     setmaxnreg_to<kLaunchRegs, kRegSoft>();
-    if (warp < 8 * w.row_tiles) role_softmax<true>(p, sh, w, smem, c, tmem);
-    if (once_more()) {
-      if (warp < 8 * w.row_tiles) role_softmax<false>(p, sh, w, smem, c, tmem);
-      once_more();
+#pragma unroll 1
+    for (int turn = 0; item(turn, sh); ++turn) {
+      const Work w = work_of(p, sh);
+      if (warp < 8 * w.row_tiles) role_softmax<true>(p, sh, w, smem, c, tmem, pass);
+      if (once_more(turn)) {
+        if (warp < 8 * w.row_tiles) role_softmax<false>(p, sh, w, smem, c, tmem, pass);
+        once_more(turn);
+      }
     }
   } else {
     setmaxnreg_to<kLaunchRegs, kRegCtl>();
     const int t = warp - 16;
-    bool again;
-    do {
-      if (t < w.row_tiles)
-        role_mma(p, t, __shfl_sync(0xffffffffu, w.tiles[t & 1], 0),
-                 __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, all, 0),
-                 __shfl_sync(0xffffffffu, w.keys, 0), smem, c, tmem);
-      else if (tid == 18 * 32)
-        role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, w.kt0, all, smem, c);
-      __syncwarp();
-      again = once_more();
-    } while (again);
+#pragma unroll 1
+    for (int turn = 0; item(turn, sh); ++turn) {
+      const Work w = work_of(p, sh);
+      bool again = false;
+      do {
+        if (t < w.row_tiles) {
+          role_mma(p, t, __shfl_sync(0xffffffffu, w.tiles[t & 1], 0),
+                   __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, w.all, 0),
+                   __shfl_sync(0xffffffffu, w.keys, 0), smem, c, tmem);
+        } else if (t == 2) {
+          uint32_t u = 0;
+          if (lane == 0) u = role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, w.kt0, w.all, smem, c);
+          __syncwarp();
+          if (!again) {                     // (the next item is taken late: the last ones go to who is free)
+            Share next = {-1, 0, 0, 0, 0, 0, 0, -1, 0, 1, 1};
+            if (p.shares > (int)gridDim.x) next = take(p, take_index(p));
+            if (lane == 0) c.item[(turn + 1) & 1] = next;
+          }
+          if (lane == 0) copy_end(u, w.row_tiles, c);
+        }
+        __syncwarp();
+        again = once_more(turn);
+      } while (again);
+    }
   }
   if (warp == 16) {
     tmem_dealloc(tmem, 512);
@@ -687,9 +769,11 @@ cudaError_t launch_latent_prefill(const ExpandedParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if ((fa.numRegs + 7) / 8 * 8 != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
   // every sequence has at most one tile that is not full; pieces are at most one an SM
-  const long long grid = ((long long)p.T / kRows + p.B) * p.H + (p.part_o ? kSms : 0);
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  e = launch_pdl(latent_prefill_kernel, (unsigned)grid, kThreads, kSmem, s, p, mq, mk, mr, mv);
+  const long long shares = ((long long)p.T / kRows + p.B) * p.H + (p.part_o ? kSms : 0);
+  if (shares > 0x3fffffffLL) return cudaErrorInvalidValue;
+  ExpandedParams a = p;
+  a.shares = (int)shares;
+  e = launch_pdl(latent_prefill_kernel, (unsigned)(shares < kSms ? shares : kSms), kThreads, kSmem, s, a, mq, mk, mr, mv);
   if (e != cudaSuccess || !p.part_o) return e;
   return launch_pdl(latent_prefill_join_kernel, 4 * kSms, 256, 0, s, p);
 }
