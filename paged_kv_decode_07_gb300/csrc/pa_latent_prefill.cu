@@ -17,12 +17,15 @@
 // tile, in a ring of eight.
 //
 // A CTA a SM takes one item after another, the longest first, from a counter (with a CTA
-// an item, in the order of the tiles: eight chunks 170 us, now 160; 4,096 tokens 790, now 772).
+// an item, in the order of the tiles: eight chunks 170 us, so 162; 4,096 tokens 790, so
+// 779), and its roles go from one to the next without a meeting: a row tile's first S of an
+// item passes under the other's last output of the one before (158 and 772 us).
 //
-// What bounds it.  4,096 tokens over 16,384 keys, 32 heads: 772 us, 1,550 TFLOP/s of 1,908
-// measured for a library product; the tensor pipe is busy 72 % of the active cycles, and
-// power counts when sustained.  Eight chunks of up to 2,048 tokens over up to 4,096 keys:
-// 160 us of 97; of an item's 20,000 to 110,000 cycles 16,000 are around its tiles.
+// What bounds it.  4,096 tokens over 16,384 keys, 32 heads: 772 us, 1,556 TFLOP/s of 1,908
+// measured for a library product: a pair of tiles takes 2,700 cycles, of which the products
+// take 2,600, and power counts when sustained.  Eight chunks of up to 2,048 tokens over up
+// to 4,096 keys: 158 us of 97; row tiles that are not full, hidden parts of tiles, and the
+// outputs.
 //
 // Roles: four softmax groups (two a row tile, 64 of a tile's keys each), a warp per
 // row tile that issues its products, a warp that copies.  Hand-offs are mbarriers;
@@ -55,12 +58,15 @@ struct Share {
   int key0, n;                              // the sequence's key rows
   int item, piece, pieces, most;            // place among the items in pieces (-1: not one); most pieces of one
 };
+constexpr int kSlots = 4;                   // items between the copying warp and the others
+constexpr int kBatch = 32;                  // items between two looks at whether some need a second pass
 struct PCtl {
   uint64_t full[kUnits], empty[kUnits];
-  uint64_t qfull[2], sfull[2], pready[2], odone[2], done;
-  uint32_t tmem;
-  int abort, again[2];                      // again: a weight of the first pass passed kMost (by passes in turn)
-  Share item[2];                            // of even and odd turns of the CTA
+  uint64_t qfull[2], qfree[2], sfull[2], pready[2], odone[2], ifull[kSlots], iempty[kSlots], done;
+  uint32_t tmem, redo;                      // redo: items of the batch of which a weight passed kMost
+  int abort, more;                          // more: the list goes on after the batch
+  int hist[kBatch];                         // the batch's items, by their index in the list
+  Share item[kSlots];
   float red[kRows];                         // a row's maximum (at the end its sum), from one half to the other
 };
 static_assert(sizeof(PCtl) <= 2048 && kSmem + 2048 <= 227 * 1024, "shared memory");
@@ -236,24 +242,45 @@ __device__ __forceinline__ Work work_of(const ExpandedParams &p, const Share &sh
 
 // ------------------------------------------------------------------- products
 
-// Row tile t; tiles that only the other one sees: their units are given back.
+// Where a stream of items stands: key tiles of each row tile, items of each, those with
+// key tiles, and units so far (the barriers' phases).
+struct At {
+  int tiles[2], items[2], some[2];          // (by constants or `of` only: they are registers)
+  uint32_t units;
+  static __device__ __forceinline__ int of(const int (&x)[2], int t) { return t ? x[1] : x[0]; }
+  __device__ __forceinline__ void add(const Work &w) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      tiles[t] += w.tiles[t];
+      items[t] += t < w.row_tiles;
+      some[t] += w.tiles[t] > 0;
+    }
+    units += kPerTile * w.all;
+  }
+};
+
+// Row tile t of an item; tiles that only the other one sees: their units are given back.
 // S of the two row tiles takes turns, row tile 0 first: left alone they run in step,
 // both at their products and then both at their softmax (5,500 cycles a pair of
-// tiles, of which the products take 2,570).  `n0`: key tiles of row tile 0 (0: there
-// is no other row tile).
-__device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all, int keys, uint8_t *smem, PCtl &c, uint32_t tmem) {
+// tiles, of which the products take 2,570).  Row tile 0 begins an item when row tile 1
+// has issued its last S of the one before.
+__device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all, int keys, const At &at, uint8_t *smem,
+                         PCtl &c, uint32_t tmem) {
   constexpr uint32_t IQK = idesc_of(true, 128, 128, false, false), IPV = idesc_of(true, 128, 64, false, true);
   const uint32_t lead = elect_one();
   const uint64_t dQ = sdesc(smem_u32(smem + t * 3 * kUnit), 16, 1024);
   const uint64_t dU = sdesc(smem_u32(smem + kOffRing), 16, 1024);
   const uint32_t S = tmem + t * 128, O = tmem + kColO + t * 128;
+  const uint32_t u0 = __shfl_sync(0xffffffffu, at.units, 0);
+  const int j0 = __shfl_sync(0xffffffffu, at.tiles[0], 0), j1 = __shfl_sync(0xffffffffu, at.tiles[1], 0);
+  const int own = t ? j1 : j0;
   auto full = [&](uint32_t u) { wait_cap(&c.full[u % kUnits], (u / kUnits) & 1, &c.abort, p.hdr); };
   auto qk = [&](int j) {
-    if (t == 1 && j < n0) wait_cap(&c.sfull[0], j & 1, &c.abort, p.hdr);
-    if (t == 0 && n0 > 0 && j > 0) wait_cap(&c.sfull[1], (j - 1) & 1, &c.abort, p.hdr);
+    if (t == 1 && j < n0) wait_cap(&c.sfull[0], (j0 + j) & 1, &c.abort, p.hdr);
+    if (t == 0 && (j > 0 ? n0 > 0 : j1 > 0)) wait_cap(&c.sfull[1], (j1 + j - 1) & 1, &c.abort, p.hdr);
 #pragma unroll
     for (int ch = 0; ch < 3; ++ch) {
-      const uint32_t u = kPerTile * j + ch;
+      const uint32_t u = u0 + kPerTile * j + ch;
       full(u);
       tc_fence_after();
       const uint64_t kb = dU + (uint64_t)((u % kUnits) * (kUnit >> 4)), qb = dQ + (uint64_t)(ch * (kUnit >> 4));
@@ -265,16 +292,16 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all,
     commit_if(lead, &c.sfull[t]);
   };
   if (n > 0) {
-    wait_cap(&c.qfull[t], 0, &c.abort, p.hdr);
+    wait_cap(&c.qfull[t], At::of(at.items, t) & 1, &c.abort, p.hdr);
     qk(0);
   }
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int steps = min(8, (keys - j * kKeys + 15) / 16);   // (the last tile's rows past the sequence are not read)
-    const uint32_t u = kPerTile * j + 3;
+    const uint32_t u = u0 + kPerTile * j + 3;
     full(u);
     full(u + 1);
-    wait_cap(&c.pready[t], j & 1, &c.abort, p.hdr);
+    wait_cap(&c.pready[t], (own + j) & 1, &c.abort, p.hdr);
     tc_fence_after();
     // P sits in two runs of 32 columns, one in each softmax group's half of S
     if (steps == 8) {
@@ -302,39 +329,44 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all,
   }
   if (n > 0) commit_if(lead, &c.odone[t]);
 #pragma unroll 1
-  for (uint32_t u = kPerTile * n; u < (uint32_t)(kPerTile * all); ++u) {
+  for (uint32_t u = u0 + kPerTile * n; u < u0 + (uint32_t)(kPerTile * all); ++u) {
     full(u);                                // (in order: an arrival belongs to its own fill)
     commit_if(lead, &c.empty[u % kUnits]);
   }
-  commit_if(lead, &c.done);                 // tensor memory is released only after every product completes
-  drain_wait(&c.done, 0);
-  __syncwarp();
 }
 
 // --------------------------------------------------------------------- copies
 
-// one lane; rows past the sequence are its neighbours' (or zeros past the tensor); gives
-// the number of units
-__device__ __forceinline__ uint32_t role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
-                                          const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, int row_tiles,
-                                          int kt0, int all, uint8_t *smem, PCtl &c) {
-  for (int t = 0; t < row_tiles; ++t) {
-    mbar_arrive_expect_tx(&c.qfull[t], 3 * kUnit);
-    for (int ch = 0; ch < 3; ++ch)
-      tma_3d(smem_u32(smem + (t * 3 + ch) * kUnit), mq, ch * 64, sh.head, sh.start + sh.first + t * 128, &c.qfull[t]);
-  }
-  uint32_t u = 0;
-  bool ok = true;
+// One lane; rows past the sequence are its neighbours' (or zeros past the tensor).  The
+// first K goes ahead of the queries, whose place holds the output of the item before until
+// that is written.  `wide`: that output reached into the ring.  false: a wait has expired.
+__device__ __forceinline__ bool role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
+                                          const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, const Work &w,
+                                          const At &at, bool wide, uint8_t *smem, PCtl &c) {
+  auto written = [&](int t) {
+    const int n = At::of(at.items, t);
+    return n == 0 || wait_cap(&c.qfree[t], (n - 1) & 1, &c.abort, p.hdr);
+  };
+  auto queries = [&]() {
+    for (int t = 0; t < w.row_tiles; ++t) {
+      if (!written(t)) return false;
+      mbar_arrive_expect_tx(&c.qfull[t], 3 * kUnit);
+      for (int ch = 0; ch < 3; ++ch)
+        tma_3d(smem_u32(smem + (t * 3 + ch) * kUnit), mq, ch * 64, sh.head, sh.start + sh.first + t * 128, &c.qfull[t]);
+    }
+    return true;
+  };
+  if (wide && (!written(0) || !written(1))) return false;
+  if (w.all == 0) return queries();
+  uint32_t u = at.units;
 #pragma unroll 1
-  for (int j = 0; j < all && ok; ++j) {
-    const int key = sh.key0 + (kt0 + j) * kKeys;
+  for (int j = 0; j < w.all; ++j) {
+    const int key = sh.key0 + (w.kt0 + j) * kKeys;
 #pragma unroll 1
     for (int i = 0; i < kPerTile; ++i, ++u) {
       const uint32_t st = u % kUnits;
-      if (u >= kUnits && !wait_cap(&c.empty[st], (u / kUnits - 1) & 1, &c.abort, p.hdr)) {
-        ok = false;
-        break;
-      }
+      if (j == 0 && i == 3 && !queries()) return false;
+      if (u >= kUnits && !wait_cap(&c.empty[st], (u / kUnits - 1) & 1, &c.abort, p.hdr)) return false;
       const uint32_t dst = smem_u32(smem + kOffRing + st * kUnit);
       mbar_arrive_expect_tx(&c.full[st], kUnit);
       if (i < 2) tma_3d(dst, mk, i * 64, sh.head, key, &c.full[st]);
@@ -342,12 +374,7 @@ __device__ __forceinline__ uint32_t role_copy(const ExpandedParams &p, const CUt
       else tma_3d(dst, mv, (i - 3) * 64, sh.head, key, &c.full[st]);
     }
   }
-  return u;
-}
-// nothing lands after the item's end
-__device__ __forceinline__ void copy_end(uint32_t u, int row_tiles, PCtl &c) {
-  for (int t = 0; t < row_tiles; ++t) drain_wait(&c.qfull[t], 0);
-  for (uint32_t k = u > kUnits ? u - kUnits : 0; k < u; ++k) drain_wait(&c.full[k % kUnits], (k / kUnits) & 1);
+  return true;
 }
 
 __device__ __forceinline__ int take_index(const ExpandedParams &p) {
@@ -358,7 +385,7 @@ __device__ __forceinline__ int take_index(const ExpandedParams &p) {
 }
 // A warp: the first share from `index` on that has work, taking further ones from the
 // counter (cleared with the header); b < 0: there is none.
-__device__ __forceinline__ Share take(const ExpandedParams &p, int index) {
+__device__ __forceinline__ Share take(const ExpandedParams &p, int &index) {
   for (;;) {
     Share r = {-1, 0, 0, 0, 0, 0, 0, -1, 0, 1, 1};
     if (index >= p.shares) return r;
@@ -368,23 +395,103 @@ __device__ __forceinline__ Share take(const ExpandedParams &p, int index) {
   }
 }
 
+// The stream of items, a warp: FIX, those of the list, from `next` on (when a batch ends,
+// `next` is the first one of the following), else those of the batch that need a second
+// pass, the bits of `redo`.
+template <bool FIX>
+__device__ __forceinline__ void stream_copies(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
+                                              const CUtensorMap *mr, const CUtensorMap *mv, uint32_t redo, Share &next,
+                                              int &index, uint8_t *smem, PCtl &c) {
+  const int lane = threadIdx.x & 31;
+  At at = {};
+  bool ok = true, wide = false;
+  for (int turn = 0;; ++turn) {
+    Share sh = next;
+    if (!FIX) {
+      sh.b = -1;
+      if (redo) sh = find_share(p, c.hist[__ffs(redo) - 1], false);
+      redo &= redo - 1;
+    } else if (turn == kBatch) {
+      sh.b = -1;
+    }
+    if (!ok) sh.b = -1;                     // (a wait has expired: the others end at the same item)
+    const int slot = turn % kSlots;
+    if (turn >= kSlots) drain_wait(&c.iempty[slot], (turn / kSlots - 1) & 1);
+    __syncwarp();
+    if (lane == 0) {
+      c.item[slot] = sh;
+      if (FIX && sh.b >= 0) c.hist[turn] = index;
+      if (FIX && sh.b < 0) c.more = next.b >= 0;
+      mbar_arrive(&c.ifull[slot]);
+    }
+    if (sh.b < 0) break;
+    const Work w = work_of(p, sh);
+    if (lane == 0) ok = role_copy(p, mq, mk, mr, mv, sh, w, at, wide, smem, c);
+    ok = __all_sync(0xffffffffu, ok);
+    at.add(w);
+    wide = sh.item >= 0 || p.out_fp32;
+    if (FIX) {                              // (the next item is taken late: the last ones go to who is free)
+      next.b = -1;
+      if (p.shares > (int)gridDim.x) {
+        index = take_index(p);
+        next = take(p, index);
+      }
+    }
+  }
+  // nothing lands after the stream's end
+  if (lane == 0) {
+    for (int t = 0; t < 2; ++t)
+      if (At::of(at.items, t) > 0) drain_wait(&c.qfull[t], (At::of(at.items, t) - 1) & 1);
+    for (uint32_t k = at.units > kUnits ? at.units - kUnits : 0; k < at.units; ++k) drain_wait(&c.full[k % kUnits], (k / kUnits) & 1);
+  }
+  __syncwarp();
+}
+// The next item of the stream, for the other warps.  (All of them end at the same one, that
+// the copying warp gives when a wait has expired too: no abort ends this wait.)
+__device__ __forceinline__ bool next_item(int turn, Share &sh, PCtl &c) {
+  const int slot = turn % kSlots;
+  for (int i = 0; i < 8 && !mbar_test(&c.ifull[slot], (turn / kSlots) & 1); ++i)
+    drain_wait(&c.ifull[slot], (turn / kSlots) & 1);
+  __syncwarp();
+  sh = c.item[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&c.iempty[slot]);
+  return sh.b >= 0;
+}
+__device__ __forceinline__ void stream_mma(const ExpandedParams &p, int t, uint8_t *smem, PCtl &c, uint32_t tmem) {
+  At at = {};
+  Share sh;
+#pragma unroll 1
+  for (int turn = 0; next_item(turn, sh, c); ++turn) {
+    const Work w = work_of(p, sh);
+    role_mma(p, t, __shfl_sync(0xffffffffu, t ? w.tiles[1] : w.tiles[0], 0),
+             __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, w.all, 0),
+             __shfl_sync(0xffffffffu, w.keys, 0), at, smem, c, tmem);
+    at.add(w);
+  }
+  commit_if(elect_one(), &c.done);          // tensor memory is released only after every product completes
+  drain_wait(&c.done, 0);
+  __syncwarp();
+}
+
 // -------------------------------------------------------------------- softmax
 
 // FIX: weights relative to the row's maximum over its first tile, whatever follows.
 // bf16 and fp32 hold 2^+-126, so a later score may well pass it; where 64 weights sum
-// to more than 2^32 the CTA takes a second pass with a running maximum.  (With one,
+// to more than 2^32 the item is taken again, with a running maximum, when the batch of
+// items ends.  (With one,
 // the two warps of a row agree on it in every tile: 4,096 tokens over 16,384 keys 970 us
 // instead of 857.)
 template <bool FIX>
 __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Work &w, uint8_t *smem, PCtl &c,
-                             uint32_t tmem, int pass) {
+                             uint32_t tmem, const At &at, int turn) {
   constexpr int NC = 64;                    // S columns a thread, and O columns
   // row tile rt, half hf of its columns; a pair of warps shares 32 rows
   const int tid = threadIdx.x, hf = (tid >> 7) & 1, rt = tid >> 8, wq = (tid >> 5) & 3, lane = tid & 31;
   const int row = rt * 128 + (tid & 127), pair = 1 + rt * 4 + wq;
   const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
   const uint32_t S = tmem + lane_off + rt * 128 + hf * NC, O = tmem + lane_off + kColO + rt * 128 + hf * NC;
-  const int n = w.tiles[rt];
+  const int n = At::of(w.tiles, rt), tiles0 = At::of(at.tiles, rt);
   const bool live = row < w.nrows;
   // keys that this thread's row sees; that some, and that every row of the warp sees
   int see = 0;
@@ -397,7 +504,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int k0 = j * kKeys + hf * NC;
-    wait_cap(&c.sfull[rt], j & 1, &c.abort, p.hdr);
+    wait_cap(&c.sfull[rt], (tiles0 + j) & 1, &c.abort, p.hdr);
     __syncwarp();
     tc_fence_after();
     const bool none = k0 >= some;
@@ -498,7 +605,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     // a step of the product takes)
     const int valid = w.keys - j * kKeys;
     if (valid < kKeys && (valid & 15)) {
-      const uint32_t u = kPerTile * j + 3;
+      const uint32_t u = at.units + kPerTile * j + 3;
       for (int h = 0; h < 2; ++h) wait_cap(&c.full[(u + h) % kUnits], ((u + h) / kUnits) & 1, &c.abort, p.hdr);
       const int r = valid + (tid & 15);     // 16 rows of eight pieces, in two units
       if (r < ((valid + 15) & ~15))
@@ -510,7 +617,7 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.pready[rt]);
   }
-  if (FIX && over && live) c.again[pass & 1] = 1;
+  if (FIX && over && live) atomicOr(&c.redo, 1u << turn);
   // ---- the sum, the last product, the output
   named_sync(pair, 64);                     // the other warp has read the last maximum
   if (hf == 0) c.red[row] = l;
@@ -522,14 +629,16 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   named_sync(pair, 64);
   if (hf == 0) l = c.red[row];
   // the queries' place takes the output: their copy has landed, and no product reads them
-  wait_cap(&c.qfull[rt], 0, &c.abort, p.hdr);
-  if (n > 0) wait_cap(&c.odone[rt], 0, &c.abort, p.hdr);
+  wait_cap(&c.qfull[rt], At::of(at.items, rt) & 1, &c.abort, p.hdr);
+  if (n > 0) wait_cap(&c.odone[rt], At::of(at.some, rt) & 1, &c.abort, p.hdr);
   const bool partial = sh.item >= 0, wide = partial || p.out_fp32;
   // (fp32 rows reach into what the other row tile's products read)
   if (wide && w.row_tiles > 1) {
-    wait_cap(&c.qfull[rt ^ 1], 0, &c.abort, p.hdr);
-    if (w.tiles[rt ^ 1] > 0) wait_cap(&c.odone[rt ^ 1], 0, &c.abort, p.hdr);
+    wait_cap(&c.qfull[rt ^ 1], At::of(at.items, rt ^ 1) & 1, &c.abort, p.hdr);
+    if (At::of(w.tiles, rt ^ 1) > 0) wait_cap(&c.odone[rt ^ 1], At::of(at.some, rt ^ 1) & 1, &c.abort, p.hdr);
   }
+  // (and into the place of row tile 1, which may hold the output of an item before)
+  if (wide && w.row_tiles == 1 && at.items[1] > 0) wait_cap(&c.qfree[1], (at.items[1] - 1) & 1, &c.abort, p.hdr);
   __syncwarp();
   tc_fence_after();
   const float inv = l != 0.f ? 1.f / l : 0.f;   // (0: the row saw no key; a NaN among its scores goes on)
@@ -574,19 +683,36 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   }
   float *const lse = partial ? p.part_lse : p.lse_out;
   if (live && hf == 0 && lse) lse[row_out(row)] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+  fence_async_smem();                       // the next item's queries come to where the output was
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&c.qfree[rt]);
 }
 
-// a warp: lane i the i-th barrier; `anew`: they have been in use
-constexpr int kBars = 2 * kUnits + 9;
-__device__ __forceinline__ void init_barriers(PCtl &c, int row_tiles, bool anew) {
-  static_assert(offsetof(PCtl, done) == (kBars - 1) * 8 && kBars <= 32, "a lane a barrier");
-  const int i = threadIdx.x & 31;
-  if (i < kBars) {
-    const bool both = (i >= kUnits && i < 2 * kUnits) || i == kBars - 1;   // empty, done: an arrival a row tile
-    if (anew) drop_barriers(c.full + i, c.full + i);
-    mbar_init(c.full + i, both ? row_tiles : i == 2 * kUnits + 4 || i == 2 * kUnits + 5 ? 8 : 1);   // (pready: eight)
-    fence_mbar_init();
+template <bool FIX>
+__device__ __forceinline__ void stream_softmax(const ExpandedParams &p, int rt, uint8_t *smem, PCtl &c, uint32_t tmem) {
+  At at = {};
+  Share sh;
+#pragma unroll 1
+  for (int turn = 0; next_item(turn, sh, c); ++turn) {
+    const Work w = work_of(p, sh);
+    if (rt < w.row_tiles) role_softmax<FIX>(p, sh, w, smem, c, tmem, at, turn);
+    at.add(w);
   }
+}
+
+// a warp: lane i the i-th barrier and the (i + 32)nd; `anew`: they have been in use
+constexpr int kBars = 2 * kUnits + 10 + 2 * kSlots + 1;
+__device__ __forceinline__ void init_barriers(PCtl &c, bool anew) {
+  static_assert(offsetof(PCtl, done) == (kBars - 1) * 8 && offsetof(PCtl, tmem) == kBars * 8, "in a row");
+  for (int i = threadIdx.x & 31; i < kBars; i += 32) {
+    uint64_t *const b = c.full + i;
+    // empty, done: a row tile's products each; qfree, pready: its eight softmax warps; iempty: these and the products
+    const bool two = (b >= c.empty && b < c.empty + kUnits) || b == &c.done;
+    const bool eight = (b >= c.qfree && b < c.qfree + 2) || (b >= c.pready && b < c.pready + 2);
+    if (anew) drop_barriers(b, b);
+    mbar_init(b, two ? 2 : eight ? 8 : b >= c.iempty && b < c.iempty + kSlots ? 18 : 1);
+  }
+  fence_mbar_init();
   __syncwarp();
 }
 __device__ __forceinline__ void prefetch_maps(const CUtensorMap *a, const CUtensorMap *b, const CUtensorMap *c,
@@ -605,87 +731,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   griddep_launch();
   if (blockIdx.x == 0) check_starts(p);
+  int index = blockIdx.x;                   // (the copying warp's)
+  Share next;
   if (warp == 16) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
+  } else if (warp == 17) {
+    init_barriers(c, false);
+    if (lane == 0) c.abort = c.redo = c.more = 0;
   } else if (warp == 18) {
     if (lane == 0) prefetch_maps(&mq, &mk, &mr, &mv);
-    const Share sh = take(p, blockIdx.x);
-    init_barriers(c, sh.len - sh.first > 128 ? 2 : 1, false);
-    if (lane == 0) {
-      c.item[0] = sh;
-      c.abort = c.again[0] = c.again[1] = 0;
-    }
+    next = take(p, index);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
-  // Every role is at its end; the barriers begin anew: for a second pass (true), or for the
-  // next item.
-  int pass = 0;
-  auto once_more = [&](int turn) {
+  // After a stream every role is at its end; the barriers begin anew.  `redo`: items of the
+  // batch that need a second pass.
+  auto ended = [&](uint32_t &redo, bool &more) {
     tc_fence_before();
-    fence_async_smem();                     // (the queries come again to where the output was)
+    fence_async_smem();                     // (copies come to where outputs were)
     __syncthreads();
     tc_fence_after();
     const bool abort = *reinterpret_cast<volatile int *>(&c.abort);
-    const bool again = *reinterpret_cast<volatile int *>(&c.again[pass & 1]) && !abort;
-    ++pass;
+    redo = abort ? 0 : *reinterpret_cast<volatile uint32_t *>(&c.redo);
+    more = !abort && *reinterpret_cast<volatile int *>(&c.more);
+    if (!redo && !more) return;
+    __syncthreads();
     if (warp == 0) {
-      Share &sh = c.item[again ? turn & 1 : (turn + 1) & 1];
-      if (sh.b >= 0) init_barriers(c, sh.len - sh.first > 128 ? 2 : 1, true);
-      if (lane == 0) {
-        c.again[pass & 1] = 0;
-        if (abort) sh.b = -1;
-      }
+      init_barriers(c, true);
+      if (lane == 0) c.redo = 0;
     }
     __syncthreads();
-    return again;
   };
-  auto item = [&](int turn, Share &sh) {
-    sh = c.item[turn & 1];
-    return sh.b >= 0;
-  };
-  Share sh;
+  uint32_t redo;
+  bool more;
   if (warp < 16) {
     setmaxnreg_to<kLaunchRegs, kRegSoft>();
-#pragma unroll 1
-    for (int turn = 0; item(turn, sh); ++turn) {
-      const Work w = work_of(p, sh);
-      if (warp < 8 * w.row_tiles) role_softmax<true>(p, sh, w, smem, c, tmem, pass);
-      if (once_more(turn)) {
-        if (warp < 8 * w.row_tiles) role_softmax<false>(p, sh, w, smem, c, tmem, pass);
-        once_more(turn);
+    do {
+      stream_softmax<true>(p, warp >> 3, smem, c, tmem);
+      ended(redo, more);
+      if (redo) {
+        stream_softmax<false>(p, warp >> 3, smem, c, tmem);
+        ended(redo, more);
       }
-    }
+    } while (more);
   } else {
     setmaxnreg_to<kLaunchRegs, kRegCtl>();
-    const int t = warp - 16;
-#pragma unroll 1
-    for (int turn = 0; item(turn, sh); ++turn) {
-      const Work w = work_of(p, sh);
-      bool again = false;
-      do {
-        if (t < w.row_tiles) {
-          role_mma(p, t, __shfl_sync(0xffffffffu, w.tiles[t & 1], 0),
-                   __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, w.all, 0),
-                   __shfl_sync(0xffffffffu, w.keys, 0), smem, c, tmem);
-        } else if (t == 2) {
-          uint32_t u = 0;
-          if (lane == 0) u = role_copy(p, &mq, &mk, &mr, &mv, sh, w.row_tiles, w.kt0, w.all, smem, c);
-          __syncwarp();
-          if (!again) {                     // (the next item is taken late: the last ones go to who is free)
-            Share next = {-1, 0, 0, 0, 0, 0, 0, -1, 0, 1, 1};
-            if (p.shares > (int)gridDim.x) next = take(p, take_index(p));
-            if (lane == 0) c.item[(turn + 1) & 1] = next;
-          }
-          if (lane == 0) copy_end(u, w.row_tiles, c);
-        }
-        __syncwarp();
-        again = once_more(turn);
-      } while (again);
-    }
+    do {
+      if (warp < 18) stream_mma(p, warp - 16, smem, c, tmem);
+      else if (warp == 18) stream_copies<true>(p, &mq, &mk, &mr, &mv, 0, next, index, smem, c);
+      ended(redo, more);
+      if (redo) {
+        if (warp < 18) stream_mma(p, warp - 16, smem, c, tmem);
+        else if (warp == 18) stream_copies<false>(p, &mq, &mk, &mr, &mv, redo, next, index, smem, c);
+        ended(redo, more);
+      }
+    } while (more);
   }
   if (warp == 16) {
     tmem_dealloc(tmem, 512);

@@ -495,3 +495,23 @@ def test_prefill_first_tile_of_minus_infinity(n, at):
     ref, rl, bound = L.prefill_reference(q, kn[left], kr[left], v[left], [150], [n - 128], SCALE, causal=False)
     L.within(o, ref, bound)
     L.lse_within(lse, rl, most=0.02)   # sums |q k| * scale of about 500: 2^-16 of them
+
+
+@pytest.mark.parametrize("B,most,H", [(32, 480, 120), (70, 60, 80)])
+def test_prefill_thousands_of_items(B, most, H):
+    """More than 32 items for each CTA, of one and of two row tiles; some need a second pass."""
+    new = [1 + (37 * i) % most for i in range(B)]
+    keys = [m + (53 * i) % 200 for i, m in enumerate(new)]
+    assert sum(-(-m // 256) for m in new) * H > 33 * 152
+    q, kn, kr, v = prefill_case(new, keys, H)
+    ks = [0] + torch.tensor(keys).cumsum(0).tolist()
+    for b, h in ((2, 5), (11, 40), (B - 1, H - 1)):
+        kn[ks[b] + 128:ks[b + 1], h] *= 200   # (where the sequence has a second tile)
+    qs, kst = L.starts_of(new), L.starts_of(keys)
+    o, lse, ws = pa.latent_prefill(q, kn, kr, v, qs, kst, SCALE, out_fp32=True, return_lse=True)
+    ref, rl, bound = L.prefill_reference(q, kn, kr, v, new, keys, SCALE)
+    L.within(o, ref, bound)
+    L.lse_within(lse, rl, most=0.5)   # sums |q k| * scale of up to 30,000 there: 2^-16 of them
+    assert pa.read_error(ws) == 0
+    ob, _ = pa.latent_prefill(q, kn, kr, v, qs, kst, SCALE, workspace=ws)
+    assert torch.equal(ob, o.bfloat16())

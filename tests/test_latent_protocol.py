@@ -7,9 +7,9 @@ copier (bf16) or two that take turns at the tiles (FP8), the queries' copier,
 a warp for S = Q K and one for O += P V, each with an engine that retires its
 products and commits in order, two softmax warps (of the four).
 
-Prefill (csrc/pa_latent_prefill.cu): two row tiles that share eight units of K
-(three a tile) and V (two), S of the two taking turns, the second one seeing
-more tiles than the first.
+Prefill (csrc/pa_latent_prefill.cu): a stream of items of two row tiles that
+share eight units of K (three a tile) and V (two), S of the two taking turns, the
+second one seeing more tiles than the first; the output takes the queries' place.
 
 The asserts check the data flow (nothing refilled, overwritten or read before
 its time); with an expired wait the data are void, and the model checks that
@@ -240,31 +240,99 @@ def test_rows_the_model_catches_a_missing_wait(method):
 
 
 class Prefill(Model):
-    NU, PER = 8, 5
+    """A stream of items (key tiles of row tile 0, of row tile 1 or None, wide output)."""
+    NU, PER, SLOTS = 8, 5, 4
 
-    def __init__(self, n0, n1, row_tiles=2):
-        self.n, self.rt = [n0, n1][:row_tiles], row_tiles
-        self.all = max(self.n)
+    def __init__(self, items):
+        self.items = items
+        self.all = [max(n0, n1 or 0) for n0, n1, _ in items]
         self.full = [Bar(1) for _ in range(self.NU)]
-        self.empty = [Bar(row_tiles) for _ in range(self.NU)]
-        self.sfull, self.pready, self.odone = ([Bar(c) for _ in range(2)] for c in (1, 2, 1))
-        self.done = Bar(row_tiles)
+        self.empty = [Bar(2) for _ in range(self.NU)]
+        self.qfull, self.qfree, self.sfull, self.pready, self.odone = ([Bar(c) for _ in range(2)] for c in (1, 2, 1, 2, 1))
+        self.ifull, self.iempty = ([Bar(c) for _ in range(self.SLOTS)] for c in (1, 6))
+        self.done = Bar(2)
         self.unit, self.readers = [None] * self.NU, [0] * self.NU
+        self.item = [None] * self.SLOTS
+        self.q = [None, None]                       # item whose queries (or "out": output) are there
         self.s = [[None, None] for _ in range(2)]   # by row tile and half
-        self.queue = [[] for _ in range(row_tiles)]
-        self.pv = [0, 0]
+        self.o = [None, None]
+        self.queue = [[], []]
+
+    def n(self, i):
+        return self.items[i][0], self.items[i][1] or 0
+
+    def at(self, i):
+        """Before item i: key tiles, items and items with key tiles of each row tile, units."""
+        done = self.items[:i]
+        rt = [[x for x in done], [x for x in done if x[1] is not None]]
+        return ([sum(x[t] for x in rt[t]) for t in range(2)], [len(rt[t]) for t in range(2)],
+                [sum(x[t] > 0 for x in rt[t]) for t in range(2)], self.PER * sum(self.all[:i]))
+
+    def long_wait(self, bar, phase):
+        while not bar.ready(phase & 1):
+            yield lambda: bar.ready(phase & 1)
 
     def copier(self):
-        for u in range(self.PER * self.all):
+        ok, wide = True, False
+        for turn in range(len(self.items) + 1):
+            i = turn if ok and turn < len(self.items) else None
+            slot = turn % self.SLOTS
+            if turn >= self.SLOTS:
+                yield from self.long_wait(self.iempty[slot], turn // self.SLOTS - 1)
+            self.item[slot] = i
+            self.ifull[slot].arrive()
+            yield None
+            if i is None:
+                return
+            ok = yield from self.copy(i, wide)
+            wide = self.items[i][2]
+
+    def ready(self, bar, phase):
+        yield from self.wait(bar, phase)
+        return bar.ready(phase & 1)
+
+    def copy(self, i, wide):
+        tiles, items, _, units = self.at(i)
+        rts = 1 if self.items[i][1] is None else 2
+
+        def written(t):
+            return items[t] == 0 or (yield from self.ready(self.qfree[t], items[t] - 1))
+
+        def queries():
+            for t in range(rts):
+                if not (yield from written(t)):
+                    return False
+                self.check(self.q[t] in (None, "free"), "queries over an output")
+                self.q[t] = i
+                self.qfull[t].arrive()
+                yield None
+            return True
+        if wide:
+            for t in range(2):
+                if not (yield from written(t)):
+                    return False
+        if not self.all[i]:
+            return (yield from queries())
+        for u in range(units, units + self.PER * self.all[i]):
+            if u == units + 3 and not (yield from queries()):
+                return False
             st = u % self.NU
-            if u >= self.NU:
-                yield from self.wait(self.empty[st], u // self.NU - 1)
-                if self.abort:
-                    return
-            self.check(self.readers[st] == 0, "unit refilled while it is read")
-            self.unit[st], self.readers[st] = u, self.rt
+            if u >= self.NU and not (yield from self.ready(self.empty[st], u // self.NU - 1)):
+                return False
+            self.check(self.readers[st] == 0 and self.unit[st] != "out", "unit refilled while it is read")
+            self.unit[st], self.readers[st] = u, 2
             self.full[st].arrive()
             yield None
+        return True
+
+    def next_item(self, turn):
+        slot = turn % self.SLOTS
+        yield from self.long_wait(self.ifull[slot], turn // self.SLOTS)
+        i = self.item[slot]
+        self.check(i in (turn, None), "another item")
+        self.iempty[slot].arrive()
+        yield None
+        return i
 
     def free(self, t, u):
         def retire():
@@ -273,96 +341,141 @@ class Prefill(Model):
         self.queue[t].append(retire)
 
     def mma(self, t):
-        n, n0 = self.n[t], self.n[0] if self.rt == 2 else 0
+        turn = 0
+        while (i := (yield from self.next_item(turn))) is not None:
+            turn += 1
+            yield from self.products(t, i)
+        self.queue[t].append(self.done.arrive)
+        yield from self.drain(self.done)
+
+    def products(self, t, i):
+        (j0, j1), items, _, u0 = self.at(i)
+        n, own = self.n(i)[t], (j0, j1)[t]
+        n0 = self.n(i)[0] if self.items[i][1] is not None else 0
 
         def qk(j):
             if t == 1 and j < n0:
-                yield from self.wait(self.sfull[0], j)
-            if t == 0 and n0 > 0 and j > 0:
-                yield from self.wait(self.sfull[1], j - 1)
+                yield from self.wait(self.sfull[0], j0 + j)
+            if t == 0 and (n0 > 0 if j else j1 > 0):
+                yield from self.wait(self.sfull[1], j1 + j - 1)
             for ch in range(3):
-                u = self.PER * j + ch
+                u = u0 + self.PER * j + ch
                 yield from self.wait(self.full[u % self.NU], u // self.NU)
 
                 def retire(u=u, ch=ch):
                     self.check(self.unit[u % self.NU] == u, "S of another unit")
+                    self.check(self.q[t] == i, "S of other queries")
                     self.check(ch or self.s[t] == [None, None], "S over unread weights")
                 self.queue[t].append(retire)
                 self.free(t, u)
 
             def ready():
-                self.s[t] = [("S", j), ("S", j)]
+                self.s[t] = [("S", i, j), ("S", i, j)]
                 self.sfull[t].arrive()
             self.queue[t].append(ready)
         if n:
+            yield from self.wait(self.qfull[t], items[t])
             yield from qk(0)
         for j in range(n):
             for h in range(2):
-                u = self.PER * j + 3 + h
+                u = u0 + self.PER * j + 3 + h
                 yield from self.wait(self.full[u % self.NU], u // self.NU)
-            yield from self.wait(self.pready[t], j)
+            yield from self.wait(self.pready[t], own + j)
             for h in range(2):
-                def retire(u=self.PER * j + 3 + h, h=h, j=j):
+                def retire(u=u0 + self.PER * j + 3 + h, h=h, j=j):
                     self.check(self.unit[u % self.NU] == u, "O of another unit")
-                    self.check(self.s[t] == [("P", j), ("P", j)], "O before its weights")
+                    self.check(self.s[t] == [("P", i, j), ("P", i, j)], "O before its weights")
+                    self.check(self.o[t] == (None if j == 0 and h == 0 else (i, j - (h == 0))), "O of another item")
+                    self.o[t] = (i, j)
                     if h:
                         self.s[t] = [None, None]
-                        self.pv[t] = j + 1
                 self.queue[t].append(retire)
-                self.free(t, self.PER * j + 3 + h)
+                self.free(t, u0 + self.PER * j + 3 + h)
             yield None
             if j + 1 < n:
                 yield from qk(j + 1)
         if n:
             self.queue[t].append(self.odone[t].arrive)
-        for u in range(self.PER * n, self.PER * self.all):
+        for u in range(u0 + self.PER * n, u0 + self.PER * self.all[i]):
             yield from self.wait(self.full[u % self.NU], u // self.NU)
             self.free(t, u)
             yield None
-        self.queue[t].append(self.done.arrive)
-        yield from self.drain(self.done)
 
     def softmax(self, t, x):
-        for j in range(self.n[t]):
-            yield from self.wait(self.sfull[t], j)
-            self.check(self.s[t][x] == ("S", j), "S read before it is there")
+        turn = 0
+        while (i := (yield from self.next_item(turn))) is not None:
+            turn += 1
+            if t == 0 or self.items[i][1] is not None:
+                yield from self.rows(t, x, i)
+
+    def rows(self, t, x, i):
+        tiles, items, some, units = self.at(i)
+        n = self.n(i)
+        for j in range(n[t]):
+            yield from self.wait(self.sfull[t], tiles[t] + j)
+            self.check(self.s[t][x] == ("S", i, j), "S read before it is there")
             if j == 0 or self.agree:
-                yield from self.meet((t, j), 2)
-                self.check(self.pv[t] == j, "O rescaled under a product")
-            self.s[t][x] = ("P", j)
+                yield from self.meet((t, i, j), 2)
+                self.check(self.o[t] == ((i, j - 1) if j else None), "O rescaled under a product")
+            self.s[t][x] = ("P", i, j)
             self.pready[t].arrive()
             yield None
-        yield from self.meet((t, "sum"), 2)
-        if self.n[t]:
-            yield from self.wait(self.odone[t], 0)
-            self.check(self.pv[t] == self.n[t], "output before the last product")
+        yield from self.meet((t, i, "sum"), 2)
+        wide = self.items[i][2]
+        for r in (t, 1 - t) if wide and self.items[i][1] is not None else (t,):
+            yield from self.wait(self.qfull[r], items[r])
+            if n[r]:
+                yield from self.wait(self.odone[r], some[r])
+        if wide and self.items[i][1] is None and items[1]:
+            yield from self.wait(self.qfree[1], items[1] - 1)
+        self.check(n[t] == 0 or self.o[t] == (i, n[t] - 1), "output before the last product")
+        self.check(self.q[t] in (i, ("out", i)), "output over other queries")
+        if wide:
+            end = units + self.PER * self.all[i]   # (row tile 1's reaches into the ring)
+            self.check(t == 0 or all(u is None or u < end for u in self.unit), "output over units of the next item")
+            self.check(self.q[1 - t] in (None, "free", i, ("out", i)), "output over another")
+        self.q[t] = ("out", i)
+        yield from self.meet((t, i, "out"), 2)
+        yield None
+        self.check(self.q[t] == ("out", i), "the output is gone")
+        yield from self.meet((t, i, "read"), 2)   # (in the kernel the barrier itself counts the warps)
+        self.q[t], self.o[t] = "free", None
+        self.qfree[t].arrive()
 
     def run(self, seed, expire=None):
         self.start(seed, expire)
         self.agree = seed % 2 == 0   # with a running maximum
-        self.play([self.copier()] + [self.mma(t) for t in range(self.rt)]
-                  + [self.softmax(t, x) for t in range(self.rt) for x in range(2)])
+        self.play([self.copier()] + [self.mma(t) for t in range(2)] + [self.softmax(t, x) for t in range(2) for x in range(2)])
 
 
-@pytest.mark.parametrize("n0,n1", [(0, 0), (0, 1), (1, 1), (1, 2), (2, 2), (4, 5), (7, 8), (0, 6), (9, 9)])
-def test_prefill_random_schedules(n0, n1):
+ITEMS = [[(2, 3, False), (1, None, True), (1, 1, False)], [(0, None, False)], [(0, 1, False)], [(1, 1, True)], [(4, 5, False), (2, 3, False), (9, 9, True), (3, None, True)],
+         [(2, None, False), (1, None, False), (0, 2, False), (0, 0, False), (1, 2, False), (3, 3, False)],
+         [(1, 1, False)] * 7, [(2, 2, True), (0, 1, True), (2, 2, False), (0, 3, False), (0, 3, False), (2, 2, False)]]
+
+
+@pytest.mark.parametrize("items", ITEMS)
+def test_prefill_random_schedules(items):
     for seed in range(60):
-        Prefill(n0, n1).run(seed)
-        Prefill(n1, 0, 1).run(seed)
+        Prefill(items).run(seed)
 
 
-def test_prefill_an_expired_wait_ends_every_role():
-    for seed in range(120):
-        Prefill(5, 6).run(seed, expire=seed % 30)
+@pytest.mark.parametrize("items", ITEMS[3:])
+def test_prefill_an_expired_wait_ends_every_role(items):
+    for seed in range(80):
+        Prefill(items).run(seed, expire=seed % 40)
 
 
-@pytest.mark.parametrize("method", ["empty", "pready", "full"])
+@pytest.mark.parametrize("method", ["empty", "pready", "full", "qfree", "qfull", "odone"])
 def test_prefill_the_model_catches_a_missing_wait(method):
     class Broken(Prefill):
         def wait(self, bar, phase):
             if bar not in getattr(self, method):
                 yield from super().wait(bar, phase)
 
+        def ready(self, bar, phase):
+            yield from self.wait(bar, phase)
+            return True
+
     with pytest.raises(AssertionError):
-        for seed in range(120):
-            Broken(6, 7).run(seed)
+        for seed in range(150):
+            Broken([(4, 5, False), (2, 3, False), (2, 2, True), (3, 3, False)]).run(seed)
