@@ -8,12 +8,13 @@
 //           head's query
 // A warp takes a run of a token's steps: the latent (16 values a lane), or eight
 // 64-value rows, four lanes each, a lane's two 8-value chunks holding whole
-// pairs, so that eight sines and cosines serve every head.
+// pairs, so that eight sines and cosines serve every head.  Each lane computes one
+// pair's and shuffles hand them out (eight a lane: 8,191 tokens 34.8 us, 31.4 so).
 //
 // Both kernels move bytes and are bound by HBM where there are many rows (8,191 tokens
-// with 64 heads' queries: 34.8 us, 0.65 of the copy's rate, for the 128-byte pieces lie 384
-// bytes apart; 4 x 32,768 rows read back: 49.3 us, 0.90), by launch and two or three
-// dependent memory latencies where there are few (one token 4.1 us, 255 tokens 8.1).
+// with 64 heads' queries: 31.4 us, 0.72 of the copy's rate; a bare copy of such 128-byte
+// pieces, at any distance, takes 0.76 to 0.8; 4 x 32,768 rows read back: 49.3 us, 0.90), by launch and two or three
+// dependent memory latencies where there are few (one token 3.7 us, 255 tokens 7 to 9).
 #include "pa_codec.cuh"
 #include "pa_latent.cuh"
 #include "pa_rotate.cuh"
@@ -70,10 +71,14 @@ __global__ void __launch_bounds__(32, kCtas) append_kernel(const LatentAppendPar
   const int pos = __ldg(p.positions + t);
   const int64_t slot = __ldg(p.slots + t);
   if (s1 > 1) {
+    float c, n;                                       // of pair `lane`
+    angle(__ldg(p.inv_freq + lane), pos, p.factor, c, n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = __ldg(p.inv_freq + (IL ? (i < 4 ? 4 * j + i : 12 + 4 * j + i) : 8 * j + i));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) angle(cs[i], pos, p.factor, cs[i], sn[i]);
+    for (int i = 0; i < 8; ++i) {
+      const int pair = IL ? (i < 4 ? 4 * j + i : 12 + 4 * j + i) : 8 * j + i;
+      cs[i] = __shfl_sync(0xffffffffu, c, pair);
+      sn[i] = __shfl_sync(0xffffffffu, n, pair);
+    }
   }
   const bool bad = slot < -1 || slot >= (int64_t)p.kv.num_blocks * kBlock;
   if (bad && part == 0 && lane == 0) set_err(p.hdr, PA_ERRF_BAD_SLOT);
