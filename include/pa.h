@@ -50,6 +50,9 @@
  *     data; the split plan is computed on the device).
  *   - All work is enqueued asynchronously on `stream` (NULL = legacy
  *     default stream).
+ *   - A workspace serves one call at a time: calls that may run at once (on
+ *     several streams, or in graphs that are replayed side by side) need one
+ *     each.
  *   - Argument errors are detected on the host and return a negative
  *     pa_status with NOTHING launched.  A failed launch returns
  *     PA_ERR_CUDA.
