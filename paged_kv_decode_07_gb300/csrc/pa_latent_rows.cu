@@ -27,8 +27,8 @@
 // What bounds it.  16 or 32 rows: HBM, 1,415 cycles a tile and SM (32 sequences of 1K to
 // 32K keys, 24 heads: 67 us with the join, 49 at the copy's rate; the rest is the first
 // copies and the pieces' ends).  64 rows: shared memory; a tile's operands take 1,195
-// cycles to read, of 1,285 (8 verify tokens at 4 x 64K keys, 24 heads: 125 us), and with an
-// FP8 cache its conversion 600 more (64 sequences, 128 heads: 141 us).
+// cycles to read, of 1,285 (8 verify tokens at 4 x 64K keys, 24 heads: 124 us), and with an
+// FP8 cache its conversion 600 more (64 sequences, 128 heads: 126 us).
 //
 // Roles: four softmax warps (they also put the queries into tensor memory and write the
 // output), a warp for each product, one that copies queries, one that copies pages or,
