@@ -515,3 +515,9 @@ def test_prefill_thousands_of_items(B, most, H):
     assert pa.read_error(ws) == 0
     ob, _ = pa.latent_prefill(q, kn, kr, v, qs, kst, SCALE, workspace=ws)
     assert torch.equal(ob, o.bfloat16())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_decode_many_rows_of_several_pieces(fmt):
+    """Rows enough for a warp each in the join, of four or five pieces."""
+    check_decode(fmt, [2500 + 37 * i for i in range(20)], 1, 128)
