@@ -263,7 +263,7 @@ struct At {
 // S of the two row tiles takes turns, row tile 0 first: left alone they run in step,
 // both at their products and then both at their softmax (5,500 cycles a pair of
 // tiles, of which the products take 2,570).  Row tile 0 begins an item when row tile 1
-// has issued its last S of the one before.
+// has issued its last S of the one before.  The queries are there: the caller has waited.
 __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all, int keys, const At &at, uint8_t *smem,
                          PCtl &c, uint32_t tmem) {
   constexpr uint32_t IQK = idesc_of(true, 128, 128, false, false), IPV = idesc_of(true, 128, 64, false, true);
@@ -291,10 +291,7 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all,
     }
     commit_if(lead, &c.sfull[t]);
   };
-  if (n > 0) {
-    wait_cap(&c.qfull[t], At::of(at.items, t) & 1, &c.abort, p.hdr);
-    qk(0);
-  }
+  if (n > 0) qk(0);
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int steps = min(8, (keys - j * kKeys + 15) / 16);   // (the last tile's rows past the sequence are not read)
@@ -464,6 +461,10 @@ __device__ __forceinline__ void stream_mma(const ExpandedParams &p, int t, uint8
 #pragma unroll 1
   for (int turn = 0; next_item(turn, sh, c); ++turn) {
     const Work w = work_of(p, sh);
+    // the queries come in every item of this row tile, and are waited for in every one,
+    // with or without key tiles: a phase passed over would let the next item through
+    // while these are still on their way
+    if (t < w.row_tiles) wait_cap(&c.qfull[t], At::of(at.items, t) & 1, &c.abort, p.hdr);
     role_mma(p, t, __shfl_sync(0xffffffffu, t ? w.tiles[1] : w.tiles[0], 0),
              __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, w.all, 0),
              __shfl_sync(0xffffffffu, w.keys, 0), at, smem, c, tmem);

@@ -1,0 +1,87 @@
+"""The stream of items of the expanded form (csrc/pa_latent_prefill.cu) with copies
+that land later than they are issued, in any order between barriers, under random
+schedules on the CPU.  The model of test_latent_protocol lets them land at once; what
+passes a barrier a phase too early can then not be seen."""
+import pytest
+
+from tests.test_latent_protocol import ITEMS, Prefill
+
+
+class InFlight(Prefill):
+    """every: a row tile's products wait for its queries in every item that has the row
+    tile, also without key tiles."""
+
+    def __init__(self, items, every=True):
+        super().__init__(items)
+        self.every = every
+        self.queue += [[] for _ in range(2 + self.NU)]   # copies on their way, by barrier
+
+    def land(self, q, f):
+        self.queue[2 + q] += [lambda: None] * self.rng.choice((0, 1, 20)) + [f]
+
+    def copy(self, i, wide):
+        tiles, items, _, units = self.at(i)
+        rts = 1 if self.items[i][1] is None else 2
+
+        def written(t):
+            return items[t] == 0 or (yield from self.ready(self.qfree[t], items[t] - 1))
+
+        def queries():
+            for t in range(rts):
+                if not (yield from written(t)):
+                    return False
+                self.check(self.q[t] in (None, "free"), "queries over an output")
+                self.q[t] = ("on its way", i)
+
+                def there(t=t):
+                    self.check(self.q[t] == ("on its way", i), "queries over something else")
+                    self.q[t] = i
+                    self.qfull[t].arrive()
+                self.land(t, there)
+                yield None
+            return True
+        if wide:
+            for t in range(2):
+                if not (yield from written(t)):
+                    return False
+        if not self.all[i]:
+            return (yield from queries())
+        for u in range(units, units + self.PER * self.all[i]):
+            if u == units + 3 and not (yield from queries()):
+                return False
+            st = u % self.NU
+            if u >= self.NU and not (yield from self.ready(self.empty[st], u // self.NU - 1)):
+                return False
+            self.check(self.readers[st] == 0, "unit refilled while it is read")
+            self.unit[st], self.readers[st] = u + 0.5, 2   # (on its way: no whole number)
+
+            def there(u=u):
+                self.unit[u % self.NU] = u
+                self.full[u % self.NU].arrive()
+            self.land(2 + st, there)
+            yield None
+        return True
+
+    def products(self, t, i):
+        if self.every and not self.n(i)[t] and (t == 0 or self.items[i][1] is not None):
+            yield from self.wait(self.qfull[t], self.at(i)[1][t])
+        yield from super().products(t, i)
+
+
+STREAMS = ITEMS + [[(0, 0, True), (2, 2, False)], [(0, 0, False), (1, 2, False), (0, 0, False), (0, 0, False), (2, 2, False)],
+                   [(0, None, True), (3, None, True), (0, 0, True), (0, 1, True), (2, 2, True)]]
+
+
+@pytest.mark.parametrize("items", STREAMS)
+def test_copies_that_land_late(items):
+    for seed in range(60):
+        InFlight(items).run(seed)
+
+
+@pytest.mark.parametrize("items", [[(0, 0, True), (2, 2, True)], [(0, 0, False), (1, 1, False)],
+                                   [(1, 1, False), (0, None, False), (1, None, False)]])
+def test_a_row_tile_without_keys_must_wait_for_its_queries(items):
+    """Else the next item passes on the phase of queries that are still on their way."""
+    with pytest.raises(AssertionError, match="queries"):
+        for seed in range(150):
+            InFlight(items, every=False).run(seed)
