@@ -461,10 +461,15 @@ __device__ __forceinline__ void stream_mma(const ExpandedParams &p, int t, uint8
 #pragma unroll 1
   for (int turn = 0; next_item(turn, sh, c); ++turn) {
     const Work w = work_of(p, sh);
-    // the queries come in every item of this row tile, and are waited for in every one,
+    // The queries come in every item of this row tile, and are waited for in every one,
     // with or without key tiles: a phase passed over would let the next item through
-    // while these are still on their way
-    if (t < w.row_tiles) wait_cap(&c.qfull[t], At::of(at.items, t) & 1, &c.abort, p.hdr);
+    // while these are still on their way.  The arrival keeps the copies of the next ones
+    // back until then, for without key tiles the softmax needs nothing of this warp.
+    if (t < w.row_tiles) {
+      wait_cap(&c.qfull[t], At::of(at.items, t) & 1, &c.abort, p.hdr);
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&c.qfree[t]);
+    }
     role_mma(p, t, __shfl_sync(0xffffffffu, t ? w.tiles[1] : w.tiles[0], 0),
              __shfl_sync(0xffffffffu, w.row_tiles > 1 ? w.tiles[0] : 0, 0), __shfl_sync(0xffffffffu, w.all, 0),
              __shfl_sync(0xffffffffu, w.keys, 0), at, smem, c, tmem);
@@ -707,11 +712,12 @@ __device__ __forceinline__ void init_barriers(PCtl &c, bool anew) {
   static_assert(offsetof(PCtl, done) == (kBars - 1) * 8 && offsetof(PCtl, tmem) == kBars * 8, "in a row");
   for (int i = threadIdx.x & 31; i < kBars; i += 32) {
     uint64_t *const b = c.full + i;
-    // empty, done: a row tile's products each; qfree, pready: its eight softmax warps; iempty: these and the products
+    // empty, done: a row tile's products each; pready: its eight softmax warps; qfree: these and its
+    // products; iempty: all of them
     const bool two = (b >= c.empty && b < c.empty + kUnits) || b == &c.done;
-    const bool eight = (b >= c.qfree && b < c.qfree + 2) || (b >= c.pready && b < c.pready + 2);
+    const bool soft = b >= c.pready && b < c.pready + 2, free = b >= c.qfree && b < c.qfree + 2;
     if (anew) drop_barriers(b, b);
-    mbar_init(b, two ? 2 : eight ? 8 : b >= c.iempty && b < c.iempty + kSlots ? 18 : 1);
+    mbar_init(b, two ? 2 : soft ? 8 : free ? 9 : b >= c.iempty && b < c.iempty + kSlots ? 18 : 1);
   }
   fence_mbar_init();
   __syncwarp();

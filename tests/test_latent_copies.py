@@ -5,15 +5,18 @@ passes a barrier a phase too early can then not be seen."""
 import pytest
 
 from tests.test_latent_protocol import ITEMS, Prefill
+from tests.test_verify_protocol import Bar
 
 
 class InFlight(Prefill):
     """every: a row tile's products wait for its queries in every item that has the row
-    tile, also without key tiles."""
+    tile, also without key tiles.  back: and hold the next ones back until then."""
 
-    def __init__(self, items, every=True):
+    def __init__(self, items, every=True, back=True):
         super().__init__(items)
-        self.every = every
+        self.every, self.back = every, back
+        if back:
+            self.qfree = [Bar(3) for _ in range(2)]
         self.queue += [[] for _ in range(2 + self.NU)]   # copies on their way, by barrier
 
     def land(self, q, f):
@@ -63,12 +66,17 @@ class InFlight(Prefill):
         return True
 
     def products(self, t, i):
-        if self.every and not self.n(i)[t] and (t == 0 or self.items[i][1] is not None):
-            yield from self.wait(self.qfull[t], self.at(i)[1][t])
+        if t == 0 or self.items[i][1] is not None:
+            if self.every:
+                yield from self.wait(self.qfull[t], self.at(i)[1][t])
+            if self.back:
+                self.qfree[t].arrive()
+                yield None
         yield from super().products(t, i)
 
 
 STREAMS = ITEMS + [[(0, 0, True), (2, 2, False)], [(0, 0, False), (1, 2, False), (0, 0, False), (0, 0, False), (2, 2, False)],
+                   [(1, 1, False)] + [(0, 0, False)] * 6 + [(0, None, False)] * 5 + [(1, 2, False)],
                    [(0, None, True), (3, None, True), (0, 0, True), (0, 1, True), (2, 2, True)]]
 
 
@@ -84,4 +92,11 @@ def test_a_row_tile_without_keys_must_wait_for_its_queries(items):
     """Else the next item passes on the phase of queries that are still on their way."""
     with pytest.raises(AssertionError, match="queries"):
         for seed in range(150):
-            InFlight(items, every=False).run(seed)
+            InFlight(items, every=False, back=False).run(seed)
+
+
+def test_a_row_tile_without_keys_must_not_be_left_behind():
+    """Else its queries' phase is over, and the next one's, before it has looked."""
+    with pytest.raises(AssertionError, match="deadlock"):
+        for seed in range(400):
+            InFlight([(0, 0, False)] * 40, back=False).run(seed)
