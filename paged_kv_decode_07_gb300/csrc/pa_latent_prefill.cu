@@ -240,6 +240,9 @@ __device__ __forceinline__ Work work_of(const ExpandedParams &p, const Share &sh
   return w;
 }
 
+// fp32 rows leave: pieces, or the caller's output is
+__device__ __forceinline__ bool wide_output(const ExpandedParams &p, const Share &s) { return s.item >= 0 || p.out_fp32; }
+
 // ------------------------------------------------------------------- products
 
 // Where a stream of items stands: key tiles of each row tile, items of each, those with
@@ -336,7 +339,10 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all,
 
 // One lane; rows past the sequence are its neighbours' (or zeros past the tensor).  The
 // first K goes ahead of the queries, whose place holds the output of the item before until
-// that is written.  `wide`: that output reached into the ring.  false: a wait has expired.
+// that is written.  `wide`: that output reached into the ring.  The queries of an item whose
+// own output is wide wait for both row tiles: that output reaches into the place of the
+// other one, whose barriers stand at an item before until its output is written (a wait
+// there for this item's phase would pass at once).  false: a wait has expired.
 __device__ __forceinline__ bool role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
                                           const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, const Work &w,
                                           const At &at, bool wide, uint8_t *smem, PCtl &c) {
@@ -345,6 +351,7 @@ __device__ __forceinline__ bool role_copy(const ExpandedParams &p, const CUtenso
     return n == 0 || wait_cap(&c.qfree[t], (n - 1) & 1, &c.abort, p.hdr);
   };
   auto queries = [&]() {
+    if (wide_output(p, sh) && !written(1)) return false;
     for (int t = 0; t < w.row_tiles; ++t) {
       if (!written(t)) return false;
       mbar_arrive_expect_tx(&c.qfull[t], 3 * kUnit);
@@ -426,7 +433,7 @@ __device__ __forceinline__ void stream_copies(const ExpandedParams &p, const CUt
     if (lane == 0) ok = role_copy(p, mq, mk, mr, mv, sh, w, at, wide, smem, c);
     ok = __all_sync(0xffffffffu, ok);
     at.add(w);
-    wide = sh.item >= 0 || p.out_fp32;
+    wide = wide_output(p, sh);
     if (FIX) {                              // (the next item is taken late: the last ones go to who is free)
       next.b = -1;
       if (p.shares > (int)gridDim.x) {
@@ -637,14 +644,13 @@ __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Wor
   // the queries' place takes the output: their copy has landed, and no product reads them
   wait_cap(&c.qfull[rt], At::of(at.items, rt) & 1, &c.abort, p.hdr);
   if (n > 0) wait_cap(&c.odone[rt], At::of(at.some, rt) & 1, &c.abort, p.hdr);
-  const bool partial = sh.item >= 0, wide = partial || p.out_fp32;
-  // (fp32 rows reach into what the other row tile's products read)
+  const bool partial = sh.item >= 0, wide = wide_output(p, sh);
+  // (fp32 rows reach into what the other row tile's products read; an item before has left
+  // its place: the copying warp has seen to that)
   if (wide && w.row_tiles > 1) {
     wait_cap(&c.qfull[rt ^ 1], At::of(at.items, rt ^ 1) & 1, &c.abort, p.hdr);
     if (At::of(w.tiles, rt ^ 1) > 0) wait_cap(&c.odone[rt ^ 1], At::of(at.some, rt ^ 1) & 1, &c.abort, p.hdr);
   }
-  // (and into the place of row tile 1, which may hold the output of an item before)
-  if (wide && w.row_tiles == 1 && at.items[1] > 0) wait_cap(&c.qfree[1], (at.items[1] - 1) & 1, &c.abort, p.hdr);
   __syncwarp();
   tc_fence_after();
   const float inv = l != 0.f ? 1.f / l : 0.f;   // (0: the row saw no key; a NaN among its scores goes on)

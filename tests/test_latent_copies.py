@@ -10,11 +10,12 @@ from tests.test_verify_protocol import Bar
 
 class InFlight(Prefill):
     """every: a row tile's products wait for its queries in every item that has the row
-    tile, also without key tiles.  back: and hold the next ones back until then."""
+    tile, also without key tiles.  back: and hold the next ones back until then.
+    both: the queries of an item with a wide output wait for what both row tiles wrote."""
 
-    def __init__(self, items, every=True, back=True):
+    def __init__(self, items, every=True, back=True, both=True):
         super().__init__(items)
-        self.every, self.back = every, back
+        self.every, self.back, self.both = every, back, both
         if back:
             self.qfree = [Bar(3) for _ in range(2)]
         self.queue += [[] for _ in range(2 + self.NU)]   # copies on their way, by barrier
@@ -30,6 +31,8 @@ class InFlight(Prefill):
             return items[t] == 0 or (yield from self.ready(self.qfree[t], items[t] - 1))
 
         def queries():
+            if self.both and self.items[i][2] and not (yield from written(1)):
+                return False
             for t in range(rts):
                 if not (yield from written(t)):
                     return False
@@ -74,10 +77,49 @@ class InFlight(Prefill):
                 yield None
         yield from super().products(t, i)
 
+    def rows(self, t, x, i):
+        tiles, items, some, units = self.at(i)
+        n, (_, second, wide) = self.n(i), self.items[i]
+        for j in range(n[t]):
+            yield from self.wait(self.sfull[t], tiles[t] + j)
+            self.check(self.s[t][x] == ("S", i, j), "S read before it is there")
+            if j == 0 or self.agree:
+                yield from self.meet((t, i, j), 2)
+                self.check(self.o[t] == ((i, j - 1) if j else None), "O rescaled under a product")
+            self.s[t][x] = ("P", i, j)
+            self.pready[t].arrive()
+            yield None
+        yield from self.meet((t, i, "sum"), 2)
+        yield from self.wait(self.qfull[t], items[t])
+        if n[t]:
+            yield from self.wait(self.odone[t], some[t])
+        if wide and second is None and items[1] and not self.both:
+            yield from self.wait(self.qfree[1], items[1] - 1)
+        if wide and second is not None:
+            yield from self.wait(self.qfull[1 - t], items[1 - t])
+            if n[1 - t]:
+                yield from self.wait(self.odone[1 - t], some[1 - t])
+        self.check(n[t] == 0 or self.o[t] == (i, n[t] - 1), "output before the last product")
+        self.check(self.q[t] in (i, ("out", i)), "output over other queries")
+        if wide:
+            end = units + self.PER * self.all[i]   # (row tile 1's reaches into the ring)
+            self.check(t == 0 or all(u is None or u < end for u in self.unit), "output over units of the next item")
+            self.check(self.q[1 - t] in (None, "free", i, ("out", i)), "output over another")
+            self.check(second is None or self.o[1 - t] in (None, (i, n[1 - t] - 1)), "output over queries in use")
+        self.q[t] = ("out", i)
+        yield from self.meet((t, i, "out"), 2)
+        yield None
+        self.check(self.q[t] == ("out", i), "the output is gone")
+        yield from self.meet((t, i, "read"), 2)   # (in the kernel the barrier itself counts the warps)
+        self.q[t], self.o[t] = "free", None
+        self.qfree[t].arrive()
+
 
 STREAMS = ITEMS + [[(0, 0, True), (2, 2, False)], [(0, 0, False), (1, 2, False), (0, 0, False), (0, 0, False), (2, 2, False)],
                    [(1, 1, False)] + [(0, 0, False)] * 6 + [(0, None, False)] * 5 + [(1, 2, False)],
-                   [(0, None, True), (3, None, True), (0, 0, True), (0, 1, True), (2, 2, True)]]
+                   [(0, None, True), (3, None, True), (0, 0, True), (0, 1, True), (2, 2, True)],
+                   [(1, 1, False), (0, 1, True)], [(3, None, False), (1, 1, True), (0, 0, False), (0, 0, True)],
+                   [(2, 2, False), (0, 1, True), (1, 1, False), (1, 1, True), (0, None, True)]]
 
 
 @pytest.mark.parametrize("items", STREAMS)
@@ -100,3 +142,10 @@ def test_a_row_tile_without_keys_must_not_be_left_behind():
     with pytest.raises(AssertionError, match="deadlock"):
         for seed in range(400):
             InFlight([(0, 0, False)] * 40, back=False).run(seed)
+
+
+def test_a_wide_output_must_wait_for_both_row_tiles():
+    """A narrow item, then one in pieces of which row tile 0 sees nothing."""
+    with pytest.raises(AssertionError, match="output over another"):
+        for seed in range(400):
+            InFlight([(1, 1, False), (0, 1, True)], both=False).run(seed)
