@@ -228,9 +228,10 @@ __device__ __forceinline__ Work work_of(const ExpandedParams &p, const Share &sh
   Work w;
   w.nrows = min(kRows, sh.len - sh.first);
   w.row_tiles = w.nrows > 128 ? 2 : 1;
-  const int all = tiles_of(p, sh, sh.first + w.nrows - 1), per = (all + sh.pieces - 1) / sh.pieces;
-  w.kt0 = min(all, sh.piece * per);
-  const int end = min(all, w.kt0 + per);
+  // key tiles in equal shares, so that no piece is empty or short of kMinTiles (16 of at most
+  // 2^23 of them)
+  const int all = tiles_of(p, sh, sh.first + w.nrows - 1), end = all * (sh.piece + 1) / sh.pieces;
+  w.kt0 = all * sh.piece / sh.pieces;
   w.all = end - w.kt0;
   w.keys = sh.n - w.kt0 * kKeys;
 #pragma unroll
