@@ -343,13 +343,17 @@ __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all,
 // that is written.  `wide`: that output reached into the ring.  The queries of an item whose
 // own output is wide wait for both row tiles: that output reaches into the place of the
 // other one, whose barriers stand at an item before until its output is written (a wait
-// there for this item's phase would pass at once).  false: a wait has expired.
+// there for this item's phase would pass at once).  false: a wait has expired; `sent` counts
+// what was issued until then, copies of queries by row tile and units.
+struct Sent {
+  uint32_t queries[2], units;
+};
 __device__ __forceinline__ bool role_copy(const ExpandedParams &p, const CUtensorMap *mq, const CUtensorMap *mk,
                                           const CUtensorMap *mr, const CUtensorMap *mv, const Share &sh, const Work &w,
-                                          const At &at, bool wide, uint8_t *smem, PCtl &c) {
+                                          Sent &sent, bool wide, uint8_t *smem, PCtl &c) {
   auto written = [&](int t) {
-    const int n = At::of(at.items, t);
-    return n == 0 || wait_cap(&c.qfree[t], (n - 1) & 1, &c.abort, p.hdr);
+    const uint32_t n = t ? sent.queries[1] : sent.queries[0];
+    return n == 0 || wait_free(&c.qfree[t], (n - 1) & 1, &c.abort, p.hdr);
   };
   auto queries = [&]() {
     if (wide_output(p, sh) && !written(1)) return false;
@@ -358,20 +362,20 @@ __device__ __forceinline__ bool role_copy(const ExpandedParams &p, const CUtenso
       mbar_arrive_expect_tx(&c.qfull[t], 3 * kUnit);
       for (int ch = 0; ch < 3; ++ch)
         tma_3d(smem_u32(smem + (t * 3 + ch) * kUnit), mq, ch * 64, sh.head, sh.start + sh.first + t * 128, &c.qfull[t]);
+      ++(t ? sent.queries[1] : sent.queries[0]);
     }
     return true;
   };
   if (wide && (!written(0) || !written(1))) return false;
   if (w.all == 0) return queries();
-  uint32_t u = at.units;
 #pragma unroll 1
   for (int j = 0; j < w.all; ++j) {
     const int key = sh.key0 + (w.kt0 + j) * kKeys;
 #pragma unroll 1
-    for (int i = 0; i < kPerTile; ++i, ++u) {
-      const uint32_t st = u % kUnits;
+    for (int i = 0; i < kPerTile; ++i, ++sent.units) {
+      const uint32_t u = sent.units, st = u % kUnits;
       if (j == 0 && i == 3 && !queries()) return false;
-      if (u >= kUnits && !wait_cap(&c.empty[st], (u / kUnits - 1) & 1, &c.abort, p.hdr)) return false;
+      if (u >= kUnits && !wait_free(&c.empty[st], (u / kUnits - 1) & 1, &c.abort, p.hdr)) return false;
       const uint32_t dst = smem_u32(smem + kOffRing + st * kUnit);
       mbar_arrive_expect_tx(&c.full[st], kUnit);
       if (i < 2) tma_3d(dst, mk, i * 64, sh.head, key, &c.full[st]);
@@ -408,7 +412,7 @@ __device__ __forceinline__ void stream_copies(const ExpandedParams &p, const CUt
                                               const CUtensorMap *mr, const CUtensorMap *mv, uint32_t redo, Share &next,
                                               int &index, uint8_t *smem, PCtl &c) {
   const int lane = threadIdx.x & 31;
-  At at = {};
+  Sent sent = {};                           // (lane 0's)
   bool ok = true, wide = false;
   for (int turn = 0;; ++turn) {
     Share sh = next;
@@ -431,9 +435,8 @@ __device__ __forceinline__ void stream_copies(const ExpandedParams &p, const CUt
     }
     if (sh.b < 0) break;
     const Work w = work_of(p, sh);
-    if (lane == 0) ok = role_copy(p, mq, mk, mr, mv, sh, w, at, wide, smem, c);
+    if (lane == 0) ok = role_copy(p, mq, mk, mr, mv, sh, w, sent, wide, smem, c);
     ok = __all_sync(0xffffffffu, ok);
-    at.add(w);
     wide = wide_output(p, sh);
     if (FIX) {                              // (the next item is taken late: the last ones go to who is free)
       next.b = -1;
@@ -443,11 +446,12 @@ __device__ __forceinline__ void stream_copies(const ExpandedParams &p, const CUt
       }
     }
   }
-  // nothing lands after the stream's end
+  // nothing lands after the stream's end: the last copies to each place
   if (lane == 0) {
-    for (int t = 0; t < 2; ++t)
-      if (At::of(at.items, t) > 0) drain_wait(&c.qfull[t], (At::of(at.items, t) - 1) & 1);
-    for (uint32_t k = at.units > kUnits ? at.units - kUnits : 0; k < at.units; ++k) drain_wait(&c.full[k % kUnits], (k / kUnits) & 1);
+    if (sent.queries[0] > 0) drain_wait(&c.qfull[0], (sent.queries[0] - 1) & 1);
+    if (sent.queries[1] > 0) drain_wait(&c.qfull[1], (sent.queries[1] - 1) & 1);
+    for (uint32_t k = sent.units > kUnits ? sent.units - kUnits : 0; k < sent.units; ++k)
+      drain_wait(&c.full[k % kUnits], (k / kUnits) & 1);
   }
   __syncwarp();
 }

@@ -34,6 +34,13 @@ __device__ __forceinline__ bool wait_cap(uint64_t *bar, uint32_t parity, int *ab
   return mbar_test(bar, parity) || wait_long(bar, parity, abort, hdr);
 }
 
+// The wait for a place that a copy is to fill.  After a wait has expired the other roles go on
+// without theirs, and their arrivals no longer say that what was copied there before has
+// landed: nothing more is copied then.
+__device__ __forceinline__ bool wait_free(uint64_t *bar, uint32_t parity, int *abort, uint32_t *hdr) {
+  return wait_cap(bar, parity, abort, hdr) && !*reinterpret_cast<volatile int *>(abort);
+}
+
 // the memory of the barriers first .. last is given back, to be initialised anew
 __device__ __forceinline__ void drop_barriers(uint64_t *first, uint64_t *last) {
   for (uint64_t *b = first; b <= last; ++b)

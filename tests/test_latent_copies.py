@@ -11,11 +11,15 @@ from tests.test_verify_protocol import Bar
 class InFlight(Prefill):
     """every: a row tile's products wait for its queries in every item that has the row
     tile, also without key tiles.  back: and hold the next ones back until then.
-    both: the queries of an item with a wide output wait for what both row tiles wrote."""
+    both: the queries of an item with a wide output wait for what both row tiles wrote.
+    stop: nothing is copied once a wait has expired (the arrivals that follow are void).
+    issued: the copies waited for at the end are those that were issued, not all of the
+    items that were begun."""
 
-    def __init__(self, items, every=True, back=True, both=True):
+    def __init__(self, items, every=True, back=True, both=True, stop=True, issued=True):
         super().__init__(items)
-        self.every, self.back, self.both = every, back, both
+        self.every, self.back, self.both, self.stop, self.issued = every, back, both, stop, issued
+        self.sent, self.units, self.begun = [0, 0], 0, 0
         if back:
             self.qfree = [Bar(3) for _ in range(2)]
         self.queue += [[] for _ in range(2 + self.NU)]   # copies on their way, by barrier
@@ -23,7 +27,24 @@ class InFlight(Prefill):
     def land(self, q, f):
         self.queue[2 + q] += [lambda: None] * self.rng.choice((0, 1, 20)) + [f]
 
+    def ready(self, bar, phase):
+        ok = yield from super().ready(bar, phase)
+        return ok and not (self.stop and self.abort)
+
+    def copier(self):
+        yield from super().copier()
+        sent, units = self.sent, self.units
+        if not self.issued:
+            _, sent, _, units = self.at(self.begun)
+        for t in range(2):
+            if sent[t]:
+                yield from self.long_wait(self.qfull[t], sent[t] - 1)
+        for u in range(max(0, units - self.NU), units):
+            yield from self.long_wait(self.full[u % self.NU], u // self.NU)
+        assert not any(self.queue[2:]), "copies in flight at the end"
+
     def copy(self, i, wide):
+        self.begun = i + 1
         tiles, items, _, units = self.at(i)
         rts = 1 if self.items[i][1] is None else 2
 
@@ -44,6 +65,7 @@ class InFlight(Prefill):
                     self.q[t] = i
                     self.qfull[t].arrive()
                 self.land(t, there)
+                self.sent[t] += 1
                 yield None
             return True
         if wide:
@@ -65,6 +87,7 @@ class InFlight(Prefill):
                 self.unit[u % self.NU] = u
                 self.full[u % self.NU].arrive()
             self.land(2 + st, there)
+            self.units += 1
             yield None
         return True
 
@@ -126,6 +149,24 @@ STREAMS = ITEMS + [[(0, 0, True), (2, 2, False)], [(0, 0, False), (1, 2, False),
 def test_copies_that_land_late(items):
     for seed in range(60):
         InFlight(items).run(seed)
+
+
+@pytest.mark.parametrize("items", STREAMS)
+def test_an_expired_wait_leaves_no_copy_in_flight(items):
+    for seed in range(60):
+        InFlight(items).run(seed, expire=seed % 30)
+
+
+def test_copies_must_end_with_an_expired_wait():
+    with pytest.raises(AssertionError, match="in flight"):
+        for seed in range(200):
+            InFlight([(4, 5, False), (2, 3, False), (2, 2, False)], stop=False).run(seed, expire=seed % 30)
+
+
+def test_copies_that_were_never_issued_must_not_be_waited_for():
+    with pytest.raises(AssertionError, match="deadlock|in flight"):
+        for seed in range(60):
+            InFlight([(4, 5, False), (2, 3, False)], issued=False).run(seed, expire=seed % 30)
 
 
 @pytest.mark.parametrize("items", [[(0, 0, True), (2, 2, True)], [(0, 0, False), (1, 1, False)],
