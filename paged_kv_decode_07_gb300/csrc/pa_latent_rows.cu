@@ -179,7 +179,7 @@ __device__ __forceinline__ void role_copy(const AbsorbedParams &p, const CUtenso
       const int id = in ? __ldg(row + key / kBlock) : 0;
       const bool bad = in && (uint32_t)id >= (uint32_t)p.kv.num_blocks;
       const uint32_t dead = __ballot_sync(0xffffffffu, bad);
-      if (g >= G::NS) ok = wait_cap(&c.empty[st], (g / G::NS - 1) & 1, &c.abort, &c.flags);
+      if (g >= G::NS) ok = wait_free(&c.empty[st], (g / G::NS - 1) & 1, &c.abort, &c.flags);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (dead && lane == 0) set_err(&c.flags, PA_ERRF_BAD_BLOCK_ID);
@@ -345,7 +345,7 @@ __device__ __forceinline__ void role_query(const AbsorbedParams &p, const CUtens
   uint32_t piece = 0;
   Piece<G::TK> x(c.run);
   while (x.next(p)) {
-    if (piece > 0 && !wait_cap(&c.qfree, (piece - 1) & 1, &c.abort, &c.flags)) break;
+    if (piece > 0 && !wait_free(&c.qfree, (piece - 1) & 1, &c.abort, &c.flags)) break;
     int rows;
     const long long r0 = group_row(p, x, sub, rows);
     mbar_arrive_expect_tx(&c.qfull, G::QBYTES);   // (rows past the group are its neighbour's, or zeros)

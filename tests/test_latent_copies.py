@@ -1,10 +1,11 @@
-"""The stream of items of the expanded form (csrc/pa_latent_prefill.cu) with copies
-that land later than they are issued, in any order between barriers, under random
-schedules on the CPU.  The model of test_latent_protocol lets them land at once; what
-passes a barrier a phase too early can then not be seen."""
+"""The stream of items of the expanded form (csrc/pa_latent_prefill.cu) and the run of
+pieces of the absorbed one (csrc/pa_latent_rows.cu) with copies that land later than they
+are issued, in any order between barriers, under random schedules on the CPU.  The models
+of test_latent_protocol let them land at once; what passes a barrier a phase too early can
+then not be seen."""
 import pytest
 
-from tests.test_latent_protocol import ITEMS, Prefill
+from tests.test_latent_protocol import ITEMS, PIECES, Prefill, Rows
 from tests.test_verify_protocol import Bar
 
 
@@ -190,3 +191,78 @@ def test_a_wide_output_must_wait_for_both_row_tiles():
     with pytest.raises(AssertionError, match="output over another"):
         for seed in range(400):
             InFlight([(1, 1, False), (0, 1, True)], both=False).run(seed)
+
+
+class RowsInFlight(Rows):
+    """stop: nothing is copied once a wait has expired."""
+
+    def __init__(self, pieces, safe=False, stages=4, early_q=True, stop=True):
+        super().__init__(pieces, False, safe, stages, early_q)
+        self.stop = stop
+        self.queue += [[] for _ in range(1 + stages)]
+
+    def land(self, q, f):
+        self.queue[2 + q] += [lambda: None] * self.rng.choice((0, 1, 20)) + [f]
+
+    def ready(self, bar, phase):
+        yield from self.wait(bar, phase)
+        return bar.ready(phase & 1) and not (self.stop and self.abort)
+
+    def copier(self, which, of):
+        g = 0
+        for _, _, g in self.tiles():
+            st = g % self.NS
+            if g >= self.NS and not (yield from self.ready(self.empty[st], g // self.NS - 1)):
+                break
+            self.check(self.readers[st] == 0, "stage refilled while it is read")
+            self.stage[st], self.readers[st] = ("on its way", g), 2
+
+            def there(g=g):
+                self.stage[g % self.NS] = g
+                self.full[g % self.NS].arrive()
+            self.land(1 + st, there)
+            yield None
+        else:
+            g = sum(1 for _ in self.tiles())
+        yield from self.landed([(self.full[u % self.NS], u // self.NS) for u in range(max(0, g - self.NS), g)])
+        assert not any(self.queue[3:]), "tiles in flight at the end"
+
+    def query(self):
+        sent = 0
+        for i in range(len(self.pieces)):
+            if i and not (yield from self.ready(self.qfree, i - 1)):
+                break
+            self.qsmem = ("on its way", i)
+
+            def there(i=i):
+                self.qsmem = i
+                self.qfull.arrive()
+            self.land(0, there)
+            sent += 1
+            yield None
+        yield from self.landed([(self.qfull, sent - 1)] if sent else [])
+        assert not self.queue[2], "queries in flight at the end"
+
+    def landed(self, last):   # no abort ends these waits
+        for bar, phase in last:
+            while not bar.ready(phase & 1):
+                yield lambda: bar.ready(phase & 1)
+
+
+@pytest.mark.parametrize("pieces", PIECES)
+def test_rows_copies_that_land_late(pieces):
+    for seed in range(60):
+        for safe in (False, True):
+            RowsInFlight(pieces, safe, 4 + seed % 2, seed % 3 > 0).run(seed)
+
+
+@pytest.mark.parametrize("pieces", PIECES)
+def test_rows_an_expired_wait_leaves_no_copy_in_flight(pieces):
+    for seed in range(100):
+        RowsInFlight(pieces, seed % 2 == 0, 4 + seed % 2, seed % 3 > 0).run(seed, expire=seed % 40)
+
+
+def test_rows_copies_must_end_with_an_expired_wait():
+    with pytest.raises(AssertionError, match="in flight"):
+        for seed in range(200):
+            RowsInFlight([3, 1, 6], stop=False).run(seed, expire=seed % 30)
