@@ -591,9 +591,11 @@ int pa_latent_prefill(const pa_latent_prefill_problem *prob, void *ws, size_t ws
  *   out = sum_t softmax(s)_t c_t                       (512 values)
  * seq_lens, flags and padded rows as in pa_verify; keys of a bad block id are
  * skipped.  Weights meet the latents rounded to bf16 (bf16 cache) or fp16
- * (FP8, as the queries and the stored rotated parts do then: up to 65,504,
- * below 2^-14 with fewer bits).  Keys that some tokens of a verify step see
- * and others do not must be finite; slots past seq_lens may hold anything. */
+ * (FP8, as q[0..511] does then: up to 65,504, past which an output is NaN;
+ * below 2^-14 with fewer bits, so that a weight is off by up to 2^-25 of the
+ * largest).  The rotated parts meet as the bf16 values that they are.  Keys
+ * that some tokens of a verify step see and others do not must be finite;
+ * slots past seq_lens may hold anything. */
 typedef struct pa_latent_problem {
   int32_t batch;               /* B >= 0 */
   int32_t num_heads;           /* H, 1..128 */

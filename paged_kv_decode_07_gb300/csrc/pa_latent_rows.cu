@@ -32,7 +32,8 @@
 //
 // Roles: four softmax warps (they also put the queries into tensor memory and write the
 // output), a warp for each product, one that copies queries, one that copies pages or,
-// FP8, eight that turn codes into f16 (exact).  Hand-offs are mbarriers; waits are capped.
+// FP8, eight that turn codes into f16 (exact; the rotated parts go as they are, a kind of
+// instruction of their own, into the same sums).  Hand-offs are mbarriers; waits are capped.
 #include "pa_latent_decode.cuh"
 
 namespace pa {
@@ -83,7 +84,8 @@ static_assert(sizeof(Ctl) <= 2048, "Geo::SMEM leaves 2 KB");
 template <bool FP8, int N, bool SAFE>
 __device__ void role_scores(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uint32_t tmem) {
   using G = Geo<FP8, N>;
-  constexpr uint32_t IQK = idesc_of(!FP8, G::M, G::TK, false, false);
+  // (the rotated part is bf16 in both caches and stays so)
+  constexpr uint32_t IQK = idesc_of(!FP8, G::M, G::TK, false, false), IQR = idesc_of(true, G::M, G::TK, false, false);
   const uint32_t lead = elect_one();
   const uint64_t dQ = sdesc(smem_u32(smem), 16, 1024);
   const uint64_t dK = sdesc(smem_u32(smem + G::OFF_K), 16, 8192);
@@ -108,10 +110,11 @@ __device__ void role_scores(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uint
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           const uint64_t kb = ch < 8 ? dK + at + (uint64_t)((ch * 1024 + ks * 32) >> 4) : dR + at + (uint64_t)((ks * 32) >> 4);
+          const uint32_t kind = ch < 8 ? IQK : IQR;
           if (ch < G::NT)
-            mma_ts_if(lead, d, tmem + ch * 32 + ks * 8, kb, IQK, ch + ks > 0 ? 1u : 0u);
+            mma_ts_if(lead, d, tmem + ch * 32 + ks * 8, kb, kind, ch + ks > 0 ? 1u : 0u);
           else
-            mma_ss_if(lead, d, dQ + (uint64_t)((ch * G::QCHUNK + ks * 32) >> 4), kb, IQK, 1u);
+            mma_ss_if(lead, d, dQ + (uint64_t)((ch * G::QCHUNK + ks * 32) >> 4), kb, kind, 1u);
         }
       commit_if(lead, &c.sfull[g & 1]);
     }
@@ -322,7 +325,7 @@ __device__ __forceinline__ void role_dequant(const AbsorbedParams &p, uint8_t *s
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = (u >> 3) + 16 * i;
-      const uint4 h = bf16x8_to_h(v.rr[i]);
+      const uint4 h = v.rr[i];
       sts_u4(dst + G::LAT + r * 128 + (((u & 7) ^ (r & 7)) << 4), h.x, h.y, h.z, h.w);
     }
     if (u == 0) {
@@ -377,7 +380,8 @@ __device__ void role_softmax(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uin
     const long long r_out = group_row(p, x, sub, rows);
     const int first_row = (x.set * p.S + sub) * p.R;
     // ---- the queries: the first chunks into tensor memory (the products with the last
-    // ones are complete: their scores have been read), FP8: the others to f16 in place
+    // ones are complete: their scores have been read), FP8: the others to f16 in place (of the
+    // latents; the rotated part meets bf16)
     wait_cap(&c.qfull, piece & 1, &c.abort, &c.flags);
     if (act) {
       const int r = w * RPW + (lane & (RPW - 1));
@@ -388,7 +392,7 @@ __device__ void role_softmax(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uin
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 u = lds_u4(q + (k >> 1) * G::QCHUNK + ((((k & 1) * 4 + i) ^ (r & 7)) << 4));
-          if (FP8) u = bf16x8_to_h(u);
+          if (FP8 && k < 16) u = bf16x8_to_h(u);
           v[4 * i] = u.x;
           v[4 * i + 1] = u.y;
           v[4 * i + 2] = u.z;
@@ -397,7 +401,7 @@ __device__ void role_softmax(const AbsorbedParams &p, uint8_t *smem, Ctl &c, uin
         tmem_st16(tmem + lane_off + k * 16, v);
       }
       if (FP8 && G::NT < 9) {
-        for (int i = lane; i < (9 - G::NT) * 8 * RPW; i += 32) {   // 16-byte pieces of the warp's rows
+        for (int i = lane; i < (8 - G::NT) * 8 * RPW; i += 32) {   // 16-byte pieces of the warp's rows
           const uint32_t at = smem_u32(smem) + (G::NT + i / (8 * RPW)) * G::QCHUNK + (w * RPW + i / 8 % RPW) * 128 + (i & 7) * 16;
           const uint4 h = bf16x8_to_h(lds_u4(at));
           sts_u4(at, h.x, h.y, h.z, h.w);

@@ -743,7 +743,8 @@ class LatentCache:
 
     dtype "bf16": latent bf16 [NB, 16, 512], rope bf16 [NB, 16, 64]; "fp8":
     latent uint8 (E4M3 codes), rope bf16, a value being the stored one times
-    scale in both."""
+    scale in both.  A scale chosen for the latents (their largest over 448) does
+    for both: the rotated part keeps bf16's range wherever it is read."""
     dtype: str
     latent: torch.Tensor
     rope: torch.Tensor
@@ -892,7 +893,12 @@ def latent_decode(kv: LatentCache, q, block_tables, seq_lens, softmax_scale, *, 
     """The absorbed form of latent attention over the paged cache: q bf16 [B,
     Q, H, 576] (the query times W_K, 512 dims, beside its 64 rotated ones) of
     the last Q tokens of each sequence, causal among them -> (out [B, Q, H,
-    512], [lse,] workspace).  A workspace that is too small is replaced."""
+    512], [lse,] workspace).  A workspace that is too small is replaced.
+
+    Over an FP8 cache q's 512 dims and the weights pass through fp16: q up to
+    65,504 (past that the output is NaN), weights off by up to 2^-25 of the
+    largest.  Over a bf16 one weights are rounded to bf16.  Keys that only some
+    of the Q tokens see must be finite."""
     if stream is None:
         r = (_ext or _fast()).latent_decode(
             DTYPE_CODES[kv.dtype], kv.block_size, kv.latent, kv.rope, kv.scale, q, block_tables, seq_lens,
