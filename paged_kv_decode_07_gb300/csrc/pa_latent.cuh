@@ -14,6 +14,8 @@ constexpr int kNope = 128;            // expanded: key dims of a head beside the
 constexpr int kQk = kNope + kRope;    // all of them,
 constexpr int kV = 128;               // and value dims
 constexpr int kMaxHeads = 128;
+// CTAs at once: one per SM of this GPU (another count would only split the work worse)
+constexpr int kSms = 152;
 
 struct LatentView {
   int dtype, num_blocks;

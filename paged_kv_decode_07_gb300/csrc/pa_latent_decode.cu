@@ -6,9 +6,6 @@ namespace pa {
 namespace lat {
 namespace {
 
-// CTAs at once: one per SM of this GPU (another count would only split the work worse)
-constexpr int kSms = 152;
-
 // ----------------------------------------------------------------- the join
 
 // W warps a row (four: a CTA each; one: four rows a CTA): zeros where there is no key, the

@@ -206,12 +206,12 @@ __device__ __forceinline__ uint4 bf16x8_to_h(const uint4 &u) {
   return make_uint4(tc::f2_to_h2(a.x, a.y), tc::f2_to_h2(b.x, b.y), tc::f2_to_h2(d.x, d.y), tc::f2_to_h2(e.x, e.y));
 }
 
-// the cache in pages as [2 row groups][chunks of 64 dims][8 rows][64 dims], `chunks` of
-// them a copy, and its rotated parts
-inline bool cache_maps(const AbsorbedParams &p, CUtensorMap *mc, CUtensorMap *mr, uint32_t chunks) {
+// the cache in pages as [2 row groups][8 chunks of 64 dims][8 rows][64 dims], a page a copy,
+// and its rotated parts
+inline bool cache_maps(const AbsorbedParams &p, CUtensorMap *mc, CUtensorMap *mr) {
   const uint64_t nb = (uint64_t)p.kv.num_blocks;
   const uint64_t dc[4] = {64, 8, 8, nb * 2}, sc[3] = {kLatent * 2, 128, 8 * kLatent * 2};
-  const uint32_t bc[4] = {64, 8, chunks, 2};
+  const uint32_t bc[4] = {64, 8, 8, 2};
   const uint64_t dr[2] = {kRope, nb * kBlock}, sr[1] = {kRope * 2};
   const uint32_t br[2] = {kRope, kBlock};
   return make_map(mc, p.kv.latent, 4, dc, sc, bc) && make_map(mr, p.kv.rope, 2, dr, sr, br);

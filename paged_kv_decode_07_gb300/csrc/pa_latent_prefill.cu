@@ -71,8 +71,6 @@ struct PCtl {
 };
 static_assert(sizeof(PCtl) <= 2048 && kSmem + 2048 <= 227 * 1024, "shared memory");
 
-// CTAs at once: one per SM of this GPU (another count would only split the work worse)
-constexpr int kSms = 152;
 constexpr int kMinTiles = 8;                // key tiles of a piece at least
 
 // Long sequences: heads go in groups of just so many that the tiles of a group fill the

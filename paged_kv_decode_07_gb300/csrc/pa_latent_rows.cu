@@ -636,7 +636,7 @@ cudaError_t launch_n(const AbsorbedParams &p, cudaStream_t s) {
   CUtensorMap mq, mc, mr;
   std::memset(&mc, 0, sizeof mc);
   std::memset(&mr, 0, sizeof mr);
-  if (!query_map(p, &mq, N) || (!FP8 && !cache_maps(p, &mc, &mr, 8))) return cudaErrorInvalidValue;
+  if (!query_map(p, &mq, N) || (!FP8 && !cache_maps(p, &mc, &mr))) return cudaErrorInvalidValue;
   auto kern = latent_rows_kernel<FP8, N>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;

@@ -94,21 +94,9 @@ __host__ __device__ constexpr uint32_t idesc_of(bool bf16, int M, int N, bool a_
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 16 lanes x 64 or 32 columns of the accumulator of an M = 64 product (its rows 16
-// w .. lie in lanes 32 w .. + 15 of warp w): v[4 i + j] is row lane / 4 + 8 (j / 2),
-// column 8 i + 2 (lane % 4) + j % 2
-__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      " tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
+// 16 lanes x 32 columns of the accumulator of an M = 64 product (its rows 16 w .. lie in
+// lanes 32 w .. + 15 of warp w): v[4 i + j] is row lane / 4 + 8 (j / 2), column 8 i +
+// 2 (lane % 4) + j % 2
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
