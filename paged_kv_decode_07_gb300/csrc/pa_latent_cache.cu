@@ -11,10 +11,13 @@
 // pairs, so that eight sines and cosines serve every head.  Each lane computes one
 // pair's and shuffles hand them out (eight a lane: 8,191 tokens 34.8 us, 31.4 so).
 //
-// Both kernels move bytes and are bound by HBM where there are many rows (8,191 tokens
-// with 64 heads' queries: 31.4 us, 0.72 of the copy's rate; a bare copy of such 128-byte
-// pieces, at any distance, takes 0.76 to 0.8; 4 x 32,768 rows read back: 49.3 us, 0.90), by launch and two or three
-// dependent memory latencies where there are few (one token 3.7 us, 255 tokens 7 to 9).
+// Both kernels move bytes.  Many rows are bound by HBM: 8,191 tokens with 64 heads'
+// queries 31.3 us, 0.72 of the copy's rate (FP8 cache: 31.6; a bare copy of pieces of 128
+// bytes that lie apart takes 0.76 to 0.8 of it); 4 x 32,768 rows read back 49.2 us, 0.90
+// (FP8, 0.78 of the bytes: 41 us, 0.84).  Few rows are bound by launch and by latencies one
+// after another: the slot and position, the rows, the write (one token 3.7 us; 255 tokens 7,
+// or 3.7 where L2 holds their rows already), or the starts, the search among them (a load
+// a step), the table, the rows (five sequences 6 to 7).
 #include "pa_codec.cuh"
 #include "pa_latent.cuh"
 #include "pa_rotate.cuh"

@@ -107,7 +107,9 @@ DecodePlan plan_latent_decode(int B, int Q, int H, int max_seq_len) {
   d.RG = groups <= 8 ? groups : (groups + 7) / 8 * 8;
   d.S = groups <= 8 ? groups : 8;
   d.R = (rows + d.RG - 1) / d.RG;
-  d.least = 4;   // (one sequence of 1,000 keys, 20 heads: runs of 2, 3, 4, 6 or 8 tiles 13.5, 13.1, 12.8, 13.3 or 13.9 us)
+  // one sequence of 1,000 keys, 20 heads: runs of 2, 3, 4, 6 or 8 tiles 13.5, 13.1, 12.8, 13.3 or
+  // 13.9 us.  (Many short sequences pay for it: 64 of 32 keys, four to a worker, take 23 us.)
+  d.least = 4;
   const long long tiles = (long long)B * (d.RG / d.S) * ((max_seq_len + 31LL) / 32), runs = (tiles + d.least - 1) / d.least;
   const long long most = kSms / d.S;
   d.workers = (int)(runs < 1 ? 1 : runs < most ? runs : most);

@@ -13,6 +13,8 @@ constexpr int kMaxStages = 5;
 // (no maximum to agree on, no output to rescale, in any tile); where they sum to more
 // than this in a thread and tile, the worker goes over its run again, each piece twice:
 // for its maximum, then for its output.  fp16 weights hold 2^15, bf16 and fp32 2^127.
+// One row of a run is enough.  64 sequences of 128 heads, a late key of each 18 (FP8) or 34
+// nats (bf16) above the others for one head: 318 us instead of 127, 248 instead of 105.
 template <bool FP8>
 constexpr float kMost = FP8 ? 0x1p13f : 0x1p32f;
 

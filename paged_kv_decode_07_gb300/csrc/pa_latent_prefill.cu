@@ -24,8 +24,10 @@
 // What bounds it.  4,096 tokens over 16,384 keys, 32 heads: 772 us, 1,556 TFLOP/s of 1,908
 // measured for a library product: a pair of tiles takes 2,700 cycles, of which the products
 // take 2,600, and power counts when sustained.  Eight chunks of up to 2,048 tokens over up
-// to 4,096 keys: 158 us of 97; row tiles that are not full, hidden parts of tiles, and the
-// outputs.
+// to 4,096 keys: 158 us of 97.  Row tiles that are not full and hidden parts of tiles are
+// 11 % more work than the pairs; at the long prompt's pace all of it would take 131 us.
+// The rest: one item in five has a single row tile, whose softmax has no products of
+// another to pass under (8 % of the work), and every item its start and its output.
 //
 // Roles: four softmax groups (two a row tile, 64 of a tile's keys each), a warp per
 // row tile that issues its products, a warp that copies.  Hand-offs are mbarriers;
@@ -495,9 +497,9 @@ __device__ __forceinline__ void stream_mma(const ExpandedParams &p, int t, uint8
 // FIX: weights relative to the row's maximum over its first tile, whatever follows.
 // bf16 and fp32 hold 2^+-126, so a later score may well pass it; where 64 weights sum
 // to more than 2^32 the item is taken again, with a running maximum, when the batch of
-// items ends.  (With one,
-// the two warps of a row agree on it in every tile: 4,096 tokens over 16,384 keys 970 us
-// instead of 857.)
+// items ends.  (With one, the two warps of a row agree on it in every tile: 4,096 tokens
+// over 16,384 keys 970 us instead of 857.  Taken again, one item of the 512: 950 us of
+// 725 on the same GPU; all of them 1,510.)
 template <bool FIX>
 __device__ void role_softmax(const ExpandedParams &p, const Share &sh, const Work &w, uint8_t *smem, PCtl &c,
                              uint32_t tmem, const At &at, int turn) {
@@ -862,7 +864,8 @@ bool map_heads(CUtensorMap *m, const void *base, int dims, int heads, int count,
 
 // Partial rows that a call may need: none where items have no keys for two pieces, or
 // fill the GPU and are short (below 64 key tiles the pieces and their join cost what they
-// save: eight chunks of up to 4,096 keys 169 -> 178 us).
+// save: eight chunks of up to 4,096 keys 169 -> 178 us).  The host knows the average alone:
+// one long sequence among many short ones is not taken in pieces.
 long long latent_prefill_parts(int B, int H, int T, int N) {
   const bool few = 2 * ((long long)T / kRows + B) * H <= kSms;
   const long long least = few ? 2 * kMinTiles : 64;

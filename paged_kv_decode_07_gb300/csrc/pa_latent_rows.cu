@@ -24,11 +24,15 @@
 // pieces of a sequence that several workers share are joined by their log-sum-exp
 // in a second kernel.
 //
-// What bounds it.  16 or 32 rows: HBM, 1,415 cycles a tile and SM (32 sequences of 1K to
-// 32K keys, 24 heads: 67 us with the join, 49 at the copy's rate; the rest is the first
-// copies and the pieces' ends).  64 rows: shared memory; a tile's operands take 1,195
-// cycles to read, of 1,285 (8 verify tokens at 4 x 64K keys, 24 heads: 124 us), and with an
-// FP8 cache its conversion 600 more (64 sequences, 128 heads: 126 us).
+// What bounds it.  16 or 32 rows, bf16: HBM, 1,415 cycles a tile and SM (32 sequences of 1K
+// to 32K keys, 24 heads: 67 us with the join, 49 at the copy's rate; the rest is the first
+// copies and the pieces' ends).  FP8: the conversion, for it takes as long with 0.56 of the
+// bytes (70 us; 32 sequences of 16,384 keys, 16 heads: 99 us both, 0.90 and 0.50 of HBM).
+// 64 rows: shared memory for the most part; by a trace a tile's operands take 1,195 cycles to
+// read, of 1,285 (8 verify tokens at 4 x 64K keys, 24 heads: 124 to 127 us, FP8 153), and an
+// FP8 cache's conversion 600 more (64 sequences, 128 heads: 127 us, bf16 105).  The counters
+// of the same calls have L1 and shared memory at 66 and 52 %, the tensor pipe at 64 and 44 %:
+// they leave room for hand-offs between the roles.
 //
 // Roles: four softmax warps (they also put the queries into tensor memory and write the
 // output), a warp for each product, one that copies queries, one that copies pages or,

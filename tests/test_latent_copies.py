@@ -3,6 +3,8 @@ pieces of the absorbed one (csrc/pa_latent_rows.cu) with copies that land later 
 are issued, in any order between barriers, under random schedules on the CPU.  The models
 of test_latent_protocol let them land at once; what passes a barrier a phase too early can
 then not be seen."""
+import random
+
 import pytest
 
 from tests.test_latent_protocol import ITEMS, PIECES, Prefill, Rows
@@ -150,6 +152,23 @@ STREAMS = ITEMS + [[(0, 0, True), (2, 2, False)], [(0, 0, False), (1, 2, False),
 def test_copies_that_land_late(items):
     for seed in range(60):
         InFlight(items).run(seed)
+
+
+def some_items(rng):
+    """Row tile 1 sees as many key tiles as row tile 0, or one more; wide or not, or mixed."""
+    wide, items = rng.choice((False, True, None)), []
+    for _ in range(rng.randint(2, 9)):
+        n = rng.choice((0, 0, 1, 2, 3))
+        items.append((n, rng.choice((None, n, n + 1)), rng.random() < 0.4 if wide is None else wide))
+    return items
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_any_stream(seed):
+    items = some_items(random.Random(seed))
+    for k in range(20):
+        InFlight(items).run(k)
+        InFlight(items).run(k, expire=3 * k)
 
 
 @pytest.mark.parametrize("items", STREAMS)
