@@ -57,3 +57,28 @@ def test_a_written_row_is_attended():
     ref, rl, bound = L.decode_reference("fp8", L.values("fp8", kv.latent, kv.rope, kv.scale), q, [T], tables, SCALE)
     L.within(o, ref, bound)
     L.lse_within(lse, rl)
+
+
+@pytest.mark.parametrize("fmt,nb", [("bf16", 300_000), ("fp8", 600_000)])
+def test_pages_past_four_gigabytes(fmt, nb):
+    """Rows written, read back and attended in the last pages of a pool of 4.9 GB."""
+    T, H = 100, 20
+    g = torch.Generator(DEV).manual_seed(4)
+    dt = torch.bfloat16 if fmt == "bf16" else torch.uint8
+    kv = pa.LatentCache(fmt, torch.zeros((nb, 16, 512), dtype=dt, device=DEV),
+                        torch.zeros((nb, 16, 64), dtype=torch.bfloat16, device=DEV), 1.0 if fmt == "bf16" else 2.0 ** -6)
+    tables = (nb - 1 - torch.randperm(7, device=DEV, generator=g)).to(torch.int32)[None]
+    t = torch.arange(T, device=DEV)
+    slots = tables[0, t // 16].long() * 16 + t % 16
+    rows = torch.randn((T, 576), device=DEV, generator=g).bfloat16()
+    inv, _ = pa.rope_frequencies(64, device=DEV)
+    pa.latent_append(kv, rows[:, :512], rows[:, 512:], t.int(), slots, inv)
+    # the same rows in the first pages of a small pool
+    few = pa.LatentCache(fmt, kv.latent[:8].clone(), kv.rope[:8].clone(), kv.scale)
+    ids = torch.arange(7, dtype=torch.int32, device=DEV)[None]
+    pa.latent_append(few, rows[:, :512], rows[:, 512:], t.int(), t, inv)
+    q = torch.randn((1, 1, H, 576), device=DEV, generator=g).bfloat16()
+    sl = torch.tensor([T], dtype=torch.int32, device=DEV)
+    for f in (lambda c, i: pa.latent_gather(c, i, L.starts_of([T]), T), lambda c, i: pa.latent_decode(c, q, i, sl, SCALE)[:1]):
+        assert all(torch.equal(x, y) and x.any() for x, y in zip(f(kv, tables), f(few, ids)))
+    assert not kv.latent[:1000].any()
