@@ -267,7 +267,10 @@ struct At {
 // S of the two row tiles takes turns, row tile 0 first: left alone they run in step,
 // both at their products and then both at their softmax (5,500 cycles a pair of
 // tiles, of which the products take 2,570).  Row tile 0 begins an item when row tile 1
-// has issued its last S of the one before.  The queries are there: the caller has waited.
+// has issued its last S of the one before.  (The turns guard no memory: a row tile that
+// sees a tile more than the other one passes over a phase, and the next turn may come
+// early.  Nor can one be missed for good: the ring holds less than two tiles.)  The queries
+// are there: the caller has waited.
 __device__ void role_mma(const ExpandedParams &p, int t, int n, int n0, int all, int keys, const At &at, uint8_t *smem,
                          PCtl &c, uint32_t tmem) {
   constexpr uint32_t IQK = idesc_of(true, 128, 128, false, false), IPV = idesc_of(true, 128, 64, false, true);
